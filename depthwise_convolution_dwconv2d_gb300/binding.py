@@ -27,10 +27,16 @@ SYMBOLS = ("dwconv2d_output_shape", "dwconv2d_fwd", "dwconv2d_bwd_data",
            "dwconv_device_timeouts", "dwconv_wait_selftest", "dwconv2d_fwd_epilogue",
            "dwconv2d_fwd_nhwc", "dwconv2d_separable_nhwc", "dwconv2d_separable_plan_name",
            "dwconv2d_filter_cache_size", "dwconv2d_filter_cache_build", "dwconv2d_fwd_cached",
-           "dwconv2d_bwd_data_cached")
+           "dwconv2d_bwd_data_cached", "dwconv_act8_encode", "dwconv_act8_decode",
+           "dwconv2d_group_norm_nhwc_workspace_size", "dwconv2d_group_norm_nhwc", "dwconv2d_group_norm_nhwc_bwd",
+           "dwconv2d_group_norm_nhwc_plan_name", "dwconv2d_bwd_nhwc_workspace_size", "dwconv2d_bwd_nhwc",
+           "dwconv2d_bwd_nhwc_plan_name")
 
-# dwconv_act_t
-ACTS = {"none": 0, "relu": 1, "relu6": 2}
+# dwconv_act_t (the fused forward epilogue has the first three)
+ACTS = {"none": 0, "relu": 1, "relu6": 2, "silu": 3, "gelu": 4}
+
+# dwconv_act8_kind_t
+ACT8_KINDS = {"i8": 0, "e4m3": 1}
 
 
 class DwconvError(RuntimeError):
@@ -53,6 +59,24 @@ class Desc(ctypes.Structure):
 assert ctypes.sizeof(Desc) == 88
 
 
+class Act8(ctypes.Structure):
+    """dwconv_act8_t (40 bytes); ``make_act8`` also keeps its tensors alive."""
+    _fields_ = [("rows", ctypes.c_int64), ("C", ctypes.c_int64), ("kind", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class NormDesc(ctypes.Structure):
+    """dwconv2d_norm_desc_t (80 bytes)."""
+    _fields_ = [("N", ctypes.c_int64), ("H", ctypes.c_int64), ("W", ctypes.c_int64), ("C", ctypes.c_int64),
+                ("groups", ctypes.c_int32), ("act", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x_c_offset", ctypes.c_int64), ("x_c_total", ctypes.c_int64),
+                ("y_c_offset", ctypes.c_int64), ("y_c_total", ctypes.c_int64)]
+
+
+assert ctypes.sizeof(Act8) == 40
+assert ctypes.sizeof(NormDesc) == 80
+
+
 def _pair(v):
     return (v, v) if isinstance(v, int) else (int(v[0]), int(v[1]))
 
@@ -65,6 +89,26 @@ def make_desc(N, C, H, W, kernel=3, stride=1, pad=0, dilation=1, multiplier=1, d
     dh, dw = _pair(dilation)
     return Desc(N, C, H, W, multiplier, kh, kw, sh, sw, ph, pw, dh, dw,
                 DTYPES[dtype] if isinstance(dtype, str) else int(dtype), out_c_offset, out_c_total)
+
+
+def make_act8(kind, block, codes, scales, rows=None, C=None) -> Act8:
+    """An 8-bit checkpoint over ``codes`` ([..., C], one byte each) and
+    ``scales`` ([..., ceil(C / block)], fp32); ``rows`` and ``C`` are read from
+    the shape of ``codes`` unless it is a raw address."""
+    if C is None:
+        C = codes.shape[-1]
+    if rows is None:
+        rows = codes.numel() // C if C else 0
+    t = Act8(rows, C, ACT8_KINDS[kind] if isinstance(kind, str) else int(kind), block, _ptr(codes), _ptr(scales))
+    t.tensors = (codes, scales)
+    return t
+
+
+def make_norm_desc(N, H, W, C, groups, act="none", eps=1e-5, dtype="f32", x_c_offset=0, x_c_total=0,
+                   y_c_offset=0, y_c_total=0) -> NormDesc:
+    return NormDesc(N, H, W, C, groups, ACTS[act] if isinstance(act, str) else int(act),
+                    DTYPES[dtype] if isinstance(dtype, str) else int(dtype), eps, x_c_offset, x_c_total,
+                    y_c_offset, y_c_total)
 
 
 _lib = None
@@ -115,9 +159,22 @@ def load():
     lib.dwconv2d_filter_cache_build.argtypes = [P, ctypes.c_int, vp, vp, ctypes.c_size_t, vp]
     lib.dwconv2d_fwd_cached.argtypes = [P, vp, vp, ctypes.c_size_t, vp, vp, vp]
     lib.dwconv2d_bwd_data_cached.argtypes = [P, vp, vp, ctypes.c_size_t, vp, ctypes.c_int, vp]
+    A, G, sz, i64 = ctypes.POINTER(Act8), ctypes.POINTER(NormDesc), ctypes.c_size_t, ctypes.c_int64
+    lib.dwconv_act8_encode.argtypes = [vp, A, i64, ctypes.c_int, vp]
+    lib.dwconv_act8_decode.argtypes = [A, vp, i64, ctypes.c_int, vp]
+    lib.dwconv2d_group_norm_nhwc_workspace_size.argtypes = [G, ctypes.c_int]
+    lib.dwconv2d_group_norm_nhwc_workspace_size.restype = sz
+    lib.dwconv2d_group_norm_nhwc.argtypes = [G, vp, vp, vp, vp, vp, vp, vp, sz, A, vp]
+    lib.dwconv2d_group_norm_nhwc_bwd.argtypes = [G, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, A, vp]
+    lib.dwconv2d_group_norm_nhwc_plan_name.argtypes = [G, ctypes.c_int]
+    lib.dwconv2d_group_norm_nhwc_plan_name.restype = ctypes.c_char_p
+    lib.dwconv2d_bwd_nhwc_workspace_size.argtypes = [P]
+    lib.dwconv2d_bwd_nhwc_workspace_size.restype = sz
+    lib.dwconv2d_bwd_nhwc.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, sz, A, ctypes.c_int, vp]
+    lib.dwconv2d_bwd_nhwc_plan_name.argtypes = [P]
+    lib.dwconv2d_bwd_nhwc_plan_name.restype = ctypes.c_char_p
     for name in SYMBOLS:
-        if name not in ("dwconv2d_bwd_weight_workspace_size", "dwconv_status_string", "dwconv2d_plan_name",
-                        "dwconv2d_multi_plan_name", "dwconv2d_separable_plan_name", "dwconv2d_filter_cache_size"):
+        if not name.endswith(("_size", "_string", "_plan_name")):
             getattr(lib, name).restype = st
     _lib = lib
     return lib
@@ -247,6 +304,76 @@ def dwconv2d_bwd_data_cached(desc: Desc, gy, cache, gx, accumulate=0, cache_byte
         cache_bytes = _nbytes(cache)
     _check(load().dwconv2d_bwd_data_cached(ctypes.byref(desc), _ptr(gy), _ptr(cache), int(cache_bytes), _ptr(gx),
                                            int(accumulate), _stream(stream)), "dwconv2d_bwd_data_cached")
+
+
+def _dtype_of(x, dtype):
+    if dtype is None:
+        dtype = {"float32": "f32", "float16": "f16", "bfloat16": "bf16"}[str(x.dtype).rpartition(".")[2]]
+    return DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+
+
+def _ref(x8):
+    return None if x8 is None else ctypes.byref(x8)
+
+
+def dwconv_act8_encode(x, x8: Act8, x_c_total=0, dtype=None, stream=None):
+    """``dtype`` is x's own unless x is a raw address."""
+    _check(load().dwconv_act8_encode(_ptr(x), _ref(x8), int(x_c_total), _dtype_of(x, dtype), _stream(stream)),
+           "dwconv_act8_encode")
+
+
+def dwconv_act8_decode(x8: Act8, x, x_c_total=0, dtype=None, stream=None):
+    """``dtype`` is x's own unless x is a raw address."""
+    _check(load().dwconv_act8_decode(_ref(x8), _ptr(x), int(x_c_total), _dtype_of(x, dtype), _stream(stream)),
+           "dwconv_act8_decode")
+
+
+def dwconv2d_group_norm_nhwc_workspace_size(desc: NormDesc, pass_: int) -> int:
+    """Bytes of workspace of pass 0 (forward) or 1 (backward)."""
+    return int(load().dwconv2d_group_norm_nhwc_workspace_size(ctypes.byref(desc), int(pass_)))
+
+
+def dwconv2d_group_norm_nhwc(desc: NormDesc, x, gamma, beta, y, mean, rstd, workspace, workspace_bytes=None,
+                             x8=None, stream=None):
+    """x [N, H, W, x_c_total], y [N, H, W, y_c_total]; mean and rstd [N, groups] fp32."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    _check(load().dwconv2d_group_norm_nhwc(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(y),
+                                           _ptr(mean), _ptr(rstd), _ptr(workspace), int(workspace_bytes),
+                                           _ref(x8), _stream(stream)), "dwconv2d_group_norm_nhwc")
+
+
+def dwconv2d_group_norm_nhwc_bwd(desc: NormDesc, x, gy, gamma, beta, mean, rstd, gx, ggamma, gbeta, workspace,
+                                 workspace_bytes=None, x8=None, stream=None):
+    """Either ``x`` or its checkpoint ``x8``."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    _check(load().dwconv2d_group_norm_nhwc_bwd(ctypes.byref(desc), _ptr(x), _ptr(gy), _ptr(gamma), _ptr(beta),
+                                               _ptr(mean), _ptr(rstd), _ptr(gx), _ptr(ggamma), _ptr(gbeta),
+                                               _ptr(workspace), int(workspace_bytes), _ref(x8),
+                                               _stream(stream)), "dwconv2d_group_norm_nhwc_bwd")
+
+
+def dwconv2d_group_norm_nhwc_plan_name(desc: NormDesc, pass_: int) -> str:
+    return load().dwconv2d_group_norm_nhwc_plan_name(ctypes.byref(desc), int(pass_)).decode()
+
+
+def dwconv2d_bwd_nhwc_workspace_size(desc: Desc) -> int:
+    return int(load().dwconv2d_bwd_nhwc_workspace_size(ctypes.byref(desc)))
+
+
+def dwconv2d_bwd_nhwc(desc: Desc, x, gy, w, gx, gw, gbias, workspace, workspace_bytes=None, x8=None, accumulate=0,
+                      stream=None):
+    """x [N, H, W, C] or its checkpoint ``x8``, gy [N, Ho, Wo, out_c_total], gx like x."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    _check(load().dwconv2d_bwd_nhwc(ctypes.byref(desc), _ptr(x), _ptr(gy), _ptr(w), _ptr(gx), _ptr(gw), _ptr(gbias),
+                                    _ptr(workspace), int(workspace_bytes), _ref(x8), int(accumulate),
+                                    _stream(stream)), "dwconv2d_bwd_nhwc")
+
+
+def dwconv2d_bwd_nhwc_plan_name(desc: Desc) -> str:
+    return load().dwconv2d_bwd_nhwc_plan_name(ctypes.byref(desc)).decode()
 
 
 def _desc_array(descs):

@@ -7,11 +7,13 @@
 // "DirectConv", reduced to fixed shape rules), and enqueues the launches on
 // the caller's stream. No allocation, no synchronisation, no global mutable
 // state.
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 
 #include "common.cuh"
 #include "nhwc.h"
+#include "norm.h"
 #include "plan.h"
 
 namespace dwconv {
@@ -338,6 +340,196 @@ dwconv_status_t dwconv2d_bwd_data_cached(const dwconv2d_desc_t* desc, const void
   DW_TRY(check_ptr(gy, 16, true));
   DW_TRY(check_ptr(gx, esize(c.dtype), true));
   return cuda_status(ibc::run(c, true, gy, cache, nullptr, gx, accumulate != 0, stream));
+}
+
+// ---- channels-last training -------------------------------------------------
+
+namespace {
+
+constexpr int64_t kMaxChannels = int64_t(1) << 20;
+
+// A checkpoint's geometry and pointers, against the rows and channels that
+// its user expects.
+dwconv_status_t make_act8(const dwconv_act8_t* d, int64_t rows, int64_t C, Act8* t) {
+  if (!d || d->rows != rows || d->C != C) return DWCONV_ERR_INVALID_ARG;
+  if (d->kind != DWCONV_ACT8_I8 && d->kind != DWCONV_ACT8_E4M3) return DWCONV_ERR_UNSUPPORTED;
+  if (d->block < 1) return DWCONV_ERR_INVALID_ARG;
+  if (d->block != 32 && d->block != 64 && d->block != 128) return DWCONV_ERR_UNSUPPORTED;
+  if (rows > 0) {
+    DW_TRY(check_ptr(d->codes, 1, true));
+    DW_TRY(check_ptr(d->scales, 4, true));
+  }
+  t->codes = (uint8_t*)d->codes;
+  t->scales = d->scales;
+  t->src = d->kind == DWCONV_ACT8_I8 ? kSrcI8 : kSrcE4M3;
+  t->shift = d->block == 32 ? 5 : d->block == 64 ? 6 : 7;
+  t->nblk = (int)((C + d->block - 1) / d->block);
+  return DWCONV_OK;
+}
+
+// rows, channels, row distance and type of an encode or decode
+dwconv_status_t make_rows(const dwconv_act8_t* d, int64_t total, int dtype, int64_t* ld, Act8* t) {
+  if (!d || d->rows < 0 || d->C < 1) return DWCONV_ERR_INVALID_ARG;
+  if (dtype != DWCONV_F32 && dtype != DWCONV_F16 && dtype != DWCONV_BF16) return DWCONV_ERR_UNSUPPORTED;
+  if (total != 0 && total < d->C) return DWCONV_ERR_INVALID_ARG;
+  *ld = total == 0 ? d->C : total;
+  if (d->C > kMaxChannels || *ld > kMaxElems || d->rows > kMaxElems / *ld) return DWCONV_ERR_UNSUPPORTED;
+  return make_act8(d, d->rows, d->C, t);
+}
+
+dwconv_status_t make_norm(const dwconv2d_norm_desc_t* d, norm::Norm* g) {
+  if (!d) return DWCONV_ERR_INVALID_ARG;
+  if (d->dtype != DWCONV_F32 && d->dtype != DWCONV_F16 && d->dtype != DWCONV_BF16)
+    return DWCONV_ERR_UNSUPPORTED;
+  if (d->N < 0 || d->H < 1 || d->W < 1 || d->C < 1 || d->groups < 1 || d->C % d->groups != 0)
+    return DWCONV_ERR_INVALID_ARG;
+  if (d->act < DWCONV_ACT_NONE || d->act > DWCONV_ACT_GELU) return DWCONV_ERR_INVALID_ARG;
+  if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return DWCONV_ERR_INVALID_ARG;
+  if (d->C > kMaxChannels || d->H > kMaxElems || d->W > kMaxElems || d->H > kMaxElems / d->W)
+    return DWCONV_ERR_UNSUPPORTED;
+  norm::Norm v{};
+  v.N = d->N;
+  v.P = d->H * d->W;
+  v.C = (int)d->C;
+  v.G = d->groups;
+  v.D = v.C / v.G;
+  v.act = d->act;
+  v.dtype = d->dtype;
+  v.eps = d->eps;
+  v.xs = d->x_c_total == 0 ? d->C : d->x_c_total;
+  v.ys = d->y_c_total == 0 ? d->C : d->y_c_total;
+  v.xo = d->x_c_offset;
+  v.yo = d->y_c_offset;
+  if (v.xo < 0 || v.yo < 0 || v.xs < 1 || v.ys < 1 || v.xo > v.xs - v.C || v.yo > v.ys - v.C)
+    return DWCONV_ERR_INVALID_ARG;
+  const int64_t wide = v.xs > v.ys ? v.xs : v.ys;
+  if (wide > kMaxElems / v.P || (v.N > 0 && v.N > kMaxElems / (v.P * wide))) return DWCONV_ERR_UNSUPPORTED;
+  *g = v;
+  return DWCONV_OK;
+}
+
+dwconv_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (need == 0) return DWCONV_OK;
+  if (!ws || bytes < need) return DWCONV_ERR_WORKSPACE;
+  return reinterpret_cast<uintptr_t>(ws) % 16 == 0 ? DWCONV_OK : DWCONV_ERR_MISALIGNED;
+}
+
+}  // namespace
+
+dwconv_status_t dwconv_act8_encode(const void* x, const dwconv_act8_t* x8, int64_t x_c_total, int dtype,
+                                   cudaStream_t stream) {
+  int64_t ld = 0;
+  Act8 t{};
+  DW_TRY(make_rows(x8, x_c_total, dtype, &ld, &t));
+  if (x8->rows == 0) return DWCONV_OK;
+  DW_TRY(check_ptr(x, esize(dtype), true));
+  return cuda_status(act8_encode(x8->rows, x8->C, ld, dtype, x, t, stream));
+}
+
+dwconv_status_t dwconv_act8_decode(const dwconv_act8_t* x8, void* x, int64_t x_c_total, int dtype,
+                                   cudaStream_t stream) {
+  int64_t ld = 0;
+  Act8 t{};
+  DW_TRY(make_rows(x8, x_c_total, dtype, &ld, &t));
+  if (x8->rows == 0) return DWCONV_OK;
+  DW_TRY(check_ptr(x, esize(dtype), true));
+  return cuda_status(act8_decode(x8->rows, x8->C, ld, dtype, t, x, stream));
+}
+
+size_t dwconv2d_group_norm_nhwc_workspace_size(const dwconv2d_norm_desc_t* desc, int pass) {
+  norm::Norm g;
+  if (make_norm(desc, &g) != DWCONV_OK || (pass != 0 && pass != 1)) return 0;
+  return norm::workspace_bytes(g, pass);
+}
+
+const char* dwconv2d_group_norm_nhwc_plan_name(const dwconv2d_norm_desc_t* desc, int pass) {
+  norm::Norm g;
+  if (make_norm(desc, &g) != DWCONV_OK || (pass != 0 && pass != 1)) return "invalid";
+  return norm::plan_name(g, pass);
+}
+
+dwconv_status_t dwconv2d_group_norm_nhwc(const dwconv2d_norm_desc_t* desc, const void* x, const void* gamma,
+                                         const void* beta, void* y, float* mean, float* rstd, void* workspace,
+                                         size_t workspace_bytes, const dwconv_act8_t* x8, cudaStream_t stream) {
+  norm::Norm g;
+  DW_TRY(make_norm(desc, &g));
+  const int es = esize(g.dtype);
+  Act8 t{};
+  if (x8) DW_TRY(make_act8(x8, g.N * g.P, g.C, &t));
+  DW_TRY(check_ptr(gamma, es, false));
+  DW_TRY(check_ptr(beta, es, false));
+  if (g.N == 0) return DWCONV_OK;
+  DW_TRY(check_ptr(x, es, true));
+  DW_TRY(check_ptr(y, es, true));
+  DW_TRY(check_ptr(mean, 4, false));
+  DW_TRY(check_ptr(rstd, 4, false));
+  DW_TRY(check_workspace(workspace, workspace_bytes, norm::workspace_bytes(g, 0)));
+  return cuda_status(norm::fwd(g, x, gamma, beta, y, mean, rstd, (float*)workspace, t, stream));
+}
+
+dwconv_status_t dwconv2d_group_norm_nhwc_bwd(const dwconv2d_norm_desc_t* desc, const void* x, const void* gy,
+                                             const void* gamma, const void* beta, const float* mean,
+                                             const float* rstd, void* gx, void* ggamma, void* gbeta,
+                                             void* workspace, size_t workspace_bytes, const dwconv_act8_t* x8,
+                                             cudaStream_t stream) {
+  norm::Norm g;
+  DW_TRY(make_norm(desc, &g));
+  const int es = esize(g.dtype);
+  Act8 t{};
+  if (x && x8) return DWCONV_ERR_INVALID_ARG;
+  if (x8) DW_TRY(make_act8(x8, g.N * g.P, g.C, &t));
+  DW_TRY(check_ptr(gamma, es, false));
+  DW_TRY(check_ptr(beta, es, false));
+  DW_TRY(check_ptr(gx, es, false));
+  DW_TRY(check_ptr(ggamma, es, false));
+  DW_TRY(check_ptr(gbeta, es, false));
+  if (!gx && !ggamma && !gbeta) return DWCONV_OK;
+  if (g.N > 0) {
+    if (!x8) DW_TRY(check_ptr(x, es, true));
+    DW_TRY(check_ptr(gy, es, true));
+    DW_TRY(check_ptr(mean, 4, true));
+    DW_TRY(check_ptr(rstd, 4, true));
+    DW_TRY(check_workspace(workspace, workspace_bytes, norm::workspace_bytes(g, 1)));
+  }
+  return cuda_status(
+      norm::bwd(g, x, t, gy, gamma, beta, mean, rstd, gx, ggamma, gbeta, (float*)workspace, stream));
+}
+
+size_t dwconv2d_bwd_nhwc_workspace_size(const dwconv2d_desc_t* desc) {
+  Conv c;
+  if (make_conv(desc, &c) != DWCONV_OK) return 0;
+  return nhwc::bwd_workspace_bytes(c);
+}
+
+const char* dwconv2d_bwd_nhwc_plan_name(const dwconv2d_desc_t* desc) {
+  Conv c;
+  if (make_conv(desc, &c) != DWCONV_OK) return "invalid";
+  return algo_name(nhwc::plan_bwd(c));
+}
+
+dwconv_status_t dwconv2d_bwd_nhwc(const dwconv2d_desc_t* desc, const void* x, const void* gy, const void* w,
+                                  void* gx, void* gw, void* gbias, void* workspace, size_t workspace_bytes,
+                                  const dwconv_act8_t* x8, int accumulate, cudaStream_t stream) {
+  Conv c;
+  DW_TRY(make_conv(desc, &c));
+  const int es = esize(c.dtype);
+  Act8 t{};
+  if (accumulate != 0 && accumulate != 1) return DWCONV_ERR_INVALID_ARG;
+  if (x && x8) return DWCONV_ERR_INVALID_ARG;
+  if (x8 && c.C > kMaxChannels) return DWCONV_ERR_UNSUPPORTED;
+  if (x8) DW_TRY(make_act8(x8, c.N * c.H * c.W, c.C, &t));
+  DW_TRY(check_ptr(gx, es, false));
+  DW_TRY(check_ptr(gw, es, false));
+  DW_TRY(check_ptr(gbias, es, false));
+  if (!gx && !gw && !gbias) return DWCONV_OK;
+  if (gx) DW_TRY(check_ptr(w, es, true));
+  if (c.N > 0) {
+    DW_TRY(check_ptr(gy, es, true));
+    if (x) DW_TRY(check_ptr(x, es, true));
+    if (gw && !x && !x8) return DWCONV_ERR_INVALID_ARG;
+  }
+  if (gw || gbias) DW_TRY(check_workspace(workspace, workspace_bytes, nhwc::bwd_workspace_bytes(c)));
+  return cuda_status(nhwc::bwd(c, x, t, gy, w, gx, gw, gbias, accumulate != 0, (float*)workspace, stream));
 }
 
 dwconv_status_t dwconv2d_fwd_multi(int nbranch, const dwconv2d_desc_t* descs, const void* x,

@@ -1,0 +1,158 @@
+// Channels-last (NHWC) backward: gx, gw and gb from gy, w and the layer's
+// input, in full or from its 8-bit checkpoint.
+//
+//   gx[n, i, j, c] = sum_{m, a, b} w[c*m, a, b] gy[n, (i + ph - a*dh) / sh, (j + pw - b*dw) / sw, c*m]
+//   gw[oc, a, b]   = sum_{n, o, q} gy[n, o, q, oc] x[n, o*sh - ph + a*dh, q*sw - pw + b*dw, oc / m]
+//   gb[oc]         = sum_{n, o, q} gy[n, o, q, oc]
+//
+// The generic kernels serve every descriptor: gx with one value per thread,
+// gw with one block per (channels, tap, chunk of output pixels) and partial
+// sums that a second launch adds in chunk order.
+#include "nhwc.h"
+#include "vec.cuh"
+
+namespace dwconv {
+namespace nhwc {
+namespace {
+
+constexpr int kNT = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kNT)
+gx_generic_kernel(Conv c, int64_t total, const T* __restrict__ gy, const T* __restrict__ w, T* gx, bool accumulate) {
+  for (int64_t i = blockIdx.x * (int64_t)kNT + threadIdx.x; i < total; i += (int64_t)gridDim.x * kNT) {
+    const int64_t ch = i % c.C;
+    int64_t r = i / c.C;
+    const int64_t iw = r % c.W;
+    r /= c.W;
+    const int64_t ih = r % c.H;
+    const int64_t n = r / c.H;
+    float acc = 0.f;
+    for (int a = 0; a < c.kh; ++a) {
+      const int64_t th = ih + c.ph - (int64_t)a * c.dh;
+      if (th < 0 || th % c.sh != 0 || th / c.sh >= c.Ho) continue;
+      for (int b = 0; b < c.kw; ++b) {
+        const int64_t tw = iw + c.pw - (int64_t)b * c.dw;
+        if (tw < 0 || tw % c.sw != 0 || tw / c.sw >= c.Wo) continue;
+        const T* g = gy + ((n * c.Ho + th / c.sh) * c.Wo + tw / c.sw) * c.ctot + c.off + ch * c.m;
+        const T* wp = w + (ch * c.m * c.kh + a) * c.kw + b;
+        for (int j = 0; j < c.m; ++j) acc = fmaf(ld(wp + (int64_t)j * c.kh * c.kw), ld(g + j), acc);
+      }
+    }
+    if (accumulate) acc += ld_rw(gx + i);
+    gx[i] = from_f<T>(acc);
+  }
+}
+
+template <typename T, int SRC>
+__device__ __forceinline__ float input_at(const T* x, const Act8& t, int64_t row, int64_t C, int64_t ch) {
+  if constexpr (SRC == kSrcFull) {
+    return ld(x + row * C + ch);
+  } else {
+    return __fmul_rn(code1<SRC>(t.codes[row * C + ch]), __ldg(t.scales + row * t.nblk + (ch >> t.shift)));
+  }
+}
+
+// ws[chunk][oc][tap] (tap == taps: bias): 32 channels x 8 pixel lanes per block
+template <typename T, int SRC>
+__global__ void __launch_bounds__(kNT)
+gw_generic_kernel(Conv c, int64_t pixels, int64_t per_chunk, const T* __restrict__ x, Act8 t,
+                  const T* __restrict__ gy, float* __restrict__ ws, bool want_w, bool want_b) {
+  __shared__ float sm[kNT];
+  const int taps = c.kh * c.kw;
+  const int tap = blockIdx.y;
+  if (tap < taps ? !want_w : !want_b) return;
+  const int64_t oc = blockIdx.x * (int64_t)32 + (threadIdx.x & 31);
+  const int64_t OC = c.C * c.m;
+  const int64_t p0 = blockIdx.z * per_chunk;
+  const int64_t p1 = min(p0 + per_chunk, pixels);
+  float acc = 0.f;
+  if (oc < OC) {
+    const int64_t a = (int64_t)(tap / c.kw) * c.dh - c.ph, b = (int64_t)(tap % c.kw) * c.dw - c.pw;
+    for (int64_t p = p0 + (threadIdx.x >> 5); p < p1; p += kNT / 32) {
+      const float g = ld(gy + p * c.ctot + c.off + oc);
+      if (tap == taps) {
+        acc += g;
+        continue;
+      }
+      const int64_t q = p % c.Wo, o = p / c.Wo;
+      const int64_t n = o / c.Ho;
+      const int64_t ih = (o - n * c.Ho) * c.sh + a, iw = q * c.sw + b;
+      if (ih < 0 || ih >= c.H || iw < 0 || iw >= c.W) continue;
+      acc = fmaf(g, input_at<T, SRC>(x, t, (n * c.H + ih) * c.W + iw, c.C, oc / c.m), acc);
+    }
+  }
+  sm[threadIdx.x] = acc;
+  __syncthreads();
+  if (threadIdx.x < 32 && oc < OC) {
+    for (int i = 1; i < kNT / 32; ++i) acc += sm[i * 32 + threadIdx.x];
+    ws[(blockIdx.z * OC + oc) * (taps + 1) + tap] = acc;
+  }
+}
+
+int64_t out_pixels(const Conv& c) { return c.N * c.Ho * c.Wo; }
+
+// Chunks of output pixels: enough blocks to fill the GPU, at least 64 pixels
+// each, partial sums of at most 64 MB where that leaves two chunks or more.
+int generic_chunks(const Conv& c) {
+  if (c.N == 0) return 0;
+  const int64_t taps1 = (int64_t)c.kh * c.kw + 1;
+  const int64_t blocks = (c.C * c.m + 31) / 32 * taps1;
+  int64_t n = (152 * 8 + blocks - 1) / blocks;
+  const int64_t most = (out_pixels(c) + 63) / 64;
+  const int64_t room = (int64_t(64) << 20) / (c.C * c.m * taps1 * 4);
+  if (n > most) n = most;
+  if (n > room) n = room;
+  if (n < 1) n = 1;
+  return (int)n;
+}
+
+template <typename T>
+cudaError_t generic(const Conv& c, const T* x, const Act8& t, const T* gy, const T* w, T* gx, T* gw, T* gb,
+                    bool accumulate, float* ws, cudaStream_t s) {
+  const int64_t OC = c.C * c.m;
+  if (gx && c.N > 0) {
+    const int64_t total = c.N * c.H * c.W * c.C;
+    const int64_t blocks = (total + kNT - 1) / kNT;
+    gx_generic_kernel<T><<<(unsigned)(blocks < 152 * 64 ? blocks : 152 * 64), kNT, 0, s>>>(c, total, gy, w, gx,
+                                                                                           accumulate);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (!gw && !gb) return cudaSuccess;
+  const int chunks = generic_chunks(c);
+  if (chunks > 0) {
+    const int64_t pixels = out_pixels(c);
+    const int64_t per = (pixels + chunks - 1) / chunks;
+    const dim3 grid((unsigned)((OC + 31) / 32), (unsigned)(c.kh * c.kw + 1), (unsigned)chunks);
+    if (x || !t.codes)
+      gw_generic_kernel<T, kSrcFull><<<grid, kNT, 0, s>>>(c, pixels, per, x, t, gy, ws, gw != nullptr, gb != nullptr);
+    else if (t.src == kSrcI8)
+      gw_generic_kernel<T, kSrcI8><<<grid, kNT, 0, s>>>(c, pixels, per, x, t, gy, ws, gw != nullptr, gb != nullptr);
+    else
+      gw_generic_kernel<T, kSrcE4M3><<<grid, kNT, 0, s>>>(c, pixels, per, x, t, gy, ws, gw != nullptr, gb != nullptr);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return bwd_weight_pass2(c, ws, chunks, gw, gb, s);
+}
+
+}  // namespace
+
+Algo plan_bwd(const Conv&) { return Algo::Generic; }
+
+size_t bwd_workspace_bytes(const Conv& c) {
+  const size_t b = (size_t)generic_chunks(c) * (size_t)c.OC() * (size_t)(c.kh * c.kw + 1) * sizeof(float);
+  return (b + 255) & ~size_t(255);
+}
+
+cudaError_t bwd(const Conv& c, const void* x, const Act8& x8, const void* gy, const void* w, void* gx, void* gw,
+                void* gb, bool accumulate, float* ws, cudaStream_t s) {
+  cudaError_t e = cudaErrorInvalidValue;
+  DWCONV_DISPATCH_DTYPE(c.dtype, T, e = generic<T>(c, (const T*)x, x8, (const T*)gy, (const T*)w, (T*)gx, (T*)gw,
+                                                   (T*)gb, accumulate, ws, s));
+  return e;
+}
+
+}  // namespace nhwc
+}  // namespace dwconv

@@ -80,11 +80,14 @@ typedef enum {
   DWCONV_BF16 = 2
 } dwconv_dtype_t;
 
-/* Activation of the fused forward epilogue (dwconv2d_fwd_epilogue). */
+/* Activations. The fused forward epilogue (dwconv2d_fwd_epilogue) has the
+ * first three, the group norm all of them. */
 typedef enum {
   DWCONV_ACT_NONE = 0,
   DWCONV_ACT_RELU = 1,   /* max(v, 0) */
-  DWCONV_ACT_RELU6 = 2   /* min(max(v, 0), 6) */
+  DWCONV_ACT_RELU6 = 2,  /* min(max(v, 0), 6) */
+  DWCONV_ACT_SILU = 3,   /* v / (1 + exp(-v)) */
+  DWCONV_ACT_GELU = 4    /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
 } dwconv_act_t;
 
 typedef enum {
@@ -92,7 +95,7 @@ typedef enum {
   DWCONV_ERR_INVALID_ARG = 1,   /* null pointer, bad size, Ho or Wo < 1, slice out of range */
   DWCONV_ERR_UNSUPPORTED = 2,   /* unknown dtype, kernel larger than 255, ... */
   DWCONV_ERR_MISALIGNED = 3,    /* pointer not aligned to its element size */
-  DWCONV_ERR_WORKSPACE = 4,     /* bwd_weight workspace missing or too small */
+  DWCONV_ERR_WORKSPACE = 4,     /* workspace missing or too small */
   DWCONV_ERR_CUDA = 5           /* a CUDA runtime call or launch failed */
 } dwconv_status_t;
 
@@ -309,6 +312,122 @@ dwconv_status_t dwconv2d_fwd_multi(int nbranch, const dwconv2d_desc_t* descs, co
  * accumulated in fp32 in one launch and rounded once (gx is overwritten). */
 dwconv_status_t dwconv2d_bwd_data_multi(int nbranch, const dwconv2d_desc_t* descs, const void* gy,
                                         const void* const* w, void* gx, cudaStream_t stream);
+
+/* ---- channels-last training --------------------------------------------
+ * A channels-last block trains with dwconv2d_fwd_nhwc, the group norm below
+ * and dwconv2d_bwd_nhwc. Between forward and backward it keeps its
+ * activations in full (a pointer x) or in 8 bits (a dwconv_act8_t x8). */
+
+/* Code type of an 8-bit activation checkpoint. */
+typedef enum {
+  DWCONV_ACT8_I8 = 0,    /* integers -127 .. 127 */
+  DWCONV_ACT8_E4M3 = 1   /* 8-bit floats: 4 exponent bits, 3 fraction bits, largest 448 */
+} dwconv_act8_kind_t;
+
+/* An 8-bit activation checkpoint: rows x C values (rows = pixels of all
+ * samples, channels innermost), as one code per value and one fp32 scale per
+ * block of channels of a row:
+ *   scale = fl(max|x| * fl(1 / Q)) over the block, Q = 127 or 448;
+ *   code  = the nearest code to fl(x * fl(1 / scale)), ties to even;
+ *   value = fl(code * scale)
+ * (fl: rounded to fp32), so codes are bit-reproducible from x. A scale below
+ * 2^-126 is stored as 0 and its block as zeros. A block that holds an
+ * infinity or a NaN decodes to NaN throughout: an overflow stays visible in
+ * the gradients. The last block of a row is shorter where block does not
+ * divide C. 40 bytes. */
+typedef struct {
+  int64_t rows, C;       /* rows >= 0, C >= 1 */
+  int32_t kind;          /* dwconv_act8_kind_t */
+  int32_t block;         /* channels per scale: 32, 64 or 128 */
+  void* codes;           /* [rows, C], one byte each */
+  float* scales;         /* [rows, ceil(C / block)] */
+} dwconv_act8_t;
+
+/* Writes the checkpoint x8 of x: rows of C values of `dtype`, x_c_total
+ * values apart (0: C apart). */
+dwconv_status_t dwconv_act8_encode(const void* x, const dwconv_act8_t* x8, int64_t x_c_total,
+                                   int dtype, cudaStream_t stream);
+
+/* Writes the values of x8 to x, rounded once to `dtype`; x's rows are
+ * x_c_total values apart (0: C apart) and nothing between them is written. */
+dwconv_status_t dwconv_act8_decode(const dwconv_act8_t* x8, void* x, int64_t x_c_total, int dtype,
+                                   cudaStream_t stream);
+
+/* A group norm over channels-last activations: x is [N, H, W, x_c_total] and
+ * its channels [x_c_offset, x_c_offset + C) are normalised in `groups` groups
+ * of C / groups channels; y (and gy) likewise. 80 bytes. */
+typedef struct {
+  int64_t N, H, W, C;          /* N >= 0, H, W, C >= 1 */
+  int32_t groups;              /* >= 1, divides C */
+  int32_t act;                 /* dwconv_act_t */
+  int32_t dtype;               /* dwconv_dtype_t of x, gamma, beta, y and their gradients */
+  float eps;                   /* finite, >= 0 */
+  int64_t x_c_offset, x_c_total;   /* slice of x / gx; total 0 means C */
+  int64_t y_c_offset, y_c_total;   /* slice of y / gy; total 0 means C */
+} dwconv2d_norm_desc_t;
+
+/* Bytes of device workspace that the forward (pass 0) or backward (pass 1)
+ * of this norm needs; 0 if the descriptor or pass is invalid. */
+size_t dwconv2d_group_norm_nhwc_workspace_size(const dwconv2d_norm_desc_t* desc, int pass);
+
+/* Group norm with an activation:
+ *   mean, rstd = average of x and 1 / sqrt(variance + eps) over the pixels and
+ *                channels of a (sample, group); variance divides by the count
+ *   xh = (x - mean) * rstd,  u = xh * gamma[c] + beta[c],  y = act(u)
+ * in fp32 (each operation of xh and u rounded by itself, so that the backward
+ * finds the same u), rounded once to desc->dtype. gamma / beta ([C]) may be
+ * NULL (1 / 0). mean and rstd ([N, groups], fp32) are what the backward reads;
+ * either may be NULL. x8, where not NULL, receives the 8-bit checkpoint of x
+ * (rows = N*H*W, C = desc->C) in the same pass over x. The workspace is
+ * 16-byte aligned, at least the size for pass 0, and not used concurrently.
+ * x, y and x8 must not overlap. */
+dwconv_status_t dwconv2d_group_norm_nhwc(const dwconv2d_norm_desc_t* desc, const void* x,
+                                         const void* gamma, const void* beta, void* y, float* mean,
+                                         float* rstd, void* workspace, size_t workspace_bytes,
+                                         const dwconv_act8_t* x8, cudaStream_t stream);
+
+/* Gradients of dwconv2d_group_norm_nhwc, from gy and either x or its
+ * checkpoint x8 (exactly one is not NULL), with the forward's mean and rstd:
+ *   du = gy * act'(u),  gbeta = sum du,  ggamma = sum du * xh   over all pixels
+ *   gx = rstd * (gamma * du - (s1 + xh * s2) / (H * W * C / groups)),
+ *   s1 = sum gamma * du and s2 = sum gamma * du * xh over the (sample, group)
+ * act' is 0 at the kinks of RELU and RELU6. gx has x's layout, gy y's; gx,
+ * ggamma and gbeta ([C]) are overwritten and each may be NULL. For N == 0
+ * ggamma and gbeta become 0. Buffers must not overlap. */
+dwconv_status_t dwconv2d_group_norm_nhwc_bwd(const dwconv2d_norm_desc_t* desc, const void* x,
+                                             const void* gy, const void* gamma, const void* beta,
+                                             const float* mean, const float* rstd, void* gx,
+                                             void* ggamma, void* gbeta, void* workspace,
+                                             size_t workspace_bytes, const dwconv_act8_t* x8,
+                                             cudaStream_t stream);
+
+/* Kernel family of the norm's pass (0 forward, 1 backward): "slab" (one read
+ * of the inputs, kept in the shared memory of a cluster of thread blocks),
+ * "split" (statistics, then a second read) or "invalid". Host only. */
+const char* dwconv2d_group_norm_nhwc_plan_name(const dwconv2d_norm_desc_t* desc, int pass);
+
+/* Bytes of device workspace dwconv2d_bwd_nhwc needs (0 if the descriptor is
+ * invalid). Depends only on the descriptor. */
+size_t dwconv2d_bwd_nhwc_workspace_size(const dwconv2d_desc_t* desc);
+
+/* Gradients of dwconv2d_fwd_nhwc (without epilogue) in one call: gx
+ * ([N, H, W, C]) as dwconv2d_bwd_data, gw ([C*m, kh, kw]) and gbias ([C*m]) as
+ * dwconv2d_bwd_weight, with gy [N, Ho, Wo, out_c_total] and x [N, H, W, C]
+ * channels-last. x may be given by its 8-bit checkpoint x8 instead (rows =
+ * N*H*W). gx, gw and gbias may each be NULL; w is needed for gx, and exactly
+ * one of x and x8 for gw. accumulate = 1 adds to gx, 0 overwrites it. The
+ * workspace (16-byte aligned) is needed for gw and gbias. For N == 0 gw and
+ * gbias become 0. Square 3x3, 5x5 and 7x7 filters with equal strides of 1 or
+ * 2, dilation 1, one filter per channel and padding up to (k - 1) / 2 run on
+ * a row-walking kernel; every other descriptor on generic kernels. */
+dwconv_status_t dwconv2d_bwd_nhwc(const dwconv2d_desc_t* desc, const void* x, const void* gy,
+                                  const void* w, void* gx, void* gw, void* gbias, void* workspace,
+                                  size_t workspace_bytes, const dwconv_act8_t* x8, int accumulate,
+                                  cudaStream_t stream);
+
+/* Kernel family of dwconv2d_bwd_nhwc: "nhwc" (the row-walking kernel),
+ * "generic" or "invalid". Host only. */
+const char* dwconv2d_bwd_nhwc_plan_name(const dwconv2d_desc_t* desc);
 
 /* Static text for a status code. */
 const char* dwconv_status_string(dwconv_status_t status);
