@@ -5,10 +5,11 @@
 //   gw[oc, a, b]   = sum_{n, o, q} gy[n, o, q, oc] x[n, o*sh - ph + a*dh, q*sw - pw + b*dw, oc / m]
 //   gb[oc]         = sum_{n, o, q} gy[n, o, q, oc]
 //
-// The generic kernels serve every descriptor: gx with one value per thread,
-// gw with one block per (channels, tap, chunk of output pixels) and partial
-// sums that a second launch adds in chunk order.
-#include "nhwc.h"
+// The row-walking kernels (nhwc_bwd_impl.cuh) serve square 3x3, 5x5 and 7x7
+// filters; the generic kernels here serve every descriptor: gx with one value
+// per thread, gw with one block per (channels, tap, chunk of output pixels)
+// and partial sums that a second launch adds in chunk order.
+#include "nhwc_bwd.h"
 #include "vec.cuh"
 
 namespace dwconv {
@@ -137,20 +138,116 @@ cudaError_t generic(const Conv& c, const T* x, const Act8& t, const T* gy, const
   return bwd_weight_pass2(c, ws, chunks, gw, gb, s);
 }
 
+// gw and gb from the row-walking kernels' sums ws[chunk][tap][channel]: 32
+// channels of one tap per block, 8 lanes over the chunks
+template <typename T>
+__global__ void __launch_bounds__(kNT)
+walk_join_kernel(int C, int taps, int chunks, const float* __restrict__ ws, T* __restrict__ gw, T* __restrict__ gb) {
+  __shared__ float sm[kNT];
+  const int tap = blockIdx.y;
+  if (tap < taps ? gw == nullptr : gb == nullptr) return;
+  const int ch = blockIdx.x * 32 + (threadIdx.x & 31);
+  float acc = 0.f;
+  if (ch < C) {
+#pragma unroll 8
+    for (int k = threadIdx.x >> 5; k < chunks; k += kNT / 32) acc += ws[((int64_t)k * (taps + 1) + tap) * C + ch];
+  }
+  sm[threadIdx.x] = acc;
+  __syncthreads();
+  if (threadIdx.x < 32 && ch < C) {
+    for (int i = 1; i < kNT / 32; ++i) acc += sm[i * 32 + threadIdx.x];
+    if (tap < taps) gw[(int64_t)ch * taps + tap] = from_f<T>(acc);
+    else gb[ch] = from_f<T>(acc);
+  }
+}
+
+template <typename T>
+cudaError_t walked(const Conv& c, const T* x, const Act8& t, const T* gy, const T* w, T* gx, T* gw, T* gb,
+                   bool accumulate, float* ws, cudaStream_t s) {
+  walk::Geom g = walk::plan(c);
+  g.want_gx = gx != nullptr;
+  g.want_gw = gw != nullptr || gb != nullptr;
+  g.accumulate = accumulate;
+  auto even = [](const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+  const bool pair = c.C % 2 == 0 && c.ctot % 2 == 0 && c.off % 2 == 0 && even(x, 2 * sizeof(T)) &&
+                    even(gy, 2 * sizeof(T)) && even(gx, 2 * sizeof(T)) && even(t.codes, 2);
+  const cudaError_t e = walk::run<T>(c, g, pair, x, t, gy, w, gx, ws, s);
+  if (e != cudaSuccess || !g.want_gw) return e;
+  const int taps = c.kh * c.kw;
+  walk_join_kernel<T><<<dim3((unsigned)((c.C + 31) / 32), (unsigned)(taps + 1)), kNT, 0, s>>>((int)c.C, taps, g.chunks,
+                                                                                          ws, gw, gb);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-Algo plan_bwd(const Conv&) { return Algo::Generic; }
+namespace walk {
+
+// Padding of at most (K - 1) / 2 makes every output's centre tap an input
+// position (see nhwc_bwd_impl.cuh); sides and channels are indexed in 32 bits.
+bool supported(const Conv& c) {
+  if (c.kh != c.kw || (c.kh != 3 && c.kh != 5 && c.kh != 7)) return false;
+  if (c.sh != c.sw || c.sh > 2 || c.dh != 1 || c.dw != 1 || c.m != 1) return false;
+  if (c.ph > c.kh / 2 || c.pw > c.kw / 2) return false;
+  return c.H < (1 << 28) && c.W < (1 << 28) && c.C <= (1 << 20) && c.N > 0;
+}
+
+Geom plan(const Conv& c) {
+  Geom g{};
+  const int K = c.kh, S = c.sh;
+  const int px = K == 3 ? 4 : 8, nt = K == 3 ? 256 : 128, step = K == 3 ? 1 : 2 / S;
+  const int64_t pairs = (c.C + 1) / 2;
+  g.ct_log = 5;
+  while (g.ct_log > 0 && (int64_t(1) << (g.ct_log - 1)) >= pairs) --g.ct_log;
+  const int ct = 1 << g.ct_log, lanes = nt >> g.ct_log;
+  g.tiles = (int)((pairs + ct - 1) / ct);
+  g.t_begin = c.ph / S;
+  g.t_end = (int)((c.H + c.ph - 1) / S) + 1;
+  g.v_begin = c.pw / S * S;
+  g.strips = (int)((c.W + c.pw - g.v_begin + px - 1) / px);
+  // Bands of rows: as many as give every block of one resident wave about four groups of items, no
+  // shorter than 4 steps (a band reads K - 1 rows of gy more than it owns).
+  const int wave = 152 * (K == 3 ? 2 : 3);
+  const int64_t per_tile = (wave + g.tiles - 1) / g.tiles;
+  const int64_t rows = g.t_end - g.t_begin;
+  int64_t bands = (4 * per_tile * lanes + c.N * g.strips - 1) / (c.N * g.strips);
+  const int64_t most = (rows + 4 * step - 1) / (4 * step);
+  if (bands > most) bands = most;
+  int64_t band = (rows + bands - 1) / bands;
+  band = (band + step - 1) / step * step;
+  g.band = (int)band;
+  g.bands = (int)((rows + band - 1) / band);
+  g.items = c.N * g.bands * (int64_t)g.strips;
+  g.groups = (g.items + lanes - 1) / lanes;
+  // one wave of blocks, more where a thread would add up over 4096 products per filter value
+  int64_t chunks = per_tile;
+  const int64_t long_chain = g.groups * band * px / 4096;
+  if (chunks < long_chain) chunks = long_chain;
+  if (chunks > g.groups) chunks = g.groups;
+  const int64_t room = (int64_t(1) << 30) / (c.C * (K * K + 1) * 4);  // at most 1 GB of partial sums
+  if (chunks > room) chunks = room < 1 ? 1 : room;
+  g.chunks = (int)chunks;
+  return g;
+}
+
+}  // namespace walk
+
+Algo plan_bwd(const Conv& c) { return walk::supported(c) ? Algo::Nhwc : Algo::Generic; }
 
 size_t bwd_workspace_bytes(const Conv& c) {
-  const size_t b = (size_t)generic_chunks(c) * (size_t)c.OC() * (size_t)(c.kh * c.kw + 1) * sizeof(float);
+  const size_t n = walk::supported(c) ? (size_t)walk::plan(c).chunks : (size_t)generic_chunks(c);
+  const size_t b = n * (size_t)c.OC() * (size_t)(c.kh * c.kw + 1) * sizeof(float);
   return (b + 255) & ~size_t(255);
 }
 
 cudaError_t bwd(const Conv& c, const void* x, const Act8& x8, const void* gy, const void* w, void* gx, void* gw,
                 void* gb, bool accumulate, float* ws, cudaStream_t s) {
   cudaError_t e = cudaErrorInvalidValue;
-  DWCONV_DISPATCH_DTYPE(c.dtype, T, e = generic<T>(c, (const T*)x, x8, (const T*)gy, (const T*)w, (T*)gx, (T*)gw,
-                                                   (T*)gb, accumulate, ws, s));
+  const bool walk = plan_bwd(c) == Algo::Nhwc;
+  DWCONV_DISPATCH_DTYPE(c.dtype, T, e = walk ? walked<T>(c, (const T*)x, x8, (const T*)gy, (const T*)w, (T*)gx, (T*)gw,
+                                                         (T*)gb, accumulate, ws, s)
+                                             : generic<T>(c, (const T*)x, x8, (const T*)gy, (const T*)w, (T*)gx,
+                                                          (T*)gw, (T*)gb, accumulate, ws, s));
   return e;
 }
 
