@@ -162,20 +162,41 @@ walk_join_kernel(int C, int taps, int chunks, const float* __restrict__ ws, T* _
 }
 
 template <typename T>
-cudaError_t walked(const Conv& c, const T* x, const Act8& t, const T* gy, const T* w, T* gx, T* gw, T* gb,
-                   bool accumulate, float* ws, cudaStream_t s) {
+cudaError_t direct(const Conv& c, const T* x, const Act8& t, const T* gy, const T* w, T* gx, bool want_gw,
+                   bool accumulate, float* ws, cudaStream_t s, int* chunks) {
   walk::Geom g = walk::plan(c);
   g.want_gx = gx != nullptr;
-  g.want_gw = gw != nullptr || gb != nullptr;
+  g.want_gw = want_gw;
   g.accumulate = accumulate;
+  *chunks = g.chunks;
   auto even = [](const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
   const bool pair = c.C % 2 == 0 && c.ctot % 2 == 0 && c.off % 2 == 0 && even(x, 2 * sizeof(T)) &&
                     even(gy, 2 * sizeof(T)) && even(gx, 2 * sizeof(T)) && even(t.codes, 2);
-  const cudaError_t e = walk::run<T>(c, g, pair, x, t, gy, w, gx, ws, s);
-  if (e != cudaSuccess || !g.want_gw) return e;
+  return walk::run<T>(c, g, pair, x, t, gy, w, gx, ws, s);
+}
+
+template <typename T>
+cudaError_t walked(const Conv& c, const T* x, const Act8& t, const T* gy, const T* w, T* gx, T* gw, T* gb,
+                   bool accumulate, float* ws, cudaStream_t s) {
+  const bool want_gw = gw != nullptr || gb != nullptr;
   const int taps = c.kh * c.kw;
-  walk_join_kernel<T><<<dim3((unsigned)((c.C + 31) / 32), (unsigned)(taps + 1)), kNT, 0, s>>>((int)c.C, taps, g.chunks,
-                                                                                          ws, gw, gb);
+  int chunks = 0;
+  walk::Staged st;
+  cudaError_t e = cudaErrorNotSupported;
+  if (walk::plan_staged(c, x || !t.codes ? kSrcFull : t.src, &st)) {
+    st.want_gx = gx != nullptr;
+    st.want_gw = want_gw;
+    st.want_x = gw != nullptr;
+    st.accumulate = accumulate;
+    chunks = st.chunks;
+    e = walk::run_staged<T>(c, st, x, t, gy, w, gx, ws, s);
+  }
+  if (e == cudaErrorNotSupported) {
+    e = direct<T>(c, x, t, gy, w, gx, want_gw, accumulate, ws, s, &chunks);
+  }
+  if (e != cudaSuccess || !want_gw) return e;
+  walk_join_kernel<T><<<dim3((unsigned)((c.C + 31) / 32), (unsigned)(taps + 1)), kNT, 0, s>>>((int)c.C, taps, chunks, ws,
+                                                                                          gw, gb);
   return cudaGetLastError();
 }
 
@@ -230,12 +251,74 @@ Geom plan(const Conv& c) {
   return g;
 }
 
+bool plan_staged(const Conv& c, int src, Staged* out) {
+  if (!supported(c) || c.kh != 3 || c.N >= (int64_t(1) << 31)) return false;
+  const int es = c.dtype == DWCONV_F32 ? 4 : 2, S = c.sh, D = 2 / S, px = 4;
+  if (c.C * es % 16 != 0 || (src != kSrcFull && c.C % 16 != 0) || c.C < 32) return false;
+  Staged g{};
+  // 64 channels per block, 32 where that leaves a quarter fewer of the last tile idle
+  const int64_t by64 = (c.C + 63) / 64 * 64, by32 = (c.C + 31) / 32 * 32;
+  g.ct_log = 4 * by64 >= 5 * by32 ? 4 : 5;
+  const int ct = 1 << g.ct_log, most = 256 / ct;
+  g.tiles = (int)((c.C + 2 * ct - 1) / (2 * ct));
+  g.t_begin = c.ph / S;
+  g.t_end = (int)((c.H + c.ph - 1) / S) + 1;
+  g.v_begin = c.pw / S * S;
+  g.strips = (int)((c.W + c.pw - g.v_begin + px - 1) / px);
+  g.segs = (g.strips + most - 1) / most;
+  g.cs = (g.strips + g.segs - 1) / g.segs;
+  g.ns = most / g.cs;
+  if (g.ns > c.N) g.ns = (int)c.N;
+  g.threads = (g.cs * g.ns * ct + 31) / 32 * 32;
+  g.gc = D + (g.cs * px - 1) / S + 1;
+  g.xc = g.cs * px;
+  const int xes = src == kSrcFull ? es : 1;
+  auto bytes = [&](int log) {
+    g.rs_log = log;
+    g.gy_bytes = (g.ns << log) * g.gc * 2 * ct * es;
+    g.x_bytes = (g.ns << log) * S * g.xc * 2 * ct * xes;
+    g.x_at = (g.gy_bytes + 127) / 128 * 128;
+    g.stage_bytes = (g.x_at + g.x_bytes + 127) / 128 * 128;
+    return g.stage_bytes;
+  };
+  if (bytes(1) > 24 * 1024) bytes(0);
+  // Bands: the cut whose longest block has the fewest rows, a band costing about the rows of gy above it and half a
+  // row on top.
+  const int64_t rows = g.t_end - g.t_begin, groups = (c.N + g.ns - 1) / g.ns;
+  const int64_t wave = (152 * 2 + g.tiles - 1) / g.tiles;
+  double best = -1;
+  for (int64_t bands = 1; bands <= rows && bands <= 512; ++bands) {
+    const int64_t band = (rows + bands - 1) / bands;
+    if ((rows + band - 1) / band != bands) continue;
+    const int64_t items = groups * g.segs * bands;
+    const double cost = (double)((items + wave - 1) / wave) * (band + 0.75 * D + 0.5);
+    if (best < 0 || cost < best) {
+      best = cost;
+      g.bands = (int)bands;
+      g.band = (int)band;
+      g.items = items;
+    }
+  }
+  int64_t chunks = g.items < wave ? g.items : wave;
+  const int64_t long_chain = g.items * g.band * px * S / 4096;  // at most 4096 products in a thread's chain
+  if (chunks < long_chain) chunks = long_chain < g.items ? long_chain : g.items;
+  const int64_t room = (int64_t(1) << 30) / (c.C * 10 * 4);
+  if (chunks > room) chunks = room < 1 ? 1 : room;
+  g.chunks = (int)chunks;
+  *out = g;
+  return true;
+}
+
 }  // namespace walk
 
 Algo plan_bwd(const Conv& c) { return walk::supported(c) ? Algo::Nhwc : Algo::Generic; }
 
 size_t bwd_workspace_bytes(const Conv& c) {
-  const size_t n = walk::supported(c) ? (size_t)walk::plan(c).chunks : (size_t)generic_chunks(c);
+  size_t n = walk::supported(c) ? (size_t)walk::plan(c).chunks : (size_t)generic_chunks(c);
+  for (int src : {kSrcFull, kSrcI8}) {  // whichever the call's pointers and source lead to
+    walk::Staged g;
+    if (walk::plan_staged(c, src, &g) && (size_t)g.chunks > n) n = (size_t)g.chunks;
+  }
   const size_t b = n * (size_t)c.OC() * (size_t)(c.kh * c.kw + 1) * sizeof(float);
   return (b + 255) & ~size_t(255);
 }

@@ -22,13 +22,36 @@ struct Geom {
   bool want_gx, want_gw, accumulate;
 };
 
+// The 3x3 kernel that stages rows with the tensor memory accelerator: a block
+// owns `cs` strips of `ns` samples, its lanes; a stage holds `rs` rows of gy
+// and the rows of x that they meet.
+struct Staged {
+  int ct_log, tiles, chunks;
+  int strips, segs, cs, ns;
+  int bands, band;
+  int t_begin, t_end, v_begin;
+  int64_t items;       // per channel tile: sample groups * segs * bands
+  int threads;
+  int rs_log;
+  int gc, xc;          // columns of a stage's rows of gy and x
+  int gy_bytes, x_bytes;      // of a stage's copies
+  int x_at, stage_bytes;      // where x begins, and the next stage (multiples of 128)
+  bool want_gx, want_gw, want_x, accumulate;  // want_gw: gw or gb; want_x: gw
+};
+
 bool supported(const Conv& c);
 Geom plan(const Conv& c);
+// false: no staged form of this shape and source (kSrc*)
+bool plan_staged(const Conv& c, int src, Staged* g);
 
 // nhwc_bwd_{f32,f16,bf16}.cu. `pair`: two channels are one aligned access.
 template <typename T>
 cudaError_t run(const Conv& c, const Geom& g, bool pair, const T* x, const Act8& x8, const T* gy, const T* w, T* gx,
                 float* ws, cudaStream_t s);
+// cudaErrorNotSupported: a pointer or distance is no multiple of 16 bytes.
+template <typename T>
+cudaError_t run_staged(const Conv& c, const Staged& g, const T* x, const Act8& x8, const T* gy, const T* w, T* gx,
+                       float* ws, cudaStream_t s);
 
 }  // namespace walk
 }  // namespace nhwc

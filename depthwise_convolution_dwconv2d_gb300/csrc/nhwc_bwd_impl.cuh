@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "nhwc_bwd.h"
+#include "tma.cuh"
 #include "vec.cuh"
 
 namespace dwconv {
@@ -124,12 +125,12 @@ __device__ __forceinline__ void store_pair(T* p, f32x2 v, bool two, bool accumul
 // ---- items -----------------------------------------------------------------
 
 // Sums the block's NACC pairs per thread over its row lanes, in lane order,
-// into ws[chunk][tap][channel].
+// into ws[chunk][tap][channel]. NT: the most threads of a block.
 template <int NT, int NACC>
-__device__ __forceinline__ void join_lanes(const Geom& g, const f32x2* acc, int C, int ch, int chunk, float* ws) {
+__device__ __forceinline__ void join_lanes(int ct_log, const f32x2* acc, int C, int ch, int chunk, float* ws) {
   constexpr int kAt = 5;  // taps joined at a time
   __shared__ f32x2 sm[kAt * NT];
-  const int ct = 1 << g.ct_log, lanes = NT >> g.ct_log;
+  const int ct = 1 << ct_log, lanes = blockDim.x >> ct_log;
 #pragma unroll
   for (int k = 0; k < NACC; k += kAt) {
     __syncthreads();
@@ -137,8 +138,8 @@ __device__ __forceinline__ void join_lanes(const Geom& g, const f32x2* acc, int 
     for (int q = 0; q < kAt; ++q)
       if (k + q < NACC) sm[q * NT + threadIdx.x] = acc[k + q];
     __syncthreads();
-    for (int i = threadIdx.x; i < kAt * ct; i += NT) {
-      const int q = i >> g.ct_log, l = i & (ct - 1);
+    for (int i = threadIdx.x; i < kAt * ct; i += blockDim.x) {
+      const int q = i >> ct_log, l = i & (ct - 1);
       if (k + q >= NACC) break;
       float a = 0.f, b = 0.f;
       for (int r = 0; r < lanes; ++r) {
@@ -283,7 +284,213 @@ ring3_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
       }
     }
   }
-  if (g.want_gw) join_lanes<NT, K * K + 1>(g, acc, C, ch0, chunk, ws);
+  if (g.want_gw) join_lanes<NT, K * K + 1>(g.ct_log, acc, C, ch0, chunk, ws);
+}
+
+// 3x3 filters, staged: the same walk with the rows of gy and x brought to
+// shared memory by the tensor memory accelerator, kStages - 1 stages ahead.
+// The copies' zero fill outside the tensors is the padding, so the loop has
+// no column masks, and its shared-memory addresses are one register and
+// constants. All lanes of a block walk the same rows.
+constexpr int kStages = 4;
+
+template <typename T, int SRC, int S, int CT>
+__global__ void __launch_bounds__(256, 2)
+staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, const __grid_constant__ CUtensorMap map_x,
+               Act8 x8, unsigned int* timeouts, const T* __restrict__ w, T* __restrict__ gx, float* __restrict__ ws) {
+  constexpr int K = 3, PX = 4, NT = 256;
+  constexpr int D = (K - 1) / S, RD = D + 1, WIN = D + (PX - 1) / S + 1;
+  constexpr int kCode = SRC != kSrcFull;
+  constexpr int GP = 2 * CT * (int)sizeof(T);             // bytes of a staged pixel of gy
+  constexpr int XP = kCode ? 2 * CT : GP;                 // of x
+  extern __shared__ __align__(16) unsigned char smdyn[];
+  __shared__ __align__(8) uint64_t full[kStages];
+  unsigned char* const sm = smdyn + ((128 - (tma::smem_u32(smdyn) & 127)) & 127);
+  const int tile = blockIdx.x % g.tiles, chunk = blockIdx.x / g.tiles;
+  const int ch0 = tile * 2 * CT;
+  const int pl = threadIdx.x & (CT - 1);
+  const int ch = ch0 + 2 * pl;
+  const int lane = threadIdx.x / CT;
+  const int ls = lane % g.cs, ln = lane / g.cs;           // strip and sample of the lane
+  const int la = min(ln, g.ns - 1);                       // a lane past the last sample reads within the stage
+  const int C = (int)c.C, H = (int)c.H, W = (int)c.W;
+  const int rs = 1 << g.rs_log;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) tma::mbar_init(&full[i], 1);
+    tma::fence_init();
+  }
+  __syncthreads();
+
+  struct Item {
+    int64_t n0;
+    int v0, tb, te;  // first column of the block, rows of the band
+  };
+  auto item_of = [&](int64_t i) {
+    Item it;
+    const int seg = (int)(i % g.segs);
+    i /= g.segs;
+    const int band = (int)(i % g.bands);
+    it.n0 = i / g.bands * g.ns;
+    it.v0 = g.v_begin + seg * g.cs * PX;
+    it.tb = g.t_begin + band * g.band;
+    it.te = min(it.tb + g.band, g.t_end);
+    return it;
+  };
+  auto stages_of = [&](const Item& it) { return (D + it.te - it.tb + rs - 1) >> g.rs_log; };
+
+  // the next copy to issue: stage p_stage of item p_item (thread 0)
+  int64_t p_item = chunk;
+  int p_stage = 0, p_slot = 0;
+  auto issue = [&]() {
+    if (p_item >= g.items) return;
+    const Item it = item_of(p_item);
+    unsigned char* const slot = sm + p_slot * g.stage_bytes;
+    const int t = it.tb - D + p_stage * rs;
+    const bool bring_x = g.want_x;
+    tma::fence_async_smem();
+    tma::mbar_expect_tx(&full[p_slot], (uint32_t)(g.gy_bytes + (bring_x ? g.x_bytes : 0)));
+    tma::load_4d(slot, &map_gy, ch0, it.v0 / S - D, t, (int)it.n0, &full[p_slot]);
+    if (bring_x)
+      tma::load_4d(slot + g.x_at, &map_x, ch0, it.v0 - c.pw, t * S - c.ph, (int)it.n0, &full[p_slot]);
+    p_slot = p_slot + 1 == kStages ? 0 : p_slot + 1;
+    if (++p_stage == stages_of(it)) {
+      p_stage = 0;
+      p_item += g.chunks;
+    }
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kStages - 1; ++i) issue();
+
+  f32x2 wr[K * K], acc[K * K + 1];
+#pragma unroll
+  for (int k = 0; k < K * K; ++k) {
+    wr[k] = 0;
+    if (ch < C && g.want_gx)
+      wr[k] = pack_f32x2(ld(w + (int64_t)ch * K * K + k), ld(w + (int64_t)(ch + 1) * K * K + k));
+  }
+#pragma unroll
+  for (int k = 0; k <= K * K; ++k) acc[k] = 0;
+  f32x2 one = pack_f32x2(1.f, 1.f);
+
+  int slot = 0;
+  uint32_t parity = 0;
+  for (int64_t item = chunk; item < g.items; item += g.chunks) {
+    const Item it = item_of(item);
+    const int64_t n = it.n0 + ln;
+    const int strip = (it.v0 - g.v_begin) / PX + ls;
+    const bool on = ln < g.ns && n < c.N && strip < g.strips && ch < C;
+    const int iw0 = it.v0 + ls * PX - c.pw;
+    uint32_t xok = 0;
+#pragma unroll
+    for (int p = 0; p < PX; ++p) xok |= (iw0 + p >= 0 && iw0 + p < W) ? 1u << p : 0u;
+    const int64_t xrow = n * H * (int64_t)W + iw0;
+    // a checkpoint's scales: lanes p + 4 b of the strip's lanes read pixel p, block b of the tile's
+    const int sl = pl & 7, sb = (ch0 >> x8.shift) + (sl >> 2);
+    const bool scaler = kCode && on && g.want_x && pl < 8 && sb < x8.nblk && ((xok >> (sl & 3)) & 1);
+    const int from = (int)(threadIdx.x & 31 & ~(CT - 1)) + 4 * ((ch >> x8.shift) - (ch0 >> x8.shift));
+    const float* const sp = x8.scales + (xrow + (sl & 3)) * x8.nblk + sb;
+    float sc[S];
+    auto fetch_scales = [&](int t) {
+#pragma unroll
+      for (int r = 0; r < S; ++r) {
+        const int ih = S * t + r - c.ph;
+        sc[r] = 0.f;
+        if (scaler && ih >= 0 && ih < H) sc[r] = __ldg(sp + (int64_t)ih * W * x8.nblk);
+      }
+    };
+    if (kCode) fetch_scales(it.tb);
+
+    f32x2 ring[RD][WIN];
+    const int steps = D + it.te - it.tb;
+    const unsigned char *gp = nullptr, *xp = nullptr;
+    for (int k = 0; k < steps;) {
+#pragma unroll
+      for (int i = 0; i < RD; ++i) {
+        if (k >= steps) break;
+        if ((k & (rs - 1)) == 0) {  // a new stage: the one before it is free once every thread is here
+          if (k > 0 || item > chunk) {
+            __syncthreads();
+            slot = slot + 1 == kStages ? 0 : slot + 1;
+            parity ^= slot == 0 ? 1u : 0u;
+          }
+          if (threadIdx.x == 0) issue();
+          if (!tma::mbar_wait(&full[slot], parity, timeouts)) {
+            // the copy never landed: let those in flight finish (bounded), then stop
+            for (int j = 1; j < kStages; ++j) {
+              const int q = (slot + j) % kStages;
+              tma::mbar_wait(&full[q], q > slot ? parity : parity ^ 1u, nullptr);
+            }
+            return;
+          }
+          const unsigned char* st = sm + slot * g.stage_bytes;
+          gp = st + ((la << g.rs_log) * g.gc + ls * (PX / S)) * GP + pl * (GP / CT);
+          xp = st + g.x_at + ((la << g.rs_log) * S * g.xc + ls * PX) * XP + pl * (XP / CT);
+        }
+        const int t = it.tb - D + k;
+        const bool owned = k >= D;
+        if (on) {
+#pragma unroll
+          for (int j = 0; j < WIN; ++j)
+            ring[i][j] = widen<T, kSrcFull>(*reinterpret_cast<const Raw<T, kSrcFull>*>(gp + j * GP));
+        }
+        float sn[S];
+#pragma unroll
+        for (int r = 0; r < S; ++r) sn[r] = sc[r];
+        if (kCode && owned && k + 1 < steps) fetch_scales(t + 1);
+        if (owned) {
+          f32x2 xv[S * PX];
+#pragma unroll
+          for (int r = 0; r < S; ++r)
+#pragma unroll
+            for (int p = 0; p < PX; ++p) {
+              const unsigned char* q = xp + (r * g.xc + p) * XP;
+              if constexpr (kCode) {
+                Raw<T, SRC> v;
+                v.s = __shfl_sync(0xffffffffu, sn[r], from + p);
+                v.v = *reinterpret_cast<const unsigned short*>(q);
+                xv[r * PX + p] = widen<T, SRC>(v);
+              } else {
+                xv[r * PX + p] = widen<T, SRC>(*reinterpret_cast<const Raw<T, SRC>*>(q));
+              }
+            }
+          if (on) {
+#pragma unroll
+            for (int r = 0; r < S; ++r) {
+              f32x2 out[PX];
+#pragma unroll
+              for (int p = 0; p < PX; ++p) out[p] = 0;
+#pragma unroll
+              for (int a = r; a < K; a += S) {
+                const int from_slot = (i - (a - r) / S + RD) % RD;
+#pragma unroll
+                for (int p = 0; p < PX; ++p)
+#pragma unroll
+                  for (int b = 0; b < K; ++b) {
+                    if ((p - b) % S != 0) continue;
+                    const f32x2 gv = ring[from_slot][D + (p - b) / S];
+                    fma_f32x2(out[p], wr[a * K + b], gv);
+                    fma_f32x2(acc[a * K + b], xv[r * PX + p], gv);
+                    if (a == K / 2 && b == K / 2) fma_f32x2(acc[K * K], one, gv);
+                  }
+              }
+              const int ih = S * t + r - c.ph;
+              if (g.want_gx && ih >= 0 && ih < H) {
+                T* o = gx + (xrow + (int64_t)ih * W) * C + ch;
+#pragma unroll
+                for (int p = 0; p < PX; ++p)
+                  if ((xok >> p) & 1) store_pair<T, true>(o + (int64_t)p * C, out[p], true, g.accumulate);
+              }
+            }
+          }
+        }
+        gp += g.gc * GP;
+        xp += S * g.xc * XP;
+        ++k;
+      }
+    }
+  }
+  if (g.want_gw) join_lanes<NT, K * K + 1>(g.ct_log, acc, C, ch0, chunk, ws);
 }
 
 // 5x5 and 7x7 filters: gx (GW = false) or gw and gb (GW = true), whose filter
@@ -390,7 +597,7 @@ block_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
       }
     }
   }
-  if constexpr (GW) join_lanes<NT, K * K + 1>(g, acc, C, ch0, chunk, ws);
+  if constexpr (GW) join_lanes<NT, K * K + 1>(g.ct_log, acc, C, ch0, chunk, ws);
 }
 
 // ---- launches --------------------------------------------------------------
@@ -427,6 +634,54 @@ cudaError_t run(const Conv& c, const Geom& g, bool pair, const T* x, const Act8&
   X(kSrcFull) X(kSrcI8) X(kSrcE4M3)
 #undef X
   return cudaErrorInvalidValue;
+}
+
+template <typename T, int SRC, int S, int CT>
+cudaError_t launch_staged(const Conv& c, const Staged& g, const T* x, const Act8& x8, const T* gy, const T* w, T* gx,
+                          float* ws, cudaStream_t s) {
+  const uint64_t es = sizeof(T), xes = SRC == kSrcFull ? es : 1;
+  CUtensorMap mg, mx;
+  const uint32_t rows = 1u << g.rs_log;
+  const uint64_t gd[4] = {(uint64_t)c.C, (uint64_t)c.Wo, (uint64_t)c.Ho, (uint64_t)c.N};
+  const uint64_t gs[3] = {c.ctot * es, c.Wo * c.ctot * es, c.Ho * c.Wo * c.ctot * es};
+  const uint32_t gb[4] = {2 * CT, (uint32_t)g.gc, rows, (uint32_t)g.ns};
+  const uint64_t xd[4] = {(uint64_t)c.C, (uint64_t)c.W, (uint64_t)c.H, (uint64_t)c.N};
+  const uint64_t xs[3] = {c.C * xes, c.W * c.C * xes, c.H * c.W * c.C * xes};
+  const uint32_t xb[4] = {2 * CT, (uint32_t)g.xc, rows * S, (uint32_t)g.ns};
+  if (!tma::encode_strided(&mg, gy + c.off, c.dtype, 4, gd, gs, gb)) return cudaErrorNotSupported;
+  mx = mg;
+  const void* xp = SRC == kSrcFull ? (const void*)x : (const void*)x8.codes;
+  if (g.want_x &&
+      !tma::encode_strided(&mx, xp, SRC == kSrcFull ? c.dtype : tma::kBytes, 4, xd, xs, xb))
+    return cudaErrorNotSupported;
+  unsigned int* to = tma::timeout_counter();
+  if (!to) return cudaErrorNotSupported;
+  auto kern = staged3_kernel<T, SRC, S, CT>;
+  const size_t smem = (size_t)kStages * g.stage_bytes + 128;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(g.tiles * g.chunks), g.threads, smem, s>>>(c, g, mg, mx, x8, to, w, gx, ws);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t run_staged(const Conv& c, const Staged& g, const T* x, const Act8& x8, const T* gy, const T* w, T* gx,
+                       float* ws, cudaStream_t s) {
+  // copies start on 16 bytes: pointers, distances between pixels
+  auto fits = [](const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && bytes % 16 == 0; };
+  const int es = sizeof(T);
+  const int src = x || !x8.codes ? kSrcFull : x8.src;
+  if (!fits(gy + c.off, c.ctot * es) || reinterpret_cast<uintptr_t>(gx) % (2 * es) != 0) return cudaErrorNotSupported;
+  if (g.want_x && src == kSrcFull && (!x || !fits(x, c.C * es))) return cudaErrorNotSupported;
+  if (g.want_x && src != kSrcFull && !fits(x8.codes, c.C)) return cudaErrorNotSupported;
+#define X(SRC, S, CT)                                      \
+  if (src == SRC && c.sh == S && (1 << g.ct_log) == CT)    \
+    return launch_staged<T, SRC, S, CT>(c, g, x, x8, gy, w, gx, ws, s);
+#define Y(SRC) X(SRC, 1, 32) X(SRC, 2, 32) X(SRC, 1, 16) X(SRC, 2, 16)
+  Y(kSrcFull) Y(kSrcI8) Y(kSrcE4M3)
+#undef Y
+#undef X
+  return cudaErrorNotSupported;
 }
 
 }  // namespace walk

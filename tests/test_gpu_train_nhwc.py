@@ -389,6 +389,8 @@ CONVS = [(1, 8, 1, 1, 3, 1, 1, 1, 1), (2, 64, 5, 6, 3, 1, 1, 1, 1), (3, 130, 7, 
          (2, 72, 12, 10, 5, 1, 2, 1, 1), (1, 20, 3, 4, 5, 1, 2, 1, 1), (2, 34, 15, 16, 5, 2, 2, 1, 1), (1, 40, 17, 9, 5, 2, 1, 1, 1),
          (2, 24, 11, 13, 7, 1, 3, 1, 1), (1, 9, 8, 21, 7, 1, 2, 1, 1), (1, 68, 19, 18, 7, 2, 3, 1, 1), (4, 256, 28, 28, 3, 1, 1, 1, 1),
          (1, 32, 60, 70, 3, 1, 1, 1, 1), (16, 12, 9, 9, 3, 2, 1, 1, 1),
+         (3, 40, 6, 37, 3, 1, 1, 1, 1), (17, 48, 7, 7, 3, 1, 1, 1, 1), (9, 96, 7, 8, 3, 2, 1, 1, 1), (2, 64, 31, 45, 3, 2, 0, 1, 1),
+         (5, 160, 4, 3, 3, 1, 0, 1, 1), (1, 80, 3, 130, 3, 2, 1, 1, 1), (2, 64, 70, 5, 3, 1, 1, 1, 1), (1, 32, 1, 1, 3, 2, 1, 1, 1),
          (2, 6, 9, 8, 3, 1, 2, 1, 1), (1, 10, 9, 9, 4, 1, 1, 1, 1), (2, 5, 11, 12, 3, 1, 2, 2, 1), (1, 6, 8, 7, 3, 1, 1, 1, 2),
          (1, 4, 9, 9, (3, 5), (2, 1), (1, 2), 1, 3), (1, 3, 12, 12, 9, 1, 4, 1, 1), (1, 5, 6, 6, 3, 3, 1, 1, 1)]
 
@@ -441,7 +443,8 @@ def test_conv_backward_from_a_checkpoint(dtype, kind, block):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_conv_backward_parts_accumulation_slices_and_pointers(dtype):
     for i, (shape, off, total) in enumerate([(CONVS[2], 8, 144), (CONVS[3], 1, 40), (CONVS[5], 2, 70), (CONVS[8], 0, 75),
-                                             (CONVS[12], 8, 40), (CONVS[19], 3, 16), (CONVS[22], 5, 20)]):
+                                             (CONVS[12], 8, 40), (CONVS[-6], 3, 16), (CONVS[-3], 5, 20),
+                                             (CONVS[18], 8, 56), (CONVS[20], 16, 128), (CONVS[21], 4, 72)]):
         d, x, w, _ = conv_inputs(*shape, dtype, 200 + i)
         d.out_c_offset, d.out_c_total = off, total
         OC = w.shape[0]
