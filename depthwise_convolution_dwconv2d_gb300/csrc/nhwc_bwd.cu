@@ -291,16 +291,20 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
     const int64_t band = (rows + bands - 1) / bands;
     if ((rows + band - 1) / band != bands) continue;
     const int64_t items = groups * g.segs * bands;
+    if (items >= (1 << 30)) break;
     const double cost = (double)((items + wave - 1) / wave) * (band + 0.75 * D + 0.5);
     if (best < 0 || cost < best) {
       best = cost;
       g.bands = (int)bands;
       g.band = (int)band;
-      g.items = items;
+      g.items = (int)items;
     }
   }
+  if (best < 0) return false;
+  g.d_segs = FastDiv((uint32_t)g.segs);
+  g.d_bands = FastDiv((uint32_t)g.bands);
   int64_t chunks = g.items < wave ? g.items : wave;
-  const int64_t long_chain = g.items * g.band * px * S / 4096;  // at most 4096 products in a thread's chain
+  const int64_t long_chain = (int64_t)g.items * g.band * px * S / 4096;  // at most 4096 products in a thread's chain
   if (chunks < long_chain) chunks = long_chain < g.items ? long_chain : g.items;
   const int64_t room = (int64_t(1) << 30) / (c.C * 10 * 4);
   if (chunks > room) chunks = room < 1 ? 1 : room;

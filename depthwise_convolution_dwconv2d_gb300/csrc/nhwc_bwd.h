@@ -30,7 +30,8 @@ struct Staged {
   int strips, segs, cs, ns;
   int bands, band;
   int t_begin, t_end, v_begin;
-  int64_t items;       // per channel tile: sample groups * segs * bands
+  int items;           // per channel tile: sample groups * segs * bands, below 2^30
+  FastDiv d_segs, d_bands;
   int threads;
   int rs_log;
   int gc, xc;          // columns of a stage's rows of gy and x

@@ -86,13 +86,13 @@ template <typename T, int SRC>
 __device__ __forceinline__ f32x2 widen(const Raw<T, SRC>& r) {
   if constexpr (SRC == kSrcI8) {
     const uint32_t u = r.v ^ 0x8080u;
-    const float a = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7650)) - 8388736.0f;
-    const float b = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7651)) - 8388736.0f;
-    return pack_f32x2(__fmul_rn(a, r.s), __fmul_rn(b, r.s));
+    const f32x2 m = pack_f32x2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7650)),
+                               __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7651)));
+    return mul_f32x2(add_f32x2(m, pack_f32x2(-8388736.0f, -8388736.0f)), pack_f32x2(r.s, r.s));
   } else if constexpr (SRC == kSrcE4M3) {
     float a, b;
     e4m3_pair((uint16_t)r.v, a, b);
-    return pack_f32x2(__fmul_rn(a, r.s), __fmul_rn(b, r.s));
+    return mul_f32x2(pack_f32x2(a, b), pack_f32x2(r.s, r.s));
   } else if constexpr (sizeof(T) == 4) {
     return r.v;
   } else if constexpr (std::is_same<T, __half>::value) {
@@ -103,6 +103,15 @@ __device__ __forceinline__ f32x2 widen(const Raw<T, SRC>& r) {
   }
 }
 
+// two aligned channels, each rounded once
+__device__ __forceinline__ void put_pair(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
+__device__ __forceinline__ void put_pair(__half* p, float a, float b) {
+  *reinterpret_cast<__half2*>(p) = __floats2half2_rn(a, b);
+}
+__device__ __forceinline__ void put_pair(__nv_bfloat16* p, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+
 template <typename T, bool PAIR>
 __device__ __forceinline__ void store_pair(T* p, f32x2 v, bool two, bool accumulate) {
   float a, b;
@@ -111,14 +120,29 @@ __device__ __forceinline__ void store_pair(T* p, f32x2 v, bool two, bool accumul
     a += to_f<T>(p[0]);
     if (PAIR || two) b += to_f<T>(p[1]);
   }
-  if constexpr (PAIR && sizeof(T) == 4) {
-    *reinterpret_cast<float2*>(p) = make_float2(a, b);
-  } else if constexpr (PAIR) {
-    T h[2] = {from_f<T>(a), from_f<T>(b)};
-    *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(h);
+  if constexpr (PAIR) {
+    put_pair(p, a, b);
   } else {
     p[0] = from_f<T>(a);
     if (two) p[1] = from_f<T>(b);
+  }
+}
+
+// Stores a strip of PX pixels, C channels apart: with no branch per pixel
+// where all of it is inside and nothing is added to.
+template <typename T, bool PAIR, int PX>
+__device__ __forceinline__ void store_strip(T* o, int64_t C, const f32x2* v, uint32_t ok, bool two, bool accumulate) {
+  if (PAIR && ok == (1u << PX) - 1 && !accumulate) {
+#pragma unroll
+    for (int p = 0; p < PX; ++p) {
+      float a, b;
+      unpack_f32x2(v[p], a, b);
+      put_pair(o + p * C, a, b);
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < PX; ++p)
+      if ((ok >> p) & 1) store_pair<T, PAIR>(o + p * C, v[p], two, accumulate);
   }
 }
 
@@ -274,10 +298,7 @@ ring3_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
           }
           const int ih = S * t + r - c.ph;
           if (g.want_gx && ih >= 0 && ih < H) {
-            T* o = gx + (xrow + (int64_t)ih * W) * C + ch;
-#pragma unroll
-            for (int p = 0; p < PX; ++p)
-              if ((xok >> p) & 1) store_pair<T, PAIR>(o + (int64_t)p * C, out[p], two, g.accumulate);
+            store_strip<T, PAIR, PX>(gx + (xrow + (int64_t)ih * W) * C + ch, C, out, xok, two, g.accumulate);
           }
         }
         ++t;
@@ -305,7 +326,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
   constexpr int XP = kCode ? 2 * CT : GP;                 // of x
   extern __shared__ __align__(16) unsigned char smdyn[];
   __shared__ __align__(8) uint64_t full[kStages];
-  unsigned char* const sm = smdyn + ((128 - (tma::smem_u32(smdyn) & 127)) & 127);
+  const int base = (int)((128 - (tma::smem_u32(smdyn) & 127)) & 127);
   const int tile = blockIdx.x % g.tiles, chunk = blockIdx.x / g.tiles;
   const int ch0 = tile * 2 * CT;
   const int pl = threadIdx.x & (CT - 1);
@@ -315,6 +336,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
   const int la = min(ln, g.ns - 1);                       // a lane past the last sample reads within the stage
   const int C = (int)c.C, H = (int)c.H, W = (int)c.W;
   const int rs = 1 << g.rs_log;
+  const int grow_bytes = g.gc * GP, xrow_bytes = g.xc * XP;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) tma::mbar_init(&full[i], 1);
@@ -323,40 +345,38 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
   __syncthreads();
 
   struct Item {
-    int64_t n0;
-    int v0, tb, te;  // first column of the block, rows of the band
+    int n0, v0, tb, te;  // first sample and column of the block, rows of the band
   };
-  auto item_of = [&](int64_t i) {
+  auto item_of = [&](int i) {
     Item it;
-    const int seg = (int)(i % g.segs);
-    i /= g.segs;
-    const int band = (int)(i % g.bands);
-    it.n0 = i / g.bands * g.ns;
-    it.v0 = g.v_begin + seg * g.cs * PX;
-    it.tb = g.t_begin + band * g.band;
+    uint32_t q, n;
+    const uint32_t seg = g.d_segs.divmod((uint32_t)i, q);
+    const uint32_t band = g.d_bands.divmod(q, n);
+    it.n0 = (int)n * g.ns;
+    it.v0 = g.v_begin + (int)seg * g.cs * PX;
+    it.tb = g.t_begin + (int)band * g.band;
     it.te = min(it.tb + g.band, g.t_end);
     return it;
   };
-  auto stages_of = [&](const Item& it) { return (D + it.te - it.tb + rs - 1) >> g.rs_log; };
 
-  // the next copy to issue: stage p_stage of item p_item (thread 0)
-  int64_t p_item = chunk;
-  int p_stage = 0, p_slot = 0;
+  // the next copy to issue (thread 0): gy rows p_t .. p_t + rs - 1 of item p_item
+  int p_item = chunk, p_t = 0, p_slot = 0;
+  Item p_it = item_of(p_item);
+  p_t = p_it.tb - D;
   auto issue = [&]() {
     if (p_item >= g.items) return;
-    const Item it = item_of(p_item);
-    unsigned char* const slot = sm + p_slot * g.stage_bytes;
-    const int t = it.tb - D + p_stage * rs;
-    const bool bring_x = g.want_x;
+    unsigned char* const slot = smdyn + base + p_slot * g.stage_bytes;
     tma::fence_async_smem();
-    tma::mbar_expect_tx(&full[p_slot], (uint32_t)(g.gy_bytes + (bring_x ? g.x_bytes : 0)));
-    tma::load_4d(slot, &map_gy, ch0, it.v0 / S - D, t, (int)it.n0, &full[p_slot]);
-    if (bring_x)
-      tma::load_4d(slot + g.x_at, &map_x, ch0, it.v0 - c.pw, t * S - c.ph, (int)it.n0, &full[p_slot]);
+    tma::mbar_expect_tx(&full[p_slot], (uint32_t)(g.gy_bytes + (g.want_x ? g.x_bytes : 0)));
+    tma::load_4d(slot, &map_gy, ch0, p_it.v0 / S - D, p_t, p_it.n0, &full[p_slot]);
+    if (g.want_x)
+      tma::load_4d(slot + g.x_at, &map_x, ch0, p_it.v0 - c.pw, p_t * S - c.ph, p_it.n0, &full[p_slot]);
     p_slot = p_slot + 1 == kStages ? 0 : p_slot + 1;
-    if (++p_stage == stages_of(it)) {
-      p_stage = 0;
+    p_t += rs;
+    if (p_t >= p_it.te) {
       p_item += g.chunks;
+      p_it = item_of(p_item);
+      p_t = p_it.tb - D;
     }
   };
   if (threadIdx.x == 0)
@@ -375,7 +395,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
 
   int slot = 0;
   uint32_t parity = 0;
-  for (int64_t item = chunk; item < g.items; item += g.chunks) {
+  for (int item = chunk; item < g.items; item += g.chunks) {
     const Item it = item_of(item);
     const int64_t n = it.n0 + ln;
     const int strip = (it.v0 - g.v_begin) / PX + ls;
@@ -385,25 +405,29 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
 #pragma unroll
     for (int p = 0; p < PX; ++p) xok |= (iw0 + p >= 0 && iw0 + p < W) ? 1u << p : 0u;
     const int64_t xrow = n * H * (int64_t)W + iw0;
+    const int64_t row = (int64_t)W * C;
+    T* op = gx + (xrow + (int64_t)(S * it.tb - c.ph) * W) * C + ch;  // gx of the strip, of the step's first row
     // a checkpoint's scales: lanes p + 4 b of the strip's lanes read pixel p, block b of the tile's
     const int sl = pl & 7, sb = (ch0 >> x8.shift) + (sl >> 2);
     const bool scaler = kCode && on && g.want_x && pl < 8 && sb < x8.nblk && ((xok >> (sl & 3)) & 1);
     const int from = (int)(threadIdx.x & 31 & ~(CT - 1)) + 4 * ((ch >> x8.shift) - (ch0 >> x8.shift));
-    const float* const sp = x8.scales + (xrow + (sl & 3)) * x8.nblk + sb;
+    const int64_t srow = (int64_t)W * x8.nblk;
+    const float* sp = x8.scales + (xrow + (sl & 3) + (int64_t)(S * it.tb - c.ph) * W) * x8.nblk + sb;
     float sc[S];
-    auto fetch_scales = [&](int t) {
+    auto fetch_scales = [&](int t) {  // t = it.tb, it.tb + 1, ...
 #pragma unroll
       for (int r = 0; r < S; ++r) {
         const int ih = S * t + r - c.ph;
         sc[r] = 0.f;
-        if (scaler && ih >= 0 && ih < H) sc[r] = __ldg(sp + (int64_t)ih * W * x8.nblk);
+        if (scaler && (S == 1 || (ih >= 0 && ih < H))) sc[r] = __ldg(sp + r * srow);
       }
+      sp += S * srow;
     };
     if (kCode) fetch_scales(it.tb);
 
     f32x2 ring[RD][WIN];
     const int steps = D + it.te - it.tb;
-    const unsigned char *gp = nullptr, *xp = nullptr;
+    int gp = 0, xp = 0;  // where the step's window and strip begin in shared memory
     for (int k = 0; k < steps;) {
 #pragma unroll
       for (int i = 0; i < RD; ++i) {
@@ -423,7 +447,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
             }
             return;
           }
-          const unsigned char* st = sm + slot * g.stage_bytes;
+          const int st = base + slot * g.stage_bytes;
           gp = st + ((la << g.rs_log) * g.gc + ls * (PX / S)) * GP + pl * (GP / CT);
           xp = st + g.x_at + ((la << g.rs_log) * S * g.xc + ls * PX) * XP + pl * (XP / CT);
         }
@@ -432,7 +456,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
         if (on) {
 #pragma unroll
           for (int j = 0; j < WIN; ++j)
-            ring[i][j] = widen<T, kSrcFull>(*reinterpret_cast<const Raw<T, kSrcFull>*>(gp + j * GP));
+            ring[i][j] = widen<T, kSrcFull>(*reinterpret_cast<const Raw<T, kSrcFull>*>(smdyn + (gp + j * GP)));
         }
         float sn[S];
 #pragma unroll
@@ -444,7 +468,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
           for (int r = 0; r < S; ++r)
 #pragma unroll
             for (int p = 0; p < PX; ++p) {
-              const unsigned char* q = xp + (r * g.xc + p) * XP;
+              const unsigned char* q = smdyn + (xp + r * xrow_bytes + p * XP);
               if constexpr (kCode) {
                 Raw<T, SRC> v;
                 v.s = __shfl_sync(0xffffffffu, sn[r], from + p);
@@ -459,8 +483,6 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
             for (int r = 0; r < S; ++r) {
               f32x2 out[PX];
 #pragma unroll
-              for (int p = 0; p < PX; ++p) out[p] = 0;
-#pragma unroll
               for (int a = r; a < K; a += S) {
                 const int from_slot = (i - (a - r) / S + RD) % RD;
 #pragma unroll
@@ -469,23 +491,22 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
                   for (int b = 0; b < K; ++b) {
                     if ((p - b) % S != 0) continue;
                     const f32x2 gv = ring[from_slot][D + (p - b) / S];
-                    fma_f32x2(out[p], wr[a * K + b], gv);
+                    if (a == r && b == p % S) out[p] = mul_f32x2(wr[a * K + b], gv);
+                    else fma_f32x2(out[p], wr[a * K + b], gv);
                     fma_f32x2(acc[a * K + b], xv[r * PX + p], gv);
                     if (a == K / 2 && b == K / 2) fma_f32x2(acc[K * K], one, gv);
                   }
               }
               const int ih = S * t + r - c.ph;
-              if (g.want_gx && ih >= 0 && ih < H) {
-                T* o = gx + (xrow + (int64_t)ih * W) * C + ch;
-#pragma unroll
-                for (int p = 0; p < PX; ++p)
-                  if ((xok >> p) & 1) store_pair<T, true>(o + (int64_t)p * C, out[p], true, g.accumulate);
+              if (g.want_gx && (S == 1 || (ih >= 0 && ih < H))) {  // at stride 1 every owned row is inside
+                store_strip<T, true, PX>(op + r * row, C, out, xok, true, g.accumulate);
               }
             }
           }
         }
-        gp += g.gc * GP;
-        xp += S * g.xc * XP;
+        if (owned) op += S * row;
+        gp += grow_bytes;
+        xp += S * xrow_bytes;
         ++k;
       }
     }
@@ -589,10 +610,7 @@ block_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
         for (int r = 0; r < RY; ++r) {
           const int ih = S * t + r - c.ph;
           if (ih < 0 || ih >= H) continue;
-          T* o = gx + (xrow + (int64_t)ih * W) * C + ch;
-#pragma unroll
-          for (int p = 0; p < PX; ++p)
-            if ((xok >> p) & 1) store_pair<T, PAIR>(o + (int64_t)p * C, own[r * PX + p], two, g.accumulate);
+          store_strip<T, PAIR, PX>(gx + (xrow + (int64_t)ih * W) * C + ch, C, own + r * PX, xok, two, g.accumulate);
         }
       }
     }
