@@ -139,23 +139,25 @@ cudaError_t generic(const Conv& c, const T* x, const Act8& t, const T* gy, const
 }
 
 // gw and gb from the row-walking kernels' sums ws[chunk][tap][channel]: 32
-// channels of one tap per block, 8 lanes over the chunks
+// channels of one tap per block, a warp for every 32nd chunk
+constexpr int kJoin = 1024;
 template <typename T>
-__global__ void __launch_bounds__(kNT)
+__global__ void __launch_bounds__(kJoin)
 walk_join_kernel(int C, int taps, int chunks, const float* __restrict__ ws, T* __restrict__ gw, T* __restrict__ gb) {
-  __shared__ float sm[kNT];
+  __shared__ float sm[kJoin];
   const int tap = blockIdx.y;
   if (tap < taps ? gw == nullptr : gb == nullptr) return;
   const int ch = blockIdx.x * 32 + (threadIdx.x & 31);
   float acc = 0.f;
   if (ch < C) {
 #pragma unroll 8
-    for (int k = threadIdx.x >> 5; k < chunks; k += kNT / 32) acc += ws[((int64_t)k * (taps + 1) + tap) * C + ch];
+    for (int k = threadIdx.x >> 5; k < chunks; k += kJoin / 32) acc += ws[((int64_t)k * (taps + 1) + tap) * C + ch];
   }
   sm[threadIdx.x] = acc;
   __syncthreads();
   if (threadIdx.x < 32 && ch < C) {
-    for (int i = 1; i < kNT / 32; ++i) acc += sm[i * 32 + threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kJoin / 32; ++i) acc += sm[i * 32 + threadIdx.x];
     if (tap < taps) gw[(int64_t)ch * taps + tap] = from_f<T>(acc);
     else gb[ch] = from_f<T>(acc);
   }
@@ -195,7 +197,7 @@ cudaError_t walked(const Conv& c, const T* x, const Act8& t, const T* gy, const 
     e = direct<T>(c, x, t, gy, w, gx, want_gw, accumulate, ws, s, &chunks);
   }
   if (e != cudaSuccess || !want_gw) return e;
-  walk_join_kernel<T><<<dim3((unsigned)((c.C + 31) / 32), (unsigned)(taps + 1)), kNT, 0, s>>>((int)c.C, taps, chunks, ws,
+  walk_join_kernel<T><<<dim3((unsigned)((c.C + 31) / 32), (unsigned)(taps + 1)), kJoin, 0, s>>>((int)c.C, taps, chunks, ws,
                                                                                           gw, gb);
   return cudaGetLastError();
 }
@@ -259,40 +261,49 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
   // 64 channels per block, 32 where that leaves a quarter fewer of the last tile idle
   const int64_t by64 = (c.C + 63) / 64 * 64, by32 = (c.C + 31) / 32 * 32;
   g.ct_log = 4 * by64 >= 5 * by32 ? 4 : 5;
-  const int ct = 1 << g.ct_log, most = 256 / ct;
+  const int ct = 1 << g.ct_log, most = kStagedThreads / ct;
   g.tiles = (int)((c.C + 2 * ct - 1) / (2 * ct));
   g.t_begin = c.ph / S;
   g.t_end = (int)((c.H + c.ph - 1) / S) + 1;
   g.v_begin = c.pw / S * S;
   g.strips = (int)((c.W + c.pw - g.v_begin + px - 1) / px);
-  g.segs = (g.strips + most - 1) / most;
-  g.cs = (g.strips + g.segs - 1) / g.segs;
-  g.ns = most / g.cs;
-  if (g.ns > c.N) g.ns = (int)c.N;
+  // Strips and samples of a block's lanes: the split that leaves the fewest lanes idle, a narrow block paying for the
+  // columns of gy that it shares with its neighbours.
+  double fit = -1;
+  for (int cs = 1; cs <= most && cs <= g.strips; ++cs) {
+    const int segs = (g.strips + cs - 1) / cs;
+    const int64_t ns = most / cs < c.N ? most / cs : c.N, groups = (c.N + ns - 1) / ns;
+    const double busy = (double)g.strips * c.N * ct / ((double)segs * groups * ((cs * ns * ct + 31) / 32 * 32));
+    const double f = busy * (cs * ns * ct >= 96 ? 1.0 : 0.7) / (1 + 0.15 * D * S / (cs * px));
+    if (f <= fit) continue;
+    fit = f;
+    g.cs = cs;
+    g.segs = segs;
+    g.ns = (int)ns;
+  }
   g.threads = (g.cs * g.ns * ct + 31) / 32 * 32;
   g.gc = D + (g.cs * px - 1) / S + 1;
   g.xc = g.cs * px;
   const int xes = src == kSrcFull ? es : 1;
-  auto bytes = [&](int log) {
-    g.rs_log = log;
-    g.gy_bytes = (g.ns << log) * g.gc * 2 * ct * es;
-    g.x_bytes = (g.ns << log) * S * g.xc * 2 * ct * xes;
-    g.x_at = (g.gy_bytes + 127) / 128 * 128;
-    g.stage_bytes = (g.x_at + g.x_bytes + 127) / 128 * 128;
-    return g.stage_bytes;
-  };
-  if (bytes(1) > 24 * 1024) bytes(0);
-  // Bands: the cut whose longest block has the fewest rows, a band costing about the rows of gy above it and half a
-  // row on top.
+  const int rd = D + 1;  // rows of gy in a stage
+  g.gy_bytes = g.ns * rd * g.gc * 2 * ct * es;
+  g.x_bytes = g.ns * rd * S * g.xc * 2 * ct * xes;
+  g.x_at = (g.gy_bytes + 127) / 128 * 128;
+  g.stage_bytes = (g.x_at + g.x_bytes + 127) / 128 * 128;
+  g.stages = (220 * 1024 / kStagedBlocks - 6 * 1024) / g.stage_bytes;  // 6 KB: what join_lanes keeps
+  if (g.stages > kMaxStages) g.stages = kMaxStages;
+  if (g.stages < 2) g.stages = 2;
+  // Bands: the cut whose longest block has the fewest rows, a band costing whole stages, the
+  // rows above it about a third of an owned row.
   const int64_t rows = g.t_end - g.t_begin, groups = (c.N + g.ns - 1) / g.ns;
-  const int64_t wave = (152 * 2 + g.tiles - 1) / g.tiles;
+  const int64_t wave = (152 * kStagedBlocks + g.tiles - 1) / g.tiles;
   double best = -1;
   for (int64_t bands = 1; bands <= rows && bands <= 512; ++bands) {
     const int64_t band = (rows + bands - 1) / bands;
     if ((rows + band - 1) / band != bands) continue;
     const int64_t items = groups * g.segs * bands;
     if (items >= (1 << 30)) break;
-    const double cost = (double)((items + wave - 1) / wave) * (band + 0.75 * D + 0.5);
+    const double cost = (double)((items + wave - 1) / wave) * ((D + band + rd - 1) / rd * rd - 0.7 * D + 0.5);
     if (best < 0 || cost < best) {
       best = cost;
       g.bands = (int)bands;

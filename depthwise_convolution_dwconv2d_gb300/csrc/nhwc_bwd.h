@@ -23,8 +23,11 @@ struct Geom {
 };
 
 // The 3x3 kernel that stages rows with the tensor memory accelerator: a block
-// owns `cs` strips of `ns` samples, its lanes; a stage holds `rs` rows of gy
-// and the rows of x that they meet.
+// owns `cs` strips of `ns` samples, its lanes; a stage holds 2 / S + 1 rows of
+// gy and the rows of x that they meet.
+constexpr int kStagedThreads = 128;  // the most threads of a block
+constexpr int kStagedBlocks = 4;     // blocks per SM
+constexpr int kMaxStages = 4;
 struct Staged {
   int ct_log, tiles, chunks;
   int strips, segs, cs, ns;
@@ -33,7 +36,7 @@ struct Staged {
   int items;           // per channel tile: sample groups * segs * bands, below 2^30
   FastDiv d_segs, d_bands;
   int threads;
-  int rs_log;
+  int stages;
   int gc, xc;          // columns of a stage's rows of gy and x
   int gy_bytes, x_bytes;      // of a stage's copies
   int x_at, stage_bytes;      // where x begins, and the next stage (multiples of 128)

@@ -309,23 +309,22 @@ ring3_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
 }
 
 // 3x3 filters, staged: the same walk with the rows of gy and x brought to
-// shared memory by the tensor memory accelerator, kStages - 1 stages ahead.
-// The copies' zero fill outside the tensors is the padding, so the loop has
-// no column masks, and its shared-memory addresses are one register and
-// constants. All lanes of a block walk the same rows.
-constexpr int kStages = 4;
-
+// shared memory by the tensor memory accelerator, some stages ahead. The
+// copies' zero fill outside the tensors is the padding, so the loop has no
+// column masks. A stage is as many rows as the ring has slots: row i of a
+// stage is slot i, and a stage costs one barrier and one wait. All lanes of a
+// block walk the same rows.
 template <typename T, int SRC, int S, int CT>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(kStagedThreads, kStagedBlocks)
 staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, const __grid_constant__ CUtensorMap map_x,
                Act8 x8, unsigned int* timeouts, const T* __restrict__ w, T* __restrict__ gx, float* __restrict__ ws) {
-  constexpr int K = 3, PX = 4, NT = 256;
+  constexpr int K = 3, PX = 4, NT = kStagedThreads;
   constexpr int D = (K - 1) / S, RD = D + 1, WIN = D + (PX - 1) / S + 1;
-  constexpr int kCode = SRC != kSrcFull;
+  constexpr bool kCode = SRC != kSrcFull;
   constexpr int GP = 2 * CT * (int)sizeof(T);             // bytes of a staged pixel of gy
   constexpr int XP = kCode ? 2 * CT : GP;                 // of x
   extern __shared__ __align__(16) unsigned char smdyn[];
-  __shared__ __align__(8) uint64_t full[kStages];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
   const int base = (int)((128 - (tma::smem_u32(smdyn) & 127)) & 127);
   const int tile = blockIdx.x % g.tiles, chunk = blockIdx.x / g.tiles;
   const int ch0 = tile * 2 * CT;
@@ -335,11 +334,12 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
   const int ls = lane % g.cs, ln = lane / g.cs;           // strip and sample of the lane
   const int la = min(ln, g.ns - 1);                       // a lane past the last sample reads within the stage
   const int C = (int)c.C, H = (int)c.H, W = (int)c.W;
-  const int rs = 1 << g.rs_log;
-  const int grow_bytes = g.gc * GP, xrow_bytes = g.xc * XP;
+  const int grow = g.gc * GP, xrow = g.xc * XP;           // bytes of a staged row
+  const int g_at = base + (la * RD * g.gc + ls * (PX / S)) * GP + pl * (GP / CT);
+  const int x_at = base + g.x_at + (la * RD * S * g.xc + ls * PX) * XP + pl * (XP / CT);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) tma::mbar_init(&full[i], 1);
+    for (int i = 0; i < g.stages; ++i) tma::mbar_init(&full[i], 1);
     tma::fence_init();
   }
   __syncthreads();
@@ -359,10 +359,10 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
     return it;
   };
 
-  // the next copy to issue (thread 0): gy rows p_t .. p_t + rs - 1 of item p_item
-  int p_item = chunk, p_t = 0, p_slot = 0;
+  // the next copy to issue (thread 0): gy rows p_t .. p_t + RD - 1 of item p_item
+  int p_item = chunk, p_slot = 0;
   Item p_it = item_of(p_item);
-  p_t = p_it.tb - D;
+  int p_t = p_it.tb - D;
   auto issue = [&]() {
     if (p_item >= g.items) return;
     unsigned char* const slot = smdyn + base + p_slot * g.stage_bytes;
@@ -371,8 +371,8 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
     tma::load_4d(slot, &map_gy, ch0, p_it.v0 / S - D, p_t, p_it.n0, &full[p_slot]);
     if (g.want_x)
       tma::load_4d(slot + g.x_at, &map_x, ch0, p_it.v0 - c.pw, p_t * S - c.ph, p_it.n0, &full[p_slot]);
-    p_slot = p_slot + 1 == kStages ? 0 : p_slot + 1;
-    p_t += rs;
+    p_slot = p_slot + 1 == g.stages ? 0 : p_slot + 1;
+    p_t += RD;
     if (p_t >= p_it.te) {
       p_item += g.chunks;
       p_it = item_of(p_item);
@@ -380,7 +380,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
     }
   };
   if (threadIdx.x == 0)
-    for (int i = 0; i < kStages - 1; ++i) issue();
+    for (int i = 0; i < g.stages - 1; ++i) issue();
 
   f32x2 wr[K * K], acc[K * K + 1];
 #pragma unroll
@@ -391,10 +391,10 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
   }
 #pragma unroll
   for (int k = 0; k <= K * K; ++k) acc[k] = 0;
-  f32x2 one = pack_f32x2(1.f, 1.f);
 
   int slot = 0;
   uint32_t parity = 0;
+  bool first = true;
   for (int item = chunk; item < g.items; item += g.chunks) {
     const Item it = item_of(item);
     const int64_t n = it.n0 + ln;
@@ -404,15 +404,15 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
     uint32_t xok = 0;
 #pragma unroll
     for (int p = 0; p < PX; ++p) xok |= (iw0 + p >= 0 && iw0 + p < W) ? 1u << p : 0u;
-    const int64_t xrow = n * H * (int64_t)W + iw0;
+    const int64_t at = n * H * (int64_t)W + (int64_t)(S * it.tb - c.ph) * W + iw0;  // pixel of the band's first row
     const int64_t row = (int64_t)W * C;
-    T* op = gx + (xrow + (int64_t)(S * it.tb - c.ph) * W) * C + ch;  // gx of the strip, of the step's first row
+    T* op = gx + at * C + ch;
     // a checkpoint's scales: lanes p + 4 b of the strip's lanes read pixel p, block b of the tile's
     const int sl = pl & 7, sb = (ch0 >> x8.shift) + (sl >> 2);
     const bool scaler = kCode && on && g.want_x && pl < 8 && sb < x8.nblk && ((xok >> (sl & 3)) & 1);
     const int from = (int)(threadIdx.x & 31 & ~(CT - 1)) + 4 * ((ch >> x8.shift) - (ch0 >> x8.shift));
     const int64_t srow = (int64_t)W * x8.nblk;
-    const float* sp = x8.scales + (xrow + (sl & 3) + (int64_t)(S * it.tb - c.ph) * W) * x8.nblk + sb;
+    const float* sp = x8.scales + (at + (sl & 3)) * x8.nblk + sb;
     float sc[S];
     auto fetch_scales = [&](int t) {  // t = it.tb, it.tb + 1, ...
 #pragma unroll
@@ -426,88 +426,74 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
     if (kCode) fetch_scales(it.tb);
 
     f32x2 ring[RD][WIN];
-    const int steps = D + it.te - it.tb;
-    int gp = 0, xp = 0;  // where the step's window and strip begin in shared memory
-    for (int k = 0; k < steps;) {
+    for (int t0 = it.tb - D; t0 < it.te; t0 += RD) {
+      if (!first) {  // the stage before this one is free once every thread is here
+        __syncthreads();
+        slot = slot + 1 == g.stages ? 0 : slot + 1;
+        parity ^= slot == 0 ? 1u : 0u;
+      }
+      first = false;
+      if (threadIdx.x == 0) issue();
+      if (!tma::mbar_wait(&full[slot], parity, timeouts)) {
+        // the copy never landed: let those in flight finish (bounded), then stop
+        for (int j = 1; j < g.stages; ++j) {
+          const int q = (slot + j) % g.stages;
+          tma::mbar_wait(&full[q], q > slot ? parity : parity ^ 1u, nullptr);
+        }
+        return;
+      }
+      const unsigned char* const gs = smdyn + (g_at + slot * g.stage_bytes);
+      const unsigned char* const xs = smdyn + (x_at + slot * g.stage_bytes);
 #pragma unroll
       for (int i = 0; i < RD; ++i) {
-        if (k >= steps) break;
-        if ((k & (rs - 1)) == 0) {  // a new stage: the one before it is free once every thread is here
-          if (k > 0 || item > chunk) {
-            __syncthreads();
-            slot = slot + 1 == kStages ? 0 : slot + 1;
-            parity ^= slot == 0 ? 1u : 0u;
-          }
-          if (threadIdx.x == 0) issue();
-          if (!tma::mbar_wait(&full[slot], parity, timeouts)) {
-            // the copy never landed: let those in flight finish (bounded), then stop
-            for (int j = 1; j < kStages; ++j) {
-              const int q = (slot + j) % kStages;
-              tma::mbar_wait(&full[q], q > slot ? parity : parity ^ 1u, nullptr);
+        const int t = t0 + i;
+#pragma unroll
+        for (int j = 0; j < WIN; ++j)
+          ring[i][j] = widen<T, kSrcFull>(*reinterpret_cast<const Raw<T, kSrcFull>*>(gs + i * grow + j * GP));
+        if (t < it.tb || t >= it.te) continue;
+        f32x2 xv[S * PX];
+#pragma unroll
+        for (int r = 0; r < S; ++r)
+#pragma unroll
+          for (int p = 0; p < PX; ++p) {
+            const unsigned char* q = xs + (i * S + r) * xrow + p * XP;
+            if constexpr (kCode) {
+              Raw<T, SRC> v;
+              v.s = __shfl_sync(0xffffffffu, sc[r], from + p);
+              v.v = *reinterpret_cast<const unsigned short*>(q);
+              xv[r * PX + p] = widen<T, SRC>(v);
+            } else {
+              xv[r * PX + p] = widen<T, SRC>(*reinterpret_cast<const Raw<T, SRC>*>(q));
             }
-            return;
           }
-          const int st = base + slot * g.stage_bytes;
-          gp = st + ((la << g.rs_log) * g.gc + ls * (PX / S)) * GP + pl * (GP / CT);
-          xp = st + g.x_at + ((la << g.rs_log) * S * g.xc + ls * PX) * XP + pl * (XP / CT);
+        if (kCode) {
+          if (t + 1 < it.te) fetch_scales(t + 1);
         }
-        const int t = it.tb - D + k;
-        const bool owned = k >= D;
         if (on) {
 #pragma unroll
-          for (int j = 0; j < WIN; ++j)
-            ring[i][j] = widen<T, kSrcFull>(*reinterpret_cast<const Raw<T, kSrcFull>*>(smdyn + (gp + j * GP)));
-        }
-        float sn[S];
+          for (int r = 0; r < S; ++r) {
+            f32x2 out[PX];
 #pragma unroll
-        for (int r = 0; r < S; ++r) sn[r] = sc[r];
-        if (kCode && owned && k + 1 < steps) fetch_scales(t + 1);
-        if (owned) {
-          f32x2 xv[S * PX];
+            for (int a = r; a < K; a += S) {
+              const int rs = (i - (a - r) / S + RD) % RD;
 #pragma unroll
-          for (int r = 0; r < S; ++r)
+              for (int b = 0; b < K; ++b)
 #pragma unroll
-            for (int p = 0; p < PX; ++p) {
-              const unsigned char* q = smdyn + (xp + r * xrow_bytes + p * XP);
-              if constexpr (kCode) {
-                Raw<T, SRC> v;
-                v.s = __shfl_sync(0xffffffffu, sn[r], from + p);
-                v.v = *reinterpret_cast<const unsigned short*>(q);
-                xv[r * PX + p] = widen<T, SRC>(v);
-              } else {
-                xv[r * PX + p] = widen<T, SRC>(*reinterpret_cast<const Raw<T, SRC>*>(q));
-              }
+                for (int p = 0; p < PX; ++p) {
+                  if ((p - b) % S != 0) continue;
+                  const f32x2 gv = ring[rs][D + (p - b) / S];
+                  if (a == r && b == p % S) out[p] = mul_f32x2(wr[a * K + b], gv);
+                  else fma_f32x2(out[p], wr[a * K + b], gv);
+                  fma_f32x2(acc[a * K + b], xv[r * PX + p], gv);
+                  if (a == K / 2 && b == K / 2) acc[K * K] = add_f32x2(acc[K * K], gv);
+                }
             }
-          if (on) {
-#pragma unroll
-            for (int r = 0; r < S; ++r) {
-              f32x2 out[PX];
-#pragma unroll
-              for (int a = r; a < K; a += S) {
-                const int from_slot = (i - (a - r) / S + RD) % RD;
-#pragma unroll
-                for (int p = 0; p < PX; ++p)
-#pragma unroll
-                  for (int b = 0; b < K; ++b) {
-                    if ((p - b) % S != 0) continue;
-                    const f32x2 gv = ring[from_slot][D + (p - b) / S];
-                    if (a == r && b == p % S) out[p] = mul_f32x2(wr[a * K + b], gv);
-                    else fma_f32x2(out[p], wr[a * K + b], gv);
-                    fma_f32x2(acc[a * K + b], xv[r * PX + p], gv);
-                    if (a == K / 2 && b == K / 2) fma_f32x2(acc[K * K], one, gv);
-                  }
-              }
-              const int ih = S * t + r - c.ph;
-              if (g.want_gx && (S == 1 || (ih >= 0 && ih < H))) {  // at stride 1 every owned row is inside
-                store_strip<T, true, PX>(op + r * row, C, out, xok, true, g.accumulate);
-              }
-            }
+            const int ih = S * t + r - c.ph;
+            if (g.want_gx && (S == 1 || (ih >= 0 && ih < H)))  // at stride 1 every owned row is inside
+              store_strip<T, true, PX>(op + r * row, C, out, xok, true, g.accumulate);
           }
         }
-        if (owned) op += S * row;
-        gp += grow_bytes;
-        xp += S * xrow_bytes;
-        ++k;
+        op += S * row;
       }
     }
   }
@@ -659,7 +645,7 @@ cudaError_t launch_staged(const Conv& c, const Staged& g, const T* x, const Act8
                           float* ws, cudaStream_t s) {
   const uint64_t es = sizeof(T), xes = SRC == kSrcFull ? es : 1;
   CUtensorMap mg, mx;
-  const uint32_t rows = 1u << g.rs_log;
+  constexpr uint32_t rows = 2 / S + 1;
   const uint64_t gd[4] = {(uint64_t)c.C, (uint64_t)c.Wo, (uint64_t)c.Ho, (uint64_t)c.N};
   const uint64_t gs[3] = {c.ctot * es, c.Wo * c.ctot * es, c.Ho * c.Wo * c.ctot * es};
   const uint32_t gb[4] = {2 * CT, (uint32_t)g.gc, rows, (uint32_t)g.ns};
@@ -675,7 +661,7 @@ cudaError_t launch_staged(const Conv& c, const Staged& g, const T* x, const Act8
   unsigned int* to = tma::timeout_counter();
   if (!to) return cudaErrorNotSupported;
   auto kern = staged3_kernel<T, SRC, S, CT>;
-  const size_t smem = (size_t)kStages * g.stage_bytes + 128;
+  const size_t smem = (size_t)g.stages * g.stage_bytes + 128;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)(g.tiles * g.chunks), g.threads, smem, s>>>(c, g, mg, mx, x8, to, w, gx, ws);
