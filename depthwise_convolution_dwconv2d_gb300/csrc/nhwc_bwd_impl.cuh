@@ -146,6 +146,29 @@ __device__ __forceinline__ void store_strip(T* o, int64_t C, const f32x2* v, uin
   }
 }
 
+// Loads from a 32-bit shared address: a register and a constant make one
+// instruction. Volatile, to stay behind the wait for the copy that wrote it.
+__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ Raw<T, kSrcFull> lds_pair(uint32_t at) {
+  Raw<T, kSrcFull> r;
+  if constexpr (sizeof(T) == 4) {
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(r.v) : "r"(at));
+  } else {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r.v) : "r"(at));
+  }
+  return r;
+}
+
 // ---- items -----------------------------------------------------------------
 
 // Sums the block's NACC pairs per thread over its row lanes, in lane order,
@@ -326,6 +349,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
   extern __shared__ __align__(16) unsigned char smdyn[];
   __shared__ __align__(8) uint64_t full[kMaxStages];
   const int base = (int)((128 - (tma::smem_u32(smdyn) & 127)) & 127);
+  const uint32_t sm0 = tma::smem_u32(smdyn) + base;
   const int tile = blockIdx.x % g.tiles, chunk = blockIdx.x / g.tiles;
   const int ch0 = tile * 2 * CT;
   const int pl = threadIdx.x & (CT - 1);
@@ -333,16 +357,33 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
   const int lane = threadIdx.x / CT;
   const int ls = lane % g.cs, ln = lane / g.cs;           // strip and sample of the lane
   const int la = min(ln, g.ns - 1);                       // a lane past the last sample reads within the stage
-  const int C = (int)c.C, H = (int)c.H, W = (int)c.W;
-  const int grow = g.gc * GP, xrow = g.xc * XP;           // bytes of a staged row
-  const int g_at = base + (la * RD * g.gc + ls * (PX / S)) * GP + pl * (GP / CT);
-  const int x_at = base + g.x_at + (la * RD * S * g.xc + ls * PX) * XP + pl * (XP / CT);
+  const int C = (int)c.C, W = (int)c.W;
+  const uint32_t g_at = sm0 + (la * RD * g.gc + ls * (PX / S)) * GP + pl * (GP / CT);
+  const uint32_t x_at = sm0 + g.x_at + (la * RD * S * g.xc + ls * PX) * XP + pl * (XP / CT);
 
+  // What a row needs besides its data goes through shared memory, so that it stays in registers: from the kernel's
+  // parameters the compiler recomputes it in every row (50 integer instructions and 13 parameter loads a row).
+  __shared__ uint32_t keep[8];
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.stages; ++i) tma::mbar_init(&full[i], 1);
     tma::fence_init();
+    const uint64_t row = (uint64_t)c.W * c.C * sizeof(T);
+    keep[0] = g.gc * GP;
+    keep[1] = g.xc * XP;
+    keep[2] = (uint32_t)(c.C * sizeof(T));
+    keep[3] = (uint32_t)row;
+    keep[4] = (uint32_t)(row >> 32);
+    keep[5] = (uint32_t)c.H;
+    keep[6] = (uint32_t)c.ph;
+    keep[7] = (uint32_t)(c.W * x8.nblk * 4);
   }
   __syncthreads();
+  const uint32_t keep0 = tma::smem_u32(keep);
+  const uint32_t grow = lds_u32(keep0), xrow = lds_u32(keep0 + 4);    // bytes of a staged row of gy, of x
+  const uint32_t pixel = lds_u32(keep0 + 8);                          // bytes of a pixel and a row of gx
+  const uint64_t row = lds_u32(keep0 + 12) | (uint64_t)lds_u32(keep0 + 16) << 32;
+  const int H = (int)lds_u32(keep0 + 20), ph = (int)lds_u32(keep0 + 24);
+  const uint32_t srow = lds_u32(keep0 + 28);                          // bytes of a row of scales
 
   struct Item {
     int n0, v0, tb, te;  // first sample and column of the block, rows of the band
@@ -405,23 +446,22 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
 #pragma unroll
     for (int p = 0; p < PX; ++p) xok |= (iw0 + p >= 0 && iw0 + p < W) ? 1u << p : 0u;
     const int64_t at = n * H * (int64_t)W + (int64_t)(S * it.tb - c.ph) * W + iw0;  // pixel of the band's first row
-    const int64_t row = (int64_t)W * C;
-    T* op = gx + at * C + ch;
+    char* op = reinterpret_cast<char*>(gx + at * C + ch);
+    const int stores = !on || !g.want_gx ? 0 : xok == (1u << PX) - 1 && !g.accumulate ? 1 : 2;
     // a checkpoint's scales: lanes p + 4 b of the strip's lanes read pixel p, block b of the tile's
     const int sl = pl & 7, sb = (ch0 >> x8.shift) + (sl >> 2);
     const bool scaler = kCode && on && g.want_x && pl < 8 && sb < x8.nblk && ((xok >> (sl & 3)) & 1);
     const int from = (int)(threadIdx.x & 31 & ~(CT - 1)) + 4 * ((ch >> x8.shift) - (ch0 >> x8.shift));
-    const int64_t srow = (int64_t)W * x8.nblk;
-    const float* sp = x8.scales + (at + (sl & 3)) * x8.nblk + sb;
+    const char* sp = reinterpret_cast<const char*>(x8.scales + (at + (sl & 3)) * x8.nblk + sb);
     float sc[S];
     auto fetch_scales = [&](int t) {  // t = it.tb, it.tb + 1, ...
 #pragma unroll
       for (int r = 0; r < S; ++r) {
-        const int ih = S * t + r - c.ph;
+        const int ih = S * t + r - ph;
         sc[r] = 0.f;
-        if (scaler && (S == 1 || (ih >= 0 && ih < H))) sc[r] = __ldg(sp + r * srow);
+        if (scaler && (S == 1 || (ih >= 0 && ih < H))) sc[r] = __ldg(reinterpret_cast<const float*>(sp));
+        sp += srow;
       }
-      sp += S * srow;
     };
     if (kCode) fetch_scales(it.tb);
 
@@ -442,30 +482,29 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
         }
         return;
       }
-      const unsigned char* const gs = smdyn + (g_at + slot * g.stage_bytes);
-      const unsigned char* const xs = smdyn + (x_at + slot * g.stage_bytes);
+      uint32_t gs = g_at + slot * g.stage_bytes, xs = x_at + slot * g.stage_bytes;
 #pragma unroll
-      for (int i = 0; i < RD; ++i) {
+      for (int i = 0; i < RD; ++i, gs += grow, xs += S * xrow) {
         const int t = t0 + i;
 #pragma unroll
-        for (int j = 0; j < WIN; ++j)
-          ring[i][j] = widen<T, kSrcFull>(*reinterpret_cast<const Raw<T, kSrcFull>*>(gs + i * grow + j * GP));
+        for (int j = 0; j < WIN; ++j) ring[i][j] = widen<T, kSrcFull>(lds_pair<T>(gs + j * GP));
         if (t < it.tb || t >= it.te) continue;
         f32x2 xv[S * PX];
 #pragma unroll
-        for (int r = 0; r < S; ++r)
+        for (int r = 0; r < S; ++r) {
+          const uint32_t q = xs + r * xrow;
 #pragma unroll
           for (int p = 0; p < PX; ++p) {
-            const unsigned char* q = xs + (i * S + r) * xrow + p * XP;
             if constexpr (kCode) {
               Raw<T, SRC> v;
               v.s = __shfl_sync(0xffffffffu, sc[r], from + p);
-              v.v = *reinterpret_cast<const unsigned short*>(q);
+              v.v = lds_u16(q + p * XP);
               xv[r * PX + p] = widen<T, SRC>(v);
             } else {
-              xv[r * PX + p] = widen<T, SRC>(*reinterpret_cast<const Raw<T, SRC>*>(q));
+              xv[r * PX + p] = widen<T, SRC>(lds_pair<T>(q + p * XP));
             }
           }
+        }
         if (kCode) {
           if (t + 1 < it.te) fetch_scales(t + 1);
         }
@@ -488,12 +527,27 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
                   if (a == K / 2 && b == K / 2) acc[K * K] = add_f32x2(acc[K * K], gv);
                 }
             }
-            const int ih = S * t + r - c.ph;
-            if (g.want_gx && (S == 1 || (ih >= 0 && ih < H)))  // at stride 1 every owned row is inside
-              store_strip<T, true, PX>(op + r * row, C, out, xok, true, g.accumulate);
+            const int ih = S * t + r - ph;
+            if (S == 1 || (ih >= 0 && ih < H)) {  // at stride 1 every owned row is inside
+              if (stores == 1) {
+                char* o = op;
+#pragma unroll
+                for (int p = 0; p < PX; ++p, o += pixel) {
+                  float a, b;
+                  unpack_f32x2(out[p], a, b);
+                  put_pair(reinterpret_cast<T*>(o), a, b);
+                }
+              } else if (stores == 2) {
+#pragma unroll
+                for (int p = 0; p < PX; ++p)
+                  if ((xok >> p) & 1) store_pair<T, true>(reinterpret_cast<T*>(op + p * pixel), out[p], true, g.accumulate);
+              }
+            }
+            op += row;
           }
+        } else {
+          op += S * row;
         }
-        op += S * row;
       }
     }
   }
