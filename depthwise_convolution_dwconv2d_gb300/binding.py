@@ -181,24 +181,32 @@ def load():
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return ctypes.c_void_p(t)
-    if hasattr(t, "data_ptr"):
-        if hasattr(t, "is_contiguous") and not t.is_contiguous():
+    """The device address of a tensor, an address or None."""
+    if t is None or isinstance(t, int):
+        return t
+    try:
+        if not t.is_contiguous():
             raise ValueError("libdwconv needs contiguous tensors")
-        return ctypes.c_void_p(t.data_ptr())
-    raise TypeError(f"cannot pass {type(t).__name__} as a device pointer")
+        return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"cannot pass {type(t).__name__} as a device pointer") from None
+
+
+_raw_stream = None  # (device -> address of its current stream, current device), once CUDA is up
 
 
 def _stream(stream):
+    global _raw_stream
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream) if torch.cuda.is_available() else None
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        if _raw_stream is None:
+            import torch
+            if not torch.cuda.is_available():
+                return None
+            torch.cuda.init()
+            _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                           or (lambda dev: torch.cuda.current_stream(dev).cuda_stream), torch.cuda.current_device)
+        return _raw_stream[0](_raw_stream[1]())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _check(status: int, where: str):
@@ -306,9 +314,12 @@ def dwconv2d_bwd_data_cached(desc: Desc, gy, cache, gx, accumulate=0, cache_byte
                                            int(accumulate), _stream(stream)), "dwconv2d_bwd_data_cached")
 
 
+_TORCH_DTYPES = {"torch.float32": 0, "torch.float16": 1, "torch.bfloat16": 2}
+
+
 def _dtype_of(x, dtype):
     if dtype is None:
-        dtype = {"float32": "f32", "float16": "f16", "bfloat16": "bf16"}[str(x.dtype).rpartition(".")[2]]
+        return _TORCH_DTYPES[str(x.dtype)]
     return DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
 
 
@@ -384,7 +395,7 @@ def _desc_array(descs):
 def _ptr_array(ts):
     if ts is None:
         return None
-    return (ctypes.c_void_p * len(ts))(*[None if p is None else _ptr(p).value for p in ts])
+    return (ctypes.c_void_p * len(ts))(*[_ptr(p) for p in ts])
 
 
 def dwconv2d_fwd_multi(descs, x, ws, biases, y, stream=None):

@@ -1,5 +1,6 @@
-// Channels-last group norm with an activation, forward and backward: the
-// split kernels, for every shape.
+// Channels-last group norm with an activation, forward and backward: plans,
+// dispatch, and the split kernels, for the shapes that the slab kernels
+// (norm_slab_impl.cuh) leave.
 //
 // A sample's group is spread over C / D channels of every pixel, so its sums
 // need all of the sample before the first output. Here that is two reads of
@@ -18,6 +19,7 @@
 // formulae and a pairwise algorithm for computing sample variances", 1979).
 // All sums are fp32; every order is fixed, so results are bit-reproducible.
 #include "norm.cuh"
+#include "norm_slab.h"
 
 namespace dwconv {
 namespace norm {
@@ -395,12 +397,6 @@ grad_apply_kernel(Norm g, Cut k, const T* __restrict__ x, Act8 x8, const T* __re
 
 unsigned grid_of(int64_t n) { return (unsigned)(n < (1 << 20) ? n : (1 << 20)); }
 
-// 16-byte vectors need every distance, offset and pointer to be a multiple of them
-bool vec_ok(const Norm& g, int V, int es, const void* x, const void* y) {
-  return g.C % V == 0 && g.xs % V == 0 && g.xo % V == 0 && g.ys % V == 0 && g.yo % V == 0 &&
-         reinterpret_cast<uintptr_t>(x) % 16 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
-}
-
 template <typename T, int V>
 cudaError_t split_fwd(const Norm& g, const T* x, const T* gamma, const T* beta, T* y, float* mean, float* rstd,
                       float* ws, cudaStream_t s) {
@@ -450,7 +446,74 @@ __global__ void zero_kernel(int C, T* a, T* b) {
 
 }  // namespace
 
-const char* plan_name(const Norm&, int) { return "split"; }
+namespace {
+
+int64_t lcm(int64_t a, int64_t b) {
+  int64_t x = a, y = b;
+  while (y) {
+    const int64_t r = x % y;
+    x = y;
+    y = r;
+  }
+  return a / x * b;
+}
+
+// The slab plan of a pass for vectors of V elements; false: split. keep: the
+// block of a checkpoint that the forward writes (0: none); x_bytes: of an
+// element of the backward's input (0: forward).
+bool plan_slab(const Norm& g, int V, int es, int keep, int x_bytes, slab::Plan* out) {
+  slab::Plan k{};
+  int64_t base = lcm(g.D, V);
+  if (keep && keep < g.C) base = lcm(base, keep);
+  if (keep && keep / V > 32) return false;  // a block's lanes are one warp's
+  const int64_t line = 128 / es;
+  int64_t S = base * ((line + base - 1) / base);
+  if (S > g.C || keep >= g.C) S = g.C;  // a slice holds whole blocks of a checkpoint, or all channels
+  k.S = (int)S;
+  k.vpr = (int)((S + V - 1) / V);
+  if (keep) k.vpr = (k.vpr + keep / V - 1) / (keep / V) * (keep / V);
+  if (k.vpr > slab::kNT) return false;
+  k.rl = slab::kNT / k.vpr;
+  k.slices = (int)((g.C + S - 1) / S);
+  k.groups = (int)(S / g.D);
+  const int64_t units = g.N * k.slices;
+  const int64_t row = (int64_t)k.vpr * V * (es + x_bytes);
+  // Shares small enough for several blocks per SM, whose reading and writing
+  // overlap; more blocks where the slabs are too few for the GPU.
+  auto rows = [&](int cl) { return (g.P + cl - 1) / cl; };
+  k.cl = 1;
+  while (k.cl < 8 && rows(k.cl) * row > 44 * 1024) k.cl *= 2;
+  while (k.cl < 8 && units * k.cl < 304 && rows(k.cl) > 2 * k.rl) k.cl *= 2;
+  if (rows(k.cl) * row > 180 * 1024 || units * k.cl >= (int64_t(1) << 31)) return false;
+  k.rows = (int)rows(k.cl);
+  k.data_bytes = (int)((k.rows * row + 15) / 16 * 16);
+  if (k.data_bytes + slab::scratch_bytes(k, V, x_bytes ? 1 : 0) > 220 * 1024) return false;
+  *out = k;
+  return true;
+}
+
+// The widest vector that distances, offsets and pointers allow: 16 bytes, 4 bytes or one element.
+int vector_of(const Norm& g, int es, const void* a, const void* b, const void* c, const void* codes) {
+  for (int bytes : {16, 4}) {
+    const int V = bytes / es;
+    if (V < 1) continue;
+    auto fits = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+    if (g.C % V == 0 && g.xs % V == 0 && g.xo % V == 0 && g.ys % V == 0 && g.yo % V == 0 && fits(a) && fits(b) &&
+        fits(c) && reinterpret_cast<uintptr_t>(codes) % V == 0)
+      return V;
+  }
+  return 1;
+}
+
+int elem_size(int dtype) { return dtype == DWCONV_F32 ? 4 : 2; }
+
+}  // namespace
+
+const char* plan_name(const Norm& g, int pass) {
+  const int es = elem_size(g.dtype);
+  slab::Plan k;
+  return plan_slab(g, vector_of(g, es, nullptr, nullptr, nullptr, nullptr), es, 0, pass ? es : 0, &k) ? "slab" : "split";
+}
 
 // (mean, rstd) or (s1, s2) per group, and a pair per chunk and channel, for
 // the finer of the two cuts (vectors or single elements)
@@ -461,17 +524,58 @@ size_t workspace_bytes(const Norm& g, int) {
   return (pairs * sizeof(float2) + 255) & ~size_t(255);
 }
 
+namespace {
+
+template <typename T>
+cudaError_t fwd_any(const Norm& g, const T* x, const T* gamma, const T* beta, T* y, float* mean, float* rstd, float* ws,
+                    const Act8& x8, cudaStream_t s) {
+  const int es = sizeof(T);
+  const int V = vector_of(g, es, x, y, nullptr, x8.codes);
+  const int block = x8.codes ? 1 << x8.shift : 0;
+  slab::Plan k;
+  if (plan_slab(g, V, es, block, 0, &k)) return slab::run_fwd<T>(g, k, V, x, gamma, beta, y, mean, rstd, x8, s);
+  cudaError_t e;
+  if (plan_slab(g, V, es, 0, 0, &k)) {
+    e = slab::run_fwd<T>(g, k, V, x, gamma, beta, y, mean, rstd, Act8{}, s);
+  } else {
+    constexpr int VV = Vec<T>::n;
+    e = V == VV ? split_fwd<T, VV>(g, x, gamma, beta, y, mean, rstd, ws, s)
+                : split_fwd<T, 1>(g, x, gamma, beta, y, mean, rstd, ws, s);
+  }
+  if (e == cudaSuccess && block) e = act8_encode(g.N * g.P, g.C, g.xs, g.dtype, x + g.xo, x8, s);
+  return e;
+}
+
+template <typename T>
+cudaError_t bwd_any(const Norm& g, const T* x, const Act8& x8, const T* gy, const T* gamma, const T* beta,
+                    const float* mean, const float* rstd, T* gx, T* ggamma, T* gbeta, float* ws, cudaStream_t s) {
+  if (g.N == 0) {
+    if (!ggamma && !gbeta) return cudaSuccess;
+    zero_kernel<T><<<(unsigned)div_up(g.C, 256), 256, 0, s>>>(g.C, ggamma, gbeta);
+    return cudaGetLastError();
+  }
+  const int es = sizeof(T);
+  const int V = vector_of(g, es, x, gy, gx, x8.codes);
+  slab::Plan k;
+  if (plan_slab(g, V, es, 0, x ? es : 1, &k)) {
+    float2* sums = reinterpret_cast<float2*>(ws);
+    const cudaError_t e = slab::run_bwd<T>(g, k, V, x, x8, gy, gamma, beta, mean, rstd, gx, sums, s);
+    if (e != cudaSuccess || (!ggamma && !gbeta)) return e;
+    param_grad_kernel<T><<<(g.C + 31) / 32, kNT, 0, s>>>(g.C, g.N, sums, ggamma, gbeta);
+    return cudaGetLastError();
+  }
+  constexpr int VV = Vec<T>::n;
+  return V == VV ? bwd_src<T, VV>(g, x, x8, gy, gamma, beta, mean, rstd, gx, ggamma, gbeta, ws, s)
+                 : bwd_src<T, 1>(g, x, x8, gy, gamma, beta, mean, rstd, gx, ggamma, gbeta, ws, s);
+}
+
+}  // namespace
+
 cudaError_t fwd(const Norm& g, const void* x, const void* gamma, const void* beta, void* y, float* mean,
                 float* rstd, float* ws, const Act8& x8, cudaStream_t s) {
   cudaError_t e = cudaErrorInvalidValue;
-  DWCONV_DISPATCH_DTYPE(g.dtype, T, {
-    constexpr int V = Vec<T>::n;
-    const T* xp = (const T*)x;
-    e = vec_ok(g, V, sizeof(T), x, y)
-            ? split_fwd<T, V>(g, xp, (const T*)gamma, (const T*)beta, (T*)y, mean, rstd, ws, s)
-            : split_fwd<T, 1>(g, xp, (const T*)gamma, (const T*)beta, (T*)y, mean, rstd, ws, s);
-    if (e == cudaSuccess && x8.codes) e = act8_encode(g.N * g.P, g.C, g.xs, g.dtype, xp + g.xo, x8, s);
-  });
+  DWCONV_DISPATCH_DTYPE(g.dtype, T, e = fwd_any<T>(g, (const T*)x, (const T*)gamma, (const T*)beta, (T*)y, mean, rstd,
+                                                   ws, x8, s));
   return e;
 }
 
@@ -479,20 +583,8 @@ cudaError_t bwd(const Norm& g, const void* x, const Act8& x8, const void* gy, co
                 const void* beta, const float* mean, const float* rstd, void* gx, void* ggamma, void* gbeta,
                 float* ws, cudaStream_t s) {
   cudaError_t e = cudaErrorInvalidValue;
-  DWCONV_DISPATCH_DTYPE(g.dtype, T, {
-    constexpr int V = Vec<T>::n;
-    if (g.N == 0) {
-      if (!ggamma && !gbeta) return cudaSuccess;
-      zero_kernel<T><<<(unsigned)div_up(g.C, 256), 256, 0, s>>>(g.C, (T*)ggamma, (T*)gbeta);
-      return cudaGetLastError();
-    }
-    const bool vec = vec_ok(g, V, sizeof(T), gx, gy) && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(x8.codes) % V == 0;
-    e = vec ? bwd_src<T, V>(g, (const T*)x, x8, (const T*)gy, (const T*)gamma, (const T*)beta, mean, rstd, (T*)gx,
-                            (T*)ggamma, (T*)gbeta, ws, s)
-            : bwd_src<T, 1>(g, (const T*)x, x8, (const T*)gy, (const T*)gamma, (const T*)beta, mean, rstd, (T*)gx,
-                            (T*)ggamma, (T*)gbeta, ws, s);
-  });
+  DWCONV_DISPATCH_DTYPE(g.dtype, T, e = bwd_any<T>(g, (const T*)x, x8, (const T*)gy, (const T*)gamma, (const T*)beta,
+                                                   mean, rstd, (T*)gx, (T*)ggamma, (T*)gbeta, ws, s));
   return e;
 }
 
