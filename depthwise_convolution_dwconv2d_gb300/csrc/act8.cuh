@@ -7,9 +7,8 @@
 //
 // max|x| is taken on the bit patterns without the sign, as integers: it needs
 // no rounding, so its order is free, and it keeps infinities and NaN (both
-// above every finite pattern). From an infinite or NaN maximum the scale is
-// infinite or NaN, every code is 0 or NaN, and 0 * inf = NaN: the block
-// decodes to NaN.
+// above every finite pattern): their block's scale is NaN, and so is every
+// value decoded from it.
 #pragma once
 
 #include "common.cuh"
@@ -38,26 +37,36 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits, float* inv) {
   const float s = __fmul_rn(__uint_as_float(amax_bits), r);
   const bool zero = s < 1.17549435e-38f;  // false for NaN
   *inv = zero ? 0.f : __frcp_rn(s);
-  return zero ? 0.f : s;
+  return zero ? 0.f : (amax_bits >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : s);
 }
 
-// four values -> four codes, first value in the low byte
+// four values (two pairs) -> four codes, first value in the low byte. The
+// integer nearest to v (|v| is at most 127 (1 + 2^-22)) is the low byte of
+// v + 1.5 * 2^23: an addition, which rounds to nearest even, instead of a
+// conversion.
 template <int SRC>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
-  a = __fmul_rn(a, inv);
-  b = __fmul_rn(b, inv);
-  c = __fmul_rn(c, inv);
-  d = __fmul_rn(d, inv);
+__device__ __forceinline__ uint32_t encode4(f32x2 ab, f32x2 cd, float inv) {
+  const f32x2 i2 = pack_f32x2(inv, inv);
+  ab = mul_f32x2(ab, i2);
+  cd = mul_f32x2(cd, i2);
+  float a, b, c, d;
   if (SRC == kSrcI8) {
-    // |v| is at most 127 (1 + 2^-22), so the nearest integer fits a byte; NaN converts to 0
-    const uint32_t p = __byte_perm((uint32_t)__float2int_rn(a), (uint32_t)__float2int_rn(b), 0x0040);
-    const uint32_t q = __byte_perm((uint32_t)__float2int_rn(c), (uint32_t)__float2int_rn(d), 0x0040);
-    return __byte_perm(p, q, 0x5410);
+    const f32x2 magic = pack_f32x2(12582912.f, 12582912.f);
+    unpack_f32x2(add_apart(ab, magic), a, b);
+    unpack_f32x2(add_apart(cd, magic), c, d);
+    return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040),
+                       __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
   }
+  unpack_f32x2(ab, a, b);
+  unpack_f32x2(cd, c, d);
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+template <int SRC>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
+  return encode4<SRC>(pack_f32x2(a, b), pack_f32x2(c, d), inv);
 }
 
 template <int SRC>
@@ -87,6 +96,28 @@ __device__ __forceinline__ void codes4(uint32_t v, float* o) {
   } else {
     e4m3_pair((uint16_t)(v & 0xffffu), o[0], o[1]);
     e4m3_pair((uint16_t)(v >> 16), o[2], o[3]);
+  }
+}
+
+// four codes -> four values (two pairs)
+template <int SRC>
+__device__ __forceinline__ void decode4(uint32_t v, float scale, f32x2* o) {
+  const f32x2 s2 = pack_f32x2(scale, scale);
+  if (SRC == kSrcI8) {
+    const uint32_t u = v ^ 0x80808080u;
+    const f32x2 bias = pack_f32x2(-8388736.0f, -8388736.0f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x2 m = pack_f32x2(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7650 + 2 * i)),
+                                 __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7651 + 2 * i)));
+      o[i] = mul_f32x2(add_f32x2(m, bias), s2);
+    }
+  } else {
+    float f[4];
+    e4m3_pair((uint16_t)(v & 0xffffu), f[0], f[1]);
+    e4m3_pair((uint16_t)(v >> 16), f[2], f[3]);
+    o[0] = mul_f32x2(pack_f32x2(f[0], f[1]), s2);
+    o[1] = mul_f32x2(pack_f32x2(f[2], f[3]), s2);
   }
 }
 

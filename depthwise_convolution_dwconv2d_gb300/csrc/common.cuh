@@ -116,6 +116,16 @@ __device__ __forceinline__ f32x2 add_f32x2(f32x2 a, f32x2 b) {
   return d;
 }
 
+// a + b lane by lane, for an addend that is a packed product: the assembler
+// contracts mul.rn.f32x2 and add.rn.f32x2 into one rounding (seen in codes
+// next to a tie), which the scalar addition prevents.
+__device__ __forceinline__ f32x2 add_apart(f32x2 a, f32x2 b) {
+  float a0, a1, b0, b1;
+  unpack_f32x2(a, a0, a1);
+  unpack_f32x2(b, b0, b1);
+  return pack_f32x2(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
+}
+
 // plain (coherent) load for data this kernel may also write
 template <typename T> __device__ __forceinline__ float ld_rw(const T* p) { return to_f<T>(*p); }
 

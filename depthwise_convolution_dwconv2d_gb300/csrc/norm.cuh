@@ -57,56 +57,123 @@ __device__ __forceinline__ float affine(float xh, float gamma, float beta) {
 constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kCubic = 0.044715f;
 
-// 1 / (1 + exp(-v)) with the fast exponential and division: a few units in
-// the last place, and 0 where exp(-v) overflows
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
-
-// act(u); NaN stays NaN
-template <int ACT>
-__device__ __forceinline__ float act_of(float u) {
-  if (ACT == DWCONV_ACT_RELU) return u < 0.f ? 0.f : u;
-  if (ACT == DWCONV_ACT_RELU6) return u < 0.f ? 0.f : (u > 6.f ? 6.f : u);
-  if (ACT == DWCONV_ACT_SILU) return __fdividef(u, 1.f + __expf(-u));
-  if (ACT == DWCONV_ACT_GELU) return __fdividef(u, 1.f + __expf(-kGelu * (u + kCubic * u * u * u)));
-  return u;
+// 2^v and 1 / v by the special-function unit: a few units in the last place
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 
-// act'(u)
+__device__ __forceinline__ f32x2 both(float v) { return pack_f32x2(v, v); }
+__device__ __forceinline__ f32x2 neg(f32x2 v) { return v ^ 0x8000000080000000ull; }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  fma_f32x2(c, a, b);
+  return c;
+}
+
+// 1 / (1 + exp(-c v)) of both lanes; c2 = -c log2(e)
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 v, float c2) {
+  float a, b;
+  unpack_f32x2(mul_f32x2(v, both(c2)), a, b);
+  unpack_f32x2(add_f32x2(pack_f32x2(exp2_fast(a), exp2_fast(b)), both(1.f)), a, b);
+  return pack_f32x2(rcp_fast(a), rcp_fast(b));
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// act(u) and act'(u) of both lanes; NaN stays NaN
 template <int ACT>
-__device__ __forceinline__ float slope_of(float u) {
-  if (ACT == DWCONV_ACT_RELU) return u > 0.f ? 1.f : 0.f;
-  if (ACT == DWCONV_ACT_RELU6) return u > 0.f && u < 6.f ? 1.f : 0.f;
-  if (ACT == DWCONV_ACT_SILU) {
-    const float q = sigmoid(u);
-    return q * (1.f + u * (1.f - q));
-  }
+__device__ __forceinline__ f32x2 act_of(f32x2 u) {
+  if (ACT == DWCONV_ACT_SILU) return mul_f32x2(u, sigmoid2(u, -kLog2e));
   if (ACT == DWCONV_ACT_GELU) {
-    const float q = sigmoid(kGelu * (u + kCubic * u * u * u));
-    return q + u * q * (1.f - q) * (kGelu * (1.f + 3.f * kCubic * u * u));
+    const f32x2 w = mul_f32x2(u, fma2(mul_f32x2(u, u), both(kCubic), both(1.f)));  // u + 0.044715 u^3
+    return mul_f32x2(u, sigmoid2(w, -kGelu * kLog2e));
   }
-  return 1.f;
+  float a, b;
+  unpack_f32x2(u, a, b);
+  if (ACT == DWCONV_ACT_RELU || ACT == DWCONV_ACT_RELU6) {
+    a = a < 0.f ? 0.f : a;
+    b = b < 0.f ? 0.f : b;
+  }
+  if (ACT == DWCONV_ACT_RELU6) {
+    a = a > 6.f ? 6.f : a;
+    b = b > 6.f ? 6.f : b;
+  }
+  return pack_f32x2(a, b);
+}
+template <int ACT>
+__device__ __forceinline__ f32x2 slope_of(f32x2 u) {
+  if (ACT == DWCONV_ACT_SILU) {  // q (1 + u (1 - q))
+    const f32x2 q = sigmoid2(u, -kLog2e);
+    return mul_f32x2(q, fma2(u, add_f32x2(both(1.f), neg(q)), both(1.f)));
+  }
+  if (ACT == DWCONV_ACT_GELU) {  // q (1 + u (1 - q) 2 sqrt(2 / pi) (1 + 3 * 0.044715 u^2))
+    const f32x2 uu = mul_f32x2(u, u);
+    const f32x2 q = sigmoid2(mul_f32x2(u, fma2(uu, both(kCubic), both(1.f))), -kGelu * kLog2e);
+    const f32x2 w = mul_f32x2(u, fma2(uu, both(3.f * kGelu * kCubic), both(kGelu)));
+    return mul_f32x2(q, fma2(w, add_f32x2(both(1.f), neg(q)), both(1.f)));
+  }
+  float a, b;
+  unpack_f32x2(u, a, b);
+  if (ACT == DWCONV_ACT_RELU) return pack_f32x2(a > 0.f ? 1.f : 0.f, b > 0.f ? 1.f : 0.f);
+  if (ACT == DWCONV_ACT_RELU6)
+    return pack_f32x2(a > 0.f && a < 6.f ? 1.f : 0.f, b > 0.f && b < 6.f ? 1.f : 0.f);
+  return both(1.f);
 }
 
-// V values at a time: one uniform branch per vector
-template <int V>
-__device__ __forceinline__ void act_v(int act, float* u) {
+// NP pairs at a time: one uniform branch per vector
+template <int NP>
+__device__ __forceinline__ void act_p(int act, f32x2* u) {
 #define X(A)                                                  \
   case A:                                                     \
-    _Pragma("unroll") for (int e = 0; e < V; ++e) u[e] = act_of<A>(u[e]); \
+    _Pragma("unroll") for (int e = 0; e < NP; ++e) u[e] = act_of<A>(u[e]); \
     break;
   switch (act) { X(DWCONV_ACT_RELU) X(DWCONV_ACT_RELU6) X(DWCONV_ACT_SILU) X(DWCONV_ACT_GELU) default: break; }
 #undef X
 }
-
 // u <- act'(u)
-template <int V>
-__device__ __forceinline__ void slope_v(int act, float* u) {
+template <int NP>
+__device__ __forceinline__ void slope_p(int act, f32x2* u) {
 #define X(A)                                                  \
   case A:                                                     \
-    _Pragma("unroll") for (int e = 0; e < V; ++e) u[e] = slope_of<A>(u[e]); \
+    _Pragma("unroll") for (int e = 0; e < NP; ++e) u[e] = slope_of<A>(u[e]); \
     break;
-  switch (act) { X(DWCONV_ACT_NONE) X(DWCONV_ACT_RELU) X(DWCONV_ACT_RELU6) X(DWCONV_ACT_SILU) X(DWCONV_ACT_GELU) default: break; }
+  switch (act) { X(DWCONV_ACT_RELU) X(DWCONV_ACT_RELU6) X(DWCONV_ACT_SILU) X(DWCONV_ACT_GELU) default: X(DWCONV_ACT_NONE) }
 #undef X
+}
+
+// the same of V values held one by one
+template <int V>
+__device__ __forceinline__ void act_v(int act, float* u) {
+  f32x2 p[(V + 1) / 2];
+#pragma unroll
+  for (int e = 0; e < (V + 1) / 2; ++e) p[e] = pack_f32x2(u[2 * e], 2 * e + 1 < V ? u[2 * e + 1] : 0.f);
+  act_p<(V + 1) / 2>(act, p);
+#pragma unroll
+  for (int e = 0; e < (V + 1) / 2; ++e) {
+    float a, b;
+    unpack_f32x2(p[e], a, b);
+    u[2 * e] = a;
+    if (2 * e + 1 < V) u[2 * e + 1] = b;
+  }
+}
+template <int V>
+__device__ __forceinline__ void slope_v(int act, float* u) {
+  f32x2 p[(V + 1) / 2];
+#pragma unroll
+  for (int e = 0; e < (V + 1) / 2; ++e) p[e] = pack_f32x2(u[2 * e], 2 * e + 1 < V ? u[2 * e + 1] : 0.f);
+  slope_p<(V + 1) / 2>(act, p);
+#pragma unroll
+  for (int e = 0; e < (V + 1) / 2; ++e) {
+    float a, b;
+    unpack_f32x2(p[e], a, b);
+    u[2 * e] = a;
+    if (2 * e + 1 < V) u[2 * e + 1] = b;
+  }
 }
 
 }  // namespace norm

@@ -40,26 +40,30 @@ template <> struct Word<4> { typedef uint32_t type; };
 template <> struct Word<2> { typedef uint16_t type; };
 template <> struct Word<1> { typedef uint8_t type; };
 
+// V elements as pairs (an odd V's last pair has 0 in its second lane)
 template <typename T, int V>
 struct Vecs {
   typedef typename Word<V * (int)sizeof(T)>::type word;
-  static __device__ __forceinline__ void unpack(word w, float* f) {
+  static constexpr int NP = (V + 1) / 2;
+  static __device__ __forceinline__ void unpack(word w, f32x2* f) {
     if constexpr (V * sizeof(T) == 16) {
-      unpack16<T>(w, f);
+      unpack16_pairs<T>(w, f);
     } else {
       const T* p = reinterpret_cast<const T*>(&w);
-#pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = to_f<T>(p[e]);
+      f[0] = pack_f32x2(to_f<T>(p[0]), V > 1 ? to_f<T>(p[V - 1]) : 0.f);
     }
   }
-  static __device__ __forceinline__ word pack(const float* f) {
+  static __device__ __forceinline__ word pack(const f32x2* f) {
+    float v[2 * NP];
+#pragma unroll
+    for (int e = 0; e < NP; ++e) unpack_f32x2(f[e], v[2 * e], v[2 * e + 1]);
     if constexpr (V * sizeof(T) == 16) {
-      return pack16<T>(f);
+      return pack16<T>(v);
     } else {
       word w;
       T* p = reinterpret_cast<T*>(&w);
 #pragma unroll
-      for (int e = 0; e < V; ++e) p[e] = from_f<T>(f[e]);
+      for (int e = 0; e < V; ++e) p[e] = from_f<T>(v[e]);
       return w;
     }
   }
@@ -67,51 +71,85 @@ struct Vecs {
 
 // codes of V values
 template <int SRC, int V>
-__device__ __forceinline__ void unpack_codes(typename Word<V>::type w, float s, float* f) {
+__device__ __forceinline__ void unpack_codes(typename Word<V>::type w, float s, f32x2* f) {
   if constexpr (V == 8) {
-    codes4<SRC>(w.x, f);
-    codes4<SRC>(w.y, f + 4);
+    decode4<SRC>(w.x, s, f);
+    decode4<SRC>(w.y, s, f + 2);
   } else if constexpr (V == 4) {
-    codes4<SRC>(w, f);
+    decode4<SRC>(w, s, f);
   } else {
-    float o[4];
-    codes4<SRC>((uint32_t)w, o);
-#pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = o[e];
+    f32x2 o[2];
+    decode4<SRC>((uint32_t)w, s, o);
+    f[0] = o[0];
   }
-#pragma unroll
-  for (int e = 0; e < V; ++e) f[e] = __fmul_rn(f[e], s);
 }
 template <int SRC, int V>
-__device__ __forceinline__ typename Word<V>::type pack_codes(const float* f, float inv) {
+__device__ __forceinline__ typename Word<V>::type pack_codes(const f32x2* f, float inv) {
   if constexpr (V == 8) {
-    return make_uint2(encode4<SRC>(f[0], f[1], f[2], f[3], inv), encode4<SRC>(f[4], f[5], f[6], f[7], inv));
+    return make_uint2(encode4<SRC>(f[0], f[1], inv), encode4<SRC>(f[2], f[3], inv));
   } else if constexpr (V == 4) {
-    return encode4<SRC>(f[0], f[1], f[2], f[3], inv);
-  } else if constexpr (V == 2) {
-    return (uint16_t)encode4<SRC>(f[0], f[1], 0.f, 0.f, inv);
+    return encode4<SRC>(f[0], f[1], inv);
   } else {
-    return encode1<SRC>(f[0], inv);
+    return (typename Word<V>::type)encode4<SRC>(f[0], 0, inv);
   }
 }
 
-// Sums v over the block's row lanes, in lane order, into chan[channel of the
-// slice]; red holds kNT * V floats.
+// The largest pattern without sign of a vector's values and its neighbours'
+// of a block of channels (`lanes` of them), as that of an fp32 value.
+// Patterns of 16-bit types are compared two at a time.
+template <typename T, int V>
+__device__ __forceinline__ uint32_t block_max(typename Vecs<T, V>::word w, int lanes) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t m = 0;
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
+#pragma unroll
+    for (int e = 0; e < V; ++e) m = max(m, u[e] & 0x7fffffffu);
+    for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+  } else {
+    uint32_t m;
+    if constexpr (V == 8) {
+      m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+    } else {
+      m = (uint32_t)w & 0x7fff7fffu;
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const unsigned short h = (unsigned short)max(m & 0xffffu, m >> 16);
+    return __float_as_uint(to_f<T>(*reinterpret_cast<const T*>(&h)));
+  }
+}
+
+// Sums v over the block's row lanes, in a fixed order, into chan[channel of
+// the slice]; red holds kNT * V floats. Where a slice's vectors are a power of
+// two of at most 16, the row lanes of a warp are added by shuffles first.
 template <int V>
-__device__ __forceinline__ void join_rows(const Plan& k, const float* v, float* red, float* chan) {
-  const int n = k.vpr * V;  // channels, idle ones included
-  const bool in = (int)threadIdx.x < k.rl * k.vpr;
+__device__ __forceinline__ void join_rows(const Plan& k, const f32x2* v, float* red, float* chan) {
+  float f[V + 1];
+#pragma unroll
+  for (int e = 0; e < (V + 1) / 2; ++e) unpack_f32x2(v[e], f[2 * e], f[2 * e + 1]);
+  const bool by_warp = k.vpr <= 16 && (k.vpr & (k.vpr - 1)) == 0;
+  if (by_warp) {
+    for (int o = 16; o >= k.vpr; o >>= 1) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] += __shfl_xor_sync(0xffffffffu, f[e], o);
+    }
+  }
+  const int n = k.vpr * V;                       // channels, idle ones included
+  const int lanes = by_warp ? kNT / 32 : k.rl;   // sums left per channel
+  const int stride = lanes * k.vpr;
+  const bool in = by_warp ? (threadIdx.x & 31) < k.vpr : (int)threadIdx.x < k.rl * k.vpr;
+  const int at = by_warp ? (threadIdx.x >> 5) * k.vpr + (threadIdx.x & 31) : threadIdx.x;
   __syncthreads();
   if (in) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) red[e * kNT + threadIdx.x] = v[e];
+    for (int e = 0; e < V; ++e) red[e * stride + at] = f[e];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kNT) {
     const int e = i / k.vpr, vl = i - e * k.vpr;
     float a = 0.f;
 #pragma unroll 8
-    for (int r = 0; r < k.rl; ++r) a += red[e * kNT + r * k.vpr + vl];
+    for (int r = 0; r < lanes; ++r) a += red[e * stride + r * k.vpr + vl];
     chan[vl * V + e] = a;
   }
   __syncthreads();
@@ -177,10 +215,11 @@ __device__ __forceinline__ Place place_of(const Norm& g, const Plan& k) {
 }
 
 template <typename T, int V, int KEEP>
-__global__ void __launch_bounds__(kNT)
+__global__ void __launch_bounds__(kNT, 3)
 fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma, const T* __restrict__ beta,
            T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, Act8 x8) {
   typedef typename Vecs<T, V>::word word;
+  constexpr int NP = Vecs<T, V>::NP;
   extern __shared__ __align__(16) unsigned char sm[];
   cg::cluster_group cluster = cg::this_cluster();
   const Place p = place_of<V>(g, k);
@@ -191,52 +230,56 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
   float2* const stat = part + k.groups;                             // (mean, rstd) of the slab's
 
   // read, sum, keep
-  float s[V], d[V], q[V];
+  f32x2 s[NP], d[NP], q[NP];
 #pragma unroll
-  for (int e = 0; e < V; ++e) s[e] = d[e] = q[e] = 0.f;
+  for (int e = 0; e < NP; ++e) s[e] = d[e] = q[e] = 0;
   int gi[V];
   groups_of<V>(g.D, min(p.vl * V, p.S - 1), gi);
-  const T* xp = x + p.row0 * g.xs + g.xo + p.c;
+  const T* xp = x + (p.row0 + p.r) * g.xs + g.xo + p.c;
+  uint8_t* cp = KEEP != kSrcFull ? x8.codes + (p.row0 + p.r) * g.C + p.c : nullptr;
+  float* scp = KEEP != kSrcFull ? x8.scales + (p.row0 + p.r) * x8.nblk + (p.c >> x8.shift) : nullptr;
+  const bool scaler = KEEP != kSrcFull && (p.c & ((1 << x8.shift) - 1)) == 0;
+  const int64_t xstep = k.rl * g.xs;
+  const int left = p.on ? p.rows - p.r : 0;  // rows from this lane's first on
+  word* dp = data + p.r * k.vpr + p.vl;
+  const int dstep = k.rl * k.vpr;
   constexpr int kAhead = V == 1 ? 8 : 4;  // rows in flight
   for (int r0 = 0; r0 < p.rows; r0 += kAhead * k.rl) {
     word w[kAhead];
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int r = r0 + a * k.rl + p.r;
+    for (int a = 0; a < kAhead; ++a, xp += xstep) {
       w[a] = word{};
-      if (p.on && r < p.rows) w[a] = *reinterpret_cast<const word*>(xp + (int64_t)r * g.xs);
+      if (r0 + a * k.rl < left) w[a] = *reinterpret_cast<const word*>(xp);
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const int r = r0 + a * k.rl + p.r;
-      const bool in = p.on && r < p.rows;
-      float f[V];
+      const bool in = r0 + a * k.rl < left;
+      f32x2 f[NP];
       Vecs<T, V>::unpack(w[a], f);
       if (in) {
-        data[r * k.vpr + p.vl] = w[a];
+        *dp = w[a];
         if (a == 0 && r0 == 0) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) s[e] = f[e];
+          for (int e = 0; e < NP; ++e) s[e] = neg(f[e]);
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float t = f[e] - s[e];
-          d[e] += t;
-          q[e] = fmaf(t, t, q[e]);
+        for (int e = 0; e < NP; ++e) {
+          const f32x2 t = add_f32x2(f[e], s[e]);
+          d[e] = add_f32x2(d[e], t);
+          fma_f32x2(q[e], t, t);
         }
       }
+      dp += dstep;
       if (KEEP != kSrcFull) {  // lanes of a block of channels are neighbours; those without data bring zeros
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < V; ++e) m = max(m, abs_bits(f[e]));
-        for (int o = (1 << x8.shift) / V >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t m = block_max<T, V>(w[a], (1 << x8.shift) / V);
         if (in) {
           float inv;
           const float sc = scale_of<KEEP>(m, &inv);
-          typedef typename Word<V>::type codes;
-          *reinterpret_cast<codes*>(x8.codes + (p.row0 + r) * g.C + p.c) = pack_codes<KEEP, V>(f, inv);
-          if ((p.c & ((1 << x8.shift) - 1)) == 0) x8.scales[(p.row0 + r) * x8.nblk + (p.c >> x8.shift)] = sc;
+          *reinterpret_cast<typename Word<V>::type*>(cp) = pack_codes<KEEP, V>(f, inv);
+          if (scaler) *scp = sc;
         }
+        cp += (int64_t)k.rl * g.C;
+        scp += (int64_t)k.rl * x8.nblk;
       }
     }
   }
@@ -246,9 +289,9 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
   const float cnt = (float)mine, icnt = mine > 0 ? 1.f / cnt : 0.f;
   const int warp = threadIdx.x >> 5, groups = p.S / g.D;
   {
-    float v[V];
+    f32x2 v[NP];
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = fmaf(cnt, s[e], d[e]);
+    for (int e = 0; e < NP; ++e) v[e] = fma2(both(-cnt), s[e], d[e]);
     join_rows<V>(k, v, red, chan);
     for (int i = warp; i < groups; i += kNT / 32) {
       const float a = warp_sum(g.D, [&](int c) { return chan[i * g.D + c]; });
@@ -256,11 +299,18 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
     }
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float m = fmaf(d[e], icnt, s[e]);
-      const float own = q[e] - d[e] * d[e] * icnt;
-      const float t = p.on ? m - part[gi[e]].x : 0.f;
-      v[e] = mine > 0 ? (own < 0.f ? 0.f : own) + cnt * t * t : 0.f;  // NaN stays
+    for (int e = 0; e < NP; ++e) {
+      const f32x2 m = fma2(d[e], both(icnt), neg(s[e]));  // the thread's mean
+      float own[2], t[2];
+      unpack_f32x2(fma2(mul_f32x2(d[e], d[e]), both(-icnt), q[e]), own[0], own[1]);
+      unpack_f32x2(m, t[0], t[1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float o = own[h] < 0.f ? 0.f : own[h];  // NaN stays
+        const float off = 2 * e + h < V && p.on ? t[h] - part[gi[2 * e + h < V ? 2 * e + h : 0]].x : 0.f;
+        t[h] = mine > 0 ? o + cnt * off * off : 0.f;
+      }
+      v[e] = pack_f32x2(t[0], t[1]);
     }
     join_rows<V>(k, v, red, chan);
     for (int i = warp; i < groups; i += kNT / 32) {
@@ -301,36 +351,41 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
 
   // write
   if (p.on) {
-    float ga[V], be[V], mu[V], rs[V];
+    f32x2 ga[NP], be[NP], mu[NP], rs[NP];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      ga[e] = gamma ? ld(gamma + p.c + e) : 1.f;
-      be[e] = beta ? ld(beta + p.c + e) : 0.f;
-      const float2 st = stat[gi[e]];
-      mu[e] = st.x;
-      rs[e] = st.y;
+    for (int e = 0; e < NP; ++e) {
+      const int i = 2 * e, j = 2 * e + 1 < V ? 2 * e + 1 : 2 * e;
+      const float2 a = stat[gi[i]], b = stat[gi[j]];
+      mu[e] = pack_f32x2(-a.x, -b.x);
+      rs[e] = pack_f32x2(a.y, b.y);
+      ga[e] = gamma ? pack_f32x2(ld(gamma + p.c + i), ld(gamma + p.c + j)) : both(1.f);
+      be[e] = beta ? pack_f32x2(ld(beta + p.c + i), ld(beta + p.c + j)) : 0;
     }
-    T* yp = y + p.row0 * g.ys + g.yo + p.c;
+    T* yp = y + (p.row0 + p.r) * g.ys + g.yo + p.c;
+    const int64_t ystep = k.rl * g.ys;
+    dp = data + p.r * k.vpr + p.vl;
 #pragma unroll 2
-    for (int r = p.r; r < p.rows; r += k.rl) {
-      float f[V];
-      Vecs<T, V>::unpack(data[r * k.vpr + p.vl], f);
+    for (int r = p.r; r < p.rows; r += k.rl, yp += ystep, dp += dstep) {
+      f32x2 f[NP];
+      Vecs<T, V>::unpack(*dp, f);
 #pragma unroll
-      for (int e = 0; e < V; ++e) f[e] = affine(xhat(f[e], mu[e], rs[e]), ga[e], be[e]);
-      act_v<V>(g.act, f);
-      *reinterpret_cast<word*>(yp + (int64_t)r * g.ys) = Vecs<T, V>::pack(f);
+      for (int e = 0; e < NP; ++e)
+        f[e] = add_apart(mul_f32x2(mul_f32x2(add_f32x2(f[e], mu[e]), rs[e]), ga[e]), be[e]);
+      act_p<NP>(g.act, f);
+      *reinterpret_cast<word*>(yp) = Vecs<T, V>::pack(f);
     }
   }
   if (k.cl > 1) cluster_wait();  // no block leaves while another reads its sums
 }
 
 template <typename T, int V, int SRC>
-__global__ void __launch_bounds__(kNT)
+__global__ void __launch_bounds__(kNT, 2)
 bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict__ gy, const T* __restrict__ gamma,
            const T* __restrict__ beta, const float* __restrict__ mean, const float* __restrict__ rstd,
            T* __restrict__ gx, float2* __restrict__ sums) {
   typedef typename Vecs<T, V>::word word;
   typedef typename Word<SRC == kSrcFull ? V * (int)sizeof(T) : V>::type xword;
+  constexpr int NP = Vecs<T, V>::NP;
   extern __shared__ __align__(16) unsigned char sm[];
   cg::cluster_group cluster = cg::this_cluster();
   const Place p = place_of<V>(g, k);
@@ -343,82 +398,93 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
 
   int gi[V];
   groups_of<V>(g.D, min(p.vl * V, p.S - 1), gi);
-  float ga[V], be[V], mu[V], rs[V];
+  f32x2 ga[NP], be[NP], mu[NP], rs[NP];
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    ga[e] = be[e] = mu[e] = rs[e] = 0.f;
+  for (int e = 0; e < NP; ++e) {
+    ga[e] = be[e] = mu[e] = rs[e] = 0;
     if (p.on) {
-      ga[e] = gamma ? ld(gamma + p.c + e) : 1.f;
-      be[e] = beta ? ld(beta + p.c + e) : 0.f;
-      const int64_t at = p.n * g.G + p.c0 / g.D + gi[e];
-      mu[e] = __ldg(mean + at);
-      rs[e] = __ldg(rstd + at);
+      const int i = 2 * e, j = 2 * e + 1 < V ? 2 * e + 1 : 2 * e;
+      const int64_t at = p.n * g.G + p.c0 / g.D;
+      mu[e] = pack_f32x2(-__ldg(mean + at + gi[i]), -__ldg(mean + at + gi[j]));
+      rs[e] = pack_f32x2(__ldg(rstd + at + gi[i]), __ldg(rstd + at + gi[j]));
+      ga[e] = gamma ? pack_f32x2(ld(gamma + p.c + i), ld(gamma + p.c + j)) : both(1.f);
+      be[e] = beta ? pack_f32x2(ld(beta + p.c + i), ld(beta + p.c + j)) : 0;
     }
   }
-  const T* gp = gy + p.row0 * g.ys + g.yo + p.c;
-  auto load_x = [&](int r) {
-    if constexpr (SRC == kSrcFull) {
-      return *reinterpret_cast<const xword*>(x + (p.row0 + r) * g.xs + g.xo + p.c);
-    } else {
-      return *reinterpret_cast<const xword*>(x8.codes + (p.row0 + r) * g.C + p.c);
-    }
-  };
-  auto scale_at = [&](int r) {
-    return SRC == kSrcFull ? 0.f : __ldg(x8.scales + (p.row0 + r) * x8.nblk + (p.c >> x8.shift));
-  };
+  const T* gp = gy + (p.row0 + p.r) * g.ys + g.yo + p.c;
+  const int64_t gstep = k.rl * g.ys;
+  // x and its scale, one row lane's step at a time
+  const int64_t first = p.row0 + p.r;
+  const xword* xp;
+  int64_t xstep;
+  if constexpr (SRC == kSrcFull) {
+    xp = reinterpret_cast<const xword*>(x + first * g.xs + g.xo + p.c);
+    xstep = k.rl * g.xs / V;
+  } else {
+    xp = reinterpret_cast<const xword*>(x8.codes + first * g.C + p.c);
+    xstep = (int64_t)k.rl * g.C / V;
+  }
+  const float* scp = SRC == kSrcFull ? nullptr : x8.scales + first * x8.nblk + (p.c >> x8.shift);
+  const int64_t scstep = SRC == kSrcFull ? 0 : (int64_t)k.rl * x8.nblk;
   // xh and du of one vector, from what was stored
-  auto eval = [&](word gw, xword xw, float sc, float* xh, float* du) {
-    float t[V];
+  auto eval = [&](word gw, xword xw, float sc, f32x2* xh, f32x2* du) {
+    f32x2 t[NP];
     if constexpr (SRC == kSrcFull) {
       Vecs<T, V>::unpack(xw, xh);
     } else {
       unpack_codes<SRC, V>(xw, sc, xh);
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      xh[e] = xhat(xh[e], mu[e], rs[e]);
-      t[e] = affine(xh[e], ga[e], be[e]);
+    for (int e = 0; e < NP; ++e) {
+      const f32x2 d = SRC == kSrcFull ? add_f32x2(xh[e], mu[e]) : add_apart(xh[e], mu[e]);
+      xh[e] = mul_f32x2(d, rs[e]);
+      t[e] = add_apart(mul_f32x2(xh[e], ga[e]), be[e]);
     }
-    slope_v<V>(g.act, t);
+    slope_p<NP>(g.act, t);
     Vecs<T, V>::unpack(gw, du);
 #pragma unroll
-    for (int e = 0; e < V; ++e) du[e] *= t[e];
+    for (int e = 0; e < NP; ++e) du[e] = mul_f32x2(du[e], t[e]);
   };
 
   // read, sum, keep
-  float a[V], b[V];
+  f32x2 a[NP], b[NP];
 #pragma unroll
-  for (int e = 0; e < V; ++e) a[e] = b[e] = 0.f;
+  for (int e = 0; e < NP; ++e) a[e] = b[e] = 0;
+  const int at0 = p.r * k.vpr + p.vl, dstep = k.rl * k.vpr;
   if (p.on) {
     constexpr int kAhead = V == 1 ? 4 : 2;
+    const float* sq = scp;
+    int at = at0;
     for (int r0 = p.r; r0 < p.rows; r0 += kAhead * k.rl) {
       word gw[kAhead];
       xword xw[kAhead];
       float sc[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int r = r0 + i * k.rl;
         gw[i] = word{};
         xw[i] = xword{};
         sc[i] = 0.f;
-        if (r < p.rows) {
-          gw[i] = *reinterpret_cast<const word*>(gp + (int64_t)r * g.ys);
-          xw[i] = load_x(r);
-          sc[i] = scale_at(r);
+        if (r0 + i * k.rl < p.rows) {
+          gw[i] = *reinterpret_cast<const word*>(gp);
+          xw[i] = *xp;
+          if (SRC != kSrcFull) sc[i] = __ldg(sq);
         }
+        gp += gstep;
+        xp += xstep;
+        sq += scstep;
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int r = r0 + i * k.rl;
-        if (r >= p.rows) break;
-        gdata[r * k.vpr + p.vl] = gw[i];
-        xdata[r * k.vpr + p.vl] = xw[i];
-        float xh[V], du[V];
+        if (r0 + i * k.rl >= p.rows) break;
+        gdata[at] = gw[i];
+        xdata[at] = xw[i];
+        at += dstep;
+        f32x2 xh[NP], du[NP];
         eval(gw[i], xw[i], sc[i], xh, du);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          a[e] += du[e];
-          b[e] = fmaf(du[e], xh[e], b[e]);
+        for (int e = 0; e < NP; ++e) {
+          a[e] = add_f32x2(a[e], du[e]);
+          fma_f32x2(b[e], du[e], xh[e]);
         }
       }
     }
@@ -458,22 +524,25 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
   __syncthreads();
   if (k.cl > 1) cluster_arrive();
 
-  // write
+  // write: gx = du * (gamma rstd) - rstd s1 - xh * (rstd s2)
   if (gx && p.on) {
-    float s1[V], s2[V];
+    f32x2 c1[NP], c2[NP], c3[NP];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float2 st = stat[gi[e]];
-      s1[e] = st.x;
-      s2[e] = st.y;
+    for (int e = 0; e < NP; ++e) {
+      const float2 u = stat[gi[2 * e]], v = stat[gi[2 * e + 1 < V ? 2 * e + 1 : 2 * e]];
+      c1[e] = mul_f32x2(ga[e], rs[e]);
+      c2[e] = neg(mul_f32x2(pack_f32x2(u.x, v.x), rs[e]));
+      c3[e] = neg(mul_f32x2(pack_f32x2(u.y, v.y), rs[e]));
     }
-    T* op = gx + p.row0 * g.xs + g.xo + p.c;
-    for (int r = p.r; r < p.rows; r += k.rl) {
-      float xh[V], du[V];
-      eval(gdata[r * k.vpr + p.vl], xdata[r * k.vpr + p.vl], scale_at(r), xh, du);
+    T* op = gx + first * g.xs + g.xo + p.c;
+    const int64_t ostep = k.rl * g.xs;
+    int at = at0;
+    for (int r = p.r; r < p.rows; r += k.rl, op += ostep, scp += scstep, at += dstep) {
+      f32x2 xh[NP], du[NP];
+      eval(gdata[at], xdata[at], SRC == kSrcFull ? 0.f : __ldg(scp), xh, du);
 #pragma unroll
-      for (int e = 0; e < V; ++e) du[e] = (du[e] * ga[e] - fmaf(xh[e], s2[e], s1[e])) * rs[e];
-      *reinterpret_cast<word*>(op + (int64_t)r * g.xs) = Vecs<T, V>::pack(du);
+      for (int e = 0; e < NP; ++e) du[e] = fma2(du[e], c1[e], fma2(xh[e], c3[e], c2[e]));
+      *reinterpret_cast<word*>(op) = Vecs<T, V>::pack(du);
     }
   }
   if (k.cl > 1) cluster_wait();
