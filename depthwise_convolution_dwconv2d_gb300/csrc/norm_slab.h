@@ -22,9 +22,10 @@ struct Plan {
 };
 
 // Shared memory behind the shares: the row lanes' sums, tables per channel
-// (two of them in the backward) and per group.
+// and per group.
 inline int scratch_bytes(const Plan& k, int V, int pass) {
-  return (kNT * V + (pass + 1) * k.vpr * V + 1) / 2 * 8 + 2 * k.groups * 8;
+  const int np = (V + 1) / 2;
+  return (kNT * 4 * np + k.vpr * 4 * np + (pass ? 0 : k.vpr * 2 * np)) * 4 + 2 * k.groups * 8;
 }
 
 // Sums per (sample, channel) of the backward go to sums[N][C].

@@ -15,10 +15,10 @@
 // Slabs that no cluster of eight blocks can hold, and slices wider than a
 // block, are left to the split kernels (norm.cu).
 //
-// The variance is joined as in norm.cu: a thread sums x - s and (x - s)^2
-// about its own first value s of a channel, the squares are moved to the
-// block's mean of the group, and the blocks' (count, mean, squares) are
-// joined by the parallel form. Every order is fixed.
+// The variance is not taken from sums of squares of x: a block sums x - s and
+// (x - s)^2 about the values s of its first pixel, one per channel, turns
+// them into a mean and squares about that mean, and joins channels and blocks
+// by the parallel form of the two (see norm.cu). Every order is fixed.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -119,56 +119,60 @@ __device__ __forceinline__ uint32_t block_max(typename Vecs<T, V>::word w, int l
   }
 }
 
-// Sums v over the block's row lanes, in a fixed order, into chan[channel of
-// the slice]; red holds kNT * V floats. Where a slice's vectors are a power of
-// two of at most 16, the row lanes of a warp are added by shuffles first.
-template <int V>
-__device__ __forceinline__ void join_rows(const Plan& k, const f32x2* v, float* red, float* chan) {
-  float f[V + 1];
+// Sums two vectors over the block's row lanes, in lane order. Afterwards
+// tot[vl * 4 NP + e] is the sum of u's element e of vector vl of the slice
+// and tot[vl * 4 NP + 2 NP + e] that of v's. red holds kNT * 4 NP floats.
+template <int NP>
+__device__ __forceinline__ void join_rows(const Plan& k, const f32x2* u, const f32x2* v, float* red, float* tot) {
+  constexpr int W = 4 * NP;
+  if ((int)threadIdx.x < k.rl * k.vpr) {
+    ulonglong2* o = reinterpret_cast<ulonglong2*>(red + threadIdx.x * W);
+    if constexpr (NP == 1) {
+      o[0] = make_ulonglong2(u[0], v[0]);
+    } else {
 #pragma unroll
-  for (int e = 0; e < (V + 1) / 2; ++e) unpack_f32x2(v[e], f[2 * e], f[2 * e + 1]);
-  const bool by_warp = k.vpr <= 16 && (k.vpr & (k.vpr - 1)) == 0;
-  if (by_warp) {
-    for (int o = 16; o >= k.vpr; o >>= 1) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) f[e] += __shfl_xor_sync(0xffffffffu, f[e], o);
+      for (int e = 0; e < NP / 2; ++e) {
+        o[e] = make_ulonglong2(u[2 * e], u[2 * e + 1]);
+        o[NP / 2 + e] = make_ulonglong2(v[2 * e], v[2 * e + 1]);
+      }
     }
   }
-  const int n = k.vpr * V;                       // channels, idle ones included
-  const int lanes = by_warp ? kNT / 32 : k.rl;   // sums left per channel
-  const int stride = lanes * k.vpr;
-  const bool in = by_warp ? (threadIdx.x & 31) < k.vpr : (int)threadIdx.x < k.rl * k.vpr;
-  const int at = by_warp ? (threadIdx.x >> 5) * k.vpr + (threadIdx.x & 31) : threadIdx.x;
   __syncthreads();
-  if (in) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) red[e * stride + at] = f[e];
-  }
-  __syncthreads();
+  const int n = k.vpr * W;
   for (int i = threadIdx.x; i < n; i += kNT) {
-    const int e = i / k.vpr, vl = i - e * k.vpr;
     float a = 0.f;
 #pragma unroll 8
-    for (int r = 0; r < lanes; ++r) a += red[e * stride + r * k.vpr + vl];
-    chan[vl * V + e] = a;
+    for (int r = 0; r < k.rl; ++r) a += red[r * n + i];
+    tot[i] = a;
   }
   __syncthreads();
 }
 
-// sum over the D channels of a group, one warp, in a fixed order
-template <typename F>
-__device__ __forceinline__ float warp_sum(int D, F value) {
-  float a = 0.f;
-  for (int c = threadIdx.x & 31; c < D; c += 32) a += value(c);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+// A group's sums are taken by `seg` neighbouring lanes, a power of two that
+// covers its D channels or a warp.
+__device__ __forceinline__ int lanes_of_group(int D) {
+  int seg = 1;
+  while (seg < D && seg < 32) seg *= 2;
+  return seg;
+}
+__device__ __forceinline__ float group_sum(float a, int seg) {
+  for (int o = seg >> 1; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   return a;
 }
 
-// shared memory after the shares: red, then per channel and per group tables
-template <int V>
-__device__ __forceinline__ float* scratch(unsigned char* sm, const Plan& k) {
-  return reinterpret_cast<float*>(sm + k.data_bytes);
+// V values of a per-channel tensor; one read where the base is aligned
+template <typename T, int V>
+__device__ __forceinline__ void load_channels(const T* base, int c, float none, f32x2* o) {
+  constexpr int NP = Vecs<T, V>::NP;
+  if (!base) {
+#pragma unroll
+    for (int e = 0; e < NP; ++e) o[e] = both(none);
+  } else if (V > 1 && reinterpret_cast<uintptr_t>(base) % sizeof(typename Vecs<T, V>::word) == 0) {
+    Vecs<T, V>::unpack(*reinterpret_cast<const typename Vecs<T, V>::word*>(base + c), o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < NP; ++e) o[e] = pack_f32x2(ld(base + c + 2 * e), 2 * e + 1 < V ? ld(base + c + 2 * e + 1) : 0.f);
+  }
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
@@ -224,10 +228,12 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
   cg::cluster_group cluster = cg::this_cluster();
   const Place p = place_of<V>(g, k);
   word* const data = reinterpret_cast<word*>(sm);
-  float* const red = scratch<V>(sm, k);
-  float* const chan = red + kNT * V;
-  float2* const part = reinterpret_cast<float2*>(chan + (k.vpr * V + 1) / 2 * 2);  // (mean, squares) of the block's groups
-  float2* const stat = part + k.groups;                             // (mean, rstd) of the slab's
+  constexpr int W = 4 * NP;
+  float* const red = reinterpret_cast<float*>(sm + k.data_bytes);
+  float* const tot = red + kNT * W;
+  float* const base = tot + k.vpr * W;                                    // what the sums are about, per channel
+  float2* const part = reinterpret_cast<float2*>(base + k.vpr * 2 * NP);  // (mean, squares) of the block's groups
+  float2* const stat = part + k.groups;                                   // (mean, rstd) of the slab's
 
   // read, sum, keep
   f32x2 s[NP], d[NP], q[NP];
@@ -241,6 +247,16 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
   const bool scaler = KEEP != kSrcFull && (p.c & ((1 << x8.shift) - 1)) == 0;
   const int64_t xstep = k.rl * g.xs;
   const int left = p.on ? p.rows - p.r : 0;  // rows from this lane's first on
+  // sums about the share's first row: one value per channel, the same for every row lane
+  if (p.on && p.rows > 0) {
+    Vecs<T, V>::unpack(*reinterpret_cast<const word*>(x + p.row0 * g.xs + g.xo + p.c), s);
+    if (p.r == 0) {
+#pragma unroll
+      for (int e = 0; e < NP; ++e) *reinterpret_cast<f32x2*>(base + p.vl * 2 * NP + 2 * e) = s[e];
+    }
+#pragma unroll
+    for (int e = 0; e < NP; ++e) s[e] = neg(s[e]);
+  }
   word* dp = data + p.r * k.vpr + p.vl;
   const int dstep = k.rl * k.vpr;
   constexpr int kAhead = V == 1 ? 8 : 4;  // rows in flight
@@ -258,10 +274,6 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
       Vecs<T, V>::unpack(w[a], f);
       if (in) {
         *dp = w[a];
-        if (a == 0 && r0 == 0) {
-#pragma unroll
-          for (int e = 0; e < NP; ++e) s[e] = neg(f[e]);
-        }
 #pragma unroll
         for (int e = 0; e < NP; ++e) {
           const f32x2 t = add_f32x2(f[e], s[e]);
@@ -284,38 +296,33 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
     }
   }
 
-  // the block's mean and squares of each group
-  const int mine = p.on && p.r < p.rows ? (p.rows - p.r + k.rl - 1) / k.rl : 0;
-  const float cnt = (float)mine, icnt = mine > 0 ? 1.f / cnt : 0.f;
-  const int warp = threadIdx.x >> 5, groups = p.S / g.D;
+  // the block's mean and squares of each group, from those of its channels
+  const int groups = p.S / g.D, seg = lanes_of_group(g.D);
+  join_rows<NP>(k, d, q, red, tot);
   {
-    f32x2 v[NP];
-#pragma unroll
-    for (int e = 0; e < NP; ++e) v[e] = fma2(both(-cnt), s[e], d[e]);
-    join_rows<V>(k, v, red, chan);
-    for (int i = warp; i < groups; i += kNT / 32) {
-      const float a = warp_sum(g.D, [&](int c) { return chan[i * g.D + c]; });
-      if ((threadIdx.x & 31) == 0) part[i].x = p.rows > 0 ? a / ((float)p.rows * (float)g.D) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      const f32x2 m = fma2(d[e], both(icnt), neg(s[e]));  // the thread's mean
-      float own[2], t[2];
-      unpack_f32x2(fma2(mul_f32x2(d[e], d[e]), both(-icnt), q[e]), own[0], own[1]);
-      unpack_f32x2(m, t[0], t[1]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float o = own[h] < 0.f ? 0.f : own[h];  // NaN stays
-        const float off = 2 * e + h < V && p.on ? t[h] - part[gi[2 * e + h < V ? 2 * e + h : 0]].x : 0.f;
-        t[h] = mine > 0 ? o + cnt * off * off : 0.f;
+    const float n = (float)p.rows, in = p.rows > 0 ? 1.f / n : 0.f;
+    auto channel = [&](int c, float* mean, float* squares) {
+      const int vl = c / V, e = c - vl * V;
+      const float sd = tot[vl * W + e], sq = tot[vl * W + 2 * NP + e], t = sq - sd * sd * in;
+      *mean = base[vl * 2 * NP + e] + sd * in;
+      *squares = t < 0.f ? 0.f : t;  // NaN stays
+    };
+    for (int i0 = 0; i0 < groups; i0 += kNT / seg) {
+      const int i = i0 + (int)threadIdx.x / seg, l = threadIdx.x & (seg - 1);
+      const bool in_slice = i < groups && p.rows > 0;
+      float a = 0.f, m, sq;
+      for (int c = l; c < g.D && in_slice; c += seg) {
+        channel(i * g.D + c, &m, &sq);
+        a += m;
       }
-      v[e] = pack_f32x2(t[0], t[1]);
-    }
-    join_rows<V>(k, v, red, chan);
-    for (int i = warp; i < groups; i += kNT / 32) {
-      const float a = warp_sum(g.D, [&](int c) { return chan[i * g.D + c]; });
-      if ((threadIdx.x & 31) == 0) part[i].y = a;
+      const float mean = group_sum(a, seg) / (float)g.D;
+      a = 0.f;
+      for (int c = l; c < g.D && in_slice; c += seg) {
+        channel(i * g.D + c, &m, &sq);
+        a += fmaf(n * (m - mean), m - mean, sq);
+      }
+      a = group_sum(a, seg);
+      if (l == 0 && i < groups) part[i] = make_float2(mean, a);
     }
   }
   // the slab's
@@ -354,13 +361,12 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
     f32x2 ga[NP], be[NP], mu[NP], rs[NP];
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
-      const int i = 2 * e, j = 2 * e + 1 < V ? 2 * e + 1 : 2 * e;
-      const float2 a = stat[gi[i]], b = stat[gi[j]];
+      const float2 a = stat[gi[2 * e]], b = stat[gi[2 * e + 1 < V ? 2 * e + 1 : 2 * e]];
       mu[e] = pack_f32x2(-a.x, -b.x);
       rs[e] = pack_f32x2(a.y, b.y);
-      ga[e] = gamma ? pack_f32x2(ld(gamma + p.c + i), ld(gamma + p.c + j)) : both(1.f);
-      be[e] = beta ? pack_f32x2(ld(beta + p.c + i), ld(beta + p.c + j)) : 0;
     }
+    load_channels<T, V>(gamma, p.c, 1.f, ga);
+    load_channels<T, V>(beta, p.c, 0.f, be);
     T* yp = y + (p.row0 + p.r) * g.ys + g.yo + p.c;
     const int64_t ystep = k.rl * g.ys;
     dp = data + p.r * k.vpr + p.vl;
@@ -391,24 +397,34 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
   const Place p = place_of<V>(g, k);
   word* const gdata = reinterpret_cast<word*>(sm);
   xword* const xdata = reinterpret_cast<xword*>(sm + (size_t)k.rows * k.vpr * sizeof(word));
-  float* const red = scratch<V>(sm, k);
-  float* const chan = red + kNT * V;                                            // sum du, then sum du * xh
-  float2* const part = reinterpret_cast<float2*>(chan + 2 * k.vpr * V);         // (s1, s2) of the block's groups
-  float2* const stat = part + k.groups;                                         // of the slab's, over the count
+  constexpr int W = 4 * NP;
+  float* const red = reinterpret_cast<float*>(sm + k.data_bytes);
+  float* const tot = red + kNT * W;                                       // sums of du and of du * xh per channel
+  float2* const part = reinterpret_cast<float2*>(tot + k.vpr * W);        // (s1, s2) of the block's groups
+  float2* const stat = part + k.groups;                                   // of the slab's, over the count
 
   int gi[V];
   groups_of<V>(g.D, min(p.vl * V, p.S - 1), gi);
   f32x2 ga[NP], be[NP], mu[NP], rs[NP];
 #pragma unroll
-  for (int e = 0; e < NP; ++e) {
-    ga[e] = be[e] = mu[e] = rs[e] = 0;
-    if (p.on) {
-      const int i = 2 * e, j = 2 * e + 1 < V ? 2 * e + 1 : 2 * e;
-      const int64_t at = p.n * g.G + p.c0 / g.D;
-      mu[e] = pack_f32x2(-__ldg(mean + at + gi[i]), -__ldg(mean + at + gi[j]));
-      rs[e] = pack_f32x2(__ldg(rstd + at + gi[i]), __ldg(rstd + at + gi[j]));
-      ga[e] = gamma ? pack_f32x2(ld(gamma + p.c + i), ld(gamma + p.c + j)) : both(1.f);
-      be[e] = beta ? pack_f32x2(ld(beta + p.c + i), ld(beta + p.c + j)) : 0;
+  for (int e = 0; e < NP; ++e) ga[e] = be[e] = mu[e] = rs[e] = 0;
+  if (p.on) {
+    load_channels<T, V>(gamma, p.c, 1.f, ga);
+    load_channels<T, V>(beta, p.c, 0.f, be);
+    const int64_t at = p.n * g.G + p.c0 / g.D;
+    const float m0 = -__ldg(mean + at + gi[0]), r0 = __ldg(rstd + at + gi[0]);
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      mu[e] = both(m0);
+      rs[e] = both(r0);
+    }
+    if (gi[0] != gi[V - 1]) {
+#pragma unroll
+      for (int e = 0; e < NP; ++e) {
+        const int i = gi[2 * e], j = gi[2 * e + 1 < V ? 2 * e + 1 : 2 * e];
+        mu[e] = pack_f32x2(-__ldg(mean + at + i), -__ldg(mean + at + j));
+        rs[e] = pack_f32x2(__ldg(rstd + at + i), __ldg(rstd + at + j));
+      }
     }
   }
   const T* gp = gy + (p.row0 + p.r) * g.ys + g.yo + p.c;
@@ -489,15 +505,20 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
       }
     }
   }
-  float* const chan2 = chan + k.vpr * V;
-  join_rows<V>(k, a, red, chan);
-  join_rows<V>(k, b, red, chan2);
-  const int warp = threadIdx.x >> 5, groups = p.S / g.D;
-  for (int i = warp; i < groups; i += kNT / 32) {
-    auto ga_of = [&](int c) { return gamma ? ld(gamma + p.c0 + i * g.D + c) : 1.f; };
-    const float s1 = warp_sum(g.D, [&](int c) { return ga_of(c) * chan[i * g.D + c]; });
-    const float s2 = warp_sum(g.D, [&](int c) { return ga_of(c) * chan2[i * g.D + c]; });
-    if ((threadIdx.x & 31) == 0) part[i] = make_float2(s1, s2);
+  join_rows<NP>(k, a, b, red, tot);
+  const int groups = p.S / g.D, seg = lanes_of_group(g.D);
+  for (int i0 = 0; i0 < groups; i0 += kNT / seg) {
+    const int i = i0 + (int)threadIdx.x / seg, l = threadIdx.x & (seg - 1);
+    float s1 = 0.f, s2 = 0.f;
+    for (int c = l; c < g.D && i < groups; c += seg) {
+      const int ch = i * g.D + c, vl = ch / V, e = ch - vl * V;
+      const float w = gamma ? ld(gamma + p.c0 + ch) : 1.f;
+      s1 = fmaf(w, tot[vl * W + e], s1);
+      s2 = fmaf(w, tot[vl * W + 2 * NP + e], s2);
+    }
+    s1 = group_sum(s1, seg);
+    s2 = group_sum(s2, seg);
+    if (l == 0 && i < groups) part[i] = make_float2(s1, s2);
   }
   cluster_arrive();
   cluster_wait();
@@ -516,8 +537,9 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
   for (int c = lo + threadIdx.x; c < min(lo + share, p.S); c += kNT) {
     float s1 = 0.f, s2 = 0.f;
     for (int j = 0; j < k.cl; ++j) {
-      s1 += cluster.map_shared_rank(chan, j)[c];
-      s2 += cluster.map_shared_rank(chan2, j)[c];
+      const float* o = cluster.map_shared_rank(tot, j) + c / V * W + c % V;
+      s1 += o[0];
+      s2 += o[2 * NP];
     }
     sums[p.n * g.C + p.c0 + c] = make_float2(s1, s2);
   }
