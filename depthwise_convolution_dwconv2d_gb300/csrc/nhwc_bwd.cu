@@ -218,9 +218,11 @@ bool supported(const Conv& c) {
 Geom plan(const Conv& c) {
   Geom g{};
   const int K = c.kh, S = c.sh;
-  const int px = K == 3 ? 4 : 8, nt = K == 3 ? 256 : 128, step = K == 3 ? 1 : 2 / S;
-  const int64_t pairs = (c.C + 1) / 2;
-  g.ct_log = 5;
+  const bool ring = K == 3;
+  const int px = ring ? 4 : 8, nt = ring ? kRingThreads : kBlockThreads, step = ring ? 1 : 2 / S;
+  // 64 channels per block, 32 where that leaves a quarter fewer of the last tile idle, fewer for few channels
+  const int64_t by64 = (c.C + 63) / 64 * 64, by32 = (c.C + 31) / 32 * 32, pairs = (c.C + 1) / 2;
+  g.ct_log = 4 * by64 >= 5 * by32 ? 4 : 5;
   while (g.ct_log > 0 && (int64_t(1) << (g.ct_log - 1)) >= pairs) --g.ct_log;
   const int ct = 1 << g.ct_log, lanes = nt >> g.ct_log;
   g.tiles = (int)((pairs + ct - 1) / ct);
@@ -228,23 +230,28 @@ Geom plan(const Conv& c) {
   g.t_end = (int)((c.H + c.ph - 1) / S) + 1;
   g.v_begin = c.pw / S * S;
   g.strips = (int)((c.W + c.pw - g.v_begin + px - 1) / px);
-  // Bands of rows: as many as give every block of one resident wave about four groups of items, no
-  // shorter than 4 steps (a band reads K - 1 rows of gy more than it owns).
-  const int wave = 152 * (K == 3 ? 2 : 3);
+  // Bands of rows: the cut whose longest block has the least to do, a band costing its steps and, where rows of gy stay
+  // in registers, those read above it. gx and gw of the larger filters run side by side.
+  const int64_t wave = ring ? 152 * kRingBlocks : 152 * kBlockBlocks / 2;
   const int64_t per_tile = (wave + g.tiles - 1) / g.tiles;
   const int64_t rows = g.t_end - g.t_begin;
-  int64_t bands = (4 * per_tile * lanes + c.N * g.strips - 1) / (c.N * g.strips);
-  const int64_t most = (rows + 4 * step - 1) / (4 * step);
-  if (bands > most) bands = most;
-  int64_t band = (rows + bands - 1) / bands;
-  band = (band + step - 1) / step * step;
-  g.band = (int)band;
-  g.bands = (int)((rows + band - 1) / band);
-  g.items = c.N * g.bands * (int64_t)g.strips;
-  g.groups = (g.items + lanes - 1) / lanes;
+  const double above = ring ? 0.75 * (2 / S) + 0.5 : 0.25;
+  double best = -1;
+  for (int64_t bands = 1; bands <= (rows + step - 1) / step && bands <= 512; ++bands) {
+    int64_t band = (rows + bands - 1) / bands;
+    band = (band + step - 1) / step * step;
+    const int64_t items = c.N * ((rows + band - 1) / band) * g.strips, groups = (items + lanes - 1) / lanes;
+    const double cost = (double)((groups + per_tile - 1) / per_tile) * ((double)band / step + above);
+    if (best >= 0 && cost >= best) continue;
+    best = cost;
+    g.band = (int)band;
+    g.bands = (int)((rows + band - 1) / band);
+    g.items = items;
+    g.groups = groups;
+  }
   // one wave of blocks, more where a thread would add up over 4096 products per filter value
   int64_t chunks = per_tile;
-  const int64_t long_chain = g.groups * band * px / 4096;
+  const int64_t long_chain = g.groups * g.band * px / 4096;
   if (chunks < long_chain) chunks = long_chain;
   if (chunks > g.groups) chunks = g.groups;
   const int64_t room = (int64_t(1) << 30) / (c.C * (K * K + 1) * 4);  // at most 1 GB of partial sums
@@ -254,19 +261,22 @@ Geom plan(const Conv& c) {
 }
 
 bool plan_staged(const Conv& c, int src, Staged* out) {
-  if (!supported(c) || c.kh != 3 || c.N >= (int64_t(1) << 31)) return false;
-  const int es = c.dtype == DWCONV_F32 ? 4 : 2, S = c.sh, D = 2 / S, px = 4;
+  if (!supported(c) || c.N >= (int64_t(1) << 31)) return false;
+  const int es = c.dtype == DWCONV_F32 ? 4 : 2, K = c.kh, S = c.sh, D = (K - 1) / S;
+  const bool ring = K == 3;
+  const int px = ring ? 4 : 8, step = ring ? 1 : 2 / S, blocks = ring ? kStagedBlocks : K == 5 ? 4 : 3;
   if (c.C * es % 16 != 0 || (src != kSrcFull && c.C % 16 != 0) || c.C < 32) return false;
   Staged g{};
   // 64 channels per block, 32 where that leaves a quarter fewer of the last tile idle
   const int64_t by64 = (c.C + 63) / 64 * 64, by32 = (c.C + 31) / 32 * 32;
   g.ct_log = 4 * by64 >= 5 * by32 ? 4 : 5;
-  const int ct = 1 << g.ct_log, most = kStagedThreads / ct;
+  const int ct = 1 << g.ct_log, most = (ring ? kStagedThreads : kTileThreads) / ct;
   g.tiles = (int)((c.C + 2 * ct - 1) / (2 * ct));
   g.t_begin = c.ph / S;
   g.t_end = (int)((c.H + c.ph - 1) / S) + 1;
   g.v_begin = c.pw / S * S;
   g.strips = (int)((c.W + c.pw - g.v_begin + px - 1) / px);
+  const int xes = src == kSrcFull ? es : 1;
   // Strips and samples of a block's lanes: the split that leaves the fewest lanes idle, a narrow block paying for the
   // columns of gy that it shares with its neighbours.
   double fit = -1;
@@ -284,26 +294,35 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
   g.threads = (g.cs * g.ns * ct + 31) / 32 * 32;
   g.gc = D + (g.cs * px - 1) / S + 1;
   g.xc = g.cs * px;
-  const int xes = src == kSrcFull ? es : 1;
-  const int rd = D + 1;  // rows of gy in a stage
-  g.gy_bytes = g.ns * rd * g.gc * 2 * ct * es;
-  g.x_bytes = g.ns * rd * S * g.xc * 2 * ct * xes;
-  g.x_at = (g.gy_bytes + 127) / 128 * 128;
-  g.stage_bytes = (g.x_at + g.x_bytes + 127) / 128 * 128;
-  g.stages = (220 * 1024 / kStagedBlocks - 6 * 1024) / g.stage_bytes;  // 6 KB: what join_lanes keeps
-  if (g.stages > kMaxStages) g.stages = kMaxStages;
-  if (g.stages < 2) g.stages = 2;
-  // Bands: the cut whose longest block has the fewest rows, a band costing whole stages, the
-  // rows above it about a third of an owned row.
+  const int room = 220 * 1024 / blocks - 6 * 1024;  // of a block; 6 KB: what join_lanes keeps
+  auto stage = [&](Staged* q, int grows, int xrows) {
+    q->grows = grows;
+    q->xrows = xrows;
+    q->gy_bytes = q->ns * grows * q->gc * 2 * ct * es;
+    q->x_bytes = q->ns * xrows * q->xc * 2 * ct * xes;
+    q->x_at = (q->gy_bytes + 127) / 128 * 128;
+    q->stage_bytes = (q->x_at + q->x_bytes + 127) / 128 * 128;
+  };
+  // Bands: the cut whose longest block has the fewest rows. A band of the 3x3 kernel costs whole stages, the rows above
+  // it about a third of an owned row; one of the larger filters is a stage, whose copy and start cost about half a step.
   const int64_t rows = g.t_end - g.t_begin, groups = (c.N + g.ns - 1) / g.ns;
-  const int64_t wave = (152 * kStagedBlocks + g.tiles - 1) / g.tiles;
+  const int rd = D + 1;
+  const int64_t wave = (152 * blocks / (ring ? 1 : 2) + g.tiles - 1) / g.tiles;
   double best = -1;
-  for (int64_t bands = 1; bands <= rows && bands <= 512; ++bands) {
-    const int64_t band = (rows + bands - 1) / bands;
+  for (int64_t bands = 1; bands <= rows && bands <= 4096; ++bands) {
+    int64_t band = (rows + bands - 1) / bands;
+    if (!ring) band = (band + step - 1) / step * step;
     if ((rows + band - 1) / band != bands) continue;
+    if (!ring) {
+      if (band > 4 * step) continue;
+      stage(&g, (int)band + D, (int)band * S);
+      if (g.stage_bytes > room && band > step) continue;
+      if (g.stage_bytes > 200 * 1024) continue;
+    }
     const int64_t items = groups * g.segs * bands;
     if (items >= (1 << 30)) break;
-    const double cost = (double)((items + wave - 1) / wave) * ((D + band + rd - 1) / rd * rd - 0.7 * D + 0.5);
+    const double one = ring ? (D + band + rd - 1) / rd * rd - 0.7 * D + 0.5 : (double)band / step + 0.5;
+    const double cost = (double)((items + wave - 1) / wave) * one;
     if (best < 0 || cost < best) {
       best = cost;
       g.bands = (int)bands;
@@ -312,13 +331,24 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
     }
   }
   if (best < 0) return false;
+  if (ring) {
+    stage(&g, rd, rd * S);
+    g.stages = room / g.stage_bytes;
+    if (g.stages < 2) g.stages = 2;
+  } else {
+    stage(&g, g.band + D, g.band * S);
+    g.stages = room / g.stage_bytes;
+    if (g.stages < 1) g.stages = 1;
+    if (g.stages > 2) g.stages = 2;
+  }
+  if (g.stages > kMaxStages) g.stages = kMaxStages;
   g.d_segs = FastDiv((uint32_t)g.segs);
   g.d_bands = FastDiv((uint32_t)g.bands);
   int64_t chunks = g.items < wave ? g.items : wave;
   const int64_t long_chain = (int64_t)g.items * g.band * px * S / 4096;  // at most 4096 products in a thread's chain
   if (chunks < long_chain) chunks = long_chain < g.items ? long_chain : g.items;
-  const int64_t room = (int64_t(1) << 30) / (c.C * 10 * 4);
-  if (chunks > room) chunks = room < 1 ? 1 : room;
+  const int64_t most_chunks = (int64_t(1) << 30) / (c.C * (K * K + 1) * 4);
+  if (chunks > most_chunks) chunks = most_chunks < 1 ? 1 : most_chunks;
   g.chunks = (int)chunks;
   *out = g;
   return true;

@@ -8,6 +8,9 @@ namespace dwconv {
 namespace nhwc {
 namespace walk {
 
+constexpr int kRingThreads = 256, kRingBlocks = 2;     // threads of a block, blocks per SM: 3x3 filters
+constexpr int kBlockThreads = 128, kBlockBlocks = 2;   // 5x5 and 7x7
+
 struct Geom {
   int64_t items;    // N * bands * strips
   int64_t groups;   // blocks' worth of items
@@ -22,9 +25,12 @@ struct Geom {
   bool want_gx, want_gw, accumulate;
 };
 
-// The 3x3 kernel that stages rows with the tensor memory accelerator: a block
-// owns `cs` strips of `ns` samples, its lanes; a stage holds 2 / S + 1 rows of
-// gy and the rows of x that they meet.
+constexpr int kTileThreads = 128;
+
+// The kernels that stage rows with the tensor memory accelerator: a block
+// owns `cs` strips of `ns` samples, its lanes; a stage holds grows rows of gy
+// and xrows of x per sample: as many as the register ring of the 3x3 kernel
+// has, a whole band with the rows above it for the larger filters.
 constexpr int kStagedThreads = 128;  // the most threads of a block
 constexpr int kStagedBlocks = 4;     // blocks per SM
 constexpr int kMaxStages = 4;
@@ -37,6 +43,7 @@ struct Staged {
   FastDiv d_segs, d_bands;
   int threads;
   int stages;
+  int grows, xrows;    // rows of a stage
   int gc, xc;          // columns of a stage's rows of gy and x
   int gy_bytes, x_bytes;      // of a stage's copies
   int x_at, stage_bytes;      // where x begins, and the next stage (multiples of 128)

@@ -208,10 +208,10 @@ __device__ __forceinline__ void join_lanes(int ct_log, const f32x2* acc, int C, 
 // each x of the strip is loaded once; the next step's loads are issued before
 // this step's arithmetic.
 template <typename T, int SRC, int S, bool PAIR>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(kRingThreads, kRingBlocks)
 ring3_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restrict__ gy, const T* __restrict__ w,
              T* __restrict__ gx, float* __restrict__ ws) {
-  constexpr int NT = 256, K = 3, PX = 4;
+  constexpr int NT = kRingThreads, K = 3, PX = 4;
   constexpr int D = (K - 1) / S, RD = D + 1, WIN = D + (PX - 1) / S + 1;
   const int ct = 1 << g.ct_log;
   const int tile = blockIdx.x % g.tiles, chunk = blockIdx.x / g.tiles;
@@ -555,14 +555,15 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
 }
 
 // 5x5 and 7x7 filters: gx (GW = false) or gw and gb (GW = true), whose filter
-// or gradient alone takes up to 98 registers. A step owns RY = 2 rows of the
-// strip and reads each row of gy that they meet once (from L1 after the
-// first step that meets it), for up to 2 K^2 PX products.
+// or gradient alone takes up to 98 registers; both in one launch, each by its
+// own blocks. A step owns RY = 2 rows of the strip and reads each row of gy
+// that they meet once (from L1 after the first step that meets it), for up to
+// 2 K^2 PX products.
 template <typename T, int SRC, int K, int S, bool GW, bool PAIR>
-__global__ void __launch_bounds__(128, 3)
-block_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restrict__ gy, const T* __restrict__ w,
-             T* __restrict__ gx, float* __restrict__ ws) {
-  constexpr int NT = 128, PX = 8, RY = 2, M = RY / S;
+__device__ __forceinline__ void block_walk(const Conv& c, const Geom& g, const T* __restrict__ x, const Act8& x8,
+                                           const T* __restrict__ gy, const T* __restrict__ w, T* __restrict__ gx,
+                                           float* __restrict__ ws) {
+  constexpr int NT = kBlockThreads, PX = 8, RY = 2, M = RY / S;
   constexpr int D = (K - 1) / S, WIN = D + (PX - 1) / S + 1;
   const int ct = 1 << g.ct_log;
   const int tile = blockIdx.x % g.tiles, chunk = blockIdx.x / g.tiles;
@@ -658,6 +659,188 @@ block_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
   if constexpr (GW) join_lanes<NT, K * K + 1>(g.ct_log, acc, C, ch0, chunk, ws);
 }
 
+template <typename T, int SRC, int K, int S, bool PAIR>
+__global__ void __launch_bounds__(kBlockThreads, kBlockBlocks)
+block_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restrict__ gy, const T* __restrict__ w,
+             T* __restrict__ gx, float* __restrict__ ws) {
+  if (g.want_gw && blockIdx.y == 0)
+    block_walk<T, SRC, K, S, true, PAIR>(c, g, x, x8, gy, w, gx, ws);
+  else
+    block_walk<T, kSrcFull, K, S, false, PAIR>(c, g, x, x8, gy, w, gx, ws);
+}
+
+// 5x5 and 7x7 filters, staged: a stage is an item, `band` rows of gy with the
+// K - 1 above them (a few steps' worth), brought by one copy, and the rows of
+// x that they meet by another. gx and gw are separate blocks, as in
+// block_kernel; each reads a row of gy for every filter row that meets it,
+// from shared memory at constant offsets.
+template <typename T, int SRC, int K, int S, int CT, bool GW>
+__device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const CUtensorMap* map_gy,
+                                          const CUtensorMap* map_x, const Act8& x8, unsigned int* timeouts,
+                                          const T* __restrict__ w, T* __restrict__ gx, float* __restrict__ ws) {
+  constexpr int PX = 8, RY = 2, M = RY / S, NT = kTileThreads;
+  constexpr int D = (K - 1) / S, WIN = D + (PX - 1) / S + 1;
+  constexpr bool kCode = GW && SRC != kSrcFull;
+  constexpr int GP = 2 * CT * (int)sizeof(T), XP = kCode ? 2 * CT : GP;
+  extern __shared__ __align__(16) unsigned char smdyn[];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  const int base = (int)((128 - (tma::smem_u32(smdyn) & 127)) & 127);
+  const uint32_t sm0 = tma::smem_u32(smdyn) + base;
+  const int tile = blockIdx.x % g.tiles, chunk = blockIdx.x / g.tiles;
+  const int ch0 = tile * 2 * CT;
+  const int pl = threadIdx.x & (CT - 1), ch = ch0 + 2 * pl;
+  const int lane = threadIdx.x / CT, ls = lane % g.cs, ln = lane / g.cs, la = min(ln, g.ns - 1);
+  const int C = (int)c.C, W = (int)c.W, H = (int)c.H;
+  const int grows = g.band + D, xrows = g.band * S;
+  const int grow = g.gc * GP, xrow = g.xc * XP;
+  const uint32_t g_at = sm0 + (la * grows * g.gc + ls * (PX / S)) * GP + pl * (GP / CT);
+  const uint32_t x_at = sm0 + g.x_at + (la * xrows * g.xc + ls * PX) * XP + pl * (XP / CT);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < g.stages; ++i) tma::mbar_init(&full[i], 1);
+    tma::fence_init();
+  }
+  __syncthreads();
+
+  struct Item {
+    int n0, v0, tb;
+  };
+  auto item_of = [&](int i) {
+    Item it;
+    uint32_t q, n;
+    const uint32_t seg = g.d_segs.divmod((uint32_t)i, q);
+    const uint32_t band = g.d_bands.divmod(q, n);
+    it.n0 = (int)n * g.ns;
+    it.v0 = g.v_begin + (int)seg * g.cs * PX;
+    it.tb = g.t_begin + (int)band * g.band;
+    return it;
+  };
+  int p_item = chunk, p_slot = 0;
+  auto issue = [&]() {
+    if (p_item >= g.items) return;
+    const Item it = item_of(p_item);
+    unsigned char* const slot = smdyn + base + p_slot * g.stage_bytes;
+    const bool bring_x = GW && g.want_x;
+    tma::fence_async_smem();
+    tma::mbar_expect_tx(&full[p_slot], (uint32_t)(g.gy_bytes + (bring_x ? g.x_bytes : 0)));
+    tma::load_4d(slot, map_gy, ch0, it.v0 / S - D, it.tb - D, it.n0, &full[p_slot]);
+    if (bring_x) tma::load_4d(slot + g.x_at, map_x, ch0, it.v0 - c.pw, it.tb * S - c.ph, it.n0, &full[p_slot]);
+    p_slot = p_slot + 1 == g.stages ? 0 : p_slot + 1;
+    p_item += g.chunks;
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < g.stages - 1; ++i) issue();
+
+  f32x2 acc[K * K + (GW ? 1 : 0)];  // the filter, or its gradient and the bias's
+#pragma unroll
+  for (int k = 0; k < K * K + (GW ? 1 : 0); ++k) {
+    acc[k] = 0;
+    if (!GW && ch < C) acc[k] = pack_f32x2(ld(w + (int64_t)ch * K * K + k), ld(w + (int64_t)(ch + 1) * K * K + k));
+  }
+
+  int slot = 0;
+  uint32_t parity = 0;
+  for (int item = chunk; item < g.items; item += g.chunks) {
+    if (item > chunk) {  // the stage before this one is free once every thread is here
+      __syncthreads();
+      slot = slot + 1 == g.stages ? 0 : slot + 1;
+      parity ^= slot == 0 ? 1u : 0u;
+    }
+    if (threadIdx.x == 0) issue();
+    const Item it = item_of(item);
+    const int64_t n = it.n0 + ln;
+    const int strip = (it.v0 - g.v_begin) / PX + ls;
+    const bool on = ln < g.ns && n < c.N && strip < g.strips && ch < C;
+    const int iw0 = it.v0 + ls * PX - c.pw, ih0 = S * it.tb - c.ph;
+    uint32_t xok = 0;
+#pragma unroll
+    for (int p = 0; p < PX; ++p) xok |= (iw0 + p >= 0 && iw0 + p < W) ? 1u << p : 0u;
+    const int64_t at = n * H * (int64_t)W + (int64_t)ih0 * W + iw0;
+    // a checkpoint's scales: lanes p + 8 b of the strip's lanes read pixel p, block b of the tile's
+    const int sb = (ch0 >> x8.shift) + (pl >> 3);
+    const bool scaler = kCode && on && g.want_x && pl < 16 && sb < x8.nblk && ((xok >> (pl & 7)) & 1);
+    const int from = (int)(threadIdx.x & 31 & ~(CT - 1)) + 8 * ((ch >> x8.shift) - (ch0 >> x8.shift));
+    const float* const sp = x8.scales + (at + (pl & 7)) * x8.nblk + sb;
+    if (!tma::mbar_wait(&full[slot], parity, timeouts)) {
+      // the copy never landed: let those in flight finish (bounded), then stop
+      for (int j = 1; j < g.stages; ++j) {
+        const int q = (slot + j) % g.stages;
+        tma::mbar_wait(&full[q], q > slot ? parity : parity ^ 1u, nullptr);
+      }
+      return;
+    }
+    uint32_t gs = g_at + slot * g.stage_bytes, xs = x_at + slot * g.stage_bytes;
+    for (int t = 0; t < g.band; t += M, gs += M * grow, xs += RY * xrow) {
+      f32x2 own[RY * PX];  // x of the strip, or its gx
+#pragma unroll
+      for (int r = 0; r < RY; ++r) {
+        float sc = 0.f;
+        if (kCode) {
+          const int ih = ih0 + S * t + r;
+          if (scaler && ih >= 0 && ih < H) sc = __ldg(sp + (int64_t)(S * t + r) * W * x8.nblk);
+        }
+#pragma unroll
+        for (int p = 0; p < PX; ++p) {
+          if constexpr (kCode) {
+            Raw<T, SRC> v;
+            v.s = __shfl_sync(0xffffffffu, sc, from + p);
+            v.v = lds_u16(xs + r * xrow + p * XP);
+            own[r * PX + p] = widen<T, SRC>(v);
+          } else if constexpr (GW) {
+            own[r * PX + p] = widen<T, SRC>(lds_pair<T>(xs + r * xrow + p * XP));
+          } else {
+            own[r * PX + p] = 0;
+          }
+        }
+      }
+      if (!on) continue;
+      uint32_t q = gs;
+#pragma unroll
+      for (int e = -D; e <= (RY - 1) / S; ++e, q += grow) {  // gy row t + e meets the filter's rows a = r - S e
+        f32x2 gv[WIN];
+#pragma unroll
+        for (int j = 0; j < WIN; ++j) gv[j] = widen<T, kSrcFull>(lds_pair<T>(q + j * GP));
+#pragma unroll
+        for (int r = 0; r < RY; ++r) {
+          const int a = r - S * e;
+          if (a < 0 || a >= K) continue;
+#pragma unroll
+          for (int b = 0; b < K; ++b)
+#pragma unroll
+            for (int p = 0; p < PX; ++p) {
+              if ((p - b) % S != 0) continue;
+              const f32x2 v = gv[D + (p - b) / S];
+              if (GW) {
+                fma_f32x2(acc[a * K + b], own[r * PX + p], v);
+                if (a == K / 2 && b == K / 2) acc[K * K] = add_f32x2(acc[K * K], v);
+              } else {
+                fma_f32x2(own[r * PX + p], acc[a * K + b], v);
+              }
+            }
+        }
+      }
+      if (!GW) {
+#pragma unroll
+        for (int r = 0; r < RY; ++r) {
+          const int ih = ih0 + S * t + r;
+          if (ih < 0 || ih >= H) continue;
+          store_strip<T, true, PX>(gx + (at + (int64_t)(S * t + r) * W) * C + ch, C, own + r * PX, xok, true, g.accumulate);
+        }
+      }
+    }
+  }
+  if constexpr (GW) join_lanes<NT, K * K + 1>(g.ct_log, acc, C, ch0, chunk, ws);
+}
+
+template <typename T, int SRC, int K, int S, int CT>
+__global__ void __launch_bounds__(kTileThreads, K == 7 ? 3 : 4)
+tile_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, const __grid_constant__ CUtensorMap map_x,
+            Act8 x8, unsigned int* timeouts, const T* __restrict__ w, T* __restrict__ gx, float* __restrict__ ws) {
+  if (g.want_gw && blockIdx.y == 0)
+    tile_walk<T, SRC, K, S, CT, true>(c, g, &map_gy, &map_x, x8, timeouts, w, gx, ws);
+  else
+    tile_walk<T, SRC, K, S, CT, false>(c, g, &map_gy, &map_x, x8, timeouts, w, gx, ws);
+}
+
 // ---- launches --------------------------------------------------------------
 
 template <typename T, int SRC, bool PAIR>
@@ -666,16 +849,15 @@ cudaError_t launch(const Conv& c, const Geom& g, const T* x, const Act8& x8, con
   const unsigned grid = (unsigned)(g.tiles * g.chunks);
   if (c.kh == 3) {
     if (c.sh == 1)
-      ring3_kernel<T, SRC, 1, PAIR><<<grid, 256, 0, s>>>(c, g, x, x8, gy, w, gx, ws);
+      ring3_kernel<T, SRC, 1, PAIR><<<grid, kRingThreads, 0, s>>>(c, g, x, x8, gy, w, gx, ws);
     else
-      ring3_kernel<T, SRC, 2, PAIR><<<grid, 256, 0, s>>>(c, g, x, x8, gy, w, gx, ws);
+      ring3_kernel<T, SRC, 2, PAIR><<<grid, kRingThreads, 0, s>>>(c, g, x, x8, gy, w, gx, ws);
     return cudaGetLastError();
   }
 #define X(K, S)                                                                                       \
-  if (c.kh == K && c.sh == S) {                                                                       \
-    if (g.want_gx) block_kernel<T, kSrcFull, K, S, false, PAIR><<<grid, 128, 0, s>>>(c, g, x, x8, gy, w, gx, ws); \
-    if (g.want_gw) block_kernel<T, SRC, K, S, true, PAIR><<<grid, 128, 0, s>>>(c, g, x, x8, gy, w, gx, ws);       \
-  }
+  if (c.kh == K && c.sh == S)                                                                         \
+    block_kernel<T, SRC, K, S, PAIR>                                                                  \
+        <<<dim3(grid, g.want_gx && g.want_gw ? 2 : 1), kBlockThreads, 0, s>>>(c, g, x, x8, gy, w, gx, ws);
   X(5, 1) X(5, 2) X(7, 1) X(7, 2)
 #undef X
   return cudaGetLastError();
@@ -694,32 +876,36 @@ cudaError_t run(const Conv& c, const Geom& g, bool pair, const T* x, const Act8&
   return cudaErrorInvalidValue;
 }
 
-template <typename T, int SRC, int S, int CT>
+template <typename T, int SRC, int K, int S, int CT>
 cudaError_t launch_staged(const Conv& c, const Staged& g, const T* x, const Act8& x8, const T* gy, const T* w, T* gx,
                           float* ws, cudaStream_t s) {
   const uint64_t es = sizeof(T), xes = SRC == kSrcFull ? es : 1;
   CUtensorMap mg, mx;
-  constexpr uint32_t rows = 2 / S + 1;
   const uint64_t gd[4] = {(uint64_t)c.C, (uint64_t)c.Wo, (uint64_t)c.Ho, (uint64_t)c.N};
   const uint64_t gs[3] = {c.ctot * es, c.Wo * c.ctot * es, c.Ho * c.Wo * c.ctot * es};
-  const uint32_t gb[4] = {2 * CT, (uint32_t)g.gc, rows, (uint32_t)g.ns};
+  const uint32_t gb[4] = {2 * CT, (uint32_t)g.gc, (uint32_t)g.grows, (uint32_t)g.ns};
   const uint64_t xd[4] = {(uint64_t)c.C, (uint64_t)c.W, (uint64_t)c.H, (uint64_t)c.N};
   const uint64_t xs[3] = {c.C * xes, c.W * c.C * xes, c.H * c.W * c.C * xes};
-  const uint32_t xb[4] = {2 * CT, (uint32_t)g.xc, rows * S, (uint32_t)g.ns};
+  const uint32_t xb[4] = {2 * CT, (uint32_t)g.xc, (uint32_t)g.xrows, (uint32_t)g.ns};
   if (!tma::encode_strided(&mg, gy + c.off, c.dtype, 4, gd, gs, gb)) return cudaErrorNotSupported;
   mx = mg;
   const void* xp = SRC == kSrcFull ? (const void*)x : (const void*)x8.codes;
-  if (g.want_x &&
-      !tma::encode_strided(&mx, xp, SRC == kSrcFull ? c.dtype : tma::kBytes, 4, xd, xs, xb))
+  if (g.want_x && !tma::encode_strided(&mx, xp, SRC == kSrcFull ? c.dtype : tma::kBytes, 4, xd, xs, xb))
     return cudaErrorNotSupported;
   unsigned int* to = tma::timeout_counter();
   if (!to) return cudaErrorNotSupported;
-  auto kern = staged3_kernel<T, SRC, S, CT>;
-  const size_t smem = (size_t)g.stages * g.stage_bytes + 128;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(g.tiles * g.chunks), g.threads, smem, s>>>(c, g, mg, mx, x8, to, w, gx, ws);
-  return cudaGetLastError();
+  const int smem = g.stages * g.stage_bytes + 128;
+  auto go = [&](auto kern, unsigned sides) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3((unsigned)(g.tiles * g.chunks), sides), g.threads, smem, s>>>(c, g, mg, mx, x8, to, w, gx, ws);
+    return cudaGetLastError();
+  };
+  if constexpr (K == 3) {
+    return go(staged3_kernel<T, SRC, S, CT>, 1);
+  } else {
+    return go(tile_kernel<T, SRC, K, S, CT>, g.want_gx && g.want_gw ? 2 : 1);
+  }
 }
 
 template <typename T>
@@ -732,12 +918,14 @@ cudaError_t run_staged(const Conv& c, const Staged& g, const T* x, const Act8& x
   if (!fits(gy + c.off, c.ctot * es) || reinterpret_cast<uintptr_t>(gx) % (2 * es) != 0) return cudaErrorNotSupported;
   if (g.want_x && src == kSrcFull && (!x || !fits(x, c.C * es))) return cudaErrorNotSupported;
   if (g.want_x && src != kSrcFull && !fits(x8.codes, c.C)) return cudaErrorNotSupported;
-#define X(SRC, S, CT)                                      \
-  if (src == SRC && c.sh == S && (1 << g.ct_log) == CT)    \
-    return launch_staged<T, SRC, S, CT>(c, g, x, x8, gy, w, gx, ws, s);
-#define Y(SRC) X(SRC, 1, 32) X(SRC, 2, 32) X(SRC, 1, 16) X(SRC, 2, 16)
+#define X(SRC, K, S, CT)                                                    \
+  if (src == SRC && c.kh == K && c.sh == S && (1 << g.ct_log) == CT)        \
+    return launch_staged<T, SRC, K, S, CT>(c, g, x, x8, gy, w, gx, ws, s);
+#define Z(SRC, K) X(SRC, K, 1, 32) X(SRC, K, 2, 32) X(SRC, K, 1, 16) X(SRC, K, 2, 16)
+#define Y(SRC) Z(SRC, 3) Z(SRC, 5) Z(SRC, 7)
   Y(kSrcFull) Y(kSrcI8) Y(kSrcE4M3)
 #undef Y
+#undef Z
 #undef X
   return cudaErrorNotSupported;
 }
