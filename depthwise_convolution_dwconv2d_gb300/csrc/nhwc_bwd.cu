@@ -177,6 +177,68 @@ cudaError_t direct(const Conv& c, const T* x, const Act8& t, const T* gy, const 
   return walk::run<T>(c, g, pair, x, t, gy, w, gx, ws, s);
 }
 
+// Pixels of `bytes` bytes, `from` apart, copied `to` apart (a multiple of 16):
+// the layout that the staged kernels read. A thread writes 16 bytes; their
+// source begins anywhere, so it is read as aligned words and shifted.
+struct Copy {
+  const uint8_t* src;
+  uint8_t* dst;
+  int64_t pixels, from, to;
+  int bytes;
+  FastDiv d_vecs;   // 16-byte vectors of a pixel
+};
+__global__ void __launch_bounds__(kNT) align_kernel(Copy a, Copy b) {
+  const Copy& k = blockIdx.y == 0 ? a : b;
+  const int64_t total = k.pixels * k.d_vecs.d;
+  const uint8_t* const end = k.src + (k.pixels - 1) * k.from + k.bytes;
+  for (int64_t i = blockIdx.x * (int64_t)kNT + threadIdx.x; i < total; i += (int64_t)gridDim.x * kNT) {
+    const int64_t p = i / k.d_vecs.d;
+    const int at = (int)(i - p * k.d_vecs.d) * 16;
+    const uint8_t* const src = k.src + p * k.from + at;
+    const int shift = (int)(reinterpret_cast<uintptr_t>(src) & 3);
+    const uint8_t* q = src - shift;
+    uint32_t v[5];
+#pragma unroll
+    for (int e = 0; e < 5; ++e) v[e] = q + 4 * e < end ? __ldg(reinterpret_cast<const uint32_t*>(q + 4 * e)) : 0u;
+    uint4 o;
+    o.x = __funnelshift_r(v[0], v[1], 8 * shift);
+    o.y = __funnelshift_r(v[1], v[2], 8 * shift);
+    o.z = __funnelshift_r(v[2], v[3], 8 * shift);
+    o.w = __funnelshift_r(v[3], v[4], 8 * shift);
+    *reinterpret_cast<uint4*>(k.dst + p * k.to + at) = o;
+  }
+}
+
+int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
+
+// Bytes of aligned copies of gy and of x that a descriptor needs (0: as they are); x8: of its codes.
+int64_t gy_copy_bytes(const Conv& c, int es) {
+  return c.ctot * es % 16 == 0 && c.off * es % 16 == 0 ? 0 : out_pixels(c) * up16(c.C * es);
+}
+int64_t x_copy_bytes(const Conv& c, int es) {
+  return c.C * es % 16 == 0 ? 0 : c.N * c.H * c.W * up16(c.C * es);
+}
+// Copies of more than this are not made: the direct kernels run.
+constexpr int64_t kMostCopy = int64_t(4) << 30;
+
+bool copies_fit(const Conv& c, int es) {
+  return gy_copy_bytes(c, es) + x_copy_bytes(c, es) <= kMostCopy && gy_copy_bytes(c, es) + x_copy_bytes(c, 1) <= kMostCopy;
+}
+
+size_t sums_bytes(const Conv& c, int64_t chunks) {
+  const size_t b = (size_t)chunks * (size_t)c.OC() * (size_t)(c.kh * c.kw + 1) * sizeof(float);
+  return (b + 255) & ~size_t(255);
+}
+// chunks of any of the walking kernels that a call's pointers and source may lead to
+int64_t walk_chunks(const Conv& c) {
+  int64_t n = walk::plan(c).chunks;
+  for (int src : {kSrcFull, kSrcI8}) {
+    walk::Staged g;
+    if (walk::plan_staged(c, src, &g) && g.chunks > n) n = g.chunks;
+  }
+  return n;
+}
+
 template <typename T>
 cudaError_t walked(const Conv& c, const T* x, const Act8& t, const T* gy, const T* w, T* gx, T* gw, T* gb,
                    bool accumulate, float* ws, cudaStream_t s) {
@@ -185,20 +247,41 @@ cudaError_t walked(const Conv& c, const T* x, const Act8& t, const T* gy, const 
   int chunks = 0;
   walk::Staged st;
   cudaError_t e = cudaErrorNotSupported;
-  if (walk::plan_staged(c, x || !t.codes ? kSrcFull : t.src, &st)) {
+  const int src = x || !t.codes ? kSrcFull : t.src, es = sizeof(T), xes = src == kSrcFull ? es : 1;
+  const int64_t gcopy = gy_copy_bytes(c, es), xcopy = gw ? x_copy_bytes(c, xes) : 0;
+  // gx alone has no workspace, so no copies
+  if (walk::plan_staged(c, src, &st) && copies_fit(c, es) && (want_gw || gcopy == 0)) {
     st.want_gx = gx != nullptr;
     st.want_gw = want_gw;
     st.want_x = gw != nullptr;
     st.accumulate = accumulate;
+    st.pair_out = c.C % 2 == 0 && reinterpret_cast<uintptr_t>(gx) % (2 * es) == 0;
     chunks = st.chunks;
-    e = walk::run_staged<T>(c, st, x, t, gy, w, gx, ws, s);
+    walk::Views v{gy + c.off, src == kSrcFull ? (const void*)x : t.codes, c.ctot * es, c.C * xes};
+    uint8_t* room = reinterpret_cast<uint8_t*>(ws) + (gcopy || xcopy ? sums_bytes(c, walk_chunks(c)) : 0);
+    Copy job[2] = {};
+    int jobs = 0;
+    auto copy = [&](const void** p, int64_t* dist, int64_t pixels, int64_t bytes) {
+      const int64_t to = up16(bytes);
+      job[jobs++] = Copy{(const uint8_t*)*p, room, pixels, *dist, to, (int)bytes, FastDiv((uint32_t)(to / 16))};
+      *p = room;
+      *dist = to;
+      room += pixels * to;
+    };
+    if (gcopy) copy(&v.gy, &v.gdist, out_pixels(c), c.C * es);
+    if (xcopy) copy(&v.x, &v.xdist, c.N * c.H * c.W, c.C * xes);
+    if (jobs) {
+      const int64_t most = (gcopy > xcopy ? gcopy : xcopy) / 16;
+      const int64_t blocks = (most + kNT - 1) / kNT;
+      align_kernel<<<dim3((unsigned)(blocks < 152 * 32 ? blocks : 152 * 32), (unsigned)jobs), kNT, 0, s>>>(job[0], job[1]);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    e = walk::run_staged<T>(c, st, src, v, t, w, gx, ws, s);
   }
-  if (e == cudaErrorNotSupported) {
-    e = direct<T>(c, x, t, gy, w, gx, want_gw, accumulate, ws, s, &chunks);
-  }
+  if (e == cudaErrorNotSupported) e = direct<T>(c, x, t, gy, w, gx, want_gw, accumulate, ws, s, &chunks);
   if (e != cudaSuccess || !want_gw) return e;
-  walk_join_kernel<T><<<dim3((unsigned)((c.C + 31) / 32), (unsigned)(taps + 1)), kJoin, 0, s>>>((int)c.C, taps, chunks, ws,
-                                                                                          gw, gb);
+  walk_join_kernel<T><<<dim3((unsigned)((c.C + 31) / 32), (unsigned)(taps + 1)), kJoin, 0, s>>>((int)c.C, taps, chunks,
+                                                                                               ws, gw, gb);
   return cudaGetLastError();
 }
 
@@ -265,7 +348,7 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
   const int es = c.dtype == DWCONV_F32 ? 4 : 2, K = c.kh, S = c.sh, D = (K - 1) / S;
   const bool ring = K == 3;
   const int px = ring ? 4 : 8, step = ring ? 1 : 2 / S, blocks = ring ? kStagedBlocks : K == 5 ? 4 : 3;
-  if (c.C * es % 16 != 0 || (src != kSrcFull && c.C % 16 != 0) || c.C < 32) return false;
+  if (c.C < 32) return false;
   Staged g{};
   // 64 channels per block, 32 where that leaves a quarter fewer of the last tile idle
   const int64_t by64 = (c.C + 63) / 64 * 64, by32 = (c.C + 31) / 32 * 32;
@@ -359,13 +442,15 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
 Algo plan_bwd(const Conv& c) { return walk::supported(c) ? Algo::Nhwc : Algo::Generic; }
 
 size_t bwd_workspace_bytes(const Conv& c) {
-  size_t n = walk::supported(c) ? (size_t)walk::plan(c).chunks : (size_t)generic_chunks(c);
-  for (int src : {kSrcFull, kSrcI8}) {  // whichever the call's pointers and source lead to
-    walk::Staged g;
-    if (walk::plan_staged(c, src, &g) && (size_t)g.chunks > n) n = (size_t)g.chunks;
+  if (!walk::supported(c)) return sums_bytes(c, generic_chunks(c));
+  size_t b = sums_bytes(c, walk_chunks(c));
+  walk::Staged g;
+  const int es = c.dtype == DWCONV_F32 ? 4 : 2;
+  if (walk::plan_staged(c, kSrcFull, &g) && copies_fit(c, es)) {
+    const int64_t full = x_copy_bytes(c, es), codes = x_copy_bytes(c, 1);
+    b += (size_t)(gy_copy_bytes(c, es) + (full > codes ? full : codes));
   }
-  const size_t b = n * (size_t)c.OC() * (size_t)(c.kh * c.kw + 1) * sizeof(float);
-  return (b + 255) & ~size_t(255);
+  return b;
 }
 
 cudaError_t bwd(const Conv& c, const void* x, const Act8& x8, const void* gy, const void* w, void* gx, void* gw,

@@ -47,7 +47,8 @@ struct Staged {
   int gc, xc;          // columns of a stage's rows of gy and x
   int gy_bytes, x_bytes;      // of a stage's copies
   int x_at, stage_bytes;      // where x begins, and the next stage (multiples of 128)
-  bool want_gx, want_gw, want_x, accumulate;  // want_gw: gw or gb; want_x: gw
+  bool want_gx, want_gw, want_x, accumulate, pair_out;  // want_gw: gw or gb; want_x: gw; pair_out: two channels of gx are
+                                                        // one aligned store
 };
 
 bool supported(const Conv& c);
@@ -59,9 +60,15 @@ bool plan_staged(const Conv& c, int src, Staged* g);
 template <typename T>
 cudaError_t run(const Conv& c, const Geom& g, bool pair, const T* x, const Act8& x8, const T* gy, const T* w, T* gx,
                 float* ws, cudaStream_t s);
+// gy (from its first channel) and x, or its codes, with the distance of their
+// pixels in bytes.
+struct Views {
+  const void *gy, *x;
+  int64_t gdist, xdist;
+};
 // cudaErrorNotSupported: a pointer or distance is no multiple of 16 bytes.
 template <typename T>
-cudaError_t run_staged(const Conv& c, const Staged& g, const T* x, const Act8& x8, const T* gy, const T* w, T* gx,
+cudaError_t run_staged(const Conv& c, const Staged& g, int src, const Views& v, const Act8& x8, const T* w, T* gx,
                        float* ws, cudaStream_t s);
 
 }  // namespace walk

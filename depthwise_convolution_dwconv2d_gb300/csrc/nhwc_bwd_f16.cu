@@ -6,8 +6,8 @@ namespace nhwc {
 namespace walk {
 template cudaError_t run<__half>(const Conv&, const Geom&, bool, const __half*, const Act8&, const __half*, const __half*, __half*, float*,
                              cudaStream_t);
-template cudaError_t run_staged<__half>(const Conv&, const Staged&, const __half*, const Act8&, const __half*, const __half*, __half*,
-                             float*, cudaStream_t);
+template cudaError_t run_staged<__half>(const Conv&, const Staged&, int, const Views&, const Act8&, const __half*, __half*, float*,
+                             cudaStream_t);
 }  // namespace walk
 }  // namespace nhwc
 }  // namespace dwconv

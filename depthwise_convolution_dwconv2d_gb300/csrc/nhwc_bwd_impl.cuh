@@ -358,6 +358,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
   const int ls = lane % g.cs, ln = lane / g.cs;           // strip and sample of the lane
   const int la = min(ln, g.ns - 1);                       // a lane past the last sample reads within the stage
   const int C = (int)c.C, W = (int)c.W;
+  const bool two = ch + 1 < C;
   const uint32_t g_at = sm0 + (la * RD * g.gc + ls * (PX / S)) * GP + pl * (GP / CT);
   const uint32_t x_at = sm0 + g.x_at + (la * RD * S * g.xc + ls * PX) * XP + pl * (XP / CT);
 
@@ -428,7 +429,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
   for (int k = 0; k < K * K; ++k) {
     wr[k] = 0;
     if (ch < C && g.want_gx)
-      wr[k] = pack_f32x2(ld(w + (int64_t)ch * K * K + k), ld(w + (int64_t)(ch + 1) * K * K + k));
+      wr[k] = pack_f32x2(ld(w + (int64_t)ch * K * K + k), two ? ld(w + (int64_t)(ch + 1) * K * K + k) : 0.f);
   }
 #pragma unroll
   for (int k = 0; k <= K * K; ++k) acc[k] = 0;
@@ -440,17 +441,17 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
     const Item it = item_of(item);
     const int64_t n = it.n0 + ln;
     const int strip = (it.v0 - g.v_begin) / PX + ls;
-    const bool on = ln < g.ns && n < c.N && strip < g.strips && ch < C;
+    const bool here = ln < g.ns && n < c.N && strip < g.strips, on = here && ch < C;
     const int iw0 = it.v0 + ls * PX - c.pw;
     uint32_t xok = 0;
 #pragma unroll
     for (int p = 0; p < PX; ++p) xok |= (iw0 + p >= 0 && iw0 + p < W) ? 1u << p : 0u;
     const int64_t at = n * H * (int64_t)W + (int64_t)(S * it.tb - c.ph) * W + iw0;  // pixel of the band's first row
     char* op = reinterpret_cast<char*>(gx + at * C + ch);
-    const int stores = !on || !g.want_gx ? 0 : xok == (1u << PX) - 1 && !g.accumulate ? 1 : 2;
+    const int stores = !on || !g.want_gx ? 0 : !g.pair_out ? 3 : xok == (1u << PX) - 1 && !g.accumulate ? 1 : 2;
     // a checkpoint's scales: lanes p + 4 b of the strip's lanes read pixel p, block b of the tile's
     const int sl = pl & 7, sb = (ch0 >> x8.shift) + (sl >> 2);
-    const bool scaler = kCode && on && g.want_x && pl < 8 && sb < x8.nblk && ((xok >> (sl & 3)) & 1);
+    const bool scaler = kCode && here && g.want_x && pl < 8 && sb < x8.nblk && ((xok >> (sl & 3)) & 1);
     const int from = (int)(threadIdx.x & 31 & ~(CT - 1)) + 4 * ((ch >> x8.shift) - (ch0 >> x8.shift));
     const char* sp = reinterpret_cast<const char*>(x8.scales + (at + (sl & 3)) * x8.nblk + sb);
     float sc[S];
@@ -541,6 +542,10 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
 #pragma unroll
                 for (int p = 0; p < PX; ++p)
                   if ((xok >> p) & 1) store_pair<T, true>(reinterpret_cast<T*>(op + p * pixel), out[p], true, g.accumulate);
+              } else if (stores == 3) {
+#pragma unroll
+                for (int p = 0; p < PX; ++p)
+                  if ((xok >> p) & 1) store_pair<T, false>(reinterpret_cast<T*>(op + p * pixel), out[p], two, g.accumulate);
               }
             }
             op += row;
@@ -691,6 +696,7 @@ __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const 
   const int pl = threadIdx.x & (CT - 1), ch = ch0 + 2 * pl;
   const int lane = threadIdx.x / CT, ls = lane % g.cs, ln = lane / g.cs, la = min(ln, g.ns - 1);
   const int C = (int)c.C, W = (int)c.W, H = (int)c.H;
+  const bool two = ch + 1 < C;
   const int grows = g.band + D, xrows = g.band * S;
   const int grow = g.gc * GP, xrow = g.xc * XP;
   const uint32_t g_at = sm0 + (la * grows * g.gc + ls * (PX / S)) * GP + pl * (GP / CT);
@@ -734,7 +740,8 @@ __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const 
 #pragma unroll
   for (int k = 0; k < K * K + (GW ? 1 : 0); ++k) {
     acc[k] = 0;
-    if (!GW && ch < C) acc[k] = pack_f32x2(ld(w + (int64_t)ch * K * K + k), ld(w + (int64_t)(ch + 1) * K * K + k));
+    if (!GW && ch < C)
+      acc[k] = pack_f32x2(ld(w + (int64_t)ch * K * K + k), two ? ld(w + (int64_t)(ch + 1) * K * K + k) : 0.f);
   }
 
   int slot = 0;
@@ -749,7 +756,7 @@ __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const 
     const Item it = item_of(item);
     const int64_t n = it.n0 + ln;
     const int strip = (it.v0 - g.v_begin) / PX + ls;
-    const bool on = ln < g.ns && n < c.N && strip < g.strips && ch < C;
+    const bool here = ln < g.ns && n < c.N && strip < g.strips, on = here && ch < C;
     const int iw0 = it.v0 + ls * PX - c.pw, ih0 = S * it.tb - c.ph;
     uint32_t xok = 0;
 #pragma unroll
@@ -757,7 +764,7 @@ __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const 
     const int64_t at = n * H * (int64_t)W + (int64_t)ih0 * W + iw0;
     // a checkpoint's scales: lanes p + 8 b of the strip's lanes read pixel p, block b of the tile's
     const int sb = (ch0 >> x8.shift) + (pl >> 3);
-    const bool scaler = kCode && on && g.want_x && pl < 16 && sb < x8.nblk && ((xok >> (pl & 7)) & 1);
+    const bool scaler = kCode && here && g.want_x && pl < 16 && sb < x8.nblk && ((xok >> (pl & 7)) & 1);
     const int from = (int)(threadIdx.x & 31 & ~(CT - 1)) + 8 * ((ch >> x8.shift) - (ch0 >> x8.shift));
     const float* const sp = x8.scales + (at + (pl & 7)) * x8.nblk + sb;
     if (!tma::mbar_wait(&full[slot], parity, timeouts)) {
@@ -823,7 +830,9 @@ __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const 
         for (int r = 0; r < RY; ++r) {
           const int ih = ih0 + S * t + r;
           if (ih < 0 || ih >= H) continue;
-          store_strip<T, true, PX>(gx + (at + (int64_t)(S * t + r) * W) * C + ch, C, own + r * PX, xok, true, g.accumulate);
+          T* o = gx + (at + (int64_t)(S * t + r) * W) * C + ch;
+          if (g.pair_out) store_strip<T, true, PX>(o, C, own + r * PX, xok, true, g.accumulate);
+          else store_strip<T, false, PX>(o, C, own + r * PX, xok, two, g.accumulate);
         }
       }
     }
@@ -877,20 +886,18 @@ cudaError_t run(const Conv& c, const Geom& g, bool pair, const T* x, const Act8&
 }
 
 template <typename T, int SRC, int K, int S, int CT>
-cudaError_t launch_staged(const Conv& c, const Staged& g, const T* x, const Act8& x8, const T* gy, const T* w, T* gx,
-                          float* ws, cudaStream_t s) {
-  const uint64_t es = sizeof(T), xes = SRC == kSrcFull ? es : 1;
+cudaError_t launch_staged(const Conv& c, const Staged& g, const Views& v, const Act8& x8, const T* w, T* gx, float* ws,
+                          cudaStream_t s) {
   CUtensorMap mg, mx;
   const uint64_t gd[4] = {(uint64_t)c.C, (uint64_t)c.Wo, (uint64_t)c.Ho, (uint64_t)c.N};
-  const uint64_t gs[3] = {c.ctot * es, c.Wo * c.ctot * es, c.Ho * c.Wo * c.ctot * es};
+  const uint64_t gs[3] = {(uint64_t)v.gdist, (uint64_t)(c.Wo * v.gdist), (uint64_t)(c.Ho * c.Wo * v.gdist)};
   const uint32_t gb[4] = {2 * CT, (uint32_t)g.gc, (uint32_t)g.grows, (uint32_t)g.ns};
   const uint64_t xd[4] = {(uint64_t)c.C, (uint64_t)c.W, (uint64_t)c.H, (uint64_t)c.N};
-  const uint64_t xs[3] = {c.C * xes, c.W * c.C * xes, c.H * c.W * c.C * xes};
+  const uint64_t xs[3] = {(uint64_t)v.xdist, (uint64_t)(c.W * v.xdist), (uint64_t)(c.H * c.W * v.xdist)};
   const uint32_t xb[4] = {2 * CT, (uint32_t)g.xc, (uint32_t)g.xrows, (uint32_t)g.ns};
-  if (!tma::encode_strided(&mg, gy + c.off, c.dtype, 4, gd, gs, gb)) return cudaErrorNotSupported;
+  if (!tma::encode_strided(&mg, v.gy, c.dtype, 4, gd, gs, gb)) return cudaErrorNotSupported;
   mx = mg;
-  const void* xp = SRC == kSrcFull ? (const void*)x : (const void*)x8.codes;
-  if (g.want_x && !tma::encode_strided(&mx, xp, SRC == kSrcFull ? c.dtype : tma::kBytes, 4, xd, xs, xb))
+  if (g.want_x && !tma::encode_strided(&mx, v.x, SRC == kSrcFull ? c.dtype : tma::kBytes, 4, xd, xs, xb))
     return cudaErrorNotSupported;
   unsigned int* to = tma::timeout_counter();
   if (!to) return cudaErrorNotSupported;
@@ -909,18 +916,14 @@ cudaError_t launch_staged(const Conv& c, const Staged& g, const T* x, const Act8
 }
 
 template <typename T>
-cudaError_t run_staged(const Conv& c, const Staged& g, const T* x, const Act8& x8, const T* gy, const T* w, T* gx,
+cudaError_t run_staged(const Conv& c, const Staged& g, int src, const Views& v, const Act8& x8, const T* w, T* gx,
                        float* ws, cudaStream_t s) {
   // copies start on 16 bytes: pointers, distances between pixels
-  auto fits = [](const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && bytes % 16 == 0; };
-  const int es = sizeof(T);
-  const int src = x || !x8.codes ? kSrcFull : x8.src;
-  if (!fits(gy + c.off, c.ctot * es) || reinterpret_cast<uintptr_t>(gx) % (2 * es) != 0) return cudaErrorNotSupported;
-  if (g.want_x && src == kSrcFull && (!x || !fits(x, c.C * es))) return cudaErrorNotSupported;
-  if (g.want_x && src != kSrcFull && !fits(x8.codes, c.C)) return cudaErrorNotSupported;
-#define X(SRC, K, S, CT)                                                    \
-  if (src == SRC && c.kh == K && c.sh == S && (1 << g.ct_log) == CT)        \
-    return launch_staged<T, SRC, K, S, CT>(c, g, x, x8, gy, w, gx, ws, s);
+  auto fits = [](const void* p, int64_t dist) { return p && reinterpret_cast<uintptr_t>(p) % 16 == 0 && dist % 16 == 0; };
+  if (!fits(v.gy, v.gdist) || (g.want_x && !fits(v.x, v.xdist))) return cudaErrorNotSupported;
+#define X(SRC, K, S, CT)                                             \
+  if (src == SRC && c.kh == K && c.sh == S && (1 << g.ct_log) == CT) \
+    return launch_staged<T, SRC, K, S, CT>(c, g, v, x8, w, gx, ws, s);
 #define Z(SRC, K) X(SRC, K, 1, 32) X(SRC, K, 2, 32) X(SRC, K, 1, 16) X(SRC, K, 2, 16)
 #define Y(SRC) Z(SRC, 3) Z(SRC, 5) Z(SRC, 7)
   Y(kSrcFull) Y(kSrcI8) Y(kSrcE4M3)
