@@ -458,14 +458,16 @@ int64_t lcm(int64_t a, int64_t b) {
   return a / x * b;
 }
 
-// The slab plan of a pass for vectors of V elements; false: split. keep: the
-// block of a checkpoint that the forward writes (0: none); x_bytes: of an
-// element of the backward's input (0: forward).
-bool plan_slab(const Norm& g, int V, int es, int keep, int x_bytes, slab::Plan* out) {
+// The layout of a pass: how a thread's channels lie, the slices and their
+// rows; false: a slice wider than a block (the split kernels run). keep: the
+// block of a checkpoint that the forward writes (0: none).
+bool plan_slices(const Norm& g, int V, bool strided, int es, int keep, slab::Plan* out) {
   slab::Plan k{};
-  int64_t base = lcm(g.D, V);
+  k.V = V;
+  k.strided = strided;
+  if (keep && (strided || keep / V > 32)) return false;  // a block's lanes are one warp's
+  int64_t base = strided ? g.D : lcm(g.D, V);
   if (keep && keep < g.C) base = lcm(base, keep);
-  if (keep && keep / V > 32) return false;  // a block's lanes are one warp's
   const int64_t line = 128 / es;
   int64_t S = base * ((line + base - 1) / base);
   if (S > g.C || keep >= g.C) S = g.C;  // a slice holds whole blocks of a checkpoint, or all channels
@@ -476,33 +478,69 @@ bool plan_slab(const Norm& g, int V, int es, int keep, int x_bytes, slab::Plan* 
   k.rl = slab::kNT / k.vpr;
   k.slices = (int)((g.C + S - 1) / S);
   k.groups = (int)(S / g.D);
-  const int64_t units = g.N * k.slices;
-  const int64_t row = (int64_t)k.vpr * V * (es + x_bytes);
-  // Shares small enough for several blocks per SM, whose reading and writing
-  // overlap; more blocks where the slabs are too few for the GPU.
-  auto rows = [&](int cl) { return (g.P + cl - 1) / cl; };
-  k.cl = 1;
-  while (k.cl < 8 && rows(k.cl) * row > 44 * 1024) k.cl *= 2;
-  while (k.cl < 8 && units * k.cl < 304 && rows(k.cl) > 2 * k.rl) k.cl *= 2;
-  if (rows(k.cl) * row > 180 * 1024 || units * k.cl >= (int64_t(1) << 31)) return false;
-  k.rows = (int)rows(k.cl);
-  k.data_bytes = (int)((k.rows * row + 15) / 16 * 16);
-  if (k.data_bytes + slab::scratch_bytes(k, V, x_bytes ? 1 : 0) > 220 * 1024) return false;
   *out = k;
   return true;
 }
 
-// The widest vector that distances, offsets and pointers allow: 16 bytes, 4 bytes or one element.
-int vector_of(const Norm& g, int es, const void* a, const void* b, const void* c, const void* codes) {
-  for (int bytes : {16, 4}) {
-    const int V = bytes / es;
-    if (V < 1) continue;
+// Clusters of up to eight blocks that hold a slab; x_bytes: of an element of
+// the backward's input (0: forward). Shares small enough for several blocks
+// per SM, whose reading and writing overlap; more blocks where the slabs are
+// too few for the GPU.
+bool plan_cluster(const Norm& g, int es, int x_bytes, slab::Plan* k) {
+  const int64_t units = g.N * k->slices, row = (int64_t)k->vpr * k->V * (es + x_bytes);
+  auto rows = [&](int parts) { return (g.P + parts - 1) / parts; };
+  int parts = 1;
+  while (parts < 8 && rows(parts) * row > 44 * 1024) parts *= 2;
+  while (parts < 8 && units * parts < 304 && rows(parts) > 2 * k->rl) parts *= 2;
+  if (rows(parts) * row > 180 * 1024 || units * parts >= (int64_t(1) << 31)) return false;
+  k->parts = parts;
+  k->rows = (int)rows(parts);
+  k->data_bytes = (int)((k->rows * row + 15) / 16 * 16);
+  return k->data_bytes + slab::scratch_bytes(*k, x_bytes ? 1 : 0) <= 220 * 1024;
+}
+
+// Chunks of pixels for the stream kernels: about six blocks per SM, at least
+// eight rows for a row lane.
+bool plan_stream(const Norm& g, slab::Plan* k) {
+  const int64_t units = g.N * k->slices;
+  int64_t parts = (152 * 6 + units - 1) / units;
+  const int64_t most = (g.P + 8 * k->rl - 1) / (8 * k->rl);
+  if (parts > most) parts = most;
+  if (parts > 256) parts = 256;
+  const int64_t rows = (g.P + parts - 1) / parts;
+  if (rows >= (int64_t(1) << 31)) return false;
+  k->rows = (int)rows;
+  k->parts = (int)((g.P + rows - 1) / rows);
+  k->data_bytes = 0;
+  return units * k->parts < (int64_t(1) << 31) && slab::scratch_bytes(*k, 0) <= 220 * 1024;
+}
+
+enum Family { kSlabs, kStream, kSplit };
+
+Family plan_family(const Norm& g, int V, bool strided, int es, int keep, int x_bytes, slab::Plan* k) {
+  if (!plan_slices(g, V, strided, es, keep, k)) return kSplit;
+  if (plan_cluster(g, es, x_bytes, k)) return kSlabs;
+  return plan_stream(g, k) ? kStream : kSplit;
+}
+
+constexpr int kBwdV = 8;  // the most channels of a thread in the backward
+
+// How a thread's channels lie: the widest access that distances, offsets and
+// pointers allow (16 bytes; 8 for 16-bit types), or four channels apart.
+void layout_of(const Norm& g, int es, int pass, const void* a, const void* b, const void* c, const void* codes, int* V,
+               bool* strided) {
+  for (int bytes : {16, 8}) {
+    *V = bytes / es;
+    if (*V < 4 || (pass == 1 && *V > kBwdV)) continue;
     auto fits = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
-    if (g.C % V == 0 && g.xs % V == 0 && g.xo % V == 0 && g.ys % V == 0 && g.yo % V == 0 && fits(a) && fits(b) &&
-        fits(c) && reinterpret_cast<uintptr_t>(codes) % V == 0)
-      return V;
+    if (g.C % *V == 0 && g.xs % *V == 0 && g.xo % *V == 0 && g.ys % *V == 0 && g.yo % *V == 0 && fits(a) && fits(b) &&
+        fits(c) && reinterpret_cast<uintptr_t>(codes) % *V == 0) {
+      *strided = false;
+      return;
+    }
   }
-  return 1;
+  *V = 4;
+  *strided = true;
 }
 
 int elem_size(int dtype) { return dtype == DWCONV_F32 ? 4 : 2; }
@@ -511,16 +549,37 @@ int elem_size(int dtype) { return dtype == DWCONV_F32 ? 4 : 2; }
 
 const char* plan_name(const Norm& g, int pass) {
   const int es = elem_size(g.dtype);
+  int V;
+  bool strided;
   slab::Plan k;
-  return plan_slab(g, vector_of(g, es, nullptr, nullptr, nullptr, nullptr), es, 0, pass ? es : 0, &k) ? "slab" : "split";
+  layout_of(g, es, pass, nullptr, nullptr, nullptr, nullptr, &V, &strided);
+  const Family f = plan_family(g, V, strided, es, 0, pass ? es : 0, &k);
+  return f == kSlabs ? "slab" : f == kStream ? "stream" : "split";
 }
 
-// (mean, rstd) or (s1, s2) per group, and a pair per chunk and channel, for
-// the finer of the two cuts (vectors or single elements)
-size_t workspace_bytes(const Norm& g, int) {
+// Sums per part and group and, in the backward, per part and channel, for the
+// family and layout with the most parts that a call's pointers may lead to.
+size_t workspace_bytes(const Norm& g, int pass) {
   if (g.N == 0) return 0;
-  const int64_t a = plan_cut(g, 1).chunks, b = plan_cut(g, g.dtype == DWCONV_F32 ? 4 : 8).chunks;
-  const size_t pairs = (size_t)(g.N * g.G) + (size_t)g.N * (size_t)(a > b ? a : b) * (size_t)g.C;
+  const int es = elem_size(g.dtype);
+  int64_t parts = 1;
+  bool split_too = false;
+  for (int V : {8, 4, 1}) {  // 1: channels apart
+    slab::Plan k;
+    if (V * es > 16) continue;
+    if (plan_slices(g, V == 1 ? 4 : V, V == 1, es, 0, &k) && plan_stream(g, &k)) {
+      if (k.parts > parts) parts = k.parts;
+    } else {
+      split_too = true;
+    }
+    // a checkpoint's blocks widen the slices
+    for (int keep : {32, 64, 128})
+      if (V > 1 && plan_slices(g, V, false, es, keep, &k) && plan_stream(g, &k) && k.parts > parts) parts = k.parts;
+  }
+  size_t pairs = (size_t)g.N * (size_t)parts * ((size_t)g.G + (pass ? (size_t)g.C : 0));
+  const int64_t a = plan_cut(g, 1).chunks, b = plan_cut(g, 16 / es).chunks;
+  const size_t split = (size_t)(g.N * g.G) + (size_t)g.N * (size_t)(a > b ? a : b) * (size_t)g.C;
+  if (split_too && split > pairs) pairs = split;
   return (pairs * sizeof(float2) + 255) & ~size_t(255);
 }
 
@@ -529,18 +588,22 @@ namespace {
 template <typename T>
 cudaError_t fwd_any(const Norm& g, const T* x, const T* gamma, const T* beta, T* y, float* mean, float* rstd, float* ws,
                     const Act8& x8, cudaStream_t s) {
-  const int es = sizeof(T);
-  const int V = vector_of(g, es, x, y, nullptr, x8.codes);
-  const int block = x8.codes ? 1 << x8.shift : 0;
+  const int es = sizeof(T), block = x8.codes ? 1 << x8.shift : 0;
+  int V;
+  bool strided;
+  layout_of(g, es, 0, x, y, nullptr, x8.codes, &V, &strided);
+  const slab::Sums sums{reinterpret_cast<float2*>(ws), nullptr};
   slab::Plan k;
-  if (plan_slab(g, V, es, block, 0, &k)) return slab::run_fwd<T>(g, k, V, x, gamma, beta, y, mean, rstd, x8, s);
+  Family f = block ? plan_family(g, V, strided, es, block, 0, &k) : kSplit;
+  if (f != kSplit) return slab::run_fwd<T>(g, k, f == kSlabs, x, gamma, beta, y, mean, rstd, x8, sums, s);
   cudaError_t e;
-  if (plan_slab(g, V, es, 0, 0, &k)) {
-    e = slab::run_fwd<T>(g, k, V, x, gamma, beta, y, mean, rstd, Act8{}, s);
+  f = plan_family(g, V, strided, es, 0, 0, &k);
+  if (f != kSplit) {
+    e = slab::run_fwd<T>(g, k, f == kSlabs, x, gamma, beta, y, mean, rstd, Act8{}, sums, s);
   } else {
     constexpr int VV = Vec<T>::n;
-    e = V == VV ? split_fwd<T, VV>(g, x, gamma, beta, y, mean, rstd, ws, s)
-                : split_fwd<T, 1>(g, x, gamma, beta, y, mean, rstd, ws, s);
+    e = V == VV && !strided ? split_fwd<T, VV>(g, x, gamma, beta, y, mean, rstd, ws, s)
+                            : split_fwd<T, 1>(g, x, gamma, beta, y, mean, rstd, ws, s);
   }
   if (e == cudaSuccess && block) e = act8_encode(g.N * g.P, g.C, g.xs, g.dtype, x + g.xo, x8, s);
   return e;
@@ -555,18 +618,24 @@ cudaError_t bwd_any(const Norm& g, const T* x, const Act8& x8, const T* gy, cons
     return cudaGetLastError();
   }
   const int es = sizeof(T);
-  const int V = vector_of(g, es, x, gy, gx, x8.codes);
+  int V;
+  bool strided;
+  layout_of(g, es, 1, x, gy, gx, x8.codes, &V, &strided);
   slab::Plan k;
-  if (plan_slab(g, V, es, 0, x ? es : 1, &k)) {
-    float2* sums = reinterpret_cast<float2*>(ws);
-    const cudaError_t e = slab::run_bwd<T>(g, k, V, x, x8, gy, gamma, beta, mean, rstd, gx, sums, s);
+  const Family f = plan_family(g, V, strided, es, 0, x ? es : 1, &k);
+  if (f != kSplit) {
+    const int64_t parts = f == kSlabs ? 1 : k.parts;
+    slab::Sums sums;
+    sums.channels = reinterpret_cast<float2*>(ws);
+    sums.groups = sums.channels + g.N * parts * g.C;
+    const cudaError_t e = slab::run_bwd<T>(g, k, f == kSlabs, x, x8, gy, gamma, beta, mean, rstd, gx, sums, s);
     if (e != cudaSuccess || (!ggamma && !gbeta)) return e;
-    param_grad_kernel<T><<<(g.C + 31) / 32, kNT, 0, s>>>(g.C, g.N, sums, ggamma, gbeta);
+    param_grad_kernel<T><<<(g.C + 31) / 32, kNT, 0, s>>>(g.C, g.N * parts, sums.channels, ggamma, gbeta);
     return cudaGetLastError();
   }
   constexpr int VV = Vec<T>::n;
-  return V == VV ? bwd_src<T, VV>(g, x, x8, gy, gamma, beta, mean, rstd, gx, ggamma, gbeta, ws, s)
-                 : bwd_src<T, 1>(g, x, x8, gy, gamma, beta, mean, rstd, gx, ggamma, gbeta, ws, s);
+  return V == VV && !strided ? bwd_src<T, VV>(g, x, x8, gy, gamma, beta, mean, rstd, gx, ggamma, gbeta, ws, s)
+                             : bwd_src<T, 1>(g, x, x8, gy, gamma, beta, mean, rstd, gx, ggamma, gbeta, ws, s);
 }
 
 }  // namespace

@@ -1,24 +1,32 @@
 // Channels-last group norm, forward and backward: the slab kernels, which
-// read their inputs once.
+// read their inputs once, and the stream kernels, which read them twice.
 //
-// A unit of work is a slab: one sample's pixels times a slice of channels
-// that holds whole groups, at least one 128-byte line wide where the channels
-// allow it. A cluster of thread blocks owns a slab, each block a share of its
-// pixels: it reads them once, 16 bytes per thread and access, takes the sums
-// on the way and leaves the data as read in shared memory; the blocks join
-// their sums through the cluster's distributed shared memory; then each
-// writes its outputs from its own shared memory. Bytes moved are the floor's:
-// inputs once, outputs once. The forward also writes the 8-bit checkpoint of
-// x from the registers that hold it (a block of channels is a few
-// neighbouring lanes).
+// A slab is one sample's pixels times a slice of channels that holds whole
+// groups, at least one 128-byte line wide where the channels allow it. A
+// cluster of thread blocks owns a slab, each block a share of its pixels: it
+// reads them once, takes the sums on the way and leaves the data as read in
+// shared memory; the blocks join their sums through the cluster's distributed
+// shared memory; then each writes its outputs from its own shared memory.
+// Bytes moved are the floor's: inputs once, outputs once. The forward also
+// writes the 8-bit checkpoint of x from the registers that hold it (a block
+// of channels is a few neighbouring lanes).
 //
-// Slabs that no cluster of eight blocks can hold, and slices wider than a
-// block, are left to the split kernels (norm.cu).
+// Slabs that no cluster of eight blocks can hold are streamed: one launch
+// leaves the sums of each chunk of pixels in the workspace, a second reads
+// the inputs again (from L2 where they fit it; it walks the chunks last to
+// first, to begin with what the first launch left there), joins the chunks'
+// sums for its groups and writes the outputs. The same code in three modes.
 //
 // The variance is not taken from sums of squares of x: a block sums x - s and
 // (x - s)^2 about the values s of its first pixel, one per channel, turns
 // them into a mean and squares about that mean, and joins channels and blocks
 // by the parallel form of the two (see norm.cu). Every order is fixed.
+//
+// Arithmetic is on pairs of channels (the two lanes of the packed fp32
+// instructions), which halves the instructions; what bounds the kernels is
+// their issue (the 16-bit SiLU forward issues about 20 instructions per
+// element of 4 bytes) and, per block, the latency of reading, joining and the
+// cluster's barrier.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -32,87 +40,166 @@ namespace slab {
 
 namespace cg = cooperative_groups;
 
-// V elements as they are stored: 16 bytes, 4 bytes or one element
+enum Mode : int { kSlab = 0, kSums = 1, kApply = 2 };
+
 template <int BYTES> struct Word;
 template <> struct Word<16> { typedef uint4 type; };
 template <> struct Word<8> { typedef uint2 type; };
 template <> struct Word<4> { typedef uint32_t type; };
-template <> struct Word<2> { typedef uint16_t type; };
-template <> struct Word<1> { typedef uint8_t type; };
 
-// V elements as pairs (an odd V's last pair has 0 in its second lane)
-template <typename T, int V>
-struct Vecs {
+// two 16-bit values as a pair, exact
+template <typename T>
+__device__ __forceinline__ f32x2 pair_of(uint32_t u) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+    return pack_f32x2(f.x, f.y);
+  } else {
+    return pack_f32x2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t word_of(f32x2 v) {
+  float a, b;
+  unpack_f32x2(v, a, b);
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// A thread's V channels of a row, as stored (word) and as pairs. n: how many
+// of them exist (side by side: V or none).
+template <typename T, int V, bool STR>
+struct Lay {
   typedef typename Word<V * (int)sizeof(T)>::type word;
-  static constexpr int NP = (V + 1) / 2;
-  static __device__ __forceinline__ void unpack(word w, f32x2* f) {
-    if constexpr (V * sizeof(T) == 16) {
-      unpack16_pairs<T>(w, f);
+  typedef typename Word<V>::type codes;
+  static constexpr int NP = V / 2;
+
+  static __device__ __forceinline__ word load(const T* p, int vpr, int n) {
+    word w{};
+    if constexpr (STR) {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < n) reinterpret_cast<T*>(&w)[e] = p[e * vpr];
     } else {
-      const T* p = reinterpret_cast<const T*>(&w);
-      f[0] = pack_f32x2(to_f<T>(p[0]), V > 1 ? to_f<T>(p[V - 1]) : 0.f);
+      if (n > 0) w = *reinterpret_cast<const word*>(p);
+    }
+    return w;
+  }
+  static __device__ __forceinline__ void store(T* p, int vpr, int n, word w) {
+    if constexpr (STR) {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < n) p[e * vpr] = reinterpret_cast<const T*>(&w)[e];
+    } else {
+      if (n > 0) *reinterpret_cast<word*>(p) = w;
+    }
+  }
+  static __device__ __forceinline__ codes load_codes(const uint8_t* p, int vpr, int n) {
+    codes w{};
+    if constexpr (STR) {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < n) reinterpret_cast<uint8_t*>(&w)[e] = p[e * vpr];
+    } else {
+      if (n > 0) w = *reinterpret_cast<const codes*>(p);
+    }
+    return w;
+  }
+  static __device__ __forceinline__ void unpack(word w, f32x2* f) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      if constexpr (sizeof(T) == 4) {
+        f[e] = pack_f32x2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
+      } else {
+        f[e] = pair_of<T>(u[e]);
+      }
     }
   }
   static __device__ __forceinline__ word pack(const f32x2* f) {
-    float v[2 * NP];
+    word w;
+    uint32_t* u = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
-    for (int e = 0; e < NP; ++e) unpack_f32x2(f[e], v[2 * e], v[2 * e + 1]);
-    if constexpr (V * sizeof(T) == 16) {
-      return pack16<T>(v);
+    for (int e = 0; e < NP; ++e) {
+      if constexpr (sizeof(T) == 4) {
+        float a, b;
+        unpack_f32x2(f[e], a, b);
+        u[2 * e] = __float_as_uint(a);
+        u[2 * e + 1] = __float_as_uint(b);
+      } else {
+        u[e] = word_of<T>(f[e]);
+      }
+    }
+    return w;
+  }
+  // V values of a per-channel tensor from channel c
+  static __device__ __forceinline__ void channels(const T* base, int c, int vpr, int n, float none, f32x2* o) {
+    if (!base) {
+#pragma unroll
+      for (int e = 0; e < NP; ++e) o[e] = both(none);
+    } else if (!STR && reinterpret_cast<uintptr_t>(base) % sizeof(word) == 0) {
+      unpack(load(base + c, vpr, n), o);
     } else {
-      word w;
-      T* p = reinterpret_cast<T*>(&w);
+      word w{};
 #pragma unroll
-      for (int e = 0; e < V; ++e) p[e] = from_f<T>(v[e]);
-      return w;
+      for (int e = 0; e < V; ++e)
+        if (e < n) reinterpret_cast<T*>(&w)[e] = base[c + (STR ? e * vpr : e)];
+      unpack(w, o);
     }
   }
 };
 
-// codes of V values
-template <int SRC, int V>
-__device__ __forceinline__ void unpack_codes(typename Word<V>::type w, float s, f32x2* f) {
-  if constexpr (V == 8) {
-    decode4<SRC>(w.x, s, f);
-    decode4<SRC>(w.y, s, f + 2);
-  } else if constexpr (V == 4) {
-    decode4<SRC>(w, s, f);
-  } else {
-    f32x2 o[2];
-    decode4<SRC>((uint32_t)w, s, o);
-    f[0] = o[0];
+// The codes of V values and their scales (one where they lie side by side).
+template <int SRC, typename L, int V, bool STR>
+struct Coded {
+  typename L::codes w;
+  float s[STR ? V : 1];
+  __device__ __forceinline__ void load_scales(const Act8& t, int64_t row, int c, int vpr, int n) {
+#pragma unroll
+    for (int e = 0; e < (STR ? V : 1); ++e)
+      s[e] = e < n ? __ldg(t.scales + row * t.nblk + ((c + e * vpr) >> t.shift)) : 0.f;
   }
-}
+  __device__ __forceinline__ void values(f32x2* f) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) {
+      decode4<SRC>(u[h], STR ? 1.f : s[0], f + 2 * h);
+      if constexpr (STR) {
+        f[2 * h] = mul_f32x2(f[2 * h], pack_f32x2(s[4 * h], s[4 * h + 1]));
+        f[2 * h + 1] = mul_f32x2(f[2 * h + 1], pack_f32x2(s[4 * h + 2], s[4 * h + 3]));
+      }
+    }
+  }
+};
+
 template <int SRC, int V>
 __device__ __forceinline__ typename Word<V>::type pack_codes(const f32x2* f, float inv) {
-  if constexpr (V == 8) {
-    return make_uint2(encode4<SRC>(f[0], f[1], inv), encode4<SRC>(f[2], f[3], inv));
-  } else if constexpr (V == 4) {
-    return encode4<SRC>(f[0], f[1], inv);
-  } else {
-    return (typename Word<V>::type)encode4<SRC>(f[0], 0, inv);
-  }
+  typename Word<V>::type w;
+  uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+  for (int h = 0; h < V / 4; ++h) u[h] = encode4<SRC>(f[2 * h], f[2 * h + 1], inv);
+  return w;
 }
 
 // The largest pattern without sign of a vector's values and its neighbours'
 // of a block of channels (`lanes` of them), as that of an fp32 value.
 // Patterns of 16-bit types are compared two at a time.
-template <typename T, int V>
-__device__ __forceinline__ uint32_t block_max(typename Vecs<T, V>::word w, int lanes) {
+template <typename T, int V, typename W>
+__device__ __forceinline__ uint32_t block_max(W w, int lanes) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
+  uint32_t m = 0;
   if constexpr (sizeof(T) == 4) {
-    uint32_t m = 0;
-    const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
 #pragma unroll
     for (int e = 0; e < V; ++e) m = max(m, u[e] & 0x7fffffffu);
     for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
   } else {
-    uint32_t m;
-    if constexpr (V == 8) {
-      m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-    } else {
-      m = (uint32_t)w & 0x7fff7fffu;
-    }
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) m = __vmaxu2(m, u[e] & 0x7fff7fffu);
     for (int o = lanes >> 1; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
     const unsigned short h = (unsigned short)max(m & 0xffffu, m >> 16);
     return __float_as_uint(to_f<T>(*reinterpret_cast<const T*>(&h)));
@@ -127,14 +214,10 @@ __device__ __forceinline__ void join_rows(const Plan& k, const f32x2* u, const f
   constexpr int W = 4 * NP;
   if ((int)threadIdx.x < k.rl * k.vpr) {
     ulonglong2* o = reinterpret_cast<ulonglong2*>(red + threadIdx.x * W);
-    if constexpr (NP == 1) {
-      o[0] = make_ulonglong2(u[0], v[0]);
-    } else {
 #pragma unroll
-      for (int e = 0; e < NP / 2; ++e) {
-        o[e] = make_ulonglong2(u[2 * e], u[2 * e + 1]);
-        o[NP / 2 + e] = make_ulonglong2(v[2 * e], v[2 * e + 1]);
-      }
+    for (int e = 0; e < NP / 2; ++e) {
+      o[e] = make_ulonglong2(u[2 * e], u[2 * e + 1]);
+      o[NP / 2 + e] = make_ulonglong2(v[2 * e], v[2 * e + 1]);
     }
   }
   __syncthreads();
@@ -146,6 +229,13 @@ __device__ __forceinline__ void join_rows(const Plan& k, const f32x2* u, const f
     tot[i] = a;
   }
   __syncthreads();
+}
+
+// where channel c of the slice lies in a table of W floats per vector
+template <int V, bool STR, int W>
+__device__ __forceinline__ int table_at(const Plan& k, int c) {
+  const int q = STR ? c / k.vpr : c / V;
+  return STR ? (c - q * k.vpr) * W + q : q * W + (c - q * V);
 }
 
 // A group's sums are taken by `seg` neighbouring lanes, a power of two that
@@ -160,151 +250,155 @@ __device__ __forceinline__ float group_sum(float a, int seg) {
   return a;
 }
 
-// V values of a per-channel tensor; one read where the base is aligned
-template <typename T, int V>
-__device__ __forceinline__ void load_channels(const T* base, int c, float none, f32x2* o) {
-  constexpr int NP = Vecs<T, V>::NP;
-  if (!base) {
-#pragma unroll
-    for (int e = 0; e < NP; ++e) o[e] = both(none);
-  } else if (V > 1 && reinterpret_cast<uintptr_t>(base) % sizeof(typename Vecs<T, V>::word) == 0) {
-    Vecs<T, V>::unpack(*reinterpret_cast<const typename Vecs<T, V>::word*>(base + c), o);
-  } else {
-#pragma unroll
-    for (int e = 0; e < NP; ++e) o[e] = pack_f32x2(ld(base + c + 2 * e), 2 * e + 1 < V ? ld(base + c + 2 * e + 1) : 0.f);
-  }
-}
-
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-// group of the slice that each of a vector's channels belongs to
-template <int V>
-__device__ __forceinline__ void groups_of(int D, int first, int* gi) {
-  int q = first / D, r = first - q * D;
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    gi[e] = q;
-    if (++r == D) {
-      r = 0;
-      ++q;
-    }
-  }
-}
-
 struct Place {
-  int64_t n, row0;   // sample, first row of the share in the tensor
-  int rows;          // of the share (0: none)
+  int64_t n, row0;   // sample, first row of the block in the tensor
+  int part, rows;    // block of the slab, its rows (0: none)
   int c0, S;         // first channel and channels of the slice
   int c, vl, r;      // this thread's first channel, vector and row lane
-  bool on;           // has channels
+  int nv;            // its channels that exist
 };
 
-template <int V>
-__device__ __forceinline__ Place place_of(const Norm& g, const Plan& k) {
+template <int V, bool STR>
+__device__ __forceinline__ Place place_of(const Norm& g, const Plan& k, uint32_t block) {
   Place p;
-  const uint32_t unit = blockIdx.x / k.cl, rank = blockIdx.x - unit * k.cl;
+  const uint32_t unit = block / k.parts;
+  p.part = (int)(block - unit * k.parts);
   p.n = unit / k.slices;
   const int slice = (int)(unit - (uint32_t)p.n * k.slices);
   p.c0 = slice * k.S;
   p.S = min(k.S, g.C - p.c0);
-  const int64_t r0 = (int64_t)rank * k.rows;
+  const int64_t r0 = (int64_t)p.part * k.rows;
   p.rows = (int)(r0 < g.P ? (g.P - r0 < k.rows ? g.P - r0 : k.rows) : 0);
   p.row0 = p.n * g.P + r0;
   p.r = threadIdx.x / k.vpr;
   p.vl = threadIdx.x - p.r * k.vpr;
-  p.c = p.c0 + p.vl * V;
-  p.on = p.r < k.rl && p.vl * V < p.S;
+  p.c = p.c0 + (STR ? p.vl : p.vl * V);
+  if (p.r >= k.rl) {
+    p.nv = 0;
+  } else if (STR) {
+    p.nv = p.vl < p.S ? min((p.S - p.vl + k.vpr - 1) / k.vpr, V) : 0;
+  } else {
+    p.nv = p.vl * V < p.S ? V : 0;
+  }
   return p;
 }
 
-template <typename T, int V, int KEEP>
+// group of the slice that each of a thread's channels belongs to (0 for those that do not exist)
+template <int V, bool STR>
+__device__ __forceinline__ void groups_of(const Norm& g, const Plan& k, const Place& p, int* gi) {
+  if (STR) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) gi[e] = e < p.nv ? (p.vl + e * k.vpr) / g.D : 0;
+  } else {
+    const int first = p.nv > 0 ? p.vl * V : 0;
+    int q = first / g.D, r = first - q * g.D;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      gi[e] = q;
+      if (++r == g.D) {
+        r = 0;
+        ++q;
+      }
+    }
+  }
+}
+
+// rows of part j of a slab
+__device__ __forceinline__ float rows_of(const Norm& g, const Plan& k, int j) {
+  const int64_t r0 = (int64_t)j * k.rows;
+  return (float)(r0 < g.P ? min((int64_t)k.rows, g.P - r0) : 0);
+}
+
+template <typename T, int V, bool STR, int KEEP, int MODE>
 __global__ void __launch_bounds__(kNT, 3)
 fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma, const T* __restrict__ beta,
-           T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, Act8 x8) {
-  typedef typename Vecs<T, V>::word word;
-  constexpr int NP = Vecs<T, V>::NP;
+           T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, Act8 x8,
+           float2* __restrict__ gsums) {
+  typedef Lay<T, V, STR> L;
+  typedef typename L::word word;
+  constexpr int NP = L::NP, W = 4 * NP;
   extern __shared__ __align__(16) unsigned char sm[];
-  cg::cluster_group cluster = cg::this_cluster();
-  const Place p = place_of<V>(g, k);
+  const Place p = place_of<V, STR>(g, k, MODE == kApply ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   word* const data = reinterpret_cast<word*>(sm);
-  constexpr int W = 4 * NP;
   float* const red = reinterpret_cast<float*>(sm + k.data_bytes);
   float* const tot = red + kNT * W;
-  float* const base = tot + k.vpr * W;                                    // what the sums are about, per channel
-  float2* const part = reinterpret_cast<float2*>(base + k.vpr * 2 * NP);  // (mean, squares) of the block's groups
-  float2* const stat = part + k.groups;                                   // (mean, rstd) of the slab's
-
-  // read, sum, keep
-  f32x2 s[NP], d[NP], q[NP];
-#pragma unroll
-  for (int e = 0; e < NP; ++e) s[e] = d[e] = q[e] = 0;
+  float* const base = tot + k.vpr * W;                               // what the sums are about, per channel
+  float2* const part = reinterpret_cast<float2*>(base + k.vpr * V);  // (mean, squares) of the block's groups
+  float2* const stat = part + k.groups;                              // (mean, rstd) of the slab's
+  const int groups = p.S / g.D;
   int gi[V];
-  groups_of<V>(g.D, min(p.vl * V, p.S - 1), gi);
+  groups_of<V, STR>(g, k, p, gi);
   const T* xp = x + (p.row0 + p.r) * g.xs + g.xo + p.c;
-  uint8_t* cp = KEEP != kSrcFull ? x8.codes + (p.row0 + p.r) * g.C + p.c : nullptr;
-  float* scp = KEEP != kSrcFull ? x8.scales + (p.row0 + p.r) * x8.nblk + (p.c >> x8.shift) : nullptr;
-  const bool scaler = KEEP != kSrcFull && (p.c & ((1 << x8.shift) - 1)) == 0;
   const int64_t xstep = k.rl * g.xs;
-  const int left = p.on ? p.rows - p.r : 0;  // rows from this lane's first on
-  // sums about the share's first row: one value per channel, the same for every row lane
-  if (p.on && p.rows > 0) {
-    Vecs<T, V>::unpack(*reinterpret_cast<const word*>(x + p.row0 * g.xs + g.xo + p.c), s);
-    if (p.r == 0) {
-#pragma unroll
-      for (int e = 0; e < NP; ++e) *reinterpret_cast<f32x2*>(base + p.vl * 2 * NP + 2 * e) = s[e];
-    }
-#pragma unroll
-    for (int e = 0; e < NP; ++e) s[e] = neg(s[e]);
-  }
-  word* dp = data + p.r * k.vpr + p.vl;
-  const int dstep = k.rl * k.vpr;
-  constexpr int kAhead = V == 1 ? 8 : 4;  // rows in flight
-  for (int r0 = 0; r0 < p.rows; r0 += kAhead * k.rl) {
-    word w[kAhead];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a, xp += xstep) {
-      w[a] = word{};
-      if (r0 + a * k.rl < left) w[a] = *reinterpret_cast<const word*>(xp);
-    }
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const bool in = r0 + a * k.rl < left;
-      f32x2 f[NP];
-      Vecs<T, V>::unpack(w[a], f);
-      if (in) {
-        *dp = w[a];
-#pragma unroll
-        for (int e = 0; e < NP; ++e) {
-          const f32x2 t = add_f32x2(f[e], s[e]);
-          d[e] = add_f32x2(d[e], t);
-          fma_f32x2(q[e], t, t);
-        }
-      }
-      dp += dstep;
-      if (KEEP != kSrcFull) {  // lanes of a block of channels are neighbours; those without data bring zeros
-        const uint32_t m = block_max<T, V>(w[a], (1 << x8.shift) / V);
-        if (in) {
-          float inv;
-          const float sc = scale_of<KEEP>(m, &inv);
-          *reinterpret_cast<typename Word<V>::type*>(cp) = pack_codes<KEEP, V>(f, inv);
-          if (scaler) *scp = sc;
-        }
-        cp += (int64_t)k.rl * g.C;
-        scp += (int64_t)k.rl * x8.nblk;
-      }
-    }
-  }
+  const int at0 = p.r * k.vpr + p.vl, dstep = k.rl * k.vpr;
+  const int left = p.nv > 0 ? p.rows - p.r : 0;  // rows from this lane's first on
+  constexpr int kAhead = 4;                      // rows in flight
 
-  // the block's mean and squares of each group, from those of its channels
-  const int groups = p.S / g.D, seg = lanes_of_group(g.D);
-  join_rows<NP>(k, d, q, red, tot);
-  {
+  if constexpr (MODE != kApply) {
+    // read, sum, keep
+    f32x2 s[NP], d[NP], q[NP];
+#pragma unroll
+    for (int e = 0; e < NP; ++e) s[e] = d[e] = q[e] = 0;
+    if (p.rows > 0) {  // one value per channel, the same for every row lane
+      L::unpack(L::load(x + p.row0 * g.xs + g.xo + p.c, k.vpr, p.nv), s);
+      if (p.r == 0) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) *reinterpret_cast<f32x2*>(base + p.vl * V + 2 * e) = s[e];
+      }
+#pragma unroll
+      for (int e = 0; e < NP; ++e) s[e] = neg(s[e]);
+    }
+    uint8_t* cp = KEEP != kSrcFull ? x8.codes + (p.row0 + p.r) * g.C + p.c : nullptr;
+    float* scp = KEEP != kSrcFull ? x8.scales + (p.row0 + p.r) * x8.nblk + (p.c >> x8.shift) : nullptr;
+    const bool scaler = KEEP != kSrcFull && (p.c & ((1 << x8.shift) - 1)) == 0;
+    int at = at0;
+    for (int r0 = 0; r0 < p.rows; r0 += kAhead * k.rl) {
+      word w[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a, xp += xstep) {
+        w[a] = word{};
+        if (r0 + a * k.rl < left) w[a] = L::load(xp, k.vpr, p.nv);
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const bool in = r0 + a * k.rl < left;
+        f32x2 f[NP];
+        L::unpack(w[a], f);
+        if (in) {
+          if (MODE == kSlab) data[at] = w[a];
+#pragma unroll
+          for (int e = 0; e < NP; ++e) {
+            const f32x2 t = add_f32x2(f[e], s[e]);
+            d[e] = add_f32x2(d[e], t);
+            fma_f32x2(q[e], t, t);
+          }
+        }
+        at += dstep;
+        if constexpr (KEEP != kSrcFull) {  // lanes of a block of channels are neighbours; those without data bring zeros
+          const uint32_t m = block_max<T, V>(w[a], (1 << x8.shift) / V);
+          if (in) {
+            float inv;
+            const float sc = scale_of<KEEP>(m, &inv);
+            *reinterpret_cast<typename L::codes*>(cp) = pack_codes<KEEP, V>(f, inv);
+            if (scaler) *scp = sc;
+          }
+          cp += (int64_t)k.rl * g.C;
+          scp += (int64_t)k.rl * x8.nblk;
+        }
+      }
+    }
+
+    // the block's mean and squares of each group, from those of its channels
+    const int seg = lanes_of_group(g.D);
+    join_rows<NP>(k, d, q, red, tot);
     const float n = (float)p.rows, in = p.rows > 0 ? 1.f / n : 0.f;
     auto channel = [&](int c, float* mean, float* squares) {
-      const int vl = c / V, e = c - vl * V;
-      const float sd = tot[vl * W + e], sq = tot[vl * W + 2 * NP + e], t = sq - sd * sd * in;
-      *mean = base[vl * 2 * NP + e] + sd * in;
+      const int i = table_at<V, STR, W>(k, c);
+      const float sd = tot[i], t = tot[i + 2 * NP] - sd * sd * in;
+      *mean = base[table_at<V, STR, V>(k, c)] + sd * in;
       *squares = t < 0.f ? 0.f : t;  // NaN stays
     };
     for (int i0 = 0; i0 < groups; i0 += kNT / seg) {
@@ -322,133 +416,165 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
         a += fmaf(n * (m - mean), m - mean, sq);
       }
       a = group_sum(a, seg);
-      if (l == 0 && i < groups) part[i] = make_float2(mean, a);
+      if (l == 0 && i < groups) {
+        if (MODE == kSlab) part[i] = make_float2(mean, a);
+        else gsums[(p.n * k.parts + p.part) * g.G + p.c0 / g.D + i] = make_float2(mean, a);
+      }
     }
+    if constexpr (MODE == kSums) return;
   }
-  // the slab's
-  cluster_arrive();
-  cluster_wait();
-  for (int i = threadIdx.x; i < groups; i += kNT) {
-    const float total = (float)g.P * (float)g.D;
-    float a = 0.f;
-    for (int b = 0; b < k.cl; ++b) {
-      const int64_t r0 = (int64_t)b * k.rows;
-      const float n = (float)(r0 < g.P ? min((int64_t)k.rows, g.P - r0) : 0) * (float)g.D;
-      a = fmaf(n, cluster.map_shared_rank(part, b)[i].x, a);
-    }
-    const float mean = a / total;
-    float sq = 0.f;
-    for (int b = 0; b < k.cl; ++b) {
-      const int64_t r0 = (int64_t)b * k.rows;
-      const float n = (float)(r0 < g.P ? min((int64_t)k.rows, g.P - r0) : 0) * (float)g.D;
-      const float2 o = cluster.map_shared_rank(part, b)[i];
-      const float t = o.x - mean;
-      sq += n > 0.f ? fmaf(n * t, t, o.y) : 0.f;
-    }
+
+  // the slab's mean and rstd from its parts'
+  const float total = (float)g.P * (float)g.D;
+  auto finish = [&](int i, float mean, float sq) {
     const float rstd = 1.f / sqrtf(sq / total + g.eps);
     stat[i] = make_float2(mean, rstd);
-    if (cluster.block_rank() == 0) {
+    if (p.part == 0) {
       const int64_t at = p.n * g.G + p.c0 / g.D + i;
       if (mean_out) mean_out[at] = mean;
       if (rstd_out) rstd_out[at] = rstd;
     }
+  };
+  if constexpr (MODE == kSlab) {
+    cluster_arrive();
+    cluster_wait();
+    cg::cluster_group cluster = cg::this_cluster();
+    for (int i = threadIdx.x; i < groups; i += kNT) {
+      float a = 0.f, sq = 0.f;
+      for (int b = 0; b < k.parts; ++b) a = fmaf(rows_of(g, k, b) * (float)g.D, cluster.map_shared_rank(part, b)[i].x, a);
+      const float mean = a / total;
+      for (int b = 0; b < k.parts; ++b) {
+        const float n = rows_of(g, k, b) * (float)g.D;
+        const float2 o = cluster.map_shared_rank(part, b)[i];
+        sq += n > 0.f ? fmaf(n * (o.x - mean), o.x - mean, o.y) : 0.f;
+      }
+      finish(i, mean, sq);
+    }
+  } else {
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < groups; i += kNT / 32) {
+      const float2* o = gsums + p.n * k.parts * (int64_t)g.G + p.c0 / g.D + i;
+      float a = 0.f, sq = 0.f;
+      for (int b = lane; b < k.parts; b += 32) a = fmaf(rows_of(g, k, b) * (float)g.D, o[(int64_t)b * g.G].x, a);
+      const float mean = group_sum(a, 32) / total;
+      for (int b = lane; b < k.parts; b += 32) {
+        const float2 v = o[(int64_t)b * g.G];
+        sq += fmaf(rows_of(g, k, b) * (float)g.D * (v.x - mean), v.x - mean, v.y);
+      }
+      sq = group_sum(sq, 32);
+      if (lane == 0) finish(i, mean, sq);
+    }
   }
   __syncthreads();
-  if (k.cl > 1) cluster_arrive();  // this block has read the others' sums
+  if (MODE == kSlab && k.parts > 1) cluster_arrive();  // this block has read the others' sums
 
   // write
-  if (p.on) {
+  if (p.nv > 0) {
     f32x2 ga[NP], be[NP], mu[NP], rs[NP];
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
-      const float2 a = stat[gi[2 * e]], b = stat[gi[2 * e + 1 < V ? 2 * e + 1 : 2 * e]];
+      const float2 a = stat[gi[2 * e]], b = stat[gi[2 * e + 1]];
       mu[e] = pack_f32x2(-a.x, -b.x);
       rs[e] = pack_f32x2(a.y, b.y);
     }
-    load_channels<T, V>(gamma, p.c, 1.f, ga);
-    load_channels<T, V>(beta, p.c, 0.f, be);
+    L::channels(gamma, p.c, k.vpr, p.nv, 1.f, ga);
+    L::channels(beta, p.c, k.vpr, p.nv, 0.f, be);
     T* yp = y + (p.row0 + p.r) * g.ys + g.yo + p.c;
     const int64_t ystep = k.rl * g.ys;
-    dp = data + p.r * k.vpr + p.vl;
-#pragma unroll 2
-    for (int r = p.r; r < p.rows; r += k.rl, yp += ystep, dp += dstep) {
+    auto put = [&](word w) {
       f32x2 f[NP];
-      Vecs<T, V>::unpack(*dp, f);
+      L::unpack(w, f);
 #pragma unroll
       for (int e = 0; e < NP; ++e)
         f[e] = add_apart(mul_f32x2(mul_f32x2(add_f32x2(f[e], mu[e]), rs[e]), ga[e]), be[e]);
       act_p<NP>(g.act, f);
-      *reinterpret_cast<word*>(yp) = Vecs<T, V>::pack(f);
-    }
-  }
-  if (k.cl > 1) cluster_wait();  // no block leaves while another reads its sums
-}
-
-template <typename T, int V, int SRC>
-__global__ void __launch_bounds__(kNT, 2)
-bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict__ gy, const T* __restrict__ gamma,
-           const T* __restrict__ beta, const float* __restrict__ mean, const float* __restrict__ rstd,
-           T* __restrict__ gx, float2* __restrict__ sums) {
-  typedef typename Vecs<T, V>::word word;
-  typedef typename Word<SRC == kSrcFull ? V * (int)sizeof(T) : V>::type xword;
-  constexpr int NP = Vecs<T, V>::NP;
-  extern __shared__ __align__(16) unsigned char sm[];
-  cg::cluster_group cluster = cg::this_cluster();
-  const Place p = place_of<V>(g, k);
-  word* const gdata = reinterpret_cast<word*>(sm);
-  xword* const xdata = reinterpret_cast<xword*>(sm + (size_t)k.rows * k.vpr * sizeof(word));
-  constexpr int W = 4 * NP;
-  float* const red = reinterpret_cast<float*>(sm + k.data_bytes);
-  float* const tot = red + kNT * W;                                       // sums of du and of du * xh per channel
-  float2* const part = reinterpret_cast<float2*>(tot + k.vpr * W);        // (s1, s2) of the block's groups
-  float2* const stat = part + k.groups;                                   // of the slab's, over the count
-
-  int gi[V];
-  groups_of<V>(g.D, min(p.vl * V, p.S - 1), gi);
-  f32x2 ga[NP], be[NP], mu[NP], rs[NP];
+      L::store(yp, k.vpr, p.nv, L::pack(f));
+    };
+    if constexpr (MODE == kSlab) {
+      int at = at0;
+#pragma unroll 2
+      for (int r = p.r; r < p.rows; r += k.rl, yp += ystep, at += dstep) put(data[at]);
+    } else {
+      for (int r0 = p.r; r0 < p.rows; r0 += kAhead * k.rl) {
+        word w[kAhead];
 #pragma unroll
-  for (int e = 0; e < NP; ++e) ga[e] = be[e] = mu[e] = rs[e] = 0;
-  if (p.on) {
-    load_channels<T, V>(gamma, p.c, 1.f, ga);
-    load_channels<T, V>(beta, p.c, 0.f, be);
-    const int64_t at = p.n * g.G + p.c0 / g.D;
-    const float m0 = -__ldg(mean + at + gi[0]), r0 = __ldg(rstd + at + gi[0]);
+        for (int a = 0; a < kAhead; ++a, xp += xstep) {
+          w[a] = word{};
+          if (r0 + a * k.rl < p.rows) w[a] = L::load(xp, k.vpr, p.nv);
+        }
 #pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      mu[e] = both(m0);
-      rs[e] = both(r0);
-    }
-    if (gi[0] != gi[V - 1]) {
-#pragma unroll
-      for (int e = 0; e < NP; ++e) {
-        const int i = gi[2 * e], j = gi[2 * e + 1 < V ? 2 * e + 1 : 2 * e];
-        mu[e] = pack_f32x2(-__ldg(mean + at + i), -__ldg(mean + at + j));
-        rs[e] = pack_f32x2(__ldg(rstd + at + i), __ldg(rstd + at + j));
+        for (int a = 0; a < kAhead; ++a, yp += ystep)
+          if (r0 + a * k.rl < p.rows) put(w[a]);
       }
     }
   }
-  const T* gp = gy + (p.row0 + p.r) * g.ys + g.yo + p.c;
-  const int64_t gstep = k.rl * g.ys;
-  // x and its scale, one row lane's step at a time
-  const int64_t first = p.row0 + p.r;
-  const xword* xp;
-  int64_t xstep;
-  if constexpr (SRC == kSrcFull) {
-    xp = reinterpret_cast<const xword*>(x + first * g.xs + g.xo + p.c);
-    xstep = k.rl * g.xs / V;
-  } else {
-    xp = reinterpret_cast<const xword*>(x8.codes + first * g.C + p.c);
-    xstep = (int64_t)k.rl * g.C / V;
+  if (MODE == kSlab && k.parts > 1) cluster_wait();  // no block leaves while another reads its sums
+}
+
+template <typename T, int V, bool STR, int SRC, int MODE>
+__global__ void __launch_bounds__(kNT, V == 8 ? 2 : 3)
+bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict__ gy, const T* __restrict__ gamma,
+           const T* __restrict__ beta, const float* __restrict__ mean, const float* __restrict__ rstd,
+           T* __restrict__ gx, Sums sums) {
+  typedef Lay<T, V, STR> L;
+  typedef typename L::word word;
+  typedef Coded<SRC, L, V, STR> Code;
+  typedef typename std::conditional<SRC == kSrcFull, word, typename L::codes>::type xword;
+  constexpr int NP = L::NP, W = 4 * NP;
+  extern __shared__ __align__(16) unsigned char sm[];
+  const Place p = place_of<V, STR>(g, k, MODE == kApply ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  word* const gdata = reinterpret_cast<word*>(sm);
+  xword* const xdata = reinterpret_cast<xword*>(sm + (size_t)k.rows * k.vpr * sizeof(word));
+  float* const red = reinterpret_cast<float*>(sm + k.data_bytes);
+  float* const tot = red + kNT * W;                                 // sums of du and of du * xh per channel
+  float2* const part = reinterpret_cast<float2*>(tot + k.vpr * W);  // (s1, s2) of the block's groups
+  float2* const stat = part + k.groups;                             // of the slab's, over the count
+  const int groups = p.S / g.D;
+  int gi[V];
+  groups_of<V, STR>(g, k, p, gi);
+
+  f32x2 ga[NP], be[NP], mu[NP], rs[NP];
+  L::channels(gamma, p.c, k.vpr, p.nv, 1.f, ga);
+  L::channels(beta, p.c, k.vpr, p.nv, 0.f, be);
+  {
+    const float* m = mean + p.n * g.G + p.c0 / g.D;
+    const float* r = rstd + p.n * g.G + p.c0 / g.D;
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      mu[e] = both(-__ldg(m + gi[0]));
+      rs[e] = both(__ldg(r + gi[0]));
+    }
+    if (STR || gi[0] != gi[V - 1]) {
+#pragma unroll
+      for (int e = 0; e < NP; ++e) {
+        mu[e] = pack_f32x2(-__ldg(m + gi[2 * e]), -__ldg(m + gi[2 * e + 1]));
+        rs[e] = pack_f32x2(__ldg(r + gi[2 * e]), __ldg(r + gi[2 * e + 1]));
+      }
+    }
   }
-  const float* scp = SRC == kSrcFull ? nullptr : x8.scales + first * x8.nblk + (p.c >> x8.shift);
-  const int64_t scstep = SRC == kSrcFull ? 0 : (int64_t)k.rl * x8.nblk;
+  const int64_t first = p.row0 + p.r;
+  const T* gp = gy + first * g.ys + g.yo + p.c;
+  const int64_t gstep = k.rl * g.ys;
+  const T* xp = SRC == kSrcFull ? x + first * g.xs + g.xo + p.c : nullptr;
+  const int64_t xstep = k.rl * g.xs;
+  const uint8_t* cp = SRC == kSrcFull ? nullptr : x8.codes + first * g.C + p.c;
+  const int64_t cstep = (int64_t)k.rl * g.C;
+  auto load_x = [&]() {
+    if constexpr (SRC == kSrcFull) {
+      return L::load(xp, k.vpr, p.nv);
+    } else {
+      return L::load_codes(cp, k.vpr, p.nv);
+    }
+  };
   // xh and du of one vector, from what was stored
-  auto eval = [&](word gw, xword xw, float sc, f32x2* xh, f32x2* du) {
+  auto eval = [&](word gw, xword xw, const Code& code, f32x2* xh, f32x2* du) {
     f32x2 t[NP];
     if constexpr (SRC == kSrcFull) {
-      Vecs<T, V>::unpack(xw, xh);
+      L::unpack(xw, xh);
     } else {
-      unpack_codes<SRC, V>(xw, sc, xh);
+      Code c = code;
+      c.w = xw;
+      c.values(xh);
     }
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
@@ -457,175 +583,264 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
       t[e] = add_apart(mul_f32x2(xh[e], ga[e]), be[e]);
     }
     slope_p<NP>(g.act, t);
-    Vecs<T, V>::unpack(gw, du);
+    L::unpack(gw, du);
 #pragma unroll
     for (int e = 0; e < NP; ++e) du[e] = mul_f32x2(du[e], t[e]);
   };
-
-  // read, sum, keep
-  f32x2 a[NP], b[NP];
-#pragma unroll
-  for (int e = 0; e < NP; ++e) a[e] = b[e] = 0;
   const int at0 = p.r * k.vpr + p.vl, dstep = k.rl * k.vpr;
-  if (p.on) {
-    constexpr int kAhead = V == 1 ? 4 : 2;
-    const float* sq = scp;
-    int at = at0;
-    for (int r0 = p.r; r0 < p.rows; r0 += kAhead * k.rl) {
-      word gw[kAhead];
-      xword xw[kAhead];
-      float sc[kAhead];
+  constexpr int kAhead = V == 8 ? 2 : 4;
+
+  if constexpr (MODE != kApply) {
+    // read, sum, keep
+    f32x2 a[NP], b[NP];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        gw[i] = word{};
-        xw[i] = xword{};
-        sc[i] = 0.f;
-        if (r0 + i * k.rl < p.rows) {
-          gw[i] = *reinterpret_cast<const word*>(gp);
-          xw[i] = *xp;
-          if (SRC != kSrcFull) sc[i] = __ldg(sq);
+    for (int e = 0; e < NP; ++e) a[e] = b[e] = 0;
+    if (p.nv > 0) {
+      int at = at0;
+      for (int r0 = p.r; r0 < p.rows; r0 += kAhead * k.rl) {
+        word gw[kAhead];
+        xword xw[kAhead];
+        Code cd[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          gw[i] = word{};
+          xw[i] = xword{};
+          const int r = r0 + i * k.rl;
+          if (r < p.rows) {
+            gw[i] = L::load(gp, k.vpr, p.nv);
+            xw[i] = load_x();
+            if (SRC != kSrcFull) cd[i].load_scales(x8, p.row0 + r, p.c, k.vpr, p.nv);
+          }
+          gp += gstep;
+          xp += xstep;
+          cp += cstep;
         }
-        gp += gstep;
-        xp += xstep;
-        sq += scstep;
-      }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (r0 + i * k.rl >= p.rows) break;
-        gdata[at] = gw[i];
-        xdata[at] = xw[i];
-        at += dstep;
-        f32x2 xh[NP], du[NP];
-        eval(gw[i], xw[i], sc[i], xh, du);
+        for (int i = 0; i < kAhead; ++i) {
+          if (r0 + i * k.rl >= p.rows) break;
+          if (MODE == kSlab) {
+            gdata[at] = gw[i];
+            xdata[at] = xw[i];
+          }
+          at += dstep;
+          f32x2 xh[NP], du[NP];
+          eval(gw[i], xw[i], cd[i], xh, du);
 #pragma unroll
-        for (int e = 0; e < NP; ++e) {
-          a[e] = add_f32x2(a[e], du[e]);
-          fma_f32x2(b[e], du[e], xh[e]);
+          for (int e = 0; e < NP; ++e) {
+            a[e] = add_f32x2(a[e], du[e]);
+            fma_f32x2(b[e], du[e], xh[e]);
+          }
         }
       }
     }
-  }
-  join_rows<NP>(k, a, b, red, tot);
-  const int groups = p.S / g.D, seg = lanes_of_group(g.D);
-  for (int i0 = 0; i0 < groups; i0 += kNT / seg) {
-    const int i = i0 + (int)threadIdx.x / seg, l = threadIdx.x & (seg - 1);
-    float s1 = 0.f, s2 = 0.f;
-    for (int c = l; c < g.D && i < groups; c += seg) {
-      const int ch = i * g.D + c, vl = ch / V, e = ch - vl * V;
-      const float w = gamma ? ld(gamma + p.c0 + ch) : 1.f;
-      s1 = fmaf(w, tot[vl * W + e], s1);
-      s2 = fmaf(w, tot[vl * W + 2 * NP + e], s2);
+    join_rows<NP>(k, a, b, red, tot);
+    const int seg = lanes_of_group(g.D);
+    for (int i0 = 0; i0 < groups; i0 += kNT / seg) {
+      const int i = i0 + (int)threadIdx.x / seg, l = threadIdx.x & (seg - 1);
+      float s1 = 0.f, s2 = 0.f;
+      for (int c = l; c < g.D && i < groups; c += seg) {
+        const int ch = i * g.D + c, t = table_at<V, STR, W>(k, ch);
+        const float w = gamma ? ld(gamma + p.c0 + ch) : 1.f;
+        s1 = fmaf(w, tot[t], s1);
+        s2 = fmaf(w, tot[t + 2 * NP], s2);
+      }
+      s1 = group_sum(s1, seg);
+      s2 = group_sum(s2, seg);
+      if (l == 0 && i < groups) {
+        if (MODE == kSlab) part[i] = make_float2(s1, s2);
+        else sums.groups[(p.n * k.parts + p.part) * g.G + p.c0 / g.D + i] = make_float2(s1, s2);
+      }
     }
-    s1 = group_sum(s1, seg);
-    s2 = group_sum(s2, seg);
-    if (l == 0 && i < groups) part[i] = make_float2(s1, s2);
+    if constexpr (MODE == kSums) {
+      for (int c = threadIdx.x; c < p.S; c += kNT) {
+        const int t = table_at<V, STR, W>(k, c);
+        sums.channels[(p.n * k.parts + p.part) * g.C + p.c0 + c] = make_float2(tot[t], tot[t + 2 * NP]);
+      }
+      return;
+    }
   }
-  cluster_arrive();
-  cluster_wait();
+
   const float inv = 1.f / ((float)g.P * (float)g.D);
-  for (int i = threadIdx.x; i < groups; i += kNT) {
-    float s1 = 0.f, s2 = 0.f;
-    for (int j = 0; j < k.cl; ++j) {
-      const float2 o = cluster.map_shared_rank(part, j)[i];
-      s1 += o.x;
-      s2 += o.y;
+  if constexpr (MODE == kSlab) {
+    cluster_arrive();
+    cluster_wait();
+    cg::cluster_group cluster = cg::this_cluster();
+    for (int i = threadIdx.x; i < groups; i += kNT) {
+      float s1 = 0.f, s2 = 0.f;
+      for (int j = 0; j < k.parts; ++j) {
+        const float2 o = cluster.map_shared_rank(part, j)[i];
+        s1 += o.x;
+        s2 += o.y;
+      }
+      stat[i] = make_float2(s1 * inv, s2 * inv);
     }
-    stat[i] = make_float2(s1 * inv, s2 * inv);
-  }
-  // the slab's sums per channel, each block its share of the channels
-  const int share = (p.S + k.cl - 1) / k.cl, lo = (int)cluster.block_rank() * share;
-  for (int c = lo + threadIdx.x; c < min(lo + share, p.S); c += kNT) {
-    float s1 = 0.f, s2 = 0.f;
-    for (int j = 0; j < k.cl; ++j) {
-      const float* o = cluster.map_shared_rank(tot, j) + c / V * W + c % V;
-      s1 += o[0];
-      s2 += o[2 * NP];
+    // the slab's sums per channel, each block its share of the channels
+    const int share = (p.S + k.parts - 1) / k.parts, lo = p.part * share;
+    for (int c = lo + threadIdx.x; c < min(lo + share, p.S); c += kNT) {
+      const int t = table_at<V, STR, W>(k, c);
+      float s1 = 0.f, s2 = 0.f;
+      for (int j = 0; j < k.parts; ++j) {
+        const float* o = cluster.map_shared_rank(tot, j) + t;
+        s1 += o[0];
+        s2 += o[2 * NP];
+      }
+      sums.channels[p.n * g.C + p.c0 + c] = make_float2(s1, s2);
     }
-    sums[p.n * g.C + p.c0 + c] = make_float2(s1, s2);
+  } else {
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < groups; i += kNT / 32) {
+      const float2* o = sums.groups + p.n * k.parts * (int64_t)g.G + p.c0 / g.D + i;
+      float s1 = 0.f, s2 = 0.f;
+      for (int j = lane; j < k.parts; j += 32) {
+        const float2 v = o[(int64_t)j * g.G];
+        s1 += v.x;
+        s2 += v.y;
+      }
+      s1 = group_sum(s1, 32);
+      s2 = group_sum(s2, 32);
+      if (lane == 0) stat[i] = make_float2(s1 * inv, s2 * inv);
+    }
   }
   __syncthreads();
-  if (k.cl > 1) cluster_arrive();
+  if (MODE == kSlab && k.parts > 1) cluster_arrive();
 
   // write: gx = du * (gamma rstd) - rstd s1 - xh * (rstd s2)
-  if (gx && p.on) {
+  if (gx && p.nv > 0) {
     f32x2 c1[NP], c2[NP], c3[NP];
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
-      const float2 u = stat[gi[2 * e]], v = stat[gi[2 * e + 1 < V ? 2 * e + 1 : 2 * e]];
+      const float2 u = stat[gi[2 * e]], v = stat[gi[2 * e + 1]];
       c1[e] = mul_f32x2(ga[e], rs[e]);
       c2[e] = neg(mul_f32x2(pack_f32x2(u.x, v.x), rs[e]));
       c3[e] = neg(mul_f32x2(pack_f32x2(u.y, v.y), rs[e]));
     }
     T* op = gx + first * g.xs + g.xo + p.c;
-    const int64_t ostep = k.rl * g.xs;
-    int at = at0;
-    for (int r = p.r; r < p.rows; r += k.rl, op += ostep, scp += scstep, at += dstep) {
+    auto put = [&](word gw, xword xw, const Code& cd) {
       f32x2 xh[NP], du[NP];
-      eval(gdata[at], xdata[at], SRC == kSrcFull ? 0.f : __ldg(scp), xh, du);
+      eval(gw, xw, cd, xh, du);
 #pragma unroll
       for (int e = 0; e < NP; ++e) du[e] = fma2(du[e], c1[e], fma2(xh[e], c3[e], c2[e]));
-      *reinterpret_cast<word*>(op) = Vecs<T, V>::pack(du);
+      L::store(op, k.vpr, p.nv, L::pack(du));
+    };
+    if constexpr (MODE == kSlab) {
+      int at = at0;
+      for (int r = p.r; r < p.rows; r += k.rl, op += xstep, at += dstep) {
+        Code cd;
+        if (SRC != kSrcFull) cd.load_scales(x8, p.row0 + r, p.c, k.vpr, p.nv);
+        put(gdata[at], xdata[at], cd);
+      }
+    } else {
+      for (int r0 = p.r; r0 < p.rows; r0 += kAhead * k.rl) {
+        word gw[kAhead];
+        xword xw[kAhead];
+        Code cd[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          gw[i] = word{};
+          xw[i] = xword{};
+          const int r = r0 + i * k.rl;
+          if (r < p.rows) {
+            gw[i] = L::load(gp, k.vpr, p.nv);
+            xw[i] = load_x();
+            if (SRC != kSrcFull) cd[i].load_scales(x8, p.row0 + r, p.c, k.vpr, p.nv);
+          }
+          gp += gstep;
+          xp += xstep;
+          cp += cstep;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i, op += xstep)
+          if (r0 + i * k.rl < p.rows) put(gw[i], xw[i], cd[i]);
+      }
     }
   }
-  if (k.cl > 1) cluster_wait();
+  if (MODE == kSlab && k.parts > 1) cluster_wait();
 }
 
 // ---- launches --------------------------------------------------------------
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kern)(P...), const Norm& g, const Plan& k, int V, int pass, cudaStream_t s, A... args) {
-  const int smem = k.data_bytes + scratch_bytes(k, V, pass);
+cudaError_t launch(void (*kern)(P...), const Norm& g, const Plan& k, bool cluster, int pass, cudaStream_t s, A... args) {
+  const int smem = (cluster ? k.data_bytes : 0) + scratch_bytes(k, pass);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)k.cl;
+  attr.val.clusterDim.x = (unsigned)k.parts;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(g.N * k.slices * k.cl));
+  cfg.gridDim = dim3((unsigned)(g.N * k.slices * k.parts));
   cfg.blockDim = dim3(kNT);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// V of a type: 16 bytes, 4 bytes, one element
-#define DW_SLAB_V(X)                                       \
-  if (V * (int)sizeof(T) == 16) { X(16 / (int)sizeof(T)) } \
-  if constexpr (sizeof(T) == 2) {                          \
-    if (V == 2) { X(2) }                                   \
-  }                                                        \
-  if (V == 1) { X(1) }
+template <typename T, int V, bool STR>
+cudaError_t fwd_of(const Norm& g, const Plan& k, bool slab, const T* x, const T* gamma, const T* beta, T* y, float* mean,
+                   float* rstd, const Act8& x8, const Sums& sums, cudaStream_t s) {
+  const int keep = x8.codes ? x8.src : kSrcFull;
+  auto one = [&](auto kern, bool cluster) {
+    return launch(kern, g, k, cluster, 0, s, g, k, x, gamma, beta, y, mean, rstd, x8, sums.groups);
+  };
+  cudaError_t e = cudaErrorInvalidValue;
+#define X(KEEP)                                                              \
+  if (keep == KEEP) e = slab ? one(fwd_kernel<T, V, STR, KEEP, kSlab>, true) \
+                             : one(fwd_kernel<T, V, STR, KEEP, kSums>, false);
+  X(kSrcFull)
+  if constexpr (!STR) {
+    X(kSrcI8) X(kSrcE4M3)
+  }
+#undef X
+  if (slab || e != cudaSuccess) return e;
+  return one(fwd_kernel<T, V, STR, kSrcFull, kApply>, false);
+}
+
+template <typename T, int V, bool STR>
+cudaError_t bwd_of(const Norm& g, const Plan& k, bool slab, const T* x, const Act8& x8, const T* gy, const T* gamma,
+                   const T* beta, const float* mean, const float* rstd, T* gx, const Sums& sums, cudaStream_t s) {
+  const int src = x ? kSrcFull : x8.src;
+  auto one = [&](auto kern, bool cluster) {
+    return launch(kern, g, k, cluster, 1, s, g, k, x, x8, gy, gamma, beta, mean, rstd, gx, sums);
+  };
+#define X(SRC)                                                               \
+  if (src == SRC) {                                                          \
+    if (slab) return one(bwd_kernel<T, V, STR, SRC, kSlab>, true);           \
+    const cudaError_t e = one(bwd_kernel<T, V, STR, SRC, kSums>, false);     \
+    return e != cudaSuccess || !gx ? e : one(bwd_kernel<T, V, STR, SRC, kApply>, false); \
+  }
+  X(kSrcFull) X(kSrcI8) X(kSrcE4M3)
+#undef X
+  return cudaErrorInvalidValue;
+}
+
+#define DW_SLAB_LAYOUTS(X)                                    \
+  if (k.strided) { X(4, true) }                               \
+  if constexpr (sizeof(T) == 2) {                             \
+    if (k.V == 8) { X(8, false) }                             \
+  }                                                           \
+  if (k.V == 4) { X(4, false) }
 
 template <typename T>
-cudaError_t run_fwd(const Norm& g, const Plan& k, int V, const T* x, const T* gamma, const T* beta, T* y, float* mean,
-                    float* rstd, const Act8& x8, cudaStream_t s) {
-  const int keep = x8.codes ? x8.src : kSrcFull;
-#define Y(VV, KEEP) \
-  if (keep == KEEP) return launch(fwd_kernel<T, VV, KEEP>, g, k, V, 0, s, g, k, x, gamma, beta, y, mean, rstd, x8);
-#define X(VV) Y(VV, kSrcFull) Y(VV, kSrcI8) Y(VV, kSrcE4M3)
-  DW_SLAB_V(X)
+cudaError_t run_fwd(const Norm& g, const Plan& k, bool slab, const T* x, const T* gamma, const T* beta, T* y,
+                    float* mean, float* rstd, const Act8& x8, const Sums& sums, cudaStream_t s) {
+#define X(V, STR) return fwd_of<T, V, STR>(g, k, slab, x, gamma, beta, y, mean, rstd, x8, sums, s);
+  DW_SLAB_LAYOUTS(X)
 #undef X
-#undef Y
   return cudaErrorInvalidValue;
 }
 
 template <typename T>
-cudaError_t run_bwd(const Norm& g, const Plan& k, int V, const T* x, const Act8& x8, const T* gy, const T* gamma,
-                    const T* beta, const float* mean, const float* rstd, T* gx, float2* sums, cudaStream_t s) {
-  const int src = x ? kSrcFull : x8.src;
-#define Y(VV, SRC) \
-  if (src == SRC)  \
-    return launch(bwd_kernel<T, VV, SRC>, g, k, V, 1, s, g, k, x, x8, gy, gamma, beta, mean, rstd, gx, sums);
-#define X(VV) Y(VV, kSrcFull) Y(VV, kSrcI8) Y(VV, kSrcE4M3)
-  DW_SLAB_V(X)
+cudaError_t run_bwd(const Norm& g, const Plan& k, bool slab, const T* x, const Act8& x8, const T* gy, const T* gamma,
+                    const T* beta, const float* mean, const float* rstd, T* gx, const Sums& sums, cudaStream_t s) {
+#define X(V, STR) return bwd_of<T, V, STR>(g, k, slab, x, x8, gy, gamma, beta, mean, rstd, gx, sums, s);
+  DW_SLAB_LAYOUTS(X)
 #undef X
-#undef Y
   return cudaErrorInvalidValue;
 }
 
