@@ -482,12 +482,17 @@ bool plan_slices(const Norm& g, int V, bool strided, int es, int keep, slab::Pla
   return true;
 }
 
-// Clusters of up to eight blocks that hold a slab; x_bytes: of an element of
-// the backward's input (0: forward). Shares small enough for several blocks
+// Bytes of shared memory that a vector of a row takes. x_bytes: of an element
+// of the backward's input (0: forward; 1: codes, with their scales).
+int64_t vector_bytes(const slab::Plan& k, int es, int x_bytes) {
+  return k.V * (es + x_bytes) + (x_bytes == 1 ? (k.strided ? 4 * k.V : 4) : 0);
+}
+
+// Clusters of up to eight blocks that hold a slab. Shares small enough for several blocks
 // per SM, whose reading and writing overlap; more blocks where the slabs are
 // too few for the GPU.
 bool plan_cluster(const Norm& g, int es, int x_bytes, slab::Plan* k) {
-  const int64_t units = g.N * k->slices, row = (int64_t)k->vpr * k->V * (es + x_bytes);
+  const int64_t units = g.N * k->slices, row = k->vpr * vector_bytes(*k, es, x_bytes);
   auto rows = [&](int parts) { return (g.P + parts - 1) / parts; };
   int parts = 1;
   while (parts < 8 && rows(parts) * row > 44 * 1024) parts *= 2;
@@ -501,7 +506,7 @@ bool plan_cluster(const Norm& g, int es, int x_bytes, slab::Plan* k) {
 
 // Chunks of pixels for the stream kernels: about six blocks per SM, at least
 // eight rows for a row lane.
-bool plan_stream(const Norm& g, slab::Plan* k) {
+bool plan_stream(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   const int64_t units = g.N * k->slices;
   int64_t parts = (152 * 6 + units - 1) / units;
   const int64_t most = (g.P + 8 * k->rl - 1) / (8 * k->rl);
@@ -511,8 +516,9 @@ bool plan_stream(const Norm& g, slab::Plan* k) {
   if (rows >= (int64_t(1) << 31)) return false;
   k->rows = (int)rows;
   k->parts = (int)((g.P + rows - 1) / rows);
-  k->data_bytes = 0;
-  return units * k->parts < (int64_t(1) << 31) && slab::scratch_bytes(*k, 0) <= 220 * 1024;
+  k->data_bytes = (int)(2 * slab::kBatch * slab::kNT * vector_bytes(*k, es, x_bytes));
+  return units * k->parts < (int64_t(1) << 31) &&
+         k->data_bytes + slab::scratch_bytes(*k, x_bytes ? 1 : 0) <= 220 * 1024;
 }
 
 enum Family { kSlabs, kStream, kSplit };
@@ -520,7 +526,7 @@ enum Family { kSlabs, kStream, kSplit };
 Family plan_family(const Norm& g, int V, bool strided, int es, int keep, int x_bytes, slab::Plan* k) {
   if (!plan_slices(g, V, strided, es, keep, k)) return kSplit;
   if (plan_cluster(g, es, x_bytes, k)) return kSlabs;
-  return plan_stream(g, k) ? kStream : kSplit;
+  return plan_stream(g, es, x_bytes, k) ? kStream : kSplit;
 }
 
 constexpr int kBwdV = 8;  // the most channels of a thread in the backward
@@ -567,14 +573,14 @@ size_t workspace_bytes(const Norm& g, int pass) {
   for (int V : {8, 4, 1}) {  // 1: channels apart
     slab::Plan k;
     if (V * es > 16) continue;
-    if (plan_slices(g, V == 1 ? 4 : V, V == 1, es, 0, &k) && plan_stream(g, &k)) {
+    if (plan_slices(g, V == 1 ? 4 : V, V == 1, es, 0, &k) && plan_stream(g, es, pass ? es : 0, &k)) {
       if (k.parts > parts) parts = k.parts;
     } else {
       split_too = true;
     }
     // a checkpoint's blocks widen the slices
     for (int keep : {32, 64, 128})
-      if (V > 1 && plan_slices(g, V, false, es, keep, &k) && plan_stream(g, &k) && k.parts > parts) parts = k.parts;
+      if (V > 1 && plan_slices(g, V, false, es, keep, &k) && plan_stream(g, es, 0, &k) && k.parts > parts) parts = k.parts;
   }
   size_t pairs = (size_t)g.N * (size_t)parts * ((size_t)g.G + (pass ? (size_t)g.C : 0));
   const int64_t a = plan_cut(g, 1).chunks, b = plan_cut(g, 16 / es).chunks;

@@ -9,6 +9,7 @@ namespace norm {
 namespace slab {
 
 constexpr int kNT = 256;
+constexpr int kBatch = 4;  // rows that a thread fetches at a time; the next batch is on its way
 
 // How a thread's V channels lie: side by side, one access of V elements; or a
 // row's vectors apart, V accesses of one element each (for distances and
@@ -23,7 +24,7 @@ struct Plan {
   int groups;      // groups of a slice
   int parts;       // blocks of a sample's slice: a cluster (slab), or chunks of pixels (stream)
   int rows;        // pixels of a block
-  int data_bytes;  // shared memory for a slab block's share of the inputs
+  int data_bytes;  // shared memory for a slab block's share of the inputs, a stream block's two batches
 };
 
 // Shared memory behind the shares: the row lanes' sums, tables per channel

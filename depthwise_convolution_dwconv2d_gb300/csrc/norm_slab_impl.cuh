@@ -47,6 +47,21 @@ template <> struct Word<16> { typedef uint4 type; };
 template <> struct Word<8> { typedef uint2 type; };
 template <> struct Word<4> { typedef uint32_t type; };
 
+// Asynchronous copies into the thread's own slots: no thread reads another's,
+// so a thread waits for its own copies only.
+template <typename W>
+__device__ __forceinline__ void copy_async(W* dst, const void* src) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  if constexpr (sizeof(W) == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"((int)sizeof(W)) : "memory");
+  }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
 // two 16-bit values as a pair, exact
 template <typename T>
 __device__ __forceinline__ f32x2 pair_of(uint32_t u) {
@@ -88,6 +103,21 @@ struct Lay {
       if (n > 0) w = *reinterpret_cast<const word*>(p);
     }
     return w;
+  }
+  // the same, into shared memory; side by side it only begins the copy
+  static __device__ __forceinline__ void fetch(word* dst, const T* p, int vpr, int n) {
+    if constexpr (STR) {
+      *dst = load(p, vpr, n);
+    } else {
+      copy_async(dst, p);
+    }
+  }
+  static __device__ __forceinline__ void fetch_codes(codes* dst, const uint8_t* p, int vpr, int n) {
+    if constexpr (STR) {
+      *dst = load_codes(p, vpr, n);
+    } else {
+      copy_async(dst, p);
+    }
   }
   static __device__ __forceinline__ void store(T* p, int vpr, int n, word w) {
     if constexpr (STR) {
@@ -153,28 +183,33 @@ struct Lay {
   }
 };
 
-// The codes of V values and their scales (one where they lie side by side).
-template <int SRC, typename L, int V, bool STR>
-struct Coded {
-  typename L::codes w;
-  float s[STR ? V : 1];
-  __device__ __forceinline__ void load_scales(const Act8& t, int64_t row, int c, int vpr, int n) {
+// The scales of V codes: one where they lie side by side.
+template <int V, bool STR>
+struct Scales {
+  static constexpr int n = STR ? V : 1;
+  float s[n];
+  static __device__ __forceinline__ void fetch(Scales* dst, const Act8& t, int64_t row, int c, int vpr, int nv) {
+    const float* p = t.scales + row * t.nblk;
+    if constexpr (STR) {
 #pragma unroll
-    for (int e = 0; e < (STR ? V : 1); ++e)
-      s[e] = e < n ? __ldg(t.scales + row * t.nblk + ((c + e * vpr) >> t.shift)) : 0.f;
-  }
-  __device__ __forceinline__ void values(f32x2* f) const {
-    const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
-#pragma unroll
-    for (int h = 0; h < V / 4; ++h) {
-      decode4<SRC>(u[h], STR ? 1.f : s[0], f + 2 * h);
-      if constexpr (STR) {
-        f[2 * h] = mul_f32x2(f[2 * h], pack_f32x2(s[4 * h], s[4 * h + 1]));
-        f[2 * h + 1] = mul_f32x2(f[2 * h + 1], pack_f32x2(s[4 * h + 2], s[4 * h + 3]));
-      }
+      for (int e = 0; e < V; ++e) dst->s[e] = e < nv ? __ldg(p + ((c + e * vpr) >> t.shift)) : 0.f;
+    } else {
+      copy_async(&dst->s[0], p + (c >> t.shift));
     }
   }
 };
+template <int SRC, int V, bool STR, typename W>
+__device__ __forceinline__ void values_of(W w, const Scales<V, STR>& sc, f32x2* f) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
+#pragma unroll
+  for (int h = 0; h < V / 4; ++h) {
+    decode4<SRC>(u[h], STR ? 1.f : sc.s[0], f + 2 * h);
+    if constexpr (STR) {
+      f[2 * h] = mul_f32x2(f[2 * h], pack_f32x2(sc.s[4 * h], sc.s[4 * h + 1]));
+      f[2 * h + 1] = mul_f32x2(f[2 * h + 1], pack_f32x2(sc.s[4 * h + 2], sc.s[4 * h + 3]));
+    }
+  }
+}
 
 template <int SRC, int V>
 __device__ __forceinline__ typename Word<V>::type pack_codes(const f32x2* f, float inv) {
@@ -334,8 +369,21 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
   const T* xp = x + (p.row0 + p.r) * g.xs + g.xo + p.c;
   const int64_t xstep = k.rl * g.xs;
   const int at0 = p.r * k.vpr + p.vl, dstep = k.rl * k.vpr;
-  const int left = p.nv > 0 ? p.rows - p.r : 0;  // rows from this lane's first on
-  constexpr int kAhead = 4;                      // rows in flight
+  // Rows p.r + j * rl of the share, j < mine, are this thread's. They come in batches of kBatch, a batch ahead of the one
+  // in use; a slab keeps every row, a stream has slots for two batches.
+  const int mine = p.nv > 0 && p.r < p.rows ? (p.rows - p.r + k.rl - 1) / k.rl : 0;
+  const int batches = ((p.rows + k.rl - 1) / k.rl + kBatch - 1) / kBatch;
+  auto slot = [&](int j) { return MODE == kSlab ? at0 + j * dstep : (j & (2 * kBatch - 1)) * kNT + (int)threadIdx.x; };
+  auto fetch = [&](int b) {
+#pragma unroll
+    for (int a = 0; a < kBatch; ++a, xp += xstep) {
+      const int j = b * kBatch + a;
+      if (j < mine) L::fetch(data + slot(j), xp, k.vpr, p.nv);
+    }
+    copies_commit();
+  };
+  fetch(0);
+  fetch(1);
 
   if constexpr (MODE != kApply) {
     // read, sum, keep
@@ -354,21 +402,17 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
     uint8_t* cp = KEEP != kSrcFull ? x8.codes + (p.row0 + p.r) * g.C + p.c : nullptr;
     float* scp = KEEP != kSrcFull ? x8.scales + (p.row0 + p.r) * x8.nblk + (p.c >> x8.shift) : nullptr;
     const bool scaler = KEEP != kSrcFull && (p.c & ((1 << x8.shift) - 1)) == 0;
-    int at = at0;
-    for (int r0 = 0; r0 < p.rows; r0 += kAhead * k.rl) {
-      word w[kAhead];
+    for (int b = 0; b < batches; ++b) {
+      copies_wait<1>();
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a, xp += xstep) {
-        w[a] = word{};
-        if (r0 + a * k.rl < left) w[a] = L::load(xp, k.vpr, p.nv);
-      }
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const bool in = r0 + a * k.rl < left;
-        f32x2 f[NP];
-        L::unpack(w[a], f);
+      for (int a = 0; a < kBatch; ++a) {
+        const int j = b * kBatch + a;
+        const bool in = j < mine;
+        word w{};
+        if (in) w = data[slot(j)];
         if (in) {
-          if (MODE == kSlab) data[at] = w[a];
+          f32x2 f[NP];
+          L::unpack(w, f);
 #pragma unroll
           for (int e = 0; e < NP; ++e) {
             const f32x2 t = add_f32x2(f[e], s[e]);
@@ -376,12 +420,13 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
             fma_f32x2(q[e], t, t);
           }
         }
-        at += dstep;
         if constexpr (KEEP != kSrcFull) {  // lanes of a block of channels are neighbours; those without data bring zeros
-          const uint32_t m = block_max<T, V>(w[a], (1 << x8.shift) / V);
+          const uint32_t m = block_max<T, V>(w, (1 << x8.shift) / V);
           if (in) {
             float inv;
             const float sc = scale_of<KEEP>(m, &inv);
+            f32x2 f[NP];
+            L::unpack(w, f);
             *reinterpret_cast<typename L::codes*>(cp) = pack_codes<KEEP, V>(f, inv);
             if (scaler) *scp = sc;
           }
@@ -389,6 +434,7 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
           scp += (int64_t)k.rl * x8.nblk;
         }
       }
+      fetch(b + 2);
     }
 
     // the block's mean and squares of each group, from those of its channels
@@ -491,20 +537,15 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
       L::store(yp, k.vpr, p.nv, L::pack(f));
     };
     if constexpr (MODE == kSlab) {
-      int at = at0;
 #pragma unroll 2
-      for (int r = p.r; r < p.rows; r += k.rl, yp += ystep, at += dstep) put(data[at]);
+      for (int j = 0; j < mine; ++j, yp += ystep) put(data[at0 + j * dstep]);
     } else {
-      for (int r0 = p.r; r0 < p.rows; r0 += kAhead * k.rl) {
-        word w[kAhead];
+      for (int b = 0; b < batches; ++b) {
+        copies_wait<1>();
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a, xp += xstep) {
-          w[a] = word{};
-          if (r0 + a * k.rl < p.rows) w[a] = L::load(xp, k.vpr, p.nv);
-        }
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a, yp += ystep)
-          if (r0 + a * k.rl < p.rows) put(w[a]);
+        for (int a = 0; a < kBatch; ++a, yp += ystep)
+          if (b * kBatch + a < mine) put(data[slot(b * kBatch + a)]);
+        fetch(b + 2);
       }
     }
   }
@@ -518,13 +559,15 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
            T* __restrict__ gx, Sums sums) {
   typedef Lay<T, V, STR> L;
   typedef typename L::word word;
-  typedef Coded<SRC, L, V, STR> Code;
+  typedef Scales<V, STR> Scale;
   typedef typename std::conditional<SRC == kSrcFull, word, typename L::codes>::type xword;
   constexpr int NP = L::NP, W = 4 * NP;
   extern __shared__ __align__(16) unsigned char sm[];
   const Place p = place_of<V, STR>(g, k, MODE == kApply ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
   word* const gdata = reinterpret_cast<word*>(sm);
-  xword* const xdata = reinterpret_cast<xword*>(sm + (size_t)k.rows * k.vpr * sizeof(word));
+  const int slots = MODE == kSlab ? k.rows * k.vpr : 2 * kBatch * kNT;
+  xword* const xdata = reinterpret_cast<xword*>(gdata + slots);
+  Scale* const sdata = reinterpret_cast<Scale*>(xdata + slots);  // a checkpoint's
   float* const red = reinterpret_cast<float*>(sm + k.data_bytes);
   float* const tot = red + kNT * W;                                 // sums of du and of du * xh per channel
   float2* const part = reinterpret_cast<float2*>(tot + k.vpr * W);  // (s1, s2) of the block's groups
@@ -532,6 +575,40 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
   const int groups = p.S / g.D;
   int gi[V];
   groups_of<V, STR>(g, k, p, gi);
+
+  const int64_t first = p.row0 + p.r;
+  const T* gp = gy + first * g.ys + g.yo + p.c;
+  const int64_t gstep = k.rl * g.ys;
+  const T* xp = SRC == kSrcFull ? x + first * g.xs + g.xo + p.c : nullptr;
+  const int64_t xstep = k.rl * g.xs;
+  const uint8_t* cp = SRC == kSrcFull ? nullptr : x8.codes + first * g.C + p.c;
+  const int64_t cstep = (int64_t)k.rl * g.C;
+  // rows and slots as in the forward
+  const int at0 = p.r * k.vpr + p.vl, dstep = k.rl * k.vpr;
+  const int mine = p.nv > 0 && p.r < p.rows ? (p.rows - p.r + k.rl - 1) / k.rl : 0;
+  const int batches = ((p.rows + k.rl - 1) / k.rl + kBatch - 1) / kBatch;
+  auto slot = [&](int j) { return MODE == kSlab ? at0 + j * dstep : (j & (2 * kBatch - 1)) * kNT + (int)threadIdx.x; };
+  auto fetch = [&](int b) {
+#pragma unroll
+    for (int a = 0; a < kBatch; ++a) {
+      const int j = b * kBatch + a;
+      if (j < mine) {
+        L::fetch(gdata + slot(j), gp, k.vpr, p.nv);
+        if constexpr (SRC == kSrcFull) {
+          L::fetch(xdata + slot(j), xp, k.vpr, p.nv);
+        } else {
+          L::fetch_codes(xdata + slot(j), cp, k.vpr, p.nv);
+          Scale::fetch(sdata + slot(j), x8, first + (int64_t)j * k.rl, p.c, k.vpr, p.nv);
+        }
+      }
+      gp += gstep;
+      if constexpr (SRC == kSrcFull) xp += xstep;
+      else cp += cstep;
+    }
+    copies_commit();
+  };
+  fetch(0);
+  fetch(1);
 
   f32x2 ga[NP], be[NP], mu[NP], rs[NP];
   L::channels(gamma, p.c, k.vpr, p.nv, 1.f, ga);
@@ -552,29 +629,13 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
       }
     }
   }
-  const int64_t first = p.row0 + p.r;
-  const T* gp = gy + first * g.ys + g.yo + p.c;
-  const int64_t gstep = k.rl * g.ys;
-  const T* xp = SRC == kSrcFull ? x + first * g.xs + g.xo + p.c : nullptr;
-  const int64_t xstep = k.rl * g.xs;
-  const uint8_t* cp = SRC == kSrcFull ? nullptr : x8.codes + first * g.C + p.c;
-  const int64_t cstep = (int64_t)k.rl * g.C;
-  auto load_x = [&]() {
-    if constexpr (SRC == kSrcFull) {
-      return L::load(xp, k.vpr, p.nv);
-    } else {
-      return L::load_codes(cp, k.vpr, p.nv);
-    }
-  };
-  // xh and du of one vector, from what was stored
-  auto eval = [&](word gw, xword xw, const Code& code, f32x2* xh, f32x2* du) {
+  // xh and du of one vector, from its slot
+  auto eval = [&](int at, f32x2* xh, f32x2* du) {
     f32x2 t[NP];
     if constexpr (SRC == kSrcFull) {
-      L::unpack(xw, xh);
+      L::unpack(xdata[at], xh);
     } else {
-      Code c = code;
-      c.w = xw;
-      c.values(xh);
+      values_of<SRC, V, STR>(xdata[at], sdata[at], xh);
     }
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
@@ -583,55 +644,30 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
       t[e] = add_apart(mul_f32x2(xh[e], ga[e]), be[e]);
     }
     slope_p<NP>(g.act, t);
-    L::unpack(gw, du);
+    L::unpack(gdata[at], du);
 #pragma unroll
     for (int e = 0; e < NP; ++e) du[e] = mul_f32x2(du[e], t[e]);
   };
-  const int at0 = p.r * k.vpr + p.vl, dstep = k.rl * k.vpr;
-  constexpr int kAhead = V == 8 ? 2 : 4;
 
   if constexpr (MODE != kApply) {
-    // read, sum, keep
+    // sum
     f32x2 a[NP], b[NP];
 #pragma unroll
     for (int e = 0; e < NP; ++e) a[e] = b[e] = 0;
-    if (p.nv > 0) {
-      int at = at0;
-      for (int r0 = p.r; r0 < p.rows; r0 += kAhead * k.rl) {
-        word gw[kAhead];
-        xword xw[kAhead];
-        Code cd[kAhead];
+    for (int i = 0; i < batches; ++i) {
+      copies_wait<1>();
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          gw[i] = word{};
-          xw[i] = xword{};
-          const int r = r0 + i * k.rl;
-          if (r < p.rows) {
-            gw[i] = L::load(gp, k.vpr, p.nv);
-            xw[i] = load_x();
-            if (SRC != kSrcFull) cd[i].load_scales(x8, p.row0 + r, p.c, k.vpr, p.nv);
-          }
-          gp += gstep;
-          xp += xstep;
-          cp += cstep;
-        }
+      for (int h = 0; h < kBatch; ++h) {
+        if (i * kBatch + h >= mine) break;
+        f32x2 xh[NP], du[NP];
+        eval(slot(i * kBatch + h), xh, du);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (r0 + i * k.rl >= p.rows) break;
-          if (MODE == kSlab) {
-            gdata[at] = gw[i];
-            xdata[at] = xw[i];
-          }
-          at += dstep;
-          f32x2 xh[NP], du[NP];
-          eval(gw[i], xw[i], cd[i], xh, du);
-#pragma unroll
-          for (int e = 0; e < NP; ++e) {
-            a[e] = add_f32x2(a[e], du[e]);
-            fma_f32x2(b[e], du[e], xh[e]);
-          }
+        for (int e = 0; e < NP; ++e) {
+          a[e] = add_f32x2(a[e], du[e]);
+          fma_f32x2(b[e], du[e], xh[e]);
         }
       }
+      fetch(i + 2);
     }
     join_rows<NP>(k, a, b, red, tot);
     const int seg = lanes_of_group(g.D);
@@ -715,42 +751,22 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
       c3[e] = neg(mul_f32x2(pack_f32x2(u.y, v.y), rs[e]));
     }
     T* op = gx + first * g.xs + g.xo + p.c;
-    auto put = [&](word gw, xword xw, const Code& cd) {
+    auto put = [&](int at) {
       f32x2 xh[NP], du[NP];
-      eval(gw, xw, cd, xh, du);
+      eval(at, xh, du);
 #pragma unroll
       for (int e = 0; e < NP; ++e) du[e] = fma2(du[e], c1[e], fma2(xh[e], c3[e], c2[e]));
       L::store(op, k.vpr, p.nv, L::pack(du));
     };
     if constexpr (MODE == kSlab) {
-      int at = at0;
-      for (int r = p.r; r < p.rows; r += k.rl, op += xstep, at += dstep) {
-        Code cd;
-        if (SRC != kSrcFull) cd.load_scales(x8, p.row0 + r, p.c, k.vpr, p.nv);
-        put(gdata[at], xdata[at], cd);
-      }
+      for (int j = 0; j < mine; ++j, op += xstep) put(at0 + j * dstep);
     } else {
-      for (int r0 = p.r; r0 < p.rows; r0 += kAhead * k.rl) {
-        word gw[kAhead];
-        xword xw[kAhead];
-        Code cd[kAhead];
+      for (int i = 0; i < batches; ++i) {
+        copies_wait<1>();
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          gw[i] = word{};
-          xw[i] = xword{};
-          const int r = r0 + i * k.rl;
-          if (r < p.rows) {
-            gw[i] = L::load(gp, k.vpr, p.nv);
-            xw[i] = load_x();
-            if (SRC != kSrcFull) cd[i].load_scales(x8, p.row0 + r, p.c, k.vpr, p.nv);
-          }
-          gp += gstep;
-          xp += xstep;
-          cp += cstep;
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i, op += xstep)
-          if (r0 + i * k.rl < p.rows) put(gw[i], xw[i], cd[i]);
+        for (int h = 0; h < kBatch; ++h, op += xstep)
+          if (i * kBatch + h < mine) put(slot(i * kBatch + h));
+        fetch(i + 2);
       }
     }
   }
@@ -761,7 +777,7 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
 
 template <typename... P, typename... A>
 cudaError_t launch(void (*kern)(P...), const Norm& g, const Plan& k, bool cluster, int pass, cudaStream_t s, A... args) {
-  const int smem = (cluster ? k.data_bytes : 0) + scratch_bytes(k, pass);
+  const int smem = k.data_bytes + scratch_bytes(k, pass);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
