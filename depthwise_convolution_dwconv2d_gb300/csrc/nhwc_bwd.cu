@@ -145,6 +145,7 @@ template <typename T>
 __global__ void __launch_bounds__(kJoin)
 walk_join_kernel(int C, int taps, int chunks, const float* __restrict__ ws, T* __restrict__ gw, T* __restrict__ gb) {
   __shared__ float sm[kJoin];
+  wait_for_previous();
   const int tap = blockIdx.y;
   if (tap < taps ? gw == nullptr : gb == nullptr) return;
   const int ch = blockIdx.x * 32 + (threadIdx.x & 31);
@@ -280,9 +281,8 @@ cudaError_t walked(const Conv& c, const T* x, const Act8& t, const T* gy, const 
   }
   if (e == cudaErrorNotSupported) e = direct<T>(c, x, t, gy, w, gx, want_gw, accumulate, ws, s, &chunks);
   if (e != cudaSuccess || !want_gw) return e;
-  walk_join_kernel<T><<<dim3((unsigned)((c.C + 31) / 32), (unsigned)(taps + 1)), kJoin, 0, s>>>((int)c.C, taps, chunks,
-                                                                                               ws, gw, gb);
-  return cudaGetLastError();
+  return launch_dependent(walk_join_kernel<T>, dim3((unsigned)((c.C + 31) / 32), (unsigned)(taps + 1)), dim3(kJoin), 0, s,
+                          (int)c.C, taps, chunks, (const float*)ws, gw, gb);
 }
 
 }  // namespace

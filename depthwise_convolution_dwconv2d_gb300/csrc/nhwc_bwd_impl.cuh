@@ -348,6 +348,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
   constexpr int XP = kCode ? 2 * CT : GP;                 // of x
   extern __shared__ __align__(16) unsigned char smdyn[];
   __shared__ __align__(8) uint64_t full[kMaxStages];
+  dependents_may_start();
   const int base = (int)((128 - (tma::smem_u32(smdyn) & 127)) & 127);
   const uint32_t sm0 = tma::smem_u32(smdyn) + base;
   const int tile = blockIdx.x % g.tiles, chunk = blockIdx.x / g.tiles;
@@ -689,6 +690,7 @@ __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const 
   constexpr int GP = 2 * CT * (int)sizeof(T), XP = kCode ? 2 * CT : GP;
   extern __shared__ __align__(16) unsigned char smdyn[];
   __shared__ __align__(8) uint64_t full[kMaxStages];
+  dependents_may_start();
   const int base = (int)((128 - (tma::smem_u32(smdyn) & 127)) & 127);
   const uint32_t sm0 = tma::smem_u32(smdyn) + base;
   const int tile = blockIdx.x % g.tiles, chunk = blockIdx.x / g.tiles;

@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(kNT)
 param_grad_kernel(int C, int64_t entries, const float2* __restrict__ part, T* __restrict__ ggamma,
                   T* __restrict__ gbeta) {
   __shared__ float2 sm[kNT];
+  wait_for_previous();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31);
   float a = 0.f, b = 0.f;
   if (c < C) {
@@ -495,7 +496,7 @@ bool plan_cluster(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   const int64_t units = g.N * k->slices, row = k->vpr * vector_bytes(*k, es, x_bytes);
   auto rows = [&](int parts) { return (g.P + parts - 1) / parts; };
   int parts = 1;
-  while (parts < 8 && rows(parts) * row > 44 * 1024) parts *= 2;
+  while (parts < 8 && rows(parts) * row > 64 * 1024) parts *= 2;
   while (parts < 8 && units * parts < 304 && rows(parts) > 2 * k->rl) parts *= 2;
   if (rows(parts) * row > 180 * 1024 || units * parts >= (int64_t(1) << 31)) return false;
   k->parts = parts;
@@ -504,14 +505,16 @@ bool plan_cluster(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   return k->data_bytes + slab::scratch_bytes(*k, x_bytes ? 1 : 0) <= 220 * 1024;
 }
 
+constexpr int kStreamBlocks = 6;
+
 // Chunks of pixels for the stream kernels: about six blocks per SM, at least
 // eight rows for a row lane.
 bool plan_stream(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   const int64_t units = g.N * k->slices;
-  int64_t parts = (152 * 6 + units - 1) / units;
+  int64_t parts = (152 * kStreamBlocks + units - 1) / units;
   const int64_t most = (g.P + 8 * k->rl - 1) / (8 * k->rl);
   if (parts > most) parts = most;
-  if (parts > 256) parts = 256;
+  if (parts > slab::kMaxParts) parts = slab::kMaxParts;
   const int64_t rows = (g.P + parts - 1) / parts;
   if (rows >= (int64_t(1) << 31)) return false;
   k->rows = (int)rows;
@@ -529,15 +532,13 @@ Family plan_family(const Norm& g, int V, bool strided, int es, int keep, int x_b
   return plan_stream(g, es, x_bytes, k) ? kStream : kSplit;
 }
 
-constexpr int kBwdV = 8;  // the most channels of a thread in the backward
-
 // How a thread's channels lie: the widest access that distances, offsets and
 // pointers allow (16 bytes; 8 for 16-bit types), or four channels apart.
-void layout_of(const Norm& g, int es, int pass, const void* a, const void* b, const void* c, const void* codes, int* V,
+void layout_of(const Norm& g, int es, int widest, const void* a, const void* b, const void* c, const void* codes, int* V,
                bool* strided) {
   for (int bytes : {16, 8}) {
     *V = bytes / es;
-    if (*V < 4 || (pass == 1 && *V > kBwdV)) continue;
+    if (*V < 4 || *V > widest) continue;
     auto fits = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
     if (g.C % *V == 0 && g.xs % *V == 0 && g.xo % *V == 0 && g.ys % *V == 0 && g.yo % *V == 0 && fits(a) && fits(b) &&
         fits(c) && reinterpret_cast<uintptr_t>(codes) % *V == 0) {
@@ -558,7 +559,7 @@ const char* plan_name(const Norm& g, int pass) {
   int V;
   bool strided;
   slab::Plan k;
-  layout_of(g, es, pass, nullptr, nullptr, nullptr, nullptr, &V, &strided);
+  layout_of(g, es, pass ? 4 : 8, nullptr, nullptr, nullptr, nullptr, &V, &strided);
   const Family f = plan_family(g, V, strided, es, 0, pass ? es : 0, &k);
   return f == kSlabs ? "slab" : f == kStream ? "stream" : "split";
 }
@@ -597,7 +598,7 @@ cudaError_t fwd_any(const Norm& g, const T* x, const T* gamma, const T* beta, T*
   const int es = sizeof(T), block = x8.codes ? 1 << x8.shift : 0;
   int V;
   bool strided;
-  layout_of(g, es, 0, x, y, nullptr, x8.codes, &V, &strided);
+  layout_of(g, es, 8, x, y, nullptr, x8.codes, &V, &strided);
   const slab::Sums sums{reinterpret_cast<float2*>(ws), nullptr};
   slab::Plan k;
   Family f = block ? plan_family(g, V, strided, es, block, 0, &k) : kSplit;
@@ -626,7 +627,9 @@ cudaError_t bwd_any(const Norm& g, const T* x, const Act8& x8, const T* gy, cons
   const int es = sizeof(T);
   int V;
   bool strided;
-  layout_of(g, es, 1, x, gy, gx, x8.codes, &V, &strided);
+  // eight channels of x and gy in full take 125 registers and two blocks per SM, four 80 and three: 45 against 39 us at
+  // 64x28x28x256 bf16; from codes eight are faster, 125 against 137 us for the step at 64x56x56x128
+  layout_of(g, es, x ? 4 : 8, x, gy, gx, x8.codes, &V, &strided);
   slab::Plan k;
   const Family f = plan_family(g, V, strided, es, 0, x ? es : 1, &k);
   if (f != kSplit) {
@@ -636,8 +639,8 @@ cudaError_t bwd_any(const Norm& g, const T* x, const Act8& x8, const T* gy, cons
     sums.groups = sums.channels + g.N * parts * g.C;
     const cudaError_t e = slab::run_bwd<T>(g, k, f == kSlabs, x, x8, gy, gamma, beta, mean, rstd, gx, sums, s);
     if (e != cudaSuccess || (!ggamma && !gbeta)) return e;
-    param_grad_kernel<T><<<(g.C + 31) / 32, kNT, 0, s>>>(g.C, g.N * parts, sums.channels, ggamma, gbeta);
-    return cudaGetLastError();
+    return launch_dependent(param_grad_kernel<T>, dim3((g.C + 31) / 32), dim3(kNT), 0, s, g.C, (int64_t)(g.N * parts),
+                            (const float2*)sums.channels, ggamma, gbeta);
   }
   constexpr int VV = Vec<T>::n;
   return V == VV && !strided ? bwd_src<T, VV>(g, x, x8, gy, gamma, beta, mean, rstd, gx, ggamma, gbeta, ws, s)

@@ -9,6 +9,7 @@ namespace norm {
 namespace slab {
 
 constexpr int kNT = 256;
+constexpr int kMaxParts = 256;  // chunks of a stream
 constexpr int kBatch = 4;  // rows that a thread fetches at a time; the next batch is on its way
 
 // How a thread's V channels lie: side by side, one access of V elements; or a

@@ -59,6 +59,7 @@ __device__ __forceinline__ void copy_async(W* dst, const void* src) {
   }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 template <int LEFT>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
@@ -287,6 +288,14 @@ __device__ __forceinline__ float group_sum(float a, int seg) {
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync(int blocks) {
+  if (blocks == 1) {
+    __syncthreads();
+  } else {
+    cluster_arrive();
+    cluster_wait();
+  }
+}
 
 struct Place {
   int64_t n, row0;   // sample, first row of the block in the tensor
@@ -384,6 +393,11 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
   };
   fetch(0);
   fetch(1);
+  if (MODE != kApply) dependents_may_start();
+  if (p.nv > 0) {  // needed after the barriers
+    if (gamma) prefetch_l2(gamma + p.c);
+    if (beta) prefetch_l2(beta + p.c);
+  }
 
   if constexpr (MODE != kApply) {
     // read, sum, keep
@@ -482,8 +496,7 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
     }
   };
   if constexpr (MODE == kSlab) {
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync(k.parts);
     cg::cluster_group cluster = cg::this_cluster();
     for (int i = threadIdx.x; i < groups; i += kNT) {
       float a = 0.f, sq = 0.f;
@@ -497,15 +510,22 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
       finish(i, mean, sq);
     }
   } else {
+    wait_for_previous();
     const int lane = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < groups; i += kNT / 32) {
       const float2* o = gsums + p.n * k.parts * (int64_t)g.G + p.c0 / g.D + i;
+      float2 v[kMaxParts / 32];  // every part's, read at once
+#pragma unroll
+      for (int h = 0; h < kMaxParts / 32; ++h)
+        v[h] = lane + 32 * h < k.parts ? o[(int64_t)(lane + 32 * h) * g.G] : make_float2(0.f, 0.f);
       float a = 0.f, sq = 0.f;
-      for (int b = lane; b < k.parts; b += 32) a = fmaf(rows_of(g, k, b) * (float)g.D, o[(int64_t)b * g.G].x, a);
+#pragma unroll
+      for (int h = 0; h < kMaxParts / 32; ++h) a = fmaf(rows_of(g, k, lane + 32 * h) * (float)g.D, v[h].x, a);
       const float mean = group_sum(a, 32) / total;
-      for (int b = lane; b < k.parts; b += 32) {
-        const float2 v = o[(int64_t)b * g.G];
-        sq += fmaf(rows_of(g, k, b) * (float)g.D * (v.x - mean), v.x - mean, v.y);
+#pragma unroll
+      for (int h = 0; h < kMaxParts / 32; ++h) {
+        const float n = rows_of(g, k, lane + 32 * h) * (float)g.D;
+        sq += n > 0.f ? fmaf(n * (v[h].x - mean), v[h].x - mean, v[h].y) : 0.f;
       }
       sq = group_sum(sq, 32);
       if (lane == 0) finish(i, mean, sq);
@@ -609,6 +629,7 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
   };
   fetch(0);
   fetch(1);
+  if (MODE != kApply) dependents_may_start();
 
   f32x2 ga[NP], be[NP], mu[NP], rs[NP];
   L::channels(gamma, p.c, k.vpr, p.nv, 1.f, ga);
@@ -698,8 +719,7 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
 
   const float inv = 1.f / ((float)g.P * (float)g.D);
   if constexpr (MODE == kSlab) {
-    cluster_arrive();
-    cluster_wait();
+    cluster_sync(k.parts);
     cg::cluster_group cluster = cg::this_cluster();
     for (int i = threadIdx.x; i < groups; i += kNT) {
       float s1 = 0.f, s2 = 0.f;
@@ -723,12 +743,15 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
       sums.channels[p.n * g.C + p.c0 + c] = make_float2(s1, s2);
     }
   } else {
+    wait_for_previous();
     const int lane = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < groups; i += kNT / 32) {
       const float2* o = sums.groups + p.n * k.parts * (int64_t)g.G + p.c0 / g.D + i;
       float s1 = 0.f, s2 = 0.f;
-      for (int j = lane; j < k.parts; j += 32) {
-        const float2 v = o[(int64_t)j * g.G];
+#pragma unroll
+      for (int h = 0; h < kMaxParts / 32; ++h) {
+        if (lane + 32 * h >= k.parts) continue;
+        const float2 v = o[(int64_t)(lane + 32 * h) * g.G];
         s1 += v.x;
         s2 += v.y;
       }
@@ -775,19 +798,23 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
 
 // ---- launches --------------------------------------------------------------
 
+// cluster: a slab's blocks; dependent: after the sums of the same call
 template <typename... P, typename... A>
-cudaError_t launch(void (*kern)(P...), const Norm& g, const Plan& k, bool cluster, int pass, cudaStream_t s, A... args) {
+cudaError_t launch(void (*kern)(P...), const Norm& g, const Plan& k, bool cluster, bool dependent, int pass,
+                   cudaStream_t s, A... args) {
   const int smem = k.data_bytes + scratch_bytes(k, pass);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
+  const dim3 grid((unsigned)(g.N * k.slices * k.parts));
+  if (dependent) return launch_dependent(kern, grid, dim3(kNT), (size_t)smem, s, args...);
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = (unsigned)k.parts;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(g.N * k.slices * k.parts));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kNT);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
@@ -801,34 +828,34 @@ template <typename T, int V, bool STR>
 cudaError_t fwd_of(const Norm& g, const Plan& k, bool slab, const T* x, const T* gamma, const T* beta, T* y, float* mean,
                    float* rstd, const Act8& x8, const Sums& sums, cudaStream_t s) {
   const int keep = x8.codes ? x8.src : kSrcFull;
-  auto one = [&](auto kern, bool cluster) {
-    return launch(kern, g, k, cluster, 0, s, g, k, x, gamma, beta, y, mean, rstd, x8, sums.groups);
+  auto one = [&](auto kern, bool cluster, bool dependent) {
+    return launch(kern, g, k, cluster, dependent, 0, s, g, k, x, gamma, beta, y, mean, rstd, x8, sums.groups);
   };
   cudaError_t e = cudaErrorInvalidValue;
 #define X(KEEP)                                                              \
-  if (keep == KEEP) e = slab ? one(fwd_kernel<T, V, STR, KEEP, kSlab>, true) \
-                             : one(fwd_kernel<T, V, STR, KEEP, kSums>, false);
+  if (keep == KEEP) e = slab ? one(fwd_kernel<T, V, STR, KEEP, kSlab>, true, false) \
+                             : one(fwd_kernel<T, V, STR, KEEP, kSums>, false, false);
   X(kSrcFull)
   if constexpr (!STR) {
     X(kSrcI8) X(kSrcE4M3)
   }
 #undef X
   if (slab || e != cudaSuccess) return e;
-  return one(fwd_kernel<T, V, STR, kSrcFull, kApply>, false);
+  return one(fwd_kernel<T, V, STR, kSrcFull, kApply>, false, true);
 }
 
 template <typename T, int V, bool STR>
 cudaError_t bwd_of(const Norm& g, const Plan& k, bool slab, const T* x, const Act8& x8, const T* gy, const T* gamma,
                    const T* beta, const float* mean, const float* rstd, T* gx, const Sums& sums, cudaStream_t s) {
   const int src = x ? kSrcFull : x8.src;
-  auto one = [&](auto kern, bool cluster) {
-    return launch(kern, g, k, cluster, 1, s, g, k, x, x8, gy, gamma, beta, mean, rstd, gx, sums);
+  auto one = [&](auto kern, bool cluster, bool dependent) {
+    return launch(kern, g, k, cluster, dependent, 1, s, g, k, x, x8, gy, gamma, beta, mean, rstd, gx, sums);
   };
 #define X(SRC)                                                               \
   if (src == SRC) {                                                          \
-    if (slab) return one(bwd_kernel<T, V, STR, SRC, kSlab>, true);           \
-    const cudaError_t e = one(bwd_kernel<T, V, STR, SRC, kSums>, false);     \
-    return e != cudaSuccess || !gx ? e : one(bwd_kernel<T, V, STR, SRC, kApply>, false); \
+    if (slab) return one(bwd_kernel<T, V, STR, SRC, kSlab>, true, false);           \
+    const cudaError_t e = one(bwd_kernel<T, V, STR, SRC, kSums>, false, false);     \
+    return e != cudaSuccess || !gx ? e : one(bwd_kernel<T, V, STR, SRC, kApply>, false, true); \
   }
   X(kSrcFull) X(kSrcI8) X(kSrcE4M3)
 #undef X

@@ -401,9 +401,10 @@ dwconv_status_t dwconv2d_group_norm_nhwc_bwd(const dwconv2d_norm_desc_t* desc, c
                                              size_t workspace_bytes, const dwconv_act8_t* x8,
                                              cudaStream_t stream);
 
-/* Kernel family of the norm's pass (0 forward, 1 backward): "slab" (one read
- * of the inputs, kept in the shared memory of a cluster of thread blocks),
- * "split" (statistics, then a second read) or "invalid". Host only. */
+/* Kernel family of the norm's pass (0 forward, 1 backward) for aligned
+ * pointers: "slab" (one read of the inputs, kept in the shared memory of a
+ * cluster of thread blocks), "stream" (sums, then a second read), "split"
+ * (the same for slices wider than a thread block) or "invalid". Host only. */
 const char* dwconv2d_group_norm_nhwc_plan_name(const dwconv2d_norm_desc_t* desc, int pass);
 
 /* Bytes of device workspace dwconv2d_bwd_nhwc needs (0 if the descriptor is
