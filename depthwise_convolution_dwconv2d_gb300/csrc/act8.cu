@@ -65,34 +65,61 @@ __global__ void __launch_bounds__(kNT) encode_kernel(EGeom g, const T* __restric
   }
 }
 
-// One warp per block of channels, neighbouring lanes on neighbouring channels.
+// The blocks of channels of a warp: kWarpBlocks at a time, `step` of them
+// further each time, as (row, block of the row) without a division per block.
+constexpr int kWarpBlocks = 4;
+struct BlockWalk {
+  int64_t b, row;
+  int blk;
+  __device__ __forceinline__ void to(int64_t block, int nblk) {
+    b = block;
+    row = block / nblk;
+    blk = (int)(block - row * nblk);
+  }
+  __device__ __forceinline__ void next(int nblk) {
+    ++b;
+    if (++blk == nblk) {
+      blk = 0;
+      ++row;
+    }
+  }
+};
+
+// A block of channels per warp, neighbouring lanes on neighbouring channels.
 template <typename T, int SRC>
 __global__ void __launch_bounds__(kNT)
 encode_elem_kernel(int64_t rows, int C, int64_t ldx, const T* __restrict__ x, Act8 t) {
   const int lane = threadIdx.x & 31;
   const int64_t blocks = rows * t.nblk;
-  const int64_t step = (int64_t)gridDim.x * (kNT / 32);
-  for (int64_t b = blockIdx.x * (int64_t)(kNT / 32) + (threadIdx.x >> 5); b < blocks; b += step) {
-    const int64_t row = b / t.nblk;
-    const int c0 = (int)(b - row * t.nblk) << t.shift;
-    const int n = min(C - c0, 1 << t.shift);
-    float f[4];
-    uint32_t m = 0;
+  const int64_t step = (int64_t)gridDim.x * (kNT / 32) * kWarpBlocks;
+  BlockWalk w;
+  for (int64_t b = (blockIdx.x * (int64_t)(kNT / 32) + (threadIdx.x >> 5)) * kWarpBlocks; b < blocks; b += step) {
+    float f[kWarpBlocks][4];
+    w.to(b, t.nblk);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = lane + 32 * j;
-      f[j] = c < n ? ld(x + row * ldx + c0 + c) : 0.f;
-      m = max(m, abs_bits(f[j]));
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
-    float inv;
-    const float s = scale_of<SRC>(m, &inv);
+    for (int u = 0; u < kWarpBlocks; ++u, w.next(t.nblk)) {
+      const int c0 = w.blk << t.shift, n = w.b < blocks ? min(C - c0, 1 << t.shift) : 0;
+      const T* p = x + w.row * ldx + c0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = lane + 32 * j;
-      if (c < n) t.codes[row * C + c0 + c] = encode1<SRC>(f[j], inv);
+      for (int j = 0; j < 4; ++j) f[u][j] = lane + 32 * j < n ? ld(p + lane + 32 * j) : 0.f;
     }
-    if (lane == 0) t.scales[b] = s;
+    w.to(b, t.nblk);
+#pragma unroll
+    for (int u = 0; u < kWarpBlocks; ++u, w.next(t.nblk)) {
+      if (w.b >= blocks) break;
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = max(m, abs_bits(f[u][j]));
+      m = __reduce_max_sync(0xffffffffu, m);
+      float inv;
+      const float s = scale_of<SRC>(m, &inv);
+      const int c0 = w.blk << t.shift, n = min(C - c0, 1 << t.shift);
+      uint8_t* q = t.codes + w.row * C + c0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (lane + 32 * j < n) q[lane + 32 * j] = encode1<SRC>(f[u][j], inv);
+      if (lane == 0) t.scales[w.b] = s;
+    }
   }
 }
 
@@ -140,14 +167,29 @@ __global__ void __launch_bounds__(kNT)
 decode_elem_kernel(int64_t rows, int C, int64_t ldx, Act8 t, T* __restrict__ x) {
   const int lane = threadIdx.x & 31;
   const int64_t blocks = rows * t.nblk;
-  const int64_t step = (int64_t)gridDim.x * (kNT / 32);
-  for (int64_t b = blockIdx.x * (int64_t)(kNT / 32) + (threadIdx.x >> 5); b < blocks; b += step) {
-    const int64_t row = b / t.nblk;
-    const int c0 = (int)(b - row * t.nblk) << t.shift;
-    const int n = min(C - c0, 1 << t.shift);
-    const float s = __ldg(t.scales + b);
-    for (int c = lane; c < n; c += 32)
-      x[row * ldx + c0 + c] = from_f<T>(__fmul_rn(code1<SRC>(t.codes[row * C + c0 + c]), s));
+  const int64_t step = (int64_t)gridDim.x * (kNT / 32) * kWarpBlocks;
+  BlockWalk w;
+  for (int64_t b = (blockIdx.x * (int64_t)(kNT / 32) + (threadIdx.x >> 5)) * kWarpBlocks; b < blocks; b += step) {
+    uint8_t v[kWarpBlocks][4];
+    float s[kWarpBlocks];
+    w.to(b, t.nblk);
+#pragma unroll
+    for (int u = 0; u < kWarpBlocks; ++u, w.next(t.nblk)) {
+      const int c0 = w.blk << t.shift, n = w.b < blocks ? min(C - c0, 1 << t.shift) : 0;
+      const uint8_t* p = t.codes + w.row * C + c0;
+      s[u] = n > 0 ? __ldg(t.scales + w.b) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[u][j] = lane + 32 * j < n ? __ldg(p + lane + 32 * j) : 0;
+    }
+    w.to(b, t.nblk);
+#pragma unroll
+    for (int u = 0; u < kWarpBlocks; ++u, w.next(t.nblk)) {
+      const int c0 = w.blk << t.shift, n = w.b < blocks ? min(C - c0, 1 << t.shift) : 0;
+      T* p = x + w.row * ldx + c0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (lane + 32 * j < n) p[lane + 32 * j] = from_f<T>(__fmul_rn(code1<SRC>(v[u][j]), s[u]));
+    }
   }
 }
 
@@ -158,7 +200,7 @@ bool vec_ok(int64_t C, int64_t ldx, int es, const void* x, const Act8& t) {
 }
 
 unsigned elem_grid(int64_t blocks) {
-  const int64_t n = (blocks + kNT / 32 - 1) / (kNT / 32);
+  const int64_t n = (blocks + kNT / 32 * kWarpBlocks - 1) / (kNT / 32 * kWarpBlocks);
   return (unsigned)(n < 152 * 32 ? n : 152 * 32);
 }
 

@@ -489,6 +489,8 @@ int64_t vector_bytes(const slab::Plan& k, int es, int x_bytes) {
   return k.V * (es + x_bytes) + (x_bytes == 1 ? (k.strided ? 4 * k.V : 4) : 0);
 }
 
+constexpr int kFewRows = 8;
+
 // Clusters of up to eight blocks that hold a slab. Shares small enough for several blocks
 // per SM, whose reading and writing overlap; more blocks where the slabs are
 // too few for the GPU.
@@ -498,6 +500,7 @@ bool plan_cluster(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   int parts = 1;
   while (parts < 8 && rows(parts) * row > 64 * 1024) parts *= 2;
   while (parts < 8 && units * parts < 304 && rows(parts) > 2 * k->rl) parts *= 2;
+  if (units * parts < 152 && rows(parts) > kFewRows * k->rl) return false;  // too few blocks for so many rows: stream
   if (rows(parts) * row > 180 * 1024 || units * parts >= (int64_t(1) << 31)) return false;
   k->parts = parts;
   k->rows = (int)rows(parts);
@@ -505,14 +508,15 @@ bool plan_cluster(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   return k->data_bytes + slab::scratch_bytes(*k, x_bytes ? 1 : 0) <= 220 * 1024;
 }
 
-constexpr int kStreamBlocks = 6;
+constexpr int kStreamBlocks = 3;
 
-// Chunks of pixels for the stream kernels: about six blocks per SM, at least
-// eight rows for a row lane.
+// Chunks of pixels for the stream kernels: one wave of blocks (at
+// 2x256x256x64 fp32: 29 us at six blocks per SM, 27 at four, 23 at three), at
+// least four rows for a row lane.
 bool plan_stream(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   const int64_t units = g.N * k->slices;
   int64_t parts = (152 * kStreamBlocks + units - 1) / units;
-  const int64_t most = (g.P + 8 * k->rl - 1) / (8 * k->rl);
+  const int64_t most = (g.P + 4 * k->rl - 1) / (4 * k->rl);
   if (parts > most) parts = most;
   if (parts > slab::kMaxParts) parts = slab::kMaxParts;
   const int64_t rows = (g.P + parts - 1) / parts;
