@@ -479,6 +479,12 @@ bool plan_slices(const Norm& g, int V, bool strided, int es, int keep, slab::Pla
   k.rl = slab::kNT / k.vpr;
   k.slices = (int)((g.C + S - 1) / S);
   k.groups = (int)(S / g.D);
+  k.d_vpr = FastDiv((uint32_t)k.vpr);
+  k.d_slices = FastDiv((uint32_t)k.slices);
+  k.d_D = FastDiv((uint32_t)g.D);
+  k.total = (float)g.P * (float)g.D;
+  k.inv_total = 1.f / k.total;
+  k.inv_D = 1.f / (float)g.D;
   *out = k;
   return true;
 }
@@ -503,6 +509,7 @@ bool plan_cluster(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   if (units * parts < 152 && rows(parts) > kFewRows * k->rl) return false;  // too few blocks for so many rows: stream
   if (rows(parts) * row > 180 * 1024 || units * parts >= (int64_t(1) << 31)) return false;
   k->parts = parts;
+  k->d_parts = FastDiv((uint32_t)parts);
   k->rows = (int)rows(parts);
   k->data_bytes = (int)((k->rows * row + 15) / 16 * 16);
   return k->data_bytes + slab::scratch_bytes(*k, x_bytes ? 1 : 0) <= 220 * 1024;
@@ -523,6 +530,7 @@ bool plan_stream(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   if (rows >= (int64_t(1) << 31)) return false;
   k->rows = (int)rows;
   k->parts = (int)((g.P + rows - 1) / rows);
+  k->d_parts = FastDiv((uint32_t)k->parts);
   k->data_bytes = (int)(2 * slab::kBatch * slab::kNT * vector_bytes(*k, es, x_bytes));
   return units * k->parts < (int64_t(1) << 31) &&
          k->data_bytes + slab::scratch_bytes(*k, x_bytes ? 1 : 0) <= 220 * 1024;

@@ -25,6 +25,8 @@ struct Plan {
   int groups;      // groups of a slice
   int parts;       // blocks of a sample's slice: a cluster (slab), or chunks of pixels (stream)
   int rows;        // pixels of a block
+  FastDiv d_vpr, d_slices, d_parts, d_D;
+  float total, inv_total, inv_D;   // values of a (sample, group), and reciprocals
   int data_bytes;  // shared memory for a slab block's share of the inputs, a stream block's two batches
 };
 

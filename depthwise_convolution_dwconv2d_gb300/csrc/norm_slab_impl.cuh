@@ -270,7 +270,7 @@ __device__ __forceinline__ void join_rows(const Plan& k, const f32x2* u, const f
 // where channel c of the slice lies in a table of W floats per vector
 template <int V, bool STR, int W>
 __device__ __forceinline__ int table_at(const Plan& k, int c) {
-  const int q = STR ? c / k.vpr : c / V;
+  const int q = STR ? (int)k.d_vpr.div((uint32_t)c) : c / V;
   return STR ? (c - q * k.vpr) * W + q : q * W + (c - q * V);
 }
 
@@ -301,6 +301,7 @@ struct Place {
   int64_t n, row0;   // sample, first row of the block in the tensor
   int part, rows;    // block of the slab, its rows (0: none)
   int c0, S;         // first channel and channels of the slice
+  int g0, groups;    // first group and groups of it
   int c, vl, r;      // this thread's first channel, vector and row lane
   int nv;            // its channels that exist
 };
@@ -308,22 +309,24 @@ struct Place {
 template <int V, bool STR>
 __device__ __forceinline__ Place place_of(const Norm& g, const Plan& k, uint32_t block) {
   Place p;
-  const uint32_t unit = block / k.parts;
-  p.part = (int)(block - unit * k.parts);
-  p.n = unit / k.slices;
-  const int slice = (int)(unit - (uint32_t)p.n * k.slices);
+  uint32_t unit, n, r;
+  p.part = (int)k.d_parts.divmod(block, unit);
+  const int slice = (int)k.d_slices.divmod(unit, n);
+  p.n = n;
   p.c0 = slice * k.S;
+  p.g0 = slice * k.groups;
   p.S = min(k.S, g.C - p.c0);
+  p.groups = p.S == k.S ? k.groups : (int)k.d_D.div((uint32_t)p.S);
   const int64_t r0 = (int64_t)p.part * k.rows;
   p.rows = (int)(r0 < g.P ? (g.P - r0 < k.rows ? g.P - r0 : k.rows) : 0);
   p.row0 = p.n * g.P + r0;
-  p.r = threadIdx.x / k.vpr;
-  p.vl = threadIdx.x - p.r * k.vpr;
+  p.vl = (int)k.d_vpr.divmod(threadIdx.x, r);
+  p.r = (int)r;
   p.c = p.c0 + (STR ? p.vl : p.vl * V);
   if (p.r >= k.rl) {
     p.nv = 0;
   } else if (STR) {
-    p.nv = p.vl < p.S ? min((p.S - p.vl + k.vpr - 1) / k.vpr, V) : 0;
+    p.nv = p.vl < p.S ? min((int)k.d_vpr.div((uint32_t)(p.S - p.vl + k.vpr - 1)), V) : 0;
   } else {
     p.nv = p.vl * V < p.S ? V : 0;
   }
@@ -335,10 +338,11 @@ template <int V, bool STR>
 __device__ __forceinline__ void groups_of(const Norm& g, const Plan& k, const Place& p, int* gi) {
   if (STR) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) gi[e] = e < p.nv ? (p.vl + e * k.vpr) / g.D : 0;
+    for (int e = 0; e < V; ++e) gi[e] = e < p.nv ? (int)k.d_D.div((uint32_t)(p.vl + e * k.vpr)) : 0;
   } else {
     const int first = p.nv > 0 ? p.vl * V : 0;
-    int q = first / g.D, r = first - q * g.D;
+    uint32_t uq;
+    int r = (int)k.d_D.divmod((uint32_t)first, uq), q = (int)uq;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       gi[e] = q;
@@ -352,8 +356,8 @@ __device__ __forceinline__ void groups_of(const Norm& g, const Plan& k, const Pl
 
 // rows of part j of a slab
 __device__ __forceinline__ float rows_of(const Norm& g, const Plan& k, int j) {
-  const int64_t r0 = (int64_t)j * k.rows;
-  return (float)(r0 < g.P ? min((int64_t)k.rows, g.P - r0) : 0);
+  const int64_t left = g.P - (int64_t)j * k.rows;
+  return (float)(left >= k.rows ? k.rows : left > 0 ? (int)left : 0);
 }
 
 template <typename T, int V, bool STR, int KEEP, int MODE>
@@ -372,7 +376,7 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
   float* const base = tot + k.vpr * W;                               // what the sums are about, per channel
   float2* const part = reinterpret_cast<float2*>(base + k.vpr * V);  // (mean, squares) of the block's groups
   float2* const stat = part + k.groups;                              // (mean, rstd) of the slab's
-  const int groups = p.S / g.D;
+  const int groups = p.groups;
   int gi[V];
   groups_of<V, STR>(g, k, p, gi);
   const T* xp = x + (p.row0 + p.r) * g.xs + g.xo + p.c;
@@ -469,7 +473,7 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
         channel(i * g.D + c, &m, &sq);
         a += m;
       }
-      const float mean = group_sum(a, seg) / (float)g.D;
+      const float mean = group_sum(a, seg) * k.inv_D;
       a = 0.f;
       for (int c = l; c < g.D && in_slice; c += seg) {
         channel(i * g.D + c, &m, &sq);
@@ -478,19 +482,18 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
       a = group_sum(a, seg);
       if (l == 0 && i < groups) {
         if (MODE == kSlab) part[i] = make_float2(mean, a);
-        else gsums[(p.n * k.parts + p.part) * g.G + p.c0 / g.D + i] = make_float2(mean, a);
+        else gsums[(p.n * k.parts + p.part) * g.G + p.g0 + i] = make_float2(mean, a);
       }
     }
     if constexpr (MODE == kSums) return;
   }
 
   // the slab's mean and rstd from its parts'
-  const float total = (float)g.P * (float)g.D;
   auto finish = [&](int i, float mean, float sq) {
-    const float rstd = 1.f / sqrtf(sq / total + g.eps);
+    const float rstd = 1.f / sqrtf(sq / k.total + g.eps);
     stat[i] = make_float2(mean, rstd);
     if (p.part == 0) {
-      const int64_t at = p.n * g.G + p.c0 / g.D + i;
+      const int64_t at = p.n * g.G + p.g0 + i;
       if (mean_out) mean_out[at] = mean;
       if (rstd_out) rstd_out[at] = rstd;
     }
@@ -498,22 +501,22 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
   if constexpr (MODE == kSlab) {
     cluster_sync(k.parts);
     cg::cluster_group cluster = cg::this_cluster();
-    for (int i = threadIdx.x; i < groups; i += kNT) {
-      float a = 0.f, sq = 0.f;
-      for (int b = 0; b < k.parts; ++b) a = fmaf(rows_of(g, k, b) * (float)g.D, cluster.map_shared_rank(part, b)[i].x, a);
-      const float mean = a / total;
-      for (int b = 0; b < k.parts; ++b) {
-        const float n = rows_of(g, k, b) * (float)g.D;
-        const float2 o = cluster.map_shared_rank(part, b)[i];
-        sq += n > 0.f ? fmaf(n * (o.x - mean), o.x - mean, o.y) : 0.f;
-      }
-      finish(i, mean, sq);
+    // a lane per block of the cluster, eight lanes per group
+    const int b = threadIdx.x & 7;
+    const float n = b < k.parts ? rows_of(g, k, b) * (float)g.D : 0.f;
+    for (int i0 = 0; i0 < groups; i0 += kNT / 8) {
+      const int i = i0 + (int)threadIdx.x / 8;
+      const bool in = i < groups && n > 0.f;
+      const float2 v = in ? cluster.map_shared_rank(part, b)[i] : make_float2(0.f, 0.f);
+      const float mean = group_sum(n * v.x, 8) / k.total;
+      const float sq = group_sum(in ? fmaf(n * (v.x - mean), v.x - mean, v.y) : 0.f, 8);
+      if (b == 0 && i < groups) finish(i, mean, sq);
     }
   } else {
     wait_for_previous();
     const int lane = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < groups; i += kNT / 32) {
-      const float2* o = gsums + p.n * k.parts * (int64_t)g.G + p.c0 / g.D + i;
+      const float2* o = gsums + p.n * k.parts * (int64_t)g.G + p.g0 + i;
       float2 v[kMaxParts / 32];  // every part's, read at once
 #pragma unroll
       for (int h = 0; h < kMaxParts / 32; ++h)
@@ -521,7 +524,7 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
       float a = 0.f, sq = 0.f;
 #pragma unroll
       for (int h = 0; h < kMaxParts / 32; ++h) a = fmaf(rows_of(g, k, lane + 32 * h) * (float)g.D, v[h].x, a);
-      const float mean = group_sum(a, 32) / total;
+      const float mean = group_sum(a, 32) / k.total;
 #pragma unroll
       for (int h = 0; h < kMaxParts / 32; ++h) {
         const float n = rows_of(g, k, lane + 32 * h) * (float)g.D;
@@ -592,7 +595,7 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
   float* const tot = red + kNT * W;                                 // sums of du and of du * xh per channel
   float2* const part = reinterpret_cast<float2*>(tot + k.vpr * W);  // (s1, s2) of the block's groups
   float2* const stat = part + k.groups;                             // of the slab's, over the count
-  const int groups = p.S / g.D;
+  const int groups = p.groups;
   int gi[V];
   groups_of<V, STR>(g, k, p, gi);
 
@@ -635,8 +638,8 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
   L::channels(gamma, p.c, k.vpr, p.nv, 1.f, ga);
   L::channels(beta, p.c, k.vpr, p.nv, 0.f, be);
   {
-    const float* m = mean + p.n * g.G + p.c0 / g.D;
-    const float* r = rstd + p.n * g.G + p.c0 / g.D;
+    const float* m = mean + p.n * g.G + p.g0;
+    const float* r = rstd + p.n * g.G + p.g0;
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
       mu[e] = both(-__ldg(m + gi[0]));
@@ -705,7 +708,7 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
       s2 = group_sum(s2, seg);
       if (l == 0 && i < groups) {
         if (MODE == kSlab) part[i] = make_float2(s1, s2);
-        else sums.groups[(p.n * k.parts + p.part) * g.G + p.c0 / g.D + i] = make_float2(s1, s2);
+        else sums.groups[(p.n * k.parts + p.part) * g.G + p.g0 + i] = make_float2(s1, s2);
       }
     }
     if constexpr (MODE == kSums) {
@@ -717,36 +720,35 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
     }
   }
 
-  const float inv = 1.f / ((float)g.P * (float)g.D);
   if constexpr (MODE == kSlab) {
     cluster_sync(k.parts);
     cg::cluster_group cluster = cg::this_cluster();
-    for (int i = threadIdx.x; i < groups; i += kNT) {
-      float s1 = 0.f, s2 = 0.f;
-      for (int j = 0; j < k.parts; ++j) {
-        const float2 o = cluster.map_shared_rank(part, j)[i];
-        s1 += o.x;
-        s2 += o.y;
-      }
-      stat[i] = make_float2(s1 * inv, s2 * inv);
+    // a lane per block of the cluster, eight lanes per group, then per channel of this block's share
+    const int b = threadIdx.x & 7;
+    for (int i0 = 0; i0 < groups; i0 += kNT / 8) {
+      const int i = i0 + (int)threadIdx.x / 8;
+      const float2 v = i < groups && b < k.parts ? cluster.map_shared_rank(part, b)[i] : make_float2(0.f, 0.f);
+      const float s1 = group_sum(v.x, 8), s2 = group_sum(v.y, 8);
+      if (b == 0 && i < groups) stat[i] = make_float2(s1 * k.inv_total, s2 * k.inv_total);
     }
-    // the slab's sums per channel, each block its share of the channels
-    const int share = (p.S + k.parts - 1) / k.parts, lo = p.part * share;
-    for (int c = lo + threadIdx.x; c < min(lo + share, p.S); c += kNT) {
-      const int t = table_at<V, STR, W>(k, c);
+    const int share = (int)k.d_parts.div((uint32_t)(p.S + k.parts - 1)), lo = p.part * share, hi = min(lo + share, p.S);
+    for (int c0 = lo; c0 < hi; c0 += kNT / 8) {
+      const int c = c0 + (int)threadIdx.x / 8;
       float s1 = 0.f, s2 = 0.f;
-      for (int j = 0; j < k.parts; ++j) {
-        const float* o = cluster.map_shared_rank(tot, j) + t;
-        s1 += o[0];
-        s2 += o[2 * NP];
+      if (c < hi && b < k.parts) {
+        const float* o = cluster.map_shared_rank(tot, b) + table_at<V, STR, W>(k, c);
+        s1 = o[0];
+        s2 = o[2 * NP];
       }
-      sums.channels[p.n * g.C + p.c0 + c] = make_float2(s1, s2);
+      s1 = group_sum(s1, 8);
+      s2 = group_sum(s2, 8);
+      if (b == 0 && c < hi) sums.channels[p.n * g.C + p.c0 + c] = make_float2(s1, s2);
     }
   } else {
     wait_for_previous();
     const int lane = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < groups; i += kNT / 32) {
-      const float2* o = sums.groups + p.n * k.parts * (int64_t)g.G + p.c0 / g.D + i;
+      const float2* o = sums.groups + p.n * k.parts * (int64_t)g.G + p.g0 + i;
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll
       for (int h = 0; h < kMaxParts / 32; ++h) {
@@ -757,7 +759,7 @@ bwd_kernel(Norm g, Plan k, const T* __restrict__ x, Act8 x8, const T* __restrict
       }
       s1 = group_sum(s1, 32);
       s2 = group_sum(s2, 32);
-      if (lane == 0) stat[i] = make_float2(s1 * inv, s2 * inv);
+      if (lane == 0) stat[i] = make_float2(s1 * k.inv_total, s2 * k.inv_total);
     }
   }
   __syncthreads();
