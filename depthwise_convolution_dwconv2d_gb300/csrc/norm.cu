@@ -497,22 +497,37 @@ int64_t vector_bytes(const slab::Plan& k, int es, int x_bytes) {
 
 constexpr int kFewRows = 8;
 
-// Clusters of up to eight blocks that hold a slab. Shares small enough for several blocks
-// per SM, whose reading and writing overlap; more blocks where the slabs are
-// too few for the GPU.
+// Clusters of up to eight blocks that hold a slab: the size whose blocks, in
+// whole waves of as many as an SM holds at a time, issue the fewest
+// instructions. A block costs about 900 per warp and 28 per element and row
+// lane (20 forward); an SM with one, two and three blocks issues at about
+// 0.25, 0.42 and 0.54 of its rate (ncu).
 bool plan_cluster(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   const int64_t units = g.N * k->slices, row = k->vpr * vector_bytes(*k, es, x_bytes);
-  auto rows = [&](int parts) { return (g.P + parts - 1) / parts; };
-  int parts = 1;
-  while (parts < 8 && rows(parts) * row > 64 * 1024) parts *= 2;
-  while (parts < 8 && units * parts < 304 && rows(parts) > 2 * k->rl) parts *= 2;
-  if (units * parts < 152 && rows(parts) > kFewRows * k->rl) return false;  // too few blocks for so many rows: stream
-  if (rows(parts) * row > 180 * 1024 || units * parts >= (int64_t(1) << 31)) return false;
-  k->parts = parts;
-  k->d_parts = FastDiv((uint32_t)parts);
-  k->rows = (int)rows(parts);
-  k->data_bytes = (int)((k->rows * row + 15) / 16 * 16);
-  return k->data_bytes + slab::scratch_bytes(*k, x_bytes ? 1 : 0) <= 220 * 1024;
+  const int pass = x_bytes ? 1 : 0, scratch = slab::scratch_bytes(*k, pass), most = pass && k->V == 8 ? 2 : 3;
+  double best = -1;
+  for (int parts = 1; parts <= 8; ++parts) {
+    const int64_t rows = (g.P + parts - 1) / parts;
+    if (parts > 1 && (rows < k->rl || rows * (parts - 1) >= g.P)) continue;  // a block without rows
+    const int64_t data = (rows * row + 15) / 16 * 16;
+    if (data + scratch > 220 * 1024 || units * parts >= (int64_t(1) << 31)) continue;
+    int64_t blocks = 226 * 1024 / (data + scratch + 1024);
+    if (blocks > most) blocks = most;
+    const int64_t here = units * parts, wave = 152 * blocks, waves = (here + wave - 1) / wave;
+    int64_t busy = (here + 151) / 152;  // blocks that the fullest SM holds at a time
+    if (busy > blocks) busy = blocks;
+    const double rate = busy == 1 ? 0.25 : busy == 2 ? 0.42 : 0.54;
+    const double lane_rows = (double)((rows + k->rl - 1) / k->rl);
+    const double cost = (double)waves * busy * (900 + (pass ? 28 : 20) * k->V * lane_rows) / rate;
+    if (best >= 0 && cost >= best) continue;
+    best = cost;
+    k->parts = parts;
+    k->rows = (int)rows;
+    k->data_bytes = (int)data;
+  }
+  if (best < 0) return false;
+  k->d_parts = FastDiv((uint32_t)k->parts);
+  return units * k->parts >= 152 || k->rows <= kFewRows * k->rl;  // too few blocks for so many rows: stream
 }
 
 constexpr int kStreamBlocks = 3;
