@@ -11,7 +11,7 @@
 // value decoded from it.
 #pragma once
 
-#include "common.cuh"
+#include "f32x2.cuh"
 
 namespace dwconv {
 

@@ -13,6 +13,7 @@
 
 #include "common.cuh"
 #include "nhwc.h"
+#include "nhwc_bwd.h"
 #include "norm.h"
 #include "plan.h"
 

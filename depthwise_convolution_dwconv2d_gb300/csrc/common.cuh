@@ -104,51 +104,6 @@ __device__ __forceinline__ void fma_f32x2(f32x2& d, f32x2 a, f32x2 b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
 
-// d = a * b and a + b on both lanes, each lane rounded by itself
-__device__ __forceinline__ f32x2 mul_f32x2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f32x2 add_f32x2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// a + b lane by lane, for an addend that is a packed product: the assembler
-// contracts mul.rn.f32x2 and add.rn.f32x2 into one rounding (seen in codes
-// next to a tie), which the scalar addition prevents.
-__device__ __forceinline__ f32x2 add_apart(f32x2 a, f32x2 b) {
-  float a0, a1, b0, b1;
-  unpack_f32x2(a, a0, a1);
-  unpack_f32x2(b, b0, b1);
-  return pack_f32x2(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
-}
-
-// Programmatic dependent launch: a kernel of a call may be brought up while
-// the call's kernel before it still runs. The later one waits (for that
-// kernel's end and its writes) before it touches what the earlier one writes;
-// launched without the attribute, the wait returns at once.
-__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... P, typename... A>
-inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 // plain (coherent) load for data this kernel may also write
 template <typename T> __device__ __forceinline__ float ld_rw(const T* p) { return to_f<T>(*p); }
 

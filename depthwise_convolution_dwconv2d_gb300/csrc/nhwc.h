@@ -1,8 +1,6 @@
-// Channels-last (NHWC) forward and backward: shape support and entry points
-// (nhwc.cu, nhwc_bwd.cu).
+// Channels-last (NHWC) forward: shape support and entry point (nhwc.cu).
 #pragma once
 
-#include "act8.cuh"
 #include "plan.h"
 
 // (K, S) combinations compiled for the tiled channels-last forward.
@@ -20,14 +18,6 @@ Algo plan(const Conv& c);
 // x [N, H, W, C], y [N, Ho, Wo, ctot] (channels [off, off + C*m) written).
 cudaError_t fwd(const Conv& c, const void* x, const void* w, const void* b, void* y, cudaStream_t s,
                 const Epi& ep);
-
-// Backward (nhwc_bwd.cu): Algo::Nhwc for the row-walking kernel.
-Algo plan_bwd(const Conv& c);
-size_t bwd_workspace_bytes(const Conv& c);
-// gx [N, H, W, C], gw [C*m, kh, kw], gb [C*m], each or null; the input is x,
-// or x8 where x is null.
-cudaError_t bwd(const Conv& c, const void* x, const Act8& x8, const void* gy, const void* w, void* gx, void* gw,
-                void* gb, bool accumulate, float* ws, cudaStream_t s);
 
 }  // namespace nhwc
 

@@ -9,6 +9,7 @@
 // filters; the generic kernels here serve every descriptor: gx with one value
 // per thread, gw with one block per (channels, tap, chunk of output pixels)
 // and partial sums that a second launch adds in chunk order.
+#include "dependent.cuh"
 #include "nhwc_bwd.h"
 #include "vec.cuh"
 

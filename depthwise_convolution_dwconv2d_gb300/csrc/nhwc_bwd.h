@@ -2,10 +2,20 @@
 // (nhwc_bwd.cu, nhwc_bwd_impl.cuh).
 #pragma once
 
+#include "act8.cuh"
 #include "nhwc.h"
 
 namespace dwconv {
 namespace nhwc {
+
+// Algo::Nhwc for the row-walking kernels, Algo::Generic otherwise.
+Algo plan_bwd(const Conv& c);
+size_t bwd_workspace_bytes(const Conv& c);
+// gx [N, H, W, C], gw [C*m, kh, kw], gb [C*m], each or null; the input is x,
+// or x8 where x is null.
+cudaError_t bwd(const Conv& c, const void* x, const Act8& x8, const void* gy, const void* w, void* gx, void* gw,
+                void* gb, bool accumulate, float* ws, cudaStream_t s);
+
 namespace walk {
 
 constexpr int kRingThreads = 256, kRingBlocks = 2;     // threads of a block, blocks per SM: 3x3 filters

@@ -26,6 +26,7 @@
 
 #include <type_traits>
 
+#include "dependent.cuh"
 #include "nhwc_bwd.h"
 #include "tma.cuh"
 #include "vec.cuh"
@@ -413,7 +414,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
     tma::mbar_expect_tx(&full[p_slot], (uint32_t)(g.gy_bytes + (g.want_x ? g.x_bytes : 0)));
     tma::load_4d(slot, &map_gy, ch0, p_it.v0 / S - D, p_t, p_it.n0, &full[p_slot]);
     if (g.want_x)
-      tma::load_4d(slot + g.x_at, &map_x, ch0, p_it.v0 - c.pw, p_t * S - c.ph, p_it.n0, &full[p_slot]);
+      tma::load_4d(slot + g.x_at, &map_x, kCode ? ch0 / 2 : ch0, p_it.v0 - c.pw, p_t * S - c.ph, p_it.n0, &full[p_slot]);
     p_slot = p_slot + 1 == g.stages ? 0 : p_slot + 1;
     p_t += RD;
     if (p_t >= p_it.te) {
@@ -731,7 +732,7 @@ __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const 
     tma::fence_async_smem();
     tma::mbar_expect_tx(&full[p_slot], (uint32_t)(g.gy_bytes + (bring_x ? g.x_bytes : 0)));
     tma::load_4d(slot, map_gy, ch0, it.v0 / S - D, it.tb - D, it.n0, &full[p_slot]);
-    if (bring_x) tma::load_4d(slot + g.x_at, map_x, ch0, it.v0 - c.pw, it.tb * S - c.ph, it.n0, &full[p_slot]);
+    if (bring_x) tma::load_4d(slot + g.x_at, map_x, kCode ? ch0 / 2 : ch0, it.v0 - c.pw, it.tb * S - c.ph, it.n0, &full[p_slot]);
     p_slot = p_slot + 1 == g.stages ? 0 : p_slot + 1;
     p_item += g.chunks;
   };
@@ -894,12 +895,14 @@ cudaError_t launch_staged(const Conv& c, const Staged& g, const Views& v, const 
   const uint64_t gd[4] = {(uint64_t)c.C, (uint64_t)c.Wo, (uint64_t)c.Ho, (uint64_t)c.N};
   const uint64_t gs[3] = {(uint64_t)v.gdist, (uint64_t)(c.Wo * v.gdist), (uint64_t)(c.Ho * c.Wo * v.gdist)};
   const uint32_t gb[4] = {2 * CT, (uint32_t)g.gc, (uint32_t)g.grows, (uint32_t)g.ns};
-  const uint64_t xd[4] = {(uint64_t)c.C, (uint64_t)c.W, (uint64_t)c.H, (uint64_t)c.N};
+  // codes go as 16-bit pairs (an odd last channel's partner is read and not used)
+  constexpr uint64_t kPer = SRC == kSrcFull ? 1 : 2;
+  const uint64_t xd[4] = {((uint64_t)c.C + kPer - 1) / kPer, (uint64_t)c.W, (uint64_t)c.H, (uint64_t)c.N};
   const uint64_t xs[3] = {(uint64_t)v.xdist, (uint64_t)(c.W * v.xdist), (uint64_t)(c.H * c.W * v.xdist)};
-  const uint32_t xb[4] = {2 * CT, (uint32_t)g.xc, (uint32_t)g.xrows, (uint32_t)g.ns};
+  const uint32_t xb[4] = {(uint32_t)(2 * CT / kPer), (uint32_t)g.xc, (uint32_t)g.xrows, (uint32_t)g.ns};
   if (!tma::encode_strided(&mg, v.gy, c.dtype, 4, gd, gs, gb)) return cudaErrorNotSupported;
   mx = mg;
-  if (g.want_x && !tma::encode_strided(&mx, v.x, SRC == kSrcFull ? c.dtype : tma::kBytes, 4, xd, xs, xb))
+  if (g.want_x && !tma::encode_strided(&mx, v.x, SRC == kSrcFull ? c.dtype : (int)DWCONV_F16, 4, xd, xs, xb))
     return cudaErrorNotSupported;
   unsigned int* to = tma::timeout_counter();
   if (!to) return cudaErrorNotSupported;

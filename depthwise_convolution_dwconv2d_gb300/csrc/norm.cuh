@@ -2,6 +2,7 @@
 // any source, the normalised value, activations and their slopes.
 #pragma once
 
+#include "dependent.cuh"
 #include "norm.h"
 #include "vec.cuh"
 

@@ -87,8 +87,7 @@ bool encode_strided(CUtensorMap* map, const void* base, int dtype, int rank, con
                     const uint64_t* strides, const uint32_t* box) {
   EncodeFn fn = encode_fn();
   if (!fn || rank < 1 || rank > 5) return false;
-  const CUtensorMapDataType dt = dtype == kBytes       ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                 : dtype == DWCONV_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+  const CUtensorMapDataType dt = dtype == DWCONV_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                  : dtype == DWCONV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   cuuint64_t d[5], st[4];

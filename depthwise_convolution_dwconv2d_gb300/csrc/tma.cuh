@@ -105,8 +105,6 @@ bool encode_4d(CUtensorMap* map, const void* base, int dtype, uint64_t cols, uin
 bool encode_3d_sw128(CUtensorMap* map, const void* base, int dtype, uint64_t cols, uint64_t rows,
                      uint64_t planes, uint32_t box_cols, uint32_t box_rows, uint32_t box_planes);
 
-constexpr int kBytes = -1;  // a dtype of encode_strided: 8-bit elements
-
 // Host: tiled tensor map of any rank (1..5) with explicit dimensions, byte
 // strides of dimensions 1.. (multiples of 16, in any order) and box.
 bool encode_strided(CUtensorMap* map, const void* base, int dtype, int rank, const uint64_t* dims,
