@@ -190,6 +190,7 @@ struct Copy {
   FastDiv d_vecs;   // 16-byte vectors of a pixel
 };
 __global__ void __launch_bounds__(kNT) align_kernel(Copy a, Copy b) {
+  dependents_may_start();
   const Copy& k = blockIdx.y == 0 ? a : b;
   const int64_t total = k.pixels * k.d_vecs.d;
   const uint8_t* const end = k.src + (k.pixels - 1) * k.from + k.bytes;
@@ -259,7 +260,7 @@ cudaError_t walked(const Conv& c, const T* x, const Act8& t, const T* gy, const 
     st.accumulate = accumulate;
     st.pair_out = c.C % 2 == 0 && reinterpret_cast<uintptr_t>(gx) % (2 * es) == 0;
     chunks = st.chunks;
-    walk::Views v{gy + c.off, src == kSrcFull ? (const void*)x : t.codes, c.ctot * es, c.C * xes};
+    walk::Views v{gy + c.off, src == kSrcFull ? (const void*)x : t.codes, c.ctot * es, c.C * xes, false};
     uint8_t* room = reinterpret_cast<uint8_t*>(ws) + (gcopy || xcopy ? sums_bytes(c, walk_chunks(c)) : 0);
     Copy job[2] = {};
     int jobs = 0;
@@ -277,6 +278,7 @@ cudaError_t walked(const Conv& c, const T* x, const Act8& t, const T* gy, const 
       const int64_t blocks = (most + kNT - 1) / kNT;
       align_kernel<<<dim3((unsigned)(blocks < 152 * 32 ? blocks : 152 * 32), (unsigned)jobs), kNT, 0, s>>>(job[0], job[1]);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      v.copied = true;
     }
     e = walk::run_staged<T>(c, st, src, v, t, w, gx, ws, s);
   }
@@ -401,7 +403,7 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
       if (band > 4 * step) continue;
       stage(&g, (int)band + D, (int)band * S);
       if (g.stage_bytes > room && band > step) continue;
-      if (g.stage_bytes > 200 * 1024) continue;
+      if (g.stage_bytes + 128 > kMostSmem) continue;
     }
     const int64_t items = groups * g.segs * bands;
     if (items >= (1 << 30)) break;
@@ -426,6 +428,7 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
     if (g.stages > 2) g.stages = 2;
   }
   if (g.stages > kMaxStages) g.stages = kMaxStages;
+  if (g.stages * g.stage_bytes + 128 > kMostSmem) return false;
   g.d_segs = FastDiv((uint32_t)g.segs);
   g.d_bands = FastDiv((uint32_t)g.bands);
   int64_t chunks = g.items < wave ? g.items : wave;

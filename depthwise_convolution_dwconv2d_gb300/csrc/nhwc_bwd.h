@@ -44,6 +44,7 @@ constexpr int kTileThreads = 128;
 constexpr int kStagedThreads = 128;  // the most threads of a block
 constexpr int kStagedBlocks = 4;     // blocks per SM
 constexpr int kMaxStages = 4;
+constexpr int kMostSmem = 208 * 1024;  // dynamic shared memory of a block at most
 struct Staged {
   int ct_log, tiles, chunks;
   int strips, segs, cs, ns;
@@ -75,6 +76,7 @@ cudaError_t run(const Conv& c, const Geom& g, bool pair, const T* x, const Act8&
 struct Views {
   const void *gy, *x;
   int64_t gdist, xdist;
+  bool copied;  // by a launch of this call
 };
 // cudaErrorNotSupported: a pointer or distance is no multiple of 16 bytes.
 template <typename T>

@@ -423,6 +423,7 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
       p_t = p_it.tb - D;
     }
   };
+  wait_for_previous();  // the aligned copies of the same call, where there are any
   if (threadIdx.x == 0)
     for (int i = 0; i < g.stages - 1; ++i) issue();
 
@@ -736,6 +737,7 @@ __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const 
     p_slot = p_slot + 1 == g.stages ? 0 : p_slot + 1;
     p_item += g.chunks;
   };
+  wait_for_previous();  // the aligned copies of the same call, where there are any
   if (threadIdx.x == 0)
     for (int i = 0; i < g.stages - 1; ++i) issue();
 
@@ -908,9 +910,12 @@ cudaError_t launch_staged(const Conv& c, const Staged& g, const Views& v, const 
   if (!to) return cudaErrorNotSupported;
   const int smem = g.stages * g.stage_bytes + 128;
   auto go = [&](auto kern, unsigned sides) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // one limit for every shape: calls from several threads do not lower each other's
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(g.tiles * g.chunks), sides), g.threads, smem, s>>>(c, g, mg, mx, x8, to, w, gx, ws);
+    const dim3 grid((unsigned)(g.tiles * g.chunks), sides);
+    if (v.copied) return launch_dependent(kern, grid, dim3(g.threads), (size_t)smem, s, c, g, mg, mx, x8, to, w, gx, ws);
+    kern<<<grid, g.threads, smem, s>>>(c, g, mg, mx, x8, to, w, gx, ws);
     return cudaGetLastError();
   };
   if constexpr (K == 3) {

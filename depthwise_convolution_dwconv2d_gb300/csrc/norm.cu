@@ -510,7 +510,7 @@ bool plan_cluster(const Norm& g, int es, int x_bytes, slab::Plan* k) {
     const int64_t rows = (g.P + parts - 1) / parts;
     if (parts > 1 && (rows < k->rl || rows * (parts - 1) >= g.P)) continue;  // a block without rows
     const int64_t data = (rows * row + 15) / 16 * 16;
-    if (data + scratch > 220 * 1024 || units * parts >= (int64_t(1) << 31)) continue;
+    if (data + scratch > slab::kMostSmem || units * parts >= (int64_t(1) << 31)) continue;
     int64_t blocks = 226 * 1024 / (data + scratch + 1024);
     if (blocks > most) blocks = most;
     const int64_t here = units * parts, wave = 152 * blocks, waves = (here + wave - 1) / wave;
@@ -548,7 +548,7 @@ bool plan_stream(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   k->d_parts = FastDiv((uint32_t)k->parts);
   k->data_bytes = (int)(2 * slab::kBatch * slab::kNT * vector_bytes(*k, es, x_bytes));
   return units * k->parts < (int64_t(1) << 31) &&
-         k->data_bytes + slab::scratch_bytes(*k, x_bytes ? 1 : 0) <= 220 * 1024;
+         k->data_bytes + slab::scratch_bytes(*k, x_bytes ? 1 : 0) <= slab::kMostSmem;
 }
 
 enum Family { kSlabs, kStream, kSplit };

@@ -9,6 +9,7 @@ namespace norm {
 namespace slab {
 
 constexpr int kNT = 256;
+constexpr int kMostSmem = 220 * 1024;  // dynamic shared memory of a block at most
 constexpr int kMaxParts = 256;  // chunks of a stream
 constexpr int kBatch = 4;  // rows that a thread fetches at a time; the next batch is on its way
 

@@ -806,7 +806,8 @@ cudaError_t launch(void (*kern)(P...), const Norm& g, const Plan& k, bool cluste
                    cudaStream_t s, A... args) {
   const int smem = k.data_bytes + scratch_bytes(k, pass);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // one limit for every shape: calls from several threads do not lower each other's
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
   }
   const dim3 grid((unsigned)(g.N * k.slices * k.parts));

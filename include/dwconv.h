@@ -417,10 +417,16 @@ size_t dwconv2d_bwd_nhwc_workspace_size(const dwconv2d_desc_t* desc);
  * channels-last. x may be given by its 8-bit checkpoint x8 instead (rows =
  * N*H*W). gx, gw and gbias may each be NULL; w is needed for gx, and exactly
  * one of x and x8 for gw. accumulate = 1 adds to gx, 0 overwrites it. The
- * workspace (16-byte aligned) is needed for gw and gbias. For N == 0 gw and
- * gbias become 0. Square 3x3, 5x5 and 7x7 filters with equal strides of 1 or
- * 2, dilation 1, one filter per channel and padding up to (k - 1) / 2 run on
- * a row-walking kernel; every other descriptor on generic kernels. */
+ * workspace (16-byte aligned, not used concurrently) is needed for gw and
+ * gbias. For N == 0 gw and gbias become 0. No output may overlap an input.
+ * Square 3x3, 5x5 and 7x7 filters with equal strides of 1 or 2, dilation 1,
+ * one filter per channel and padding up to (k - 1) / 2 run on row-walking
+ * kernels; from 32 channels on these stage rows with the tensor memory
+ * accelerator, which needs gy, x and their pixel distances on 16 bytes: where
+ * the descriptor's distances are not, one launch copies gy and x to aligned
+ * pixels in the workspace (its size includes them; for gx alone, without a
+ * workspace, and for pointers off 16 bytes, kernels with plain loads run).
+ * Every other descriptor runs on generic kernels. */
 dwconv_status_t dwconv2d_bwd_nhwc(const dwconv2d_desc_t* desc, const void* x, const void* gy,
                                   const void* w, void* gx, void* gw, void* gbias, void* workspace,
                                   size_t workspace_bytes, const dwconv_act8_t* x8, int accumulate,

@@ -294,6 +294,20 @@ def test_norm_variance_of_a_far_level(shape):
     R.within(rstd, rrstd, R.CHAIN * R.EPS32 * rrstd * (1 + (1000 * R.CHAIN * R.EPS32) ** 2), "f32", "rstd")
 
 
+@pytest.mark.parametrize("shape", [(2, 40, 40, 64, 4), (1, 200, 150, 8, 1), (2, 21, 20, 33, 3)])
+def test_norm_variance_beside_an_outlier(shape):
+    """The first pixel, which the sums are taken about, a thousand spreads off: the outlier is part of the variance, and
+    a block of r rows has at most r roundings of it."""
+    N, H, W, C, G = shape
+    x = normal(gen(3), N, H, W, C)
+    x[:, 0, 0] += 1000
+    d = B.make_norm_desc(N, H, W, C, G, "none", EPS, "f32")
+    _, mean, rstd = run_fwd(d, x, None, None, N, G, (N, H, W, C), "f32")
+    rmean, rrstd = R.moments(x.double(), G, EPS)
+    R.within(mean, rmean, R.EPS32 * (1000 + R.CHAIN), "f32", "mean")
+    R.within(rstd, rrstd, R.EPS32 * (H * W + R.CHAIN) * rrstd, "f32", "rstd")
+
+
 @pytest.mark.parametrize("shape", [(2, 6, 6, 64, 2), (2, 5, 5, 33, 3)])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
 def test_norm_keeps_nan_inside_its_group(shape, bad):

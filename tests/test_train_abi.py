@@ -131,3 +131,28 @@ def test_conv_backward_refusals():
     assert status_of(f, d, P, P + 1, P, P, P, P, P, BIG, stream=0) == MISALIGNED
     assert status_of(f, d, P, P, P, P, P + 1, P, P, BIG, stream=0) == MISALIGNED
     assert status_of(f, d, None, P, None, None, None, None, None, 0, stream=0) == 0  # nothing asked for
+
+
+def test_plan_names():
+    """Slabs that a cluster holds, slabs that it does not, and slices wider than a thread block."""
+    name = B.dwconv2d_group_norm_nhwc_plan_name
+    assert [name(norm(N=64, H=56, W=56, C=128, groups=32), p) for p in (0, 1)] == ["slab", "slab"]
+    assert [name(norm(N=2, H=256, W=256, C=64, groups=8, dtype="f32"), p) for p in (0, 1)] == ["stream", "stream"]
+    assert [name(norm(N=1, H=9, W=9, C=4110, groups=1), p) for p in (0, 1)] == ["split", "split"]
+    assert name(norm(N=0), 0) in ("slab", "stream", "split")
+    conv = B.dwconv2d_bwd_nhwc_plan_name
+    for k, s, pad in ((3, 1, 1), (3, 2, 0), (5, 1, 2), (7, 2, 3)):
+        assert conv(B.make_desc(2, 40, 20, 20, k, s, pad)) == "nhwc"
+    for kw in (dict(kernel=4, pad=1), dict(kernel=3, pad=2), dict(kernel=3, pad=2, dilation=2), dict(kernel=3, pad=1, stride=3),
+               dict(kernel=3, pad=1, multiplier=2), dict(kernel=(3, 5), pad=(1, 2))):
+        assert conv(B.make_desc(2, 40, 20, 20, **kw)) == "generic"
+
+
+def test_workspaces_cover_aligned_copies():
+    """Channels that are no multiple of 16 bytes: room for gy and x (or its codes) on aligned pixels beside the sums."""
+    size = B.dwconv2d_bwd_nhwc_workspace_size
+    assert size(B.make_desc(4, 65, 20, 20, 3, 1, 1, dtype="bf16")) > 2 * 4 * 400 * 72 * 2
+    # a channel slice off 16 bytes needs gy's copy alone
+    a = size(B.make_desc(4, 64, 20, 20, 3, 1, 1, dtype="bf16", out_c_offset=8, out_c_total=80))
+    b = size(B.make_desc(4, 64, 20, 20, 3, 1, 1, dtype="bf16", out_c_offset=3, out_c_total=80))
+    assert b - a == 4 * 400 * 64 * 2
