@@ -12,7 +12,13 @@ namespace dwconv {
 namespace {
 
 constexpr int kNT = 256;
-constexpr int kItems = 4;  // independent 16-byte reads in flight per thread
+// 16-byte vectors of a thread, all of them read before the first is used: four
+// where there are many, one where two waves of blocks cover them all (45 x 51 x
+// 200 fp32, three samples: 9.1 us for the round trip against 12.3 with four;
+// 112 x 112 x 64 bf16, 64 samples: 52.5 us with four, 55.4 with two, 56.3 with
+// eight).
+constexpr int kMany = 4;
+constexpr uint32_t kFew = 152 * 16 * kNT;
 
 // Lanes: L = block / VEC per block; `per_row` = nblk * L vectors per row, the
 // last ones of a ragged row idle.
@@ -24,7 +30,7 @@ struct EGeom {
   int C, L;
 };
 
-template <typename T, int SRC>
+template <typename T, int SRC, int kItems>
 __global__ void __launch_bounds__(kNT) encode_kernel(EGeom g, const T* __restrict__ x, Act8 t) {
   constexpr int VEC = Vec<T>::n;
   const uint32_t base = blockIdx.x * (uint32_t)(kNT * kItems) + threadIdx.x;
@@ -43,23 +49,17 @@ __global__ void __launch_bounds__(kNT) encode_kernel(EGeom g, const T* __restric
   }
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    float f[VEC];
-    unpack16<T>(v[k], f);
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) m = max(m, abs_bits(f[e]));
-    // a power of two of aligned lanes; idle lanes bring zeros
-    for (int o = g.L >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t m = block_max<T, VEC>(v[k], g.L);  // a power of two of aligned lanes; idle lanes bring zeros
     if (c[k] >= g.C) continue;
+    f32x2 f[VEC / 2];
+    unpack16_pairs<T>(v[k], f);
     float inv;
     const float s = scale_of<SRC>(m, &inv);
     uint8_t* q = t.codes + row[k] * g.C + c[k];
-    if (VEC == 8) {
-      const uint32_t lo = encode4<SRC>(f[0], f[1], f[2], f[3], inv);
-      const uint32_t hi = encode4<SRC>(f[VEC - 4], f[VEC - 3], f[VEC - 2], f[VEC - 1], inv);
-      *reinterpret_cast<uint2*>(q) = make_uint2(lo, hi);
+    if constexpr (VEC == 8) {
+      *reinterpret_cast<uint2*>(q) = make_uint2(encode4<SRC>(f[0], f[1], inv), encode4<SRC>(f[2], f[3], inv));
     } else {
-      *reinterpret_cast<uint32_t*>(q) = encode4<SRC>(f[0], f[1], f[2], f[3], inv);
+      *reinterpret_cast<uint32_t*>(q) = encode4<SRC>(f[0], f[1], inv);
     }
     if ((c[k] & ((1 << t.shift) - 1)) == 0) t.scales[row[k] * t.nblk + (c[k] >> t.shift)] = s;
   }
@@ -123,7 +123,7 @@ encode_elem_kernel(int64_t rows, int C, int64_t ldx, const T* __restrict__ x, Ac
   }
 }
 
-template <typename T, int SRC>
+template <typename T, int SRC, int kItems>
 __global__ void __launch_bounds__(kNT) decode_kernel(EGeom g, Act8 t, T* __restrict__ x) {
   constexpr int VEC = Vec<T>::n;
   const uint32_t base = blockIdx.x * (uint32_t)(kNT * kItems) + threadIdx.x;
@@ -199,15 +199,17 @@ bool vec_ok(int64_t C, int64_t ldx, int es, const void* x, const Act8& t) {
          reinterpret_cast<uintptr_t>(t.codes) % vec == 0;
 }
 
+unsigned grid_of(uint32_t vectors, int items) { return (vectors + kNT * items - 1) / (kNT * items); }
+
 unsigned elem_grid(int64_t blocks) {
   const int64_t n = (blocks + kNT / 32 * kWarpBlocks - 1) / (kNT / 32 * kWarpBlocks);
   return (unsigned)(n < 152 * 32 ? n : 152 * 32);
 }
 
-// fn(grid, geom) for launches of below 2^31 vectors each
+// fn(geom) for launches of below 2^31 vectors each
 template <typename F>
 cudaError_t over_rows(int64_t rows, int64_t per_row, int64_t C, int64_t ldx, int L, F fn) {
-  const int64_t most = ((int64_t(1) << 31) - kNT * kItems) / per_row;
+  const int64_t most = ((int64_t(1) << 31) - kNT * kMany) / per_row;
   for (int64_t r = 0; r < rows; r += most) {
     const int64_t n = rows - r < most ? rows - r : most;
     EGeom g{};
@@ -217,7 +219,7 @@ cudaError_t over_rows(int64_t rows, int64_t per_row, int64_t C, int64_t ldx, int
     g.ldx = ldx;
     g.C = (int)C;
     g.L = L;
-    fn((unsigned)((g.total + kNT * kItems - 1) / (kNT * kItems)), g);
+    fn(g);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -231,8 +233,9 @@ cudaError_t encode(int64_t rows, int64_t C, int64_t ldx, const T* x, const Act8&
     return cudaGetLastError();
   }
   const int L = (1 << t.shift) / Vec<T>::n;
-  return over_rows(rows, (int64_t)t.nblk * L, C, ldx, L, [&](unsigned grid, const EGeom& g) {
-    encode_kernel<T, SRC><<<grid, kNT, 0, s>>>(g, x, t);
+  return over_rows(rows, (int64_t)t.nblk * L, C, ldx, L, [&](const EGeom& g) {
+    if (g.total > kFew) encode_kernel<T, SRC, kMany><<<grid_of(g.total, kMany), kNT, 0, s>>>(g, x, t);
+    else encode_kernel<T, SRC, 1><<<grid_of(g.total, 1), kNT, 0, s>>>(g, x, t);
   });
 }
 
@@ -242,8 +245,9 @@ cudaError_t decode(int64_t rows, int64_t C, int64_t ldx, const Act8& t, T* x, cu
     decode_elem_kernel<T, SRC><<<elem_grid(rows * t.nblk), kNT, 0, s>>>(rows, (int)C, ldx, t, x);
     return cudaGetLastError();
   }
-  return over_rows(rows, C / Vec<T>::n, C, ldx, 0, [&](unsigned grid, const EGeom& g) {
-    decode_kernel<T, SRC><<<grid, kNT, 0, s>>>(g, t, x);
+  return over_rows(rows, C / Vec<T>::n, C, ldx, 0, [&](const EGeom& g) {
+    if (g.total > kFew) decode_kernel<T, SRC, kMany><<<grid_of(g.total, kMany), kNT, 0, s>>>(g, t, x);
+    else decode_kernel<T, SRC, 1><<<grid_of(g.total, 1), kNT, 0, s>>>(g, t, x);
   });
 }
 

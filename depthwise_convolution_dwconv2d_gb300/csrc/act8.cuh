@@ -29,6 +29,27 @@ struct Act8 {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// The largest pattern without sign of a vector's values and its neighbours'
+// of a block of channels (`lanes` of them), as that of an fp32 value.
+// Patterns of 16-bit types are compared two at a time.
+template <typename T, int V, typename W>
+__device__ __forceinline__ uint32_t block_max(W w, int lanes) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
+  uint32_t m = 0;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) m = max(m, u[e] & 0x7fffffffu);
+    for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+  } else {
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) m = __vmaxu2(m, u[e] & 0x7fff7fffu);
+    for (int o = lanes >> 1; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const unsigned short h = (unsigned short)max(m & 0xffffu, m >> 16);
+    return __float_as_uint(to_f<T>(*reinterpret_cast<const T*>(&h)));
+  }
+}
+
 // scale and its reciprocal from the block's largest pattern (0 / 0 for a
 // block of zeros or of values too small for a normal scale)
 template <int SRC>
