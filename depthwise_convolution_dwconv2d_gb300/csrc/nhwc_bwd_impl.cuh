@@ -816,18 +816,17 @@ __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const 
           const int a = r - S * e;
           if (a < 0 || a >= K) continue;
 #pragma unroll
-          for (int b = 0; b < K; ++b)
-#pragma unroll
-            for (int p = 0; p < PX; ++p) {
-              if ((p - b) % S != 0) continue;
-              const f32x2 v = gv[D + (p - b) / S];
-              if (GW) {
-                fma_f32x2(acc[a * K + b], own[r * PX + p], v);
-                if (a == K / 2 && b == K / 2) acc[K * K] = add_f32x2(acc[K * K], v);
-              } else {
-                fma_f32x2(own[r * PX + p], acc[a * K + b], v);
-              }
+          for (int m = 0; m < K * PX; ++m) {  // neighbouring products go to different sums
+            const int b = GW ? m % K : m / PX, p = GW ? m / K : m % PX;
+            if ((p - b) % S != 0) continue;
+            const f32x2 v = gv[D + (p - b) / S];
+            if (GW) {
+              fma_f32x2(acc[a * K + b], own[r * PX + p], v);
+              if (a == K / 2 && b == K / 2) acc[K * K] = add_f32x2(acc[K * K], v);
+            } else {
+              fma_f32x2(own[r * PX + p], acc[a * K + b], v);
             }
+          }
         }
       }
       if (!GW) {
