@@ -181,7 +181,9 @@ cudaError_t direct(const Conv& c, const T* x, const Act8& t, const T* gy, const 
 
 // Pixels of `bytes` bytes, `from` apart, copied `to` apart (a multiple of 16):
 // the layout that the staged kernels read. A thread writes 16 bytes; their
-// source begins anywhere, so it is read as aligned words and shifted.
+// source begins anywhere, so it is read as aligned words and shifted. The
+// detour pays: 10x17x52x287 fp16 5x5 takes 27 us with it, 111 without (every
+// access of two channels being two).
 struct Copy {
   const uint8_t* src;
   uint8_t* dst;

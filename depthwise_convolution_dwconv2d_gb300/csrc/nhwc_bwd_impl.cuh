@@ -204,10 +204,13 @@ __device__ __forceinline__ void join_lanes(int ct_log, const f32x2* acc, int C, 
   }
 }
 
-// 3x3 filters: gx, gw and gb in one walk. The gy rows of the last steps stay
-// in registers (a ring whose slots the unrolled loop names), so each gy and
-// each x of the strip is loaded once; the next step's loads are issued before
-// this step's arithmetic.
+// 3x3 filters with plain loads: gx, gw and gb in one walk. The gy rows of the
+// last steps stay in registers (a ring whose slots the unrolled loop names),
+// so each gy and each x of the strip is loaded once; the next step's loads
+// are issued before this step's arithmetic. It serves what the staged kernel
+// does not: fewer than 32 channels, pointers off 16 bytes. Masks, addresses
+// and scales make six instructions of every product: 77 us at 64x56x56x128
+// bf16 from integer codes (1.7 TB/s), where the staged kernel takes 41.
 template <typename T, int SRC, int S, bool PAIR>
 __global__ void __launch_bounds__(kRingThreads, kRingBlocks)
 ring3_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restrict__ gy, const T* __restrict__ w,
@@ -338,6 +341,15 @@ ring3_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
 // column masks. A stage is as many rows as the ring has slots: row i of a
 // stage is slot i, and a stage costs one barrier and one wait. All lanes of a
 // block walk the same rows.
+//
+// Bound by issue: 64x56x56x128 bf16 from integer codes takes 41 us (3.2 TB/s
+// of the floor's bytes, 0.48 of the measured copy; 22.6 TFLOP/s) for 24.9 M
+// warp instructions, about 190 for the 78 packed products of a row of four
+// pixels (unpacking, decoding, stores and the item's start are the rest);
+// fp32 at 128 samples, with nothing to unpack, runs at 5.9 TB/s, at the
+// memory. Four blocks of four warps per SM at up to 128 registers: two of
+// seven warps took 55 us (fewer warps, coarser items), five at 96 registers
+// spill (68 us for the call against 54).
 template <typename T, int SRC, int S, int CT>
 __global__ void __launch_bounds__(kStagedThreads, kStagedBlocks)
 staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, const __grid_constant__ CUtensorMap map_x,
@@ -566,7 +578,9 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
 // or gradient alone takes up to 98 registers; both in one launch, each by its
 // own blocks. A step owns RY = 2 rows of the strip and reads each row of gy
 // that they meet once (from L1 after the first step that meets it), for up to
-// 2 K^2 PX products.
+// 2 K^2 PX products. Plain loads, for what the staged tiles do not serve: two
+// blocks per SM, since at three (168 registers) the 7x7 gradient spills (74
+// us against 51 at 5x45x51x96 fp32).
 template <typename T, int SRC, int K, int S, bool GW, bool PAIR>
 __device__ __forceinline__ void block_walk(const Conv& c, const Geom& g, const T* __restrict__ x, const Act8& x8,
                                            const T* __restrict__ gy, const T* __restrict__ w, T* __restrict__ gx,
@@ -682,6 +696,13 @@ block_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
 // x that they meet by another. gx and gw are separate blocks, as in
 // block_kernel; each reads a row of gy for every filter row that meets it,
 // from shared memory at constant offsets.
+//
+// 32x28x28x128 bf16: 31 us for the call at 7x7 (20 TFLOP/s), 19 at 5x5 (17),
+// against 99 and 36 with plain loads. The packed products bound it (about 52
+// TFLOP/s where all three operands change); on small layers the cold
+// instruction cache does: a step is some 800 products of straight code, and
+// 5x45x51x96 fp32 7x7 (one or two steps per block, 22 us) loses four of every
+// six issue slots to it.
 template <typename T, int SRC, int K, int S, int CT, bool GW>
 __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const CUtensorMap* map_gy,
                                           const CUtensorMap* map_x, const Act8& x8, unsigned int* timeouts,

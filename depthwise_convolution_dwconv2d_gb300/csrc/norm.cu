@@ -1,6 +1,7 @@
 // Channels-last group norm with an activation, forward and backward: plans,
-// dispatch, and the split kernels, for the shapes that the slab kernels
-// (norm_slab_impl.cuh) leave.
+// dispatch, and the split kernels, for the shapes that the slab and stream
+// kernels (norm_slab_impl.cuh) leave: slices wider than a block, that is
+// groups of more than 1024 channels (2048 in aligned 16-bit rows).
 //
 // A sample's group is spread over C / D channels of every pixel, so its sums
 // need all of the sample before the first output. Here that is two reads of

@@ -23,10 +23,15 @@
 // by the parallel form of the two (see norm.cu). Every order is fixed.
 //
 // Arithmetic is on pairs of channels (the two lanes of the packed fp32
-// instructions), which halves the instructions; what bounds the kernels is
-// their issue (the 16-bit SiLU forward issues about 20 instructions per
-// element of 4 bytes) and, per block, the latency of reading, joining and the
-// cluster's barrier.
+// instructions). Rows are fetched by asynchronous copies, a batch ahead.
+// What bounds the kernels is issue, at 0.54 of the rate with 24 warps an SM:
+// 64x56x56x128 bf16, 32 groups, SiLU takes 48 us forward with its checkpoint
+// (2.7 TB/s of the floor's bytes) and 65 backward from it (2.0), 28.8 and
+// 37.3 M warp instructions, of which about 900 per warp are a block's start,
+// joins and cluster barrier; 64x28x28x256 bf16, 16 groups, ReLU 31 us
+// backward (2.4 TB/s). Streamed, 2x256x256x64 fp32 takes 12 + 15 us (the
+// second read comes from L2). Sums per thread instead of about the block's
+// first pixel need a second join (9 us more for the step).
 #pragma once
 
 #include <cooperative_groups.h>

@@ -146,7 +146,7 @@ EPS = 1e-5
 # wider than a vector's slice, planes that one block holds and that it does not, fewer pixels than thread blocks
 NORMS = [(1, 1, 1, 8, 2), (2, 1, 1, 7, 7), (1, 2, 3, 5, 1), (3, 7, 7, 64, 32), (2, 5, 9, 30, 3), (1, 14, 14, 512, 32),
          (2, 19, 23, 40, 4), (2, 37, 29, 320, 32), (4, 28, 28, 128, 1), (1, 64, 65, 24, 3), (1, 128, 128, 16, 2),
-         (2, 3, 3, 1024, 8), (1, 9, 9, 2056, 1), (5, 11, 3, 33, 11), (1, 200, 150, 8, 1), (2, 56, 56, 128, 32)]
+         (2, 3, 3, 1024, 8), (1, 9, 9, 2056, 1), (5, 11, 3, 33, 11), (1, 200, 150, 8, 1), (2, 56, 56, 128, 32), (1, 5, 4, 1031, 1), (2, 4, 5, 1044, 2)]
 
 
 def norm_inputs(N, H, W, C, dtype, seed, level=0.5):
