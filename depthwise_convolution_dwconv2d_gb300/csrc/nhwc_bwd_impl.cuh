@@ -208,7 +208,7 @@ __device__ __forceinline__ void join_lanes(int ct_log, const f32x2* acc, int C, 
 // last steps stay in registers (a ring whose slots the unrolled loop names),
 // so each gy and each x of the strip is loaded once; the next step's loads
 // are issued before this step's arithmetic. It serves what the staged kernel
-// does not: fewer than 32 channels, pointers off 16 bytes. Masks, addresses
+// does not: fewer than 24 channels, pointers off 16 bytes. Masks, addresses
 // and scales make six instructions of every product: 77 us at 64x56x56x128
 // bf16 from integer codes (1.7 TB/s), where the staged kernel takes 41.
 template <typename T, int SRC, int S, bool PAIR>

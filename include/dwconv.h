@@ -421,8 +421,8 @@ size_t dwconv2d_bwd_nhwc_workspace_size(const dwconv2d_desc_t* desc);
  * gbias. For N == 0 gw and gbias become 0. No output may overlap an input.
  * Square 3x3, 5x5 and 7x7 filters with equal strides of 1 or 2, dilation 1,
  * one filter per channel and padding up to (k - 1) / 2 run on row-walking
- * kernels; from 32 channels on these stage rows with the tensor memory
- * accelerator, which needs gy, x and their pixel distances on 16 bytes: where
+ * kernels; from 24 channels on (5x5 and 7x7: 9) these stage rows with the
+ * tensor memory accelerator, which needs gy, x and their pixel distances on 16 bytes: where
  * the descriptor's distances are not, one launch copies gy and x to aligned
  * pixels in the workspace (its size includes them; for gx alone, without a
  * workspace, and for pointers off 16 bytes, kernels with plain loads run).
