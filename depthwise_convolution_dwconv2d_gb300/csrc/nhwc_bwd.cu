@@ -352,10 +352,10 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
   if (!supported(c) || c.N >= (int64_t(1) << 31)) return false;
   const int es = c.dtype == DWCONV_F32 ? 4 : 2, K = c.kh, S = c.sh, D = (K - 1) / S;
   const bool ring = K == 3;
-  const int px = ring ? 4 : 8, step = ring ? 1 : 2 / S, blocks = ring ? kStagedBlocks : K == 5 ? 4 : 3;
+  const int px = ring ? 4 : tile_px(K), step = ring ? 1 : 2 / S, blocks = ring ? kStagedBlocks : K == 5 ? 4 : 3;
   // A tile has 32 channels at least. With fewer the direct kernels' narrower blocks win sooner or later: 3x3 bf16 at 64
   // samples, 8 channels 23 us against 56, 24 the same; 5x5 bf16, 24 channels 39 against 23, 9 channels 49 against 31;
-  // 7x7, 17 channels 117 against 81, 12 channels 29 against 32.
+  // 7x7, 17 channels 117 against 64, 12 channels 29 against 31.
   if (c.C < (K == 3 ? 24 : 9)) return false;
   Staged g{};
   // 64 channels per block, 32 where that leaves a quarter fewer of the last tile idle

@@ -697,17 +697,17 @@ block_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
 // block_kernel; each reads a row of gy for every filter row that meets it,
 // from shared memory at constant offsets.
 //
-// 32x28x28x128 bf16: 31 us for the call at 7x7 (20 TFLOP/s), 19 at 5x5 (17),
+// 32x28x28x128 bf16: 33 us for the call at 7x7 (19 TFLOP/s), 19 at 5x5 (17),
 // against 99 and 36 with plain loads. The packed products bound it (about 52
 // TFLOP/s where all three operands change); on small layers the cold
-// instruction cache does: a step is some 800 products of straight code, and
-// 5x45x51x96 fp32 7x7 (one or two steps per block, 22 us) loses four of every
-// six issue slots to it.
+// instruction cache does: a step is some 400 products of straight code, and a
+// block of 5x45x51x96 fp32 7x7 (18 us) takes only a few. With strips of eight
+// columns, 800 products, it took 22 us and lost four of every six issue slots.
 template <typename T, int SRC, int K, int S, int CT, bool GW>
 __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const CUtensorMap* map_gy,
                                           const CUtensorMap* map_x, const Act8& x8, unsigned int* timeouts,
                                           const T* __restrict__ w, T* __restrict__ gx, float* __restrict__ ws) {
-  constexpr int PX = 8, RY = 2, M = RY / S, NT = kTileThreads;
+  constexpr int PX = tile_px(K), RY = 2, M = RY / S, NT = kTileThreads;
   constexpr int D = (K - 1) / S, WIN = D + (PX - 1) / S + 1;
   constexpr bool kCode = GW && SRC != kSrcFull;
   constexpr int GP = 2 * CT * (int)sizeof(T), XP = kCode ? 2 * CT : GP;
@@ -788,11 +788,11 @@ __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const 
 #pragma unroll
     for (int p = 0; p < PX; ++p) xok |= (iw0 + p >= 0 && iw0 + p < W) ? 1u << p : 0u;
     const int64_t at = n * H * (int64_t)W + (int64_t)ih0 * W + iw0;
-    // a checkpoint's scales: lanes p + 8 b of the strip's lanes read pixel p, block b of the tile's
-    const int sb = (ch0 >> x8.shift) + (pl >> 3);
-    const bool scaler = kCode && here && g.want_x && pl < 16 && sb < x8.nblk && ((xok >> (pl & 7)) & 1);
-    const int from = (int)(threadIdx.x & 31 & ~(CT - 1)) + 8 * ((ch >> x8.shift) - (ch0 >> x8.shift));
-    const float* const sp = x8.scales + (at + (pl & 7)) * x8.nblk + sb;
+    // a checkpoint's scales: lanes p + PX b of the strip's lanes read pixel p, block b of the tile's
+    const int sb = (ch0 >> x8.shift) + pl / PX;
+    const bool scaler = kCode && here && g.want_x && pl < 2 * PX && sb < x8.nblk && ((xok >> (pl % PX)) & 1);
+    const int from = (int)(threadIdx.x & 31 & ~(CT - 1)) + PX * ((ch >> x8.shift) - (ch0 >> x8.shift));
+    const float* const sp = x8.scales + (at + pl % PX) * x8.nblk + sb;
     if (!tma::mbar_wait(&full[slot], parity, timeouts)) {
       // the copy never landed: let those in flight finish (bounded), then stop
       for (int j = 1; j < g.stages; ++j) {
