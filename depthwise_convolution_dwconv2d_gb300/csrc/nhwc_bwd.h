@@ -38,7 +38,7 @@ struct Geom {
 constexpr int kTileThreads = 128;
 // Columns of a strip. A step is straight code, K * K * px * 2 / S packed
 // products of it, and at 7x7 half as much of it pays: 5x45x51x96 fp32 22 us at
-// eight columns, 18 at four; 22x147x17 of 55 samples 80 and 64; where blocks
+// eight columns, 17 at four; 22x147x17 of 55 samples 80 and 64; where blocks
 // take many steps the repeated reads cost a little (32x28x28x128 bf16 31, 33).
 // 5x5 at 32x28x28x128: 18.7 at eight, 20.7 at four.
 constexpr int tile_px(int K) { return K == 7 ? 4 : 8; }

@@ -701,7 +701,7 @@ block_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
 // against 99 and 36 with plain loads. The packed products bound it (about 52
 // TFLOP/s where all three operands change); on small layers the cold
 // instruction cache does: a step is some 400 products of straight code, and a
-// block of 5x45x51x96 fp32 7x7 (18 us) takes only a few. With strips of eight
+// block of 5x45x51x96 fp32 7x7 (17 us) takes only a few. With strips of eight
 // columns, 800 products, it took 22 us and lost four of every six issue slots.
 template <typename T, int SRC, int K, int S, int CT, bool GW>
 __device__ __forceinline__ void tile_walk(const Conv& c, const Staged& g, const CUtensorMap* map_gy,
