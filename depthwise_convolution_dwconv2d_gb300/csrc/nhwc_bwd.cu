@@ -234,6 +234,19 @@ size_t sums_bytes(const Conv& c, int64_t chunks) {
   const size_t b = (size_t)chunks * (size_t)c.OC() * (size_t)(c.kh * c.kw + 1) * sizeof(float);
   return (b + 255) & ~size_t(255);
 }
+// The staged plan of a call from this source and the bytes of its aligned copies of gy and of x (or its codes): what the
+// workspace is sized by and what a call lays out in it. A source's plan says nothing of another's: a stage of codes is
+// smaller than one of full values, and on tall images only it may fit. false: the direct kernels run.
+struct Copies {
+  int64_t gy, x;
+};
+bool staged_of(const Conv& c, int src, walk::Staged* g, Copies* k) {
+  const int es = c.dtype == DWCONV_F32 ? 4 : 2;
+  if (!walk::plan_staged(c, src, g) || !copies_fit(c, es)) return false;
+  *k = Copies{gy_copy_bytes(c, es), x_copy_bytes(c, src == kSrcFull ? es : 1)};
+  return true;
+}
+
 // chunks of any of the walking kernels that a call's pointers and source may lead to
 int64_t walk_chunks(const Conv& c) {
   int64_t n = walk::plan(c).chunks;
@@ -253,9 +266,10 @@ cudaError_t walked(const Conv& c, const T* x, const Act8& t, const T* gy, const 
   walk::Staged st;
   cudaError_t e = cudaErrorNotSupported;
   const int src = x || !t.codes ? kSrcFull : t.src, es = sizeof(T), xes = src == kSrcFull ? es : 1;
-  const int64_t gcopy = gy_copy_bytes(c, es), xcopy = gw ? x_copy_bytes(c, xes) : 0;
+  Copies need;
   // gx alone has no workspace, so no copies
-  if (walk::plan_staged(c, src, &st) && copies_fit(c, es) && (want_gw || gcopy == 0)) {
+  if (staged_of(c, src, &st, &need) && (want_gw || need.gy == 0)) {
+    const int64_t gcopy = need.gy, xcopy = gw ? need.x : 0;
     st.want_gx = gx != nullptr;
     st.want_gw = want_gw;
     st.want_x = gw != nullptr;
@@ -396,6 +410,8 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
   };
   // Bands: the cut whose longest block has the fewest rows. A band of the 3x3 kernel costs whole stages, the rows above
   // it about a third of an owned row; one of the larger filters is a stage, whose copy and start cost about half a step.
+  // Cuts into over 4096 bands are not looked at, so that planning stays within tens of microseconds: images whose rows
+  // need more (a large filter's stage holds at most four steps) take the direct kernels.
   const int64_t rows = g.t_end - g.t_begin, groups = (c.N + g.ns - 1) / g.ns;
   const int rd = D + 1;
   const int64_t wave = (152 * blocks / (ring ? 1 : 2) + g.tiles - 1) / g.tiles;
@@ -453,12 +469,13 @@ Algo plan_bwd(const Conv& c) { return walk::supported(c) ? Algo::Nhwc : Algo::Ge
 size_t bwd_workspace_bytes(const Conv& c) {
   if (!walk::supported(c)) return sums_bytes(c, generic_chunks(c));
   size_t b = sums_bytes(c, walk_chunks(c));
-  walk::Staged g;
-  const int es = c.dtype == DWCONV_F32 ? 4 : 2;
-  if (walk::plan_staged(c, kSrcFull, &g) && copies_fit(c, es)) {
-    const int64_t full = x_copy_bytes(c, es), codes = x_copy_bytes(c, 1);
-    b += (size_t)(gy_copy_bytes(c, es) + (full > codes ? full : codes));
+  int64_t most = 0;
+  for (int src : {kSrcFull, kSrcI8}) {
+    walk::Staged g;
+    Copies k;
+    if (staged_of(c, src, &g, &k) && k.gy + k.x > most) most = k.gy + k.x;
   }
+  b += (size_t)most;
   return b;
 }
 

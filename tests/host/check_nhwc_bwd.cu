@@ -1,0 +1,76 @@
+// CPU check of the channels-last backward's plans: the workspace holds what a
+// call from any source lays out in it, and the staged kernels get only rows
+// whose distances their 32-bit steps hold.
+#include <cstdio>
+#include "nhwc_bwd.h"
+
+namespace dwconv {
+// what the planner's file calls in others; nothing here is launched
+cudaError_t bwd_weight_pass2(const Conv&, const float*, int, void*, void*, cudaStream_t) { return cudaErrorNotSupported; }
+const char* algo_name(Algo) { return ""; }
+namespace nhwc {
+namespace walk {
+#define X(T)                                                                                                          \
+  template <>                                                                                                         \
+  cudaError_t run<T>(const Conv&, const Geom&, bool, const T*, const Act8&, const T*, const T*, T*, float*, cudaStream_t) { \
+    return cudaErrorNotSupported;                                                                                     \
+  }                                                                                                                   \
+  template <>                                                                                                         \
+  cudaError_t run_staged<T>(const Conv&, const Staged&, int, const Views&, const Act8&, const T*, T*, float*,         \
+                            cudaStream_t) {                                                                           \
+    return cudaErrorNotSupported;                                                                                     \
+  }
+X(float) X(__half) X(__nv_bfloat16)
+#undef X
+}  // namespace walk
+}  // namespace nhwc
+}  // namespace dwconv
+#include "nhwc_bwd.cu"
+
+using namespace dwconv;
+static int fails = 0, checks = 0, tall = 0;
+
+static Conv mk(int64_t N, int64_t C, int64_t H, int64_t W, int k, int s, int p, int dtype) {
+  Conv c{};
+  c.N = N; c.C = C; c.H = H; c.W = W; c.m = 1; c.kh = c.kw = k; c.sh = c.sw = s; c.ph = c.pw = p; c.dh = c.dw = 1;
+  c.Ho = (H + 2 * p - k) / s + 1; c.Wo = (W + 2 * p - k) / s + 1;
+  c.off = 0; c.ctot = C; c.dtype = dtype;
+  return c;
+}
+
+// every source's sums and aligned copies lie inside the workspace
+static void check_room(const Conv& c) {
+  const int es = c.dtype == DWCONV_F32 ? 4 : 2;
+  const size_t size = nhwc::bwd_workspace_bytes(c);
+  bool staged[2];
+  for (int i = 0; i < 2; ++i) {
+    nhwc::walk::Staged g;
+    staged[i] = nhwc::walk::plan_staged(c, i ? kSrcI8 : kSrcFull, &g) && nhwc::copies_fit(c, es);
+    if (!staged[i]) continue;
+    const size_t copies = (size_t)(nhwc::gy_copy_bytes(c, es) + nhwc::x_copy_bytes(c, i ? 1 : es));
+    const size_t sums = nhwc::sums_bytes(c, copies ? nhwc::walk_chunks(c) : g.chunks);
+    ++checks;
+    if (sums + copies > size) {
+      ++fails;
+      printf("FAIL %s N=%lld C=%lld H=%lld W=%lld k=%d s=%d: %zu of sums and %zu of copies in %zu\n", i ? "codes" : "full",
+             (long long)c.N, (long long)c.C, (long long)c.H, (long long)c.W, c.kh, c.sh, sums, copies, size);
+    }
+  }
+  tall += staged[0] != staged[1];
+}
+
+int main() {
+  for (int dtype : {DWCONV_F32, DWCONV_BF16})
+    for (int k : {3, 5, 7})
+      for (int s : {1, 2})
+        for (int64_t N : {1, 3})
+          for (int64_t C : {17, 33, 65, 130, 287})
+            for (int64_t H : {9, 31, 500, 2000, 4100, 8300, 10000, 16500, 33000, 70000})
+              for (int64_t W : {5, 32, 61, 200}) check_room(mk(N, C, H, W, k, s, k / 2, dtype));
+  if (!tall) {
+    ++fails;
+    printf("FAIL no shape is staged from one source alone\n");
+  }
+  printf("%d checks, %d shapes staged from one source alone, fails: %d\n", checks, tall, fails);
+  return fails != 0;
+}

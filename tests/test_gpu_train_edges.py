@@ -1,0 +1,66 @@
+"""Channels-last training operators at the edges of their plans: tall images,
+long chains of additions, checkpoints at any byte, and gradients whose group
+sums weigh as much as their other terms. 64-bit forms are train_ref.py's."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import train_ref as R
+from depthwise_convolution_dwconv2d_gb300 import binding as B
+from test_gpu_train_nhwc import conv_inputs, filled, gen, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from depthwise_convolution_dwconv2d_gb300 import build
+    build.build()
+    B.load()
+
+
+class Guarded:
+    """`nbytes` of workspace with 64 KB behind it that a call must leave as they are."""
+
+    def __init__(self, nbytes):
+        self.buf = torch.full((nbytes + (1 << 16),), 0x7f, dtype=torch.uint8, device="cuda")
+        self.ws, self.behind = self.buf[:nbytes], self.buf[nbytes:]
+
+    def check(self):
+        assert bool((self.behind == 0x7f).all()), "written behind the workspace"
+
+
+def conv_backward(d, x, gy, w, dtype, x8=None):
+    gx, gw, gb = filled(d.N, d.H, d.W, d.C, dtype=dtype), filled(*w.shape, dtype=dtype), filled(w.shape[0], dtype=dtype)
+    room = Guarded(B.dwconv2d_bwd_nhwc_workspace_size(d))
+    B.dwconv2d_bwd_nhwc(d, x, gy, w, gx, gw, gb, room.ws, x8=x8)
+    room.check()
+    return gx, gw, gb
+
+
+def check_conv(out, d, x, gy, w, dtype, chain, what):
+    """chain: the most additions behind a value of gw or gb."""
+    rgx, rgw, rgb, sx, sw, sb = R.conv_bwd(x.double(), gy.double(), w.double(), d)
+    R.within(out[0], rgx, R.EPS32 * (d.kh * d.kw + 2) * sx, dtype, what + " gx")
+    R.within(out[1], rgw, R.EPS32 * chain * sw, dtype, what + " gw")
+    R.within(out[2], rgb, R.EPS32 * chain * sb, dtype, what + " gb")
+
+
+# ---- layer backward: tall images -------------------------------------------
+
+
+@pytest.mark.parametrize("dtype,C,H,W,k,s", [("f32", 17, 10000, 32, 5, 1), ("f32", 17, 8300, 32, 5, 1), ("bf16", 35, 17000, 9, 5, 1),
+                                             ("f16", 17, 17000, 32, 7, 2), ("f32", 17, 10000, 32, 3, 1)])
+@pytest.mark.parametrize("kind", ["none", "i8", "e4m3"])
+def test_conv_backward_of_tall_images(dtype, C, H, W, k, s, kind):
+    """Channels off 16 bytes: aligned copies of gy and of x or its codes, whichever of them the call's plan makes, stay
+    inside the workspace that the descriptor alone decides. A thread adds at most 4096 products, then lanes and blocks."""
+    d, x, w, gy = conv_inputs(1, C, H, W, k, s, k // 2, 1, 1, dtype, H + k)
+    x8 = None
+    if kind != "none":
+        codes, scales = R.encode(x, kind, 32)
+        x8 = B.make_act8(kind, 32, codes, scales)
+    out = conv_backward(d, None if x8 else x, gy, w, dtype, x8)
+    check_conv(out, d, R.decode(codes, scales, 32) if x8 else x, gy, w, dtype, 4096 + 256, f"{kind} {C}x{H}x{W} k{k}")
