@@ -371,6 +371,9 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
   // samples, 8 channels 23 us against 56, 24 the same; 5x5 bf16, 24 channels 39 against 23, 9 channels 49 against 31;
   // 7x7, 17 channels 117 against 64, 12 channels 29 against 31.
   if (c.C < (K == 3 ? 24 : 9)) return false;
+  // The 3x3 kernel steps from a row's scales to the next row's by 32 bits of bytes: longer rows (2^35 values from blocks
+  // of 32) take the direct kernel.
+  if (ring && src != kSrcFull && c.W * ((c.C + 31) / 32) * 4 >= (int64_t(1) << 32)) return false;
   Staged g{};
   // 64 channels per block, 32 where that leaves a quarter fewer of the last tile idle
   const int64_t by64 = (c.C + 63) / 64 * 64, by32 = (c.C + 31) / 32 * 32;

@@ -59,7 +59,23 @@ static void check_room(const Conv& c) {
   tall += staged[0] != staged[1];
 }
 
+// rows whose scales (blocks of 32) are 2^32 bytes apart or more are not staged from codes
+static void check_rows(const Conv& c, bool from_codes) {
+  nhwc::walk::Staged g;
+  const bool full = nhwc::walk::plan_staged(c, kSrcFull, &g), codes = nhwc::walk::plan_staged(c, kSrcI8, &g);
+  ++checks;
+  if (full && codes == from_codes) return;
+  ++fails;
+  printf("FAIL N=%lld C=%lld H=%lld W=%lld: staged from full values %d, from codes %d\n", (long long)c.N, (long long)c.C,
+         (long long)c.H, (long long)c.W, (int)full, (int)codes);
+}
+
 int main() {
+  for (int s : {1, 2}) {
+    check_rows(mk(1, 1 << 14, 2, 1 << 21, 3, s, 1, DWCONV_BF16), false);
+    check_rows(mk(1, 1 << 14, 2, (1 << 21) - 1, 3, s, 1, DWCONV_BF16), true);
+    check_rows(mk(1, 33, 2, 1 << 27, 3, s, 1, DWCONV_BF16), true);
+  }
   for (int dtype : {DWCONV_F32, DWCONV_BF16})
     for (int k : {3, 5, 7})
       for (int s : {1, 2})
