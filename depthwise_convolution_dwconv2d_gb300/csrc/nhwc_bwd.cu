@@ -191,6 +191,34 @@ struct Copy {
   int bytes;
   FastDiv d_vecs;   // 16-byte vectors of a pixel
 };
+
+// The five aligned words that hold the 16 bytes at `src`, from reads inside [lo, end) alone: next to either end the words
+// are put together from their bytes there, the others being 0.
+struct GlobalBytes {
+  static __device__ __forceinline__ uint32_t word(const uint8_t* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
+  static __device__ __forceinline__ uint32_t byte(const uint8_t* p) { return __ldg(p); }
+};
+#pragma nv_exec_check_disable
+template <typename Load>
+__host__ __device__ __forceinline__ void words_at(const uint8_t* src, const uint8_t* lo, const uint8_t* end, uint32_t* v) {
+  const uint8_t* q = src - (reinterpret_cast<uintptr_t>(src) & 3);
+  if (q >= lo && end - q >= 20) {
+#pragma unroll
+    for (int e = 0; e < 5; ++e) v[e] = Load::word(q + 4 * e);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 5; ++e) {
+      uint32_t w = 0;
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        const uint8_t* const p = q + 4 * e + b;
+        if (p >= lo && p < end) w |= Load::byte(p) << (8 * b);
+      }
+      v[e] = w;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kNT) align_kernel(Copy a, Copy b) {
   dependents_may_start();
   const Copy& k = blockIdx.y == 0 ? a : b;
@@ -201,10 +229,8 @@ __global__ void __launch_bounds__(kNT) align_kernel(Copy a, Copy b) {
     const int at = (int)(i - p * k.d_vecs.d) * 16;
     const uint8_t* const src = k.src + p * k.from + at;
     const int shift = (int)(reinterpret_cast<uintptr_t>(src) & 3);
-    const uint8_t* q = src - shift;
     uint32_t v[5];
-#pragma unroll
-    for (int e = 0; e < 5; ++e) v[e] = q + 4 * e < end ? __ldg(reinterpret_cast<const uint32_t*>(q + 4 * e)) : 0u;
+    words_at<GlobalBytes>(src, k.src, end, v);
     uint4 o;
     o.x = __funnelshift_r(v[0], v[1], 8 * shift);
     o.y = __funnelshift_r(v[1], v[2], 8 * shift);

@@ -1,6 +1,7 @@
 // CPU check of the channels-last backward's plans: the workspace holds what a
-// call from any source lays out in it, and the staged kernels get only rows
-// whose distances their 32-bit steps hold.
+// call from any source lays out in it, the staged kernels get only rows whose
+// distances their 32-bit steps hold, and the aligned copies read no byte
+// outside their tensor.
 #include <cstdio>
 #include "nhwc_bwd.h"
 
@@ -70,7 +71,48 @@ static void check_rows(const Conv& c, bool from_codes) {
          (long long)c.H, (long long)c.W, (int)full, (int)codes);
 }
 
+// the aligned copies' reads: inside the tensor, each byte of a pixel brought
+static uint8_t arena[4096];
+static const uint8_t *inside_lo, *inside_end;
+static bool outside;
+struct Recorded {
+  static uint32_t word(const uint8_t* p) {
+    if (p < inside_lo || p + 4 > inside_end || (uintptr_t)p % 4) outside = true;
+    return (uint32_t)p[0] | (uint32_t)p[1] << 8 | (uint32_t)p[2] << 16 | (uint32_t)p[3] << 24;
+  }
+  static uint32_t byte(const uint8_t* p) {
+    if (p < inside_lo || p >= inside_end) outside = true;
+    return *p;
+  }
+};
+static void check_reads(int offset, int pixels, int from, int bytes) {
+  inside_lo = arena + 64 + offset;
+  inside_end = inside_lo + (pixels - 1) * from + bytes;
+  outside = false;
+  bool same = true;
+  for (int p = 0; p < pixels; ++p)
+    for (int at = 0; at < bytes; at += 16) {
+      const uint8_t* src = inside_lo + p * from + at;
+      uint32_t v[5];
+      nhwc::words_at<Recorded>(src, inside_lo, inside_end, v);
+      const int shift = (int)((uintptr_t)src & 3);
+      for (int b = 0; b < 16 && at + b < bytes; ++b)
+        same &= (uint8_t)(v[(b + shift) / 4] >> (8 * ((b + shift) % 4))) == src[b];
+    }
+  ++checks;
+  if (outside || !same) {
+    ++fails;
+    printf("FAIL reads at offset %d, %d pixels of %d bytes %d apart: outside %d, same %d\n", offset, pixels, bytes, from,
+           (int)outside, (int)same);
+  }
+}
+
 int main() {
+  for (int i = 0; i < 4096; ++i) arena[i] = (uint8_t)(i * 37 + (i >> 8));
+  for (int offset = 0; offset < 8; ++offset)
+    for (int pixels : {1, 2, 7})
+      for (int bytes = 1; bytes < 90; ++bytes)
+        for (int gap : {0, 1, 6, 40}) check_reads(offset, pixels, bytes + gap, bytes);
   for (int s : {1, 2}) {
     check_rows(mk(1, 1 << 14, 2, 1 << 21, 3, s, 1, DWCONV_BF16), false);
     check_rows(mk(1, 1 << 14, 2, (1 << 21) - 1, 3, s, 1, DWCONV_BF16), true);

@@ -64,3 +64,26 @@ def test_conv_backward_of_tall_images(dtype, C, H, W, k, s, kind):
         x8 = B.make_act8(kind, 32, codes, scales)
     out = conv_backward(d, None if x8 else x, gy, w, dtype, x8)
     check_conv(out, d, R.decode(codes, scales, 32) if x8 else x, gy, w, dtype, 4096 + 256, f"{kind} {C}x{H}x{W} k{k}")
+
+
+# ---- layer backward: codes at any byte -------------------------------------
+
+
+def at_byte(t, by):
+    """A contiguous copy of a one-byte tensor that starts `by` bytes after an allocation."""
+    buf = torch.empty(t.numel() + by, dtype=torch.uint8, device="cuda")
+    v = buf[by:].view(t.shape)
+    v.copy_(t.view(torch.uint8))
+    return v.view(t.dtype)
+
+
+@pytest.mark.parametrize("by", [1, 2, 3, 4, 8])
+@pytest.mark.parametrize("N,C,H,W,k,s", [(2, 33, 9, 12, 3, 1), (2, 64, 13, 11, 3, 2), (3, 17, 12, 10, 5, 1), (1, 20, 15, 16, 5, 2),
+                                         (1, 287, 8, 21, 7, 1), (2, 48, 19, 18, 7, 2), (2, 6, 9, 8, 3, 1)])
+def test_conv_backward_from_codes_at_any_byte(N, C, H, W, k, s, by):
+    """Copied to aligned pixels where channels are off 16 bytes, read by the direct kernels where only the pointer is."""
+    for dtype, kind in (("bf16", "i8"), ("f32", "e4m3")):
+        d, x, w, gy = conv_inputs(N, C, H, W, k, s, k // 2, 1, 1, dtype, C + by)
+        codes, scales = R.encode(x, kind, 32)
+        out = conv_backward(d, None, gy, w, dtype, B.make_act8(kind, 32, at_byte(codes, by), scales))
+        check_conv(out, d, R.decode(codes, scales, 32), gy, w, dtype, 512, f"{dtype} {kind} at {by}")

@@ -5,7 +5,8 @@ arithmetic; it prints its failures and exits non-zero on any:
   * check_nhwc_bwd.cu: the layer backward's workspace holds the sums and the
     aligned copies of a call from any source (the input, its codes), over
     images of up to 70000 rows; rows whose scales lie 2^32 bytes apart are
-    left to the kernel that steps over them in 64 bits.
+    left to the kernel that steps over them in 64 bits; the aligned copies
+    bring every byte of a pixel and read none outside the tensor.
 """
 import os
 import shutil
