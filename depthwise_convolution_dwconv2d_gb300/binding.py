@@ -181,7 +181,7 @@ def load():
 
 
 def _ptr(t):
-    """The device address of a tensor, an address or None."""
+    """The device address of a tensor (anything with ``data_ptr``), an address or None."""
     if t is None or isinstance(t, int):
         return t
     try:
@@ -189,7 +189,11 @@ def _ptr(t):
             raise ValueError("libdwconv needs contiguous tensors")
         return t.data_ptr()
     except AttributeError:
-        raise TypeError(f"cannot pass {type(t).__name__} as a device pointer") from None
+        if not hasattr(t, "data_ptr"):
+            raise TypeError(f"cannot pass {type(t).__name__} as a device pointer") from None
+        if hasattr(t, "is_contiguous"):
+            raise
+    return t.data_ptr()
 
 
 _raw_stream = None  # (device -> address of its current stream, current device), once CUDA is up
