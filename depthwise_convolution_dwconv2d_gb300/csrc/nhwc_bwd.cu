@@ -55,7 +55,11 @@ __device__ __forceinline__ float input_at(const T* x, const Act8& t, int64_t row
   }
 }
 
-// ws[chunk][oc][tap] (tap == taps: bias): 32 channels x 8 pixel lanes per block
+// ws[chunk][oc][tap] (tap == taps: bias): 32 channels x 8 pixel lanes per
+// block, and a sum for every kRun pixels: where channels and taps alone fill
+// the GPU there are few chunks, and a chain of n additions of like terms can
+// be off by n / 4 * 2^-24 of the sum
+constexpr int64_t kRun = 1024 * (kNT / 32);
 template <typename T, int SRC>
 __global__ void __launch_bounds__(kNT)
 gw_generic_kernel(Conv c, int64_t pixels, int64_t per_chunk, const T* __restrict__ x, Act8 t,
@@ -71,17 +75,22 @@ gw_generic_kernel(Conv c, int64_t pixels, int64_t per_chunk, const T* __restrict
   float acc = 0.f;
   if (oc < OC) {
     const int64_t a = (int64_t)(tap / c.kw) * c.dh - c.ph, b = (int64_t)(tap % c.kw) * c.dw - c.pw;
-    for (int64_t p = p0 + (threadIdx.x >> 5); p < p1; p += kNT / 32) {
-      const float g = ld(gy + p * c.ctot + c.off + oc);
-      if (tap == taps) {
-        acc += g;
-        continue;
+    for (int64_t r0 = p0; r0 < p1; r0 += kRun) {
+      const int64_t r1 = min(r0 + kRun, p1);
+      float run = 0.f;
+      for (int64_t p = r0 + (threadIdx.x >> 5); p < r1; p += kNT / 32) {
+        const float g = ld(gy + p * c.ctot + c.off + oc);
+        if (tap == taps) {
+          run += g;
+          continue;
+        }
+        const int64_t q = p % c.Wo, o = p / c.Wo;
+        const int64_t n = o / c.Ho;
+        const int64_t ih = (o - n * c.Ho) * c.sh + a, iw = q * c.sw + b;
+        if (ih < 0 || ih >= c.H || iw < 0 || iw >= c.W) continue;
+        run = fmaf(g, input_at<T, SRC>(x, t, (n * c.H + ih) * c.W + iw, c.C, oc / c.m), run);
       }
-      const int64_t q = p % c.Wo, o = p / c.Wo;
-      const int64_t n = o / c.Ho;
-      const int64_t ih = (o - n * c.Ho) * c.sh + a, iw = q * c.sw + b;
-      if (ih < 0 || ih >= c.H || iw < 0 || iw >= c.W) continue;
-      acc = fmaf(g, input_at<T, SRC>(x, t, (n * c.H + ih) * c.W + iw, c.C, oc / c.m), acc);
+      acc += run;
     }
   }
   sm[threadIdx.x] = acc;

@@ -28,6 +28,10 @@ namespace {
 
 constexpr int kNT = 256;
 
+// Rows that a thread adds up one after another, as far as chunks go. A chain of n fp32 additions of like terms can be off
+// by n / 4 * 2^-24 of the sum (constant terms), so samples that would fill the GPU with a long chunk each are cut too.
+constexpr int64_t kChain = 4096;
+
 // How the split kernels cut a sample: channels into slices of tc vectors,
 // pixels into chunks.
 struct Cut {
@@ -47,7 +51,8 @@ Cut plan_cut(const Norm& g, int V) {
   k.slices = (vecs + k.tc - 1) / k.tc;
   // enough blocks to fill the GPU a few times over, chunks of at least 4 rows per row lane
   int64_t want = (152 * 8 + g.N * k.slices - 1) / (g.N * k.slices);
-  const int64_t most = (g.P + 4 * k.rl - 1) / (4 * k.rl);
+  const int64_t chains = (g.P + kChain * k.rl - 1) / (kChain * k.rl), most = (g.P + 4 * k.rl - 1) / (4 * k.rl);
+  if (want < chains) want = chains;
   if (want > most) want = most;
   if (want > 256) want = 256;
   if (want < 1) want = 1;
@@ -327,7 +332,8 @@ group_sums_kernel(Norm g, Cut k, const float2* __restrict__ part, const T* __res
 }
 
 // ggamma, gbeta from entries = N * chunks partial sums per channel: 32
-// channels per block, 8 row lanes
+// channels per block, 8 row lanes, a sum for every kRun entries
+constexpr int64_t kRun = 1024 * (kNT / 32);
 template <typename T>
 __global__ void __launch_bounds__(kNT)
 param_grad_kernel(int C, int64_t entries, const float2* __restrict__ part, T* __restrict__ ggamma,
@@ -336,13 +342,17 @@ param_grad_kernel(int C, int64_t entries, const float2* __restrict__ part, T* __
   wait_for_previous();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31);
   float a = 0.f, b = 0.f;
-  if (c < C) {
+  for (int64_t i0 = 0; i0 < entries && c < C; i0 += kRun) {
+    const int64_t i1 = min(i0 + kRun, entries);
+    float u = 0.f, v = 0.f;
 #pragma unroll 8
-    for (int64_t i = threadIdx.x >> 5; i < entries; i += kNT / 32) {
+    for (int64_t i = i0 + (threadIdx.x >> 5); i < i1; i += kNT / 32) {
       const float2 p = part[i * C + c];
-      a += p.x;
-      b += p.y;
+      u += p.x;
+      v += p.y;
     }
+    a += u;
+    b += v;
   }
   sm[threadIdx.x] = make_float2(a, b);
   __syncthreads();
@@ -535,11 +545,12 @@ constexpr int kStreamBlocks = 3;
 
 // Chunks of pixels for the stream kernels: one wave of blocks (at
 // 2x256x256x64 fp32: 29 us at six blocks per SM, 27 at four, 23 at three), at
-// least four rows for a row lane.
+// least four rows for a row lane and at most kChain.
 bool plan_stream(const Norm& g, int es, int x_bytes, slab::Plan* k) {
   const int64_t units = g.N * k->slices;
   int64_t parts = (152 * kStreamBlocks + units - 1) / units;
-  const int64_t most = (g.P + 4 * k->rl - 1) / (4 * k->rl);
+  const int64_t chains = (g.P + kChain * k->rl - 1) / (kChain * k->rl), most = (g.P + 4 * k->rl - 1) / (4 * k->rl);
+  if (parts < chains) parts = chains;
   if (parts > most) parts = most;
   if (parts > slab::kMaxParts) parts = slab::kMaxParts;
   const int64_t rows = (g.P + parts - 1) / parts;

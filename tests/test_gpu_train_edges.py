@@ -87,3 +87,41 @@ def test_conv_backward_from_codes_at_any_byte(N, C, H, W, k, s, by):
         codes, scales = R.encode(x, kind, 32)
         out = conv_backward(d, None, gy, w, dtype, B.make_act8(kind, 32, at_byte(codes, by), scales))
         check_conv(out, d, R.decode(codes, scales, 32), gy, w, dtype, 512, f"{dtype} {kind} at {by}")
+
+
+# ---- long sums -------------------------------------------------------------
+
+
+def test_conv_backward_filter_gradient_of_many_pixels():
+    """131072 pixels of constant terms, in one chunk (1024 channels and 82 sums of them fill the GPU), a 9x9 filter: 1024
+    additions in a run, 16 runs, 8 lanes. One chain of 16384 is off by up to 4000 * 2^-24."""
+    C, H, W, k = 1024, 264, 520, 9
+    d = B.make_desc(1, C, H, W, k, 1, 0, 1, 1, "f32")
+    g = gen(41)
+    vx, vg = (torch.rand(C, generator=g, device="cuda") * 0.3 + 0.2 for _ in range(2))
+    x, gy = vx.expand(1, H, W, C).contiguous(), vg.expand(1, H - 8, W - 8, C).contiguous()
+    gw, gb = filled(C, k, k), filled(C)
+    room = Guarded(B.dwconv2d_bwd_nhwc_workspace_size(d))
+    B.dwconv2d_bwd_nhwc(d, x, gy, None, None, gw, gb, room.ws)
+    room.check()
+    n = (H - 8) * (W - 8)
+    rgw, rgb = (n * vx.double() * vg.double())[:, None, None].expand(C, k, k), n * vg.double()
+    R.within(gw, rgw, R.EPS32 * 1056 * rgw, "f32", "gw")
+    R.within(gb, rgb, R.EPS32 * 1056 * rgb, "f32", "gb")
+
+
+def test_norm_parameter_gradients_of_many_samples():
+    """131075 samples of one pixel: as above, one sum per sample."""
+    N, C, G = 131075, 32, 4
+    d = B.make_norm_desc(N, 1, 1, C, G, "none", 1e-5, "f32")
+    g = gen(42)
+    vx, vg = (torch.rand(C, generator=g, device="cuda") * 0.3 + 0.2 for _ in range(2))
+    x, gy = vx.expand(N, 1, 1, C).contiguous(), vg.expand(N, 1, 1, C).contiguous()
+    mean, rstd = torch.zeros(N, G, device="cuda"), torch.ones(N, G, device="cuda")
+    gg, gb = filled(C), filled(C)
+    room = Guarded(B.dwconv2d_group_norm_nhwc_workspace_size(d, 1))
+    B.dwconv2d_group_norm_nhwc_bwd(d, x, gy, None, None, mean, rstd, None, gg, gb, room.ws)
+    room.check()
+    rgg, rgb = N * vx.double() * vg.double(), N * vg.double()
+    R.within(gg, rgg, R.EPS32 * 1056 * rgg, "f32", "ggamma")
+    R.within(gb, rgb, R.EPS32 * 1056 * rgb, "f32", "gbeta")

@@ -6,7 +6,10 @@ arithmetic; it prints its failures and exits non-zero on any:
     aligned copies of a call from any source (the input, its codes), over
     images of up to 70000 rows; rows whose scales lie 2^32 bytes apart are
     left to the kernel that steps over them in 64 bits; the aligned copies
-    bring every byte of a pixel and read none outside the tensor.
+    bring every byte of a pixel and read none outside the tensor;
+  * check_norm.cu: the group norm's threads add up at most 4096 rows each as
+    long as the kernels take more chunks, and every family's sums lie inside
+    the workspace and the shared memory.
 """
 import os
 import shutil
@@ -18,7 +21,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "depthwise_convolution_dwconv2d_gb300", "csrc")
 
 
-@pytest.mark.parametrize("name", ["check_nhwc_bwd"])
+@pytest.mark.parametrize("name", ["check_nhwc_bwd", "check_norm"])
 def test_planner(tmp_path, name):
     nvcc = shutil.which("nvcc") or ("/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else None)
     if nvcc is None:
