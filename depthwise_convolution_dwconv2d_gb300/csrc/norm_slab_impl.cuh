@@ -18,9 +18,12 @@
 // sums for its groups and writes the outputs. The same code in three modes.
 //
 // The variance is not taken from sums of squares of x: a block sums x - s and
-// (x - s)^2 about the values s of its first pixel, one per channel, turns
-// them into a mean and squares about that mean, and joins channels and blocks
-// by the parallel form of the two (see norm.cu). Every order is fixed.
+// (x - s)^2 about one value s per channel, turns them into a mean and squares
+// about that mean, and joins channels and blocks by the parallel form of the
+// two (see norm.cu). s is the middle one of the values of three of the block's
+// pixels: the sums lose what s is away from the rest, squared, so no single
+// pixel may decide it. The three lie at multiples of the golden section, which
+// no width of an image puts into one of its columns. Every order is fixed.
 //
 // Arithmetic is on pairs of channels (the two lanes of the packed fp32
 // instructions). Rows are fetched by asynchronous copies, a batch ahead.
@@ -88,6 +91,20 @@ __device__ __forceinline__ uint32_t word_of(f32x2 v) {
   } else {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// the middle one of three values, or of three pairs of 16-bit values
+template <typename T>
+__device__ __forceinline__ uint32_t middle_word(uint32_t a, uint32_t b, uint32_t c) {
+  if constexpr (sizeof(T) == 4) {
+    const float x = __uint_as_float(a), y = __uint_as_float(b);
+    return __float_as_uint(fmaxf(fminf(x, y), fminf(fmaxf(x, y), __uint_as_float(c))));
+  } else {
+    typedef typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type P;
+    const P x = *reinterpret_cast<const P*>(&a), y = *reinterpret_cast<const P*>(&b), z = *reinterpret_cast<const P*>(&c);
+    const P m = __hmax2(__hmin2(x, y), __hmin2(__hmax2(x, y), z));
+    return *reinterpret_cast<const uint32_t*>(&m);
   }
 }
 
@@ -170,6 +187,16 @@ struct Lay {
         u[e] = word_of<T>(f[e]);
       }
     }
+    return w;
+  }
+  // per channel the middle one of three values; of a NaN and two others, one of those
+  static __device__ __forceinline__ word middle(word a, word b, word c) {
+    word w;
+    const uint32_t *ua = reinterpret_cast<const uint32_t*>(&a), *ub = reinterpret_cast<const uint32_t*>(&b),
+                   *uc = reinterpret_cast<const uint32_t*>(&c);
+    uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int e = 0; e < (int)sizeof(word) / 4; ++e) u[e] = middle_word<T>(ua[e], ub[e], uc[e]);
     return w;
   }
   // V values of a per-channel tensor from channel c
@@ -393,7 +420,11 @@ fwd_kernel(Norm g, Plan k, const T* __restrict__ x, const T* __restrict__ gamma,
 #pragma unroll
     for (int e = 0; e < NP; ++e) s[e] = d[e] = q[e] = 0;
     if (p.rows > 0) {  // one value per channel, the same for every row lane
-      L::unpack(L::load(x + p.row0 * g.xs + g.xo + p.c, k.vpr, p.nv), s);
+      const T* const rows = x + p.row0 * g.xs + g.xo + p.c;
+      auto pixel = [&](uint32_t part) {  // at part / 2^32 of the share
+        return L::load(rows + (int64_t)__umulhi((uint32_t)p.rows, part) * g.xs, k.vpr, p.nv);
+      };
+      L::unpack(L::middle(pixel(0x3c6ef372u), pixel(0x9e3779b9u), pixel(0xdaa66d2bu)), s);
       if (p.r == 0) {
 #pragma unroll
         for (int e = 0; e < NP; ++e) *reinterpret_cast<f32x2*>(base + p.vl * V + 2 * e) = s[e];

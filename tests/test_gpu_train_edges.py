@@ -125,3 +125,26 @@ def test_norm_parameter_gradients_of_many_samples():
     rgg, rgb = N * vx.double() * vg.double(), N * vg.double()
     R.within(gg, rgg, R.EPS32 * 1056 * rgg, "f32", "ggamma")
     R.within(gb, rgb, R.EPS32 * 1056 * rgb, "f32", "gbeta")
+
+
+# ---- group norm: sums about a value that is not an outlier's ----------------
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,H,W,C,G", [(456, 256, 256, 8, 8), (152, 40, 40, 32, 32), (2, 56, 56, 128, 64), (456, 67, 61, 9, 3)])
+def test_norm_moments_with_the_first_pixel_far_off(N, H, W, C, G, dtype):
+    """All pixels of a channel alike but the first, 1000 away. About any value near the others the sums hold next to
+    nothing but the outlier's own square, so what is left are the roundings of chained additions: 512 rows, 128 row lanes
+    and 8 blocks or less, then channels. About the outlier each of a block's r rows brings its square, up to r / 4 chained
+    roundings of r times the variance."""
+    level = normal(gen(N + C), C, std=0.25).to(R.DT[dtype])
+    x = level.expand(N, H, W, C).contiguous()
+    x[:, 0, 0] = (level.float() + 1000).to(x.dtype)
+    d = B.make_norm_desc(N, H, W, C, G, "none", 1e-5, dtype)
+    y, mean, rstd = torch.empty_like(x), filled(N, G), filled(N, G)
+    room = Guarded(B.dwconv2d_group_norm_nhwc_workspace_size(d, 0))
+    B.dwconv2d_group_norm_nhwc(d, x, None, None, y, mean, rstd, room.ws)
+    room.check()
+    rmean, rrstd = R.moments(x[:1].double(), G, 1e-5)
+    R.within(mean, rmean.expand(N, G), R.EPS32 * 768 * (1 + rmean.abs()).expand(N, G), "f32", "mean")
+    R.within(rstd, rrstd.expand(N, G), R.EPS32 * 768 * rrstd.expand(N, G), "f32", "rstd")
