@@ -5,9 +5,10 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import train_bounds as T
 import train_ref as R
 from depthwise_convolution_dwconv2d_gb300 import binding as B
-from test_gpu_train_nhwc import conv_inputs, filled, gen, normal
+from test_gpu_train_nhwc import NORMS, conv_inputs, filled, gen, new_act8, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +149,93 @@ def test_norm_moments_with_the_first_pixel_far_off(N, H, W, C, G, dtype):
     rmean, rrstd = R.moments(x[:1].double(), G, 1e-5)
     R.within(mean, rmean.expand(N, G), R.EPS32 * 768 * (1 + rmean.abs()).expand(N, G), "f32", "mean")
     R.within(rstd, rrstd.expand(N, G), R.EPS32 * 768 * rrstd.expand(N, G), "f32", "rstd")
+
+
+# ---- group norm: every term of the gradients, from any source ---------------
+
+
+def norm_pass(d, x, gamma, beta, shape, G, dtype, x8=None):
+    y, mean, rstd = filled(*shape, dtype=dtype), filled(shape[0], G), filled(shape[0], G)
+    room = Guarded(B.dwconv2d_group_norm_nhwc_workspace_size(d, 0))
+    B.dwconv2d_group_norm_nhwc(d, x, gamma, beta, y, mean, rstd, room.ws, x8=x8)
+    room.check()
+    return y, mean, rstd
+
+
+def norm_back(d, x, gy, gamma, beta, mean, rstd, dtype, x8=None):
+    out = filled(*gy.shape, dtype=dtype), filled(gy.shape[-1], dtype=dtype), filled(gy.shape[-1], dtype=dtype)
+    room = Guarded(B.dwconv2d_group_norm_nhwc_workspace_size(d, 1))
+    B.dwconv2d_group_norm_nhwc_bwd(d, x, gy, gamma, beta, mean, rstd, *out, room.ws, x8=x8)
+    room.check()
+    return out
+
+
+def check_gradients(out, x, gy, gamma, beta, mean, rstd, act, dtype, what):
+    want, slack = T.backward(*(t.double() for t in (x, gy, gamma, beta, mean, rstd)), act)
+    for name, o, w, s in zip(("gx", "ggamma", "gbeta"), out, want, slack):
+        R.within(o, w, s, dtype, f"{what} {name}")
+
+
+def away_from_kinks(gy, x, gamma, beta, mean, rstd, act):
+    """gy, with no part where rounding may decide the slope."""
+    if act not in ("relu", "relu6"):
+        return gy
+    C = x.shape[-1]
+    u = (x.double() - R.per_channel(mean, C)) * R.per_channel(rstd, C) * gamma.double() + beta.double()
+    return torch.where(u.abs() * (u - 6).abs() < 1e-4, torch.zeros_like(gy), gy)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "relu6", "silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_norm_to_its_roundings(dtype, act):
+    """y from the kernel's own moments, and gradients of a gy that gives both sums of a group the size of the term beside
+    them: slabs, streams and slices wider than a block."""
+    for i, (N, H, W, C, G) in enumerate(NORMS):
+        what = f"{N}x{H}x{W}x{C} G{G}"
+        x, gamma, beta, gy = T.inputs(N, H, W, C, G, dtype, i, "cuda")
+        d = B.make_norm_desc(N, H, W, C, G, act, 1e-5, dtype)
+        y, mean, rstd = norm_pass(d, x, gamma, beta, (N, H, W, C), G, dtype)
+        ry, ey = T.forward(*(t.double() for t in (x, gamma, beta, mean, rstd)), act)
+        R.within(y, ry, ey, dtype, what + " y")
+        gy = away_from_kinks(gy, x, gamma, beta, mean, rstd, act)
+        check_gradients(norm_back(d, x, gy, gamma, beta, mean, rstd, dtype), x, gy, gamma, beta, mean, rstd, act, dtype, what)
+
+
+@pytest.mark.parametrize("by", [0, 1, 2, 4])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_norm_from_codes_at_any_byte(dtype, by):
+    """The forward writes its checkpoint, and the backward reads it, at any byte."""
+    for i, (N, H, W, C, G) in enumerate(NORMS):
+        kind, block = (("i8", 32), ("e4m3", 64), ("i8", 128))[i % 3]
+        what = f"{N}x{H}x{W}x{C} G{G} {kind} at {by}"
+        x, gamma, beta, gy = T.inputs(N, H, W, C, G, dtype, 40 + i, "cuda")
+        d = B.make_norm_desc(N, H, W, C, G, "silu", 1e-5, dtype)
+        fresh = new_act8((N, H, W, C), kind, block)
+        codes, scales = at_byte(fresh.tensors[0], by), fresh.tensors[1]
+        x8 = B.make_act8(kind, block, codes, scales)
+        y, mean, rstd = norm_pass(d, x, gamma, beta, (N, H, W, C), G, dtype, x8)
+        ry, ey = T.forward(*(t.double() for t in (x, gamma, beta, mean, rstd)), "silu")
+        R.within(y, ry, ey, dtype, what + " y")
+        want, wscales = R.encode(x, kind, block)
+        assert torch.equal(codes.view(torch.uint8), want.view(torch.uint8)) and torch.equal(scales, wscales), what
+        out = norm_back(d, None, gy, gamma, beta, mean, rstd, dtype, x8)
+        check_gradients(out, R.decode(want, wscales, block), gy, gamma, beta, mean, rstd, "silu", dtype, what)
+
+
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+@pytest.mark.parametrize("by", [1, 2, 4, 12])
+def test_act8_codes_at_any_byte(kind, by):
+    """Bit for bit the definition's codes and values; the bytes before and behind them stay."""
+    for dtype, rows, C, block in (("bf16", 33, 64, 32), ("f32", 7, 40, 32), ("f16", 257, 8, 64), ("bf16", 5, 200, 128), ("f32", 3, 33, 32)):
+        x = normal(gen(by + C), rows, C, dtype=dtype)
+        buf = torch.full((by + rows * C + 32,), 0x55, dtype=torch.uint8, device="cuda")
+        codes = buf[by:by + rows * C].view(rows, C)
+        scales = torch.empty(rows, -(-C // block), device="cuda")
+        x8 = B.make_act8(kind, block, codes, scales)
+        B.dwconv_act8_encode(x, x8)
+        want, wscales = R.encode(x, kind, block)
+        assert torch.equal(codes, want.view(torch.uint8)) and torch.equal(scales, wscales), (dtype, rows, C)
+        assert bool((buf[:by] == 0x55).all()) and bool((buf[by + rows * C:] == 0x55).all())
+        y = filled(rows, C, dtype=dtype)
+        B.dwconv_act8_decode(x8, y)
+        assert torch.equal(y, R.decode(want, wscales, block).float().to(R.DT[dtype])), (dtype, rows, C)
