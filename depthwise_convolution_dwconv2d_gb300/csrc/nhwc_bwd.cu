@@ -55,11 +55,7 @@ __device__ __forceinline__ float input_at(const T* x, const Act8& t, int64_t row
   }
 }
 
-// ws[chunk][oc][tap] (tap == taps: bias): 32 channels x 8 pixel lanes per
-// block, and a sum for every kRun pixels: where channels and taps alone fill
-// the GPU there are few chunks, and a chain of n additions of like terms can
-// be off by n / 4 * 2^-24 of the sum
-constexpr int64_t kRun = 1024 * (kNT / 32);
+// ws[chunk][oc][tap] (tap == taps: bias): 32 channels x 8 pixel lanes per block
 template <typename T, int SRC>
 __global__ void __launch_bounds__(kNT)
 gw_generic_kernel(Conv c, int64_t pixels, int64_t per_chunk, const T* __restrict__ x, Act8 t,
@@ -75,22 +71,17 @@ gw_generic_kernel(Conv c, int64_t pixels, int64_t per_chunk, const T* __restrict
   float acc = 0.f;
   if (oc < OC) {
     const int64_t a = (int64_t)(tap / c.kw) * c.dh - c.ph, b = (int64_t)(tap % c.kw) * c.dw - c.pw;
-    for (int64_t r0 = p0; r0 < p1; r0 += kRun) {
-      const int64_t r1 = min(r0 + kRun, p1);
-      float run = 0.f;
-      for (int64_t p = r0 + (threadIdx.x >> 5); p < r1; p += kNT / 32) {
-        const float g = ld(gy + p * c.ctot + c.off + oc);
-        if (tap == taps) {
-          run += g;
-          continue;
-        }
-        const int64_t q = p % c.Wo, o = p / c.Wo;
-        const int64_t n = o / c.Ho;
-        const int64_t ih = (o - n * c.Ho) * c.sh + a, iw = q * c.sw + b;
-        if (ih < 0 || ih >= c.H || iw < 0 || iw >= c.W) continue;
-        run = fmaf(g, input_at<T, SRC>(x, t, (n * c.H + ih) * c.W + iw, c.C, oc / c.m), run);
+    for (int64_t p = p0 + (threadIdx.x >> 5); p < p1; p += kNT / 32) {
+      const float g = ld(gy + p * c.ctot + c.off + oc);
+      if (tap == taps) {
+        acc += g;
+        continue;
       }
-      acc += run;
+      const int64_t q = p % c.Wo, o = p / c.Wo;
+      const int64_t n = o / c.Ho;
+      const int64_t ih = (o - n * c.Ho) * c.sh + a, iw = q * c.sw + b;
+      if (ih < 0 || ih >= c.H || iw < 0 || iw >= c.W) continue;
+      acc = fmaf(g, input_at<T, SRC>(x, t, (n * c.H + ih) * c.W + iw, c.C, oc / c.m), acc);
     }
   }
   sm[threadIdx.x] = acc;
@@ -104,16 +95,25 @@ gw_generic_kernel(Conv c, int64_t pixels, int64_t per_chunk, const T* __restrict
 int64_t out_pixels(const Conv& c) { return c.N * c.Ho * c.Wo; }
 
 // Chunks of output pixels: enough blocks to fill the GPU, at least 64 pixels
-// each, partial sums of at most 64 MB where that leaves two chunks or more.
+// each, partial sums of at most 64 MB where that leaves two chunks or more;
+// and no more than 1024 pixels of a lane, as far as 4096 chunks and 1 GB go,
+// since a chain of n additions of like terms can be off by n / 4 * 2^-24 of
+// the sum. (64x56x56x128 9x9 bf16 from codes: 19.3 ms with the last rule, 20.6
+// without; a second sum inside the kernel cost 4 to 12 % of the call.)
 int generic_chunks(const Conv& c) {
   if (c.N == 0) return 0;
-  const int64_t taps1 = (int64_t)c.kh * c.kw + 1;
+  const int64_t taps1 = (int64_t)c.kh * c.kw + 1, one = c.C * c.m * taps1 * 4;
   const int64_t blocks = (c.C * c.m + 31) / 32 * taps1;
   int64_t n = (152 * 8 + blocks - 1) / blocks;
   const int64_t most = (out_pixels(c) + 63) / 64;
-  const int64_t room = (int64_t(64) << 20) / (c.C * c.m * taps1 * 4);
+  const int64_t room = (int64_t(64) << 20) / one, wide = (int64_t(1) << 30) / one;
   if (n > most) n = most;
   if (n > room) n = room;
+  constexpr int64_t kRun = 1024 * (kNT / 32);
+  int64_t runs = (out_pixels(c) + kRun - 1) / kRun;
+  if (runs > wide) runs = wide;
+  if (runs > 4096) runs = 4096;  // a second pass adds them up in one chain
+  if (n < runs) n = runs;
   if (n < 1) n = 1;
   return (int)n;
 }

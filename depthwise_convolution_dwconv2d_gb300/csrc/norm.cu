@@ -332,8 +332,8 @@ group_sums_kernel(Norm g, Cut k, const float2* __restrict__ part, const T* __res
 }
 
 // ggamma, gbeta from entries = N * chunks partial sums per channel: 32
-// channels per block, 8 row lanes, a sum for every kRun entries
-constexpr int64_t kRun = 1024 * (kNT / 32);
+// channels per block, 8 row lanes, a sum for every kRun entries of a lane
+constexpr int kRun = 1024;
 template <typename T>
 __global__ void __launch_bounds__(kNT)
 param_grad_kernel(int C, int64_t entries, const float2* __restrict__ part, T* __restrict__ ggamma,
@@ -342,17 +342,21 @@ param_grad_kernel(int C, int64_t entries, const float2* __restrict__ part, T* __
   wait_for_previous();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31);
   float a = 0.f, b = 0.f;
-  for (int64_t i0 = 0; i0 < entries && c < C; i0 += kRun) {
-    const int64_t i1 = min(i0 + kRun, entries);
-    float u = 0.f, v = 0.f;
+  if (c < C) {
+    const float2* p = part + (threadIdx.x >> 5) * (int64_t)C + c;
+    const int64_t step = (int64_t)(kNT / 32) * C;
+    for (int64_t left = (entries - (threadIdx.x >> 5) + kNT / 32 - 1) / (kNT / 32); left > 0; left -= kRun) {
+      const int n = (int)min(left, (int64_t)kRun);
+      float u = 0.f, v = 0.f;
 #pragma unroll 8
-    for (int64_t i = i0 + (threadIdx.x >> 5); i < i1; i += kNT / 32) {
-      const float2 p = part[i * C + c];
-      u += p.x;
-      v += p.y;
+      for (int i = 0; i < n; ++i, p += step) {
+        const float2 f = *p;
+        u += f.x;
+        v += f.y;
+      }
+      a += u;
+      b += v;
     }
-    a += u;
-    b += v;
   }
   sm[threadIdx.x] = make_float2(a, b);
   __syncthreads();

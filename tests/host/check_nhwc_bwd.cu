@@ -1,7 +1,7 @@
 // CPU check of the channels-last backward's plans: the workspace holds what a
 // call from any source lays out in it, the staged kernels get only rows whose
-// distances their 32-bit steps hold, and the aligned copies read no byte
-// outside their tensor.
+// distances their 32-bit steps hold, the aligned copies read no byte outside
+// their tensor, and the generic filter gradient chains few additions.
 #include <cstdio>
 #include "nhwc_bwd.h"
 
@@ -107,7 +107,25 @@ static void check_reads(int offset, int pixels, int from, int bytes) {
   }
 }
 
+// the generic filter gradient: additions of a lane, chunks of a grid, and the workspace of its sums
+static void check_generic(const Conv& c) {
+  const int64_t chunks = nhwc::generic_chunks(c), per = (nhwc::out_pixels(c) + chunks - 1) / chunks;
+  const int64_t one = c.C * c.m * (c.kh * c.kw + 1) * 4;
+  ++checks;
+  const bool full = chunks == 4096 || (chunks + 1) * one > (int64_t(1) << 30);
+  if ((per + 7) / 8 <= 1024 || full)
+    if (chunks <= 4096 && nhwc::bwd_workspace_bytes(c) >= (size_t)(chunks * one)) return;
+  ++fails;
+  printf("FAIL generic N=%lld C=%lld H=%lld W=%lld k=%d: %lld chunks of %lld pixels, workspace %zu\n", (long long)c.N,
+         (long long)c.C, (long long)c.H, (long long)c.W, c.kh, (long long)chunks, (long long)per, nhwc::bwd_workspace_bytes(c));
+}
+
 int main() {
+  for (int64_t N : {1, 5, 64})
+    for (int64_t C : {1, 40, 1024, 40000})
+      for (int64_t side : {9, 31, 300, 3000})
+        for (int k : {1, 4, 9, 31})
+          if (side >= k) check_generic(mk(N, C, side, side + 1, k, 1, 0, DWCONV_F32));
   for (int i = 0; i < 4096; ++i) arena[i] = (uint8_t)(i * 37 + (i >> 8));
   for (int offset = 0; offset < 8; ++offset)
     for (int pixels : {1, 2, 7})

@@ -94,8 +94,8 @@ def test_conv_backward_from_codes_at_any_byte(N, C, H, W, k, s, by):
 
 
 def test_conv_backward_filter_gradient_of_many_pixels():
-    """131072 pixels of constant terms, in one chunk (1024 channels and 82 sums of them fill the GPU), a 9x9 filter: 1024
-    additions in a run, 16 runs, 8 lanes. One chain of 16384 is off by up to 4000 * 2^-24."""
+    """131072 pixels of constant terms, a 9x9 filter (1024 channels and 82 sums of them fill the GPU with one chunk): 1024
+    additions of a lane, 8 lanes, 16 chunks. One chain of 16384 is off by up to 4000 * 2^-24."""
     C, H, W, k = 1024, 264, 520, 9
     d = B.make_desc(1, C, H, W, k, 1, 0, 1, 1, "f32")
     g = gen(41)
@@ -112,7 +112,7 @@ def test_conv_backward_filter_gradient_of_many_pixels():
 
 
 def test_norm_parameter_gradients_of_many_samples():
-    """131075 samples of one pixel: as above, one sum per sample."""
+    """131075 samples of one pixel, a sum of each: 1024 additions in a run, 17 runs, 8 lanes."""
     N, C, G = 131075, 32, 4
     d = B.make_norm_desc(N, 1, 1, C, G, "none", 1e-5, "f32")
     g = gen(42)

@@ -6,7 +6,8 @@ arithmetic; it prints its failures and exits non-zero on any:
     aligned copies of a call from any source (the input, its codes), over
     images of up to 70000 rows; rows whose scales lie 2^32 bytes apart are
     left to the kernel that steps over them in 64 bits; the aligned copies
-    bring every byte of a pixel and read none outside the tensor;
+    bring every byte of a pixel and read none outside the tensor; a lane of
+    the generic filter gradient adds up at most 1024 pixels;
   * check_norm.cu: the group norm's threads add up at most 4096 rows each as
     long as the kernels take more chunks, and every family's sums lie inside
     the workspace and the shared memory.
