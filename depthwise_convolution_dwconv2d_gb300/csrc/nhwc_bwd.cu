@@ -403,8 +403,9 @@ bool plan_staged(const Conv& c, int src, Staged* out) {
   const bool ring = K == 3;
   const int px = ring ? 4 : tile_px(K), step = ring ? 1 : 2 / S, blocks = ring ? kStagedBlocks : K == 5 ? 4 : 3;
   // A tile has 32 channels at least. With fewer the direct kernels' narrower blocks win sooner or later: 3x3 bf16 at 64
-  // samples, 8 channels 23 us against 56, 24 the same; 5x5 bf16, 24 channels 39 against 23, 9 channels 49 against 31;
-  // 7x7, 17 channels 117 against 64, 12 channels 29 against 31.
+  // samples, 8 channels 23 us (direct) against 56 (staged), 24 the same; 5x5 bf16, 24 channels 39 against 23, 9 channels 49
+  // against 31; 7x7, 17 channels 117 against 64, 12 channels 29 against 31: one bound for both serves 7x7 with 9 to about
+  // 12 channels a little worse.
   if (c.C < (K == 3 ? 24 : 9)) return false;
   // The 3x3 kernel steps from a row's scales to the next row's by 32 bits of bytes: longer rows (2^35 values from blocks
   // of 32) take the direct kernel.

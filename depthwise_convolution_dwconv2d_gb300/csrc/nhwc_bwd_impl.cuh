@@ -210,7 +210,8 @@ __device__ __forceinline__ void join_lanes(int ct_log, const f32x2* acc, int C, 
 // are issued before this step's arithmetic. It serves what the staged kernel
 // does not: fewer than 24 channels, pointers off 16 bytes. Masks, addresses
 // and scales make six instructions of every product: 77 us at 64x56x56x128
-// bf16 from integer codes (1.7 TB/s), where the staged kernel takes 41.
+// bf16 from integer codes (1.7 TB/s), where the staged kernel takes 41. At
+// stride 1 the fp32 forms spill 212 to 296 bytes of a thread.
 template <typename T, int SRC, int S, bool PAIR>
 __global__ void __launch_bounds__(kRingThreads, kRingBlocks)
 ring3_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restrict__ gy, const T* __restrict__ w,
@@ -342,9 +343,10 @@ ring3_kernel(Conv c, Geom g, const T* __restrict__ x, Act8 x8, const T* __restri
 // stage is slot i, and a stage costs one barrier and one wait. All lanes of a
 // block walk the same rows.
 //
-// Bound by issue: 64x56x56x128 bf16 from integer codes takes 41 us (3.2 TB/s
-// of the floor's bytes, 0.48 of the measured copy; 22.6 TFLOP/s) for 24.9 M
-// warp instructions, about 190 for the 78 packed products of a row of four
+// Bound by latency with 14 warps an SM: 64x56x56x128 bf16 from integer codes
+// takes 41 us (3.2 TB/s of the floor's bytes, 0.48 of the measured copy; 22.6
+// TFLOP/s), issue active 55 % of the time, fixed waits the first stall (27 %),
+// for 24.9 M warp instructions, about 190 for the 78 packed products of a row of four
 // pixels (unpacking, decoding, stores and the item's start are the rest);
 // fp32 at 128 samples, with nothing to unpack, runs at 5.9 TB/s, at the
 // memory. Four blocks of four warps per SM at up to 128 registers: two of
@@ -580,7 +582,8 @@ staged3_kernel(Conv c, Staged g, const __grid_constant__ CUtensorMap map_gy, con
 // that they meet once (from L1 after the first step that meets it), for up to
 // 2 K^2 PX products. Plain loads, for what the staged tiles do not serve: two
 // blocks per SM, since at three (168 registers) the 7x7 gradient spills (74
-// us against 51 at 5x45x51x96 fp32).
+// us against 51 at 5x45x51x96 fp32); at two, 7x7 at stride 1 spills 92 to 108
+// bytes in bf16, 20 in fp32.
 template <typename T, int SRC, int K, int S, bool GW, bool PAIR>
 __device__ __forceinline__ void block_walk(const Conv& c, const Geom& g, const T* __restrict__ x, const Act8& x8,
                                            const T* __restrict__ gy, const T* __restrict__ w, T* __restrict__ gx,

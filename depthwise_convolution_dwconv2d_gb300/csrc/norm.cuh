@@ -58,7 +58,7 @@ __device__ __forceinline__ float affine(float xh, float gamma, float beta) {
 constexpr float kGelu = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kCubic = 0.044715f;
 
-// 2^v and 1 / v by the special-function unit: a few units in the last place
+// 2^v and 1 / v by the special-function unit: 2 and 1 units in the last place, results below 2^-126 flushed to 0
 __device__ __forceinline__ float exp2_fast(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -77,7 +77,9 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return c;
 }
 
-// 1 / (1 + exp(-c v)) of both lanes; c2 = -c log2(e)
+// 1 / (1 + exp(-c v)) of both lanes; c2 = -c log2(e). The product is rounded
+// before the power is taken, so far out on the negative side the result is
+// off by about |c v| * 2^-24 of itself.
 __device__ __forceinline__ f32x2 sigmoid2(f32x2 v, float c2) {
   float a, b;
   unpack_f32x2(mul_f32x2(v, both(c2)), a, b);

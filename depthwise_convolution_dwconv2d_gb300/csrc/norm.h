@@ -17,7 +17,7 @@ struct Norm {
   int64_t ys, yo;     // the same of y
 };
 
-// "slab" or "split"; a function of the descriptor alone
+// "slab", "stream" or "split"; a function of the descriptor alone
 const char* plan_name(const Norm& g, int pass);
 size_t workspace_bytes(const Norm& g, int pass);
 

@@ -27,12 +27,14 @@
 //
 // Arithmetic is on pairs of channels (the two lanes of the packed fp32
 // instructions). Rows are fetched by asynchronous copies, a batch ahead.
-// What bounds the kernels is issue, at 0.54 of the rate with 24 warps an SM:
-// 64x56x56x128 bf16, 32 groups, SiLU takes 48 us forward with its checkpoint
-// (2.7 TB/s of the floor's bytes) and 65 backward from it (2.0), 28.8 and
-// 37.3 M warp instructions, of which about 900 per warp are a block's start,
-// joins and cluster barrier; 64x28x28x256 bf16, 16 groups, ReLU 31 us
-// backward (2.4 TB/s). Streamed, 2x256x256x64 fp32 takes 12 + 15 us (the
+// What bounds the kernels is latency with few warps and a block's fixed cost:
+// issue is active 53 to 61 % of the time and DRAM 18 to 21 %, a fifth of the
+// warps' time are fixed waits and a tenth to a sixth shared memory's, the last
+// wave of blocks is part full, and about 900 instructions per warp are a
+// block's start, joins and cluster barrier. 64x56x56x128 bf16, 32 groups, SiLU
+// takes 49 us forward with its checkpoint (2.7 TB/s of the floor's bytes) and
+// 65 backward from it (2.0), 29.0 and 37.3 M warp instructions; 64x28x28x256
+// bf16, 16 groups, ReLU 31 us backward (2.4 TB/s). Streamed, 2x256x256x64 fp32 takes 13 + 15 us (the
 // second read comes from L2). Sums per thread instead of about the block's
 // first pixel need a second join (9 us more for the step).
 #pragma once

@@ -408,7 +408,8 @@ dwconv_status_t dwconv2d_group_norm_nhwc_bwd(const dwconv2d_norm_desc_t* desc, c
 const char* dwconv2d_group_norm_nhwc_plan_name(const dwconv2d_norm_desc_t* desc, int pass);
 
 /* Bytes of device workspace dwconv2d_bwd_nhwc needs (0 if the descriptor is
- * invalid). Depends only on the descriptor. */
+ * invalid). Depends only on the descriptor: it holds for every call of it,
+ * from x or from codes. */
 size_t dwconv2d_bwd_nhwc_workspace_size(const dwconv2d_desc_t* desc);
 
 /* Gradients of dwconv2d_fwd_nhwc (without epilogue) in one call: gx
@@ -419,6 +420,8 @@ size_t dwconv2d_bwd_nhwc_workspace_size(const dwconv2d_desc_t* desc);
  * one of x and x8 for gw. accumulate = 1 adds to gx, 0 overwrites it. The
  * workspace (16-byte aligned, not used concurrently) is needed for gw and
  * gbias. For N == 0 gw and gbias become 0. No output may overlap an input.
+ * Padding may be read as zeros that take part in products: an infinity or NaN
+ * in w, x or gy can leave NaN in other values of its channel, never elsewhere.
  * Square 3x3, 5x5 and 7x7 filters with equal strides of 1 or 2, dilation 1,
  * one filter per channel and padding up to (k - 1) / 2 run on row-walking
  * kernels; from 24 channels on (5x5 and 7x7: 9) these stage rows with the
