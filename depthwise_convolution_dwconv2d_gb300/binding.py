@@ -30,7 +30,10 @@ SYMBOLS = ("dwconv2d_output_shape", "dwconv2d_fwd", "dwconv2d_bwd_data",
            "dwconv2d_bwd_data_cached", "dwconv_act8_encode", "dwconv_act8_decode",
            "dwconv2d_group_norm_nhwc_workspace_size", "dwconv2d_group_norm_nhwc", "dwconv2d_group_norm_nhwc_bwd",
            "dwconv2d_group_norm_nhwc_plan_name", "dwconv2d_bwd_nhwc_workspace_size", "dwconv2d_bwd_nhwc",
-           "dwconv2d_bwd_nhwc_plan_name")
+           "dwconv2d_bwd_nhwc_plan_name", "dwconv_rms_norm", "dwconv_rms_norm_bwd_workspace_size", "dwconv_rms_norm_bwd",
+           "dwconv_rms_norm_plan_name", "dwconv_weight8_encode", "dwconv2d_pointwise8_workspace_size",
+           "dwconv2d_pointwise8", "dwconv2d_pointwise8_plan_name", "dwconv_grad_norm_clip_workspace_size",
+           "dwconv_grad_norm_clip")
 
 # dwconv_act_t (the fused forward epilogue has the first three)
 ACTS = {"none": 0, "relu": 1, "relu6": 2, "silu": 3, "gelu": 4}
@@ -73,7 +76,28 @@ class NormDesc(ctypes.Structure):
                 ("y_c_offset", ctypes.c_int64), ("y_c_total", ctypes.c_int64)]
 
 
+class RmsDesc(ctypes.Structure):
+    """dwconv_rms_desc_t (56 bytes)."""
+    _fields_ = [("rows", ctypes.c_int64), ("C", ctypes.c_int64), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x_c_offset", ctypes.c_int64), ("x_c_total", ctypes.c_int64),
+                ("y_c_offset", ctypes.c_int64), ("y_c_total", ctypes.c_int64)]
+
+
+class Weight8(ctypes.Structure):
+    """dwconv_weight8_t (32 bytes); ``make_weight8`` also keeps its tensors alive."""
+    _fields_ = [("cout", ctypes.c_int64), ("cin", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class Grad(ctypes.Structure):
+    """dwconv_grad_t (32 bytes)."""
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 assert ctypes.sizeof(Act8) == 40
+assert ctypes.sizeof(RmsDesc) == 56
+assert ctypes.sizeof(Weight8) == 32
+assert ctypes.sizeof(Grad) == 32
 assert ctypes.sizeof(NormDesc) == 80
 
 
@@ -109,6 +133,39 @@ def make_norm_desc(N, H, W, C, groups, act="none", eps=1e-5, dtype="f32", x_c_of
     return NormDesc(N, H, W, C, groups, ACTS[act] if isinstance(act, str) else int(act),
                     DTYPES[dtype] if isinstance(dtype, str) else int(dtype), eps, x_c_offset, x_c_total,
                     y_c_offset, y_c_total)
+
+
+def make_rms_desc(rows, C, eps=1e-6, dtype="f32", x_c_offset=0, x_c_total=0, y_c_offset=0, y_c_total=0) -> RmsDesc:
+    return RmsDesc(rows, C, DTYPES[dtype] if isinstance(dtype, str) else int(dtype), eps, x_c_offset, x_c_total,
+                   y_c_offset, y_c_total)
+
+
+def weight8_pitch(cin) -> int:
+    """Bytes between the rows of 8-bit weights: ``cin`` rounded up to a multiple of 128."""
+    return -(-cin // 128) * 128
+
+
+def make_weight8(cout, cin, codes, scales) -> Weight8:
+    """8-bit weights over ``codes`` ([cout, weight8_pitch(cin)], one byte each) and ``scales``
+    ([ceil(cout / 128), ceil(cin / 128)], fp32)."""
+    t = Weight8(cout, cin, _ptr(codes), _ptr(scales))
+    t.tensors = (codes, scales)
+    return t
+
+
+def make_grads(grads, outs=None):
+    """The gradients of a model and where their clipped values go: ``outs`` (tensors, or None for one that only
+    counts), or the gradients themselves. The list keeps its tensors alive and serves every step."""
+    outs = list(grads) if outs is None else list(outs)
+    if len(outs) != len(grads):
+        raise ValueError("one output (or None) per gradient")
+    for g, o in zip(grads, outs):
+        if o is not None and (o.dtype != g.dtype or o.numel() != g.numel()):
+            raise ValueError("an output has its gradient's type and size")
+    t = (Grad * len(grads))(*[Grad(_ptr(g) or None, _ptr(o) or None, g.numel(), _dtype_of(g, None), 0)
+                              for g, o in zip(grads, outs)])
+    t.tensors = (list(grads), outs)
+    return t
 
 
 _lib = None
@@ -173,6 +230,22 @@ def load():
     lib.dwconv2d_bwd_nhwc.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, sz, A, ctypes.c_int, vp]
     lib.dwconv2d_bwd_nhwc_plan_name.argtypes = [P]
     lib.dwconv2d_bwd_nhwc_plan_name.restype = ctypes.c_char_p
+    D, W8, L = ctypes.POINTER(RmsDesc), ctypes.POINTER(Weight8), ctypes.POINTER(Grad)
+    lib.dwconv_rms_norm.argtypes = [D, vp, vp, vp, vp, vp, vp, A, vp]
+    lib.dwconv_rms_norm_bwd_workspace_size.argtypes = [D]
+    lib.dwconv_rms_norm_bwd_workspace_size.restype = sz
+    lib.dwconv_rms_norm_bwd.argtypes = [D, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.dwconv_rms_norm_plan_name.argtypes = [D, ctypes.c_int]
+    lib.dwconv_rms_norm_plan_name.restype = ctypes.c_char_p
+    lib.dwconv_weight8_encode.argtypes = [vp, W8, ctypes.c_int, ctypes.c_int, vp]
+    lib.dwconv2d_pointwise8_workspace_size.argtypes = [i64, i64, i64]
+    lib.dwconv2d_pointwise8_workspace_size.restype = sz
+    lib.dwconv2d_pointwise8.argtypes = [A, W8, vp, ctypes.c_int, vp, i64, i64, ctypes.c_int, vp, sz, vp]
+    lib.dwconv2d_pointwise8_plan_name.argtypes = [i64, i64, i64]
+    lib.dwconv2d_pointwise8_plan_name.restype = ctypes.c_char_p
+    lib.dwconv_grad_norm_clip_workspace_size.argtypes = [ctypes.c_int, L]
+    lib.dwconv_grad_norm_clip_workspace_size.restype = sz
+    lib.dwconv_grad_norm_clip.argtypes = [ctypes.c_int, L, ctypes.c_float, vp, vp, sz, vp]
     for name in SYMBOLS:
         if not name.endswith(("_size", "_string", "_plan_name")):
             getattr(lib, name).restype = st
@@ -389,6 +462,65 @@ def dwconv2d_bwd_nhwc(desc: Desc, x, gy, w, gx, gw, gbias, workspace, workspace_
 
 def dwconv2d_bwd_nhwc_plan_name(desc: Desc) -> str:
     return load().dwconv2d_bwd_nhwc_plan_name(ctypes.byref(desc)).decode()
+
+
+def dwconv_rms_norm(desc: RmsDesc, x, residual, gamma, h, y, rstd=None, y8=None, stream=None):
+    """x, residual, h [rows, x_c_total], y [rows, y_c_total], rstd [rows] fp32; ``y8`` an Act8 of (rows, C)."""
+    _check(load().dwconv_rms_norm(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(gamma), _ptr(h), _ptr(y), _ptr(rstd),
+                                  _ref(y8), _stream(stream)), "dwconv_rms_norm")
+
+
+def dwconv_rms_norm_bwd_workspace_size(desc: RmsDesc) -> int:
+    return int(load().dwconv_rms_norm_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def dwconv_rms_norm_bwd(desc: RmsDesc, h, gy, gamma, rstd, gres, gx, ggamma, workspace, workspace_bytes=None, stream=None):
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    _check(load().dwconv_rms_norm_bwd(ctypes.byref(desc), _ptr(h), _ptr(gy), _ptr(gamma), _ptr(rstd), _ptr(gres), _ptr(gx),
+                                      _ptr(ggamma), _ptr(workspace), int(workspace_bytes), _stream(stream)),
+           "dwconv_rms_norm_bwd")
+
+
+def dwconv_rms_norm_plan_name(desc: RmsDesc, pass_: int) -> str:
+    return load().dwconv_rms_norm_plan_name(ctypes.byref(desc), int(pass_)).decode()
+
+
+def dwconv_weight8_encode(w, w8: Weight8, transpose=0, dtype=None, stream=None):
+    """``w`` [cout, cin] ([cin, cout] with ``transpose``); ``dtype`` is w's own unless w is a raw address."""
+    _check(load().dwconv_weight8_encode(_ptr(w), _ref(w8), int(transpose), _dtype_of(w, dtype), _stream(stream)),
+           "dwconv_weight8_encode")
+
+
+def dwconv2d_pointwise8_workspace_size(rows: int, cin: int, cout: int) -> int:
+    return int(load().dwconv2d_pointwise8_workspace_size(int(rows), int(cin), int(cout)))
+
+
+def dwconv2d_pointwise8(x8: Act8, w8: Weight8, bias, act, y, workspace=None, workspace_bytes=None, y_c_offset=0,
+                        y_c_total=0, dtype=None, stream=None):
+    """y [rows, y_c_total]; ``dtype`` is y's own unless y is a raw address; ``act`` a value or name of ``ACTS``."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    a = ACTS[act] if isinstance(act, str) else int(act)
+    _check(load().dwconv2d_pointwise8(_ref(x8), _ref(w8), _ptr(bias), a, _ptr(y), int(y_c_offset), int(y_c_total),
+                                      _dtype_of(y, dtype), _ptr(workspace), int(workspace_bytes), _stream(stream)),
+           "dwconv2d_pointwise8")
+
+
+def dwconv2d_pointwise8_plan_name(rows: int, cin: int, cout: int) -> str:
+    return load().dwconv2d_pointwise8_plan_name(int(rows), int(cin), int(cout)).decode()
+
+
+def dwconv_grad_norm_clip_workspace_size(grads) -> int:
+    return int(load().dwconv_grad_norm_clip_workspace_size(len(grads), grads))
+
+
+def dwconv_grad_norm_clip(grads, max_norm: float, norm, workspace, workspace_bytes=None, stream=None):
+    """``grads`` from ``make_grads``; ``norm`` an fp32 tensor of one value, or None."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    _check(load().dwconv_grad_norm_clip(len(grads), grads, float(max_norm), _ptr(norm), _ptr(workspace),
+                                        int(workspace_bytes), _stream(stream)), "dwconv_grad_norm_clip")
 
 
 def _desc_array(descs):

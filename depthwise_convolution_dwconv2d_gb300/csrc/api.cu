@@ -12,10 +12,13 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "gradclip.h"
 #include "nhwc.h"
 #include "nhwc_bwd.h"
 #include "norm.h"
 #include "plan.h"
+#include "pointwise8.h"
+#include "rms.h"
 
 namespace dwconv {
 namespace {
@@ -531,6 +534,186 @@ dwconv_status_t dwconv2d_bwd_nhwc(const dwconv2d_desc_t* desc, const void* x, co
   }
   if (gw || gbias) DW_TRY(check_workspace(workspace, workspace_bytes, nhwc::bwd_workspace_bytes(c)));
   return cuda_status(nhwc::bwd(c, x, t, gy, w, gx, gw, gbias, accumulate != 0, (float*)workspace, stream));
+}
+
+// ---- around the layers of a channels-last block ------------------------------
+
+namespace {
+
+bool dtype_ok(int dtype) { return dtype == DWCONV_F32 || dtype == DWCONV_F16 || dtype == DWCONV_BF16; }
+
+// a slice of C channels of rows `total` values apart (0: C)
+dwconv_status_t make_slice(int64_t rows, int64_t C, int64_t off, int64_t total, int64_t* ld) {
+  *ld = total == 0 ? C : total;
+  if (off < 0 || *ld < 1 || off > *ld - C) return DWCONV_ERR_INVALID_ARG;
+  return *ld > kMaxElems || rows > kMaxElems / *ld ? DWCONV_ERR_UNSUPPORTED : DWCONV_OK;
+}
+
+dwconv_status_t make_rms(const dwconv_rms_desc_t* d, rms::Rms* g) {
+  if (!d) return DWCONV_ERR_INVALID_ARG;
+  if (!dtype_ok(d->dtype)) return DWCONV_ERR_UNSUPPORTED;
+  if (d->rows < 0 || d->C < 1 || !(d->eps >= 0.f) || !std::isfinite(d->eps)) return DWCONV_ERR_INVALID_ARG;
+  if (d->C > kMaxChannels) return DWCONV_ERR_UNSUPPORTED;
+  rms::Rms v{};
+  v.rows = d->rows;
+  v.C = (int)d->C;
+  v.dtype = d->dtype;
+  v.eps = d->eps;
+  v.xo = d->x_c_offset;
+  v.yo = d->y_c_offset;
+  DW_TRY(make_slice(d->rows, d->C, d->x_c_offset, d->x_c_total, &v.xs));
+  DW_TRY(make_slice(d->rows, d->C, d->y_c_offset, d->y_c_total, &v.ys));
+  *g = v;
+  return DWCONV_OK;
+}
+
+dwconv_status_t make_pw8(int64_t rows, int64_t cin, int64_t cout, pw8::Pw* g) {
+  if (rows < 0 || cin < 1 || cout < 1) return DWCONV_ERR_INVALID_ARG;
+  if (cin > kMaxChannels || cout > kMaxChannels || rows > kMaxElems / cin || rows > kMaxElems / cout)
+    return DWCONV_ERR_UNSUPPORTED;
+  pw8::Pw v{};
+  v.rows = rows;
+  v.cin = (int)cin;
+  v.cout = (int)cout;
+  v.pitch = pw8::pitch_of(cin);
+  v.nkb = (int)(v.pitch / pw8::kBlock);
+  *g = v;
+  return DWCONV_OK;
+}
+
+dwconv_status_t check_weight8(const dwconv_weight8_t* w8) {
+  if (!w8 || w8->cout < 1 || w8->cin < 1) return DWCONV_ERR_INVALID_ARG;
+  if (w8->cout > kMaxChannels || w8->cin > kMaxChannels) return DWCONV_ERR_UNSUPPORTED;
+  DW_TRY(check_ptr(w8->codes, 1, true));
+  return check_ptr(w8->scales, 4, true);
+}
+
+dwconv_status_t check_grads(int count, const dwconv_grad_t* grads) {
+  if (count < 0 || (count > 0 && !grads)) return DWCONV_ERR_INVALID_ARG;
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    if (!dtype_ok(grads[i].dtype)) return DWCONV_ERR_UNSUPPORTED;
+    if (grads[i].n < 0) return DWCONV_ERR_INVALID_ARG;
+    if (grads[i].n > kMaxElems || (total += grads[i].n) > kMaxElems) return DWCONV_ERR_UNSUPPORTED;
+  }
+  return DWCONV_OK;
+}
+
+}  // namespace
+
+dwconv_status_t dwconv_rms_norm(const dwconv_rms_desc_t* desc, const void* x, const void* residual, const void* gamma,
+                                void* h, void* y, float* rstd, const dwconv_act8_t* y8, cudaStream_t stream) {
+  rms::Rms g;
+  DW_TRY(make_rms(desc, &g));
+  const int es = esize(g.dtype);
+  Act8 t{};
+  if (y8) DW_TRY(make_act8(y8, g.rows, g.C, &t));
+  DW_TRY(check_ptr(gamma, es, false));
+  if (g.rows == 0) return DWCONV_OK;
+  DW_TRY(check_ptr(x, es, true));
+  DW_TRY(check_ptr(residual, es, false));
+  DW_TRY(check_ptr(h, es, false));
+  DW_TRY(check_ptr(y, es, !y8));
+  DW_TRY(check_ptr(rstd, 4, false));
+  return cuda_status(rms::fwd(g, x, residual, gamma, h, y, rstd, t, stream));
+}
+
+size_t dwconv_rms_norm_bwd_workspace_size(const dwconv_rms_desc_t* desc) {
+  rms::Rms g;
+  if (make_rms(desc, &g) != DWCONV_OK) return 0;
+  return rms::bwd_workspace_bytes(g);
+}
+
+const char* dwconv_rms_norm_plan_name(const dwconv_rms_desc_t* desc, int pass) {
+  rms::Rms g;
+  if (make_rms(desc, &g) != DWCONV_OK || (pass != 0 && pass != 1)) return "invalid";
+  return rms::plan_name(g, pass);
+}
+
+dwconv_status_t dwconv_rms_norm_bwd(const dwconv_rms_desc_t* desc, const void* h, const void* gy, const void* gamma,
+                                    const float* rstd, const void* gres, void* gx, void* ggamma, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+  rms::Rms g;
+  DW_TRY(make_rms(desc, &g));
+  const int es = esize(g.dtype);
+  DW_TRY(check_ptr(gamma, es, false));
+  DW_TRY(check_ptr(gx, es, false));
+  DW_TRY(check_ptr(ggamma, es, false));
+  if (!gx && !ggamma) return DWCONV_OK;
+  if (g.rows > 0) {
+    DW_TRY(check_ptr(h, es, true));
+    DW_TRY(check_ptr(gy, es, true));
+    DW_TRY(check_ptr(rstd, 4, true));
+    DW_TRY(check_ptr(gres, es, false));
+    if (ggamma) DW_TRY(check_workspace(workspace, workspace_bytes, rms::bwd_workspace_bytes(g)));
+  }
+  return cuda_status(rms::bwd(g, h, gy, gamma, rstd, gres, gx, ggamma, (float*)workspace, stream));
+}
+
+dwconv_status_t dwconv_weight8_encode(const void* w, const dwconv_weight8_t* w8, int transpose, int dtype,
+                                      cudaStream_t stream) {
+  DW_TRY(check_weight8(w8));
+  if (transpose != 0 && transpose != 1) return DWCONV_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype)) return DWCONV_ERR_UNSUPPORTED;
+  DW_TRY(check_ptr(w, esize(dtype), true));
+  return cuda_status(pw8::encode_weights(w8->cout, w8->cin, transpose != 0, dtype, w, (uint8_t*)w8->codes, w8->scales,
+                                         stream));
+}
+
+size_t dwconv2d_pointwise8_workspace_size(int64_t rows, int64_t cin, int64_t cout) {
+  pw8::Pw g;
+  if (make_pw8(rows, cin, cout, &g) != DWCONV_OK) return 0;
+  return pw8::workspace_bytes(g);
+}
+
+const char* dwconv2d_pointwise8_plan_name(int64_t rows, int64_t cin, int64_t cout) {
+  pw8::Pw g;
+  if (make_pw8(rows, cin, cout, &g) != DWCONV_OK) return "invalid";
+  return pw8::plan(g) == pw8::Plan::Row ? "row" : "tile";
+}
+
+dwconv_status_t dwconv2d_pointwise8(const dwconv_act8_t* x8, const dwconv_weight8_t* w8, const void* bias, int act,
+                                    void* y, int64_t y_c_offset, int64_t y_c_total, int dtype, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+  DW_TRY(check_weight8(w8));
+  if (!x8) return DWCONV_ERR_INVALID_ARG;
+  pw8::Pw g;
+  DW_TRY(make_pw8(x8->rows, w8->cin, w8->cout, &g));
+  Act8 t{};
+  DW_TRY(make_act8(x8, x8->rows, w8->cin, &t));
+  if (t.src != kSrcE4M3 || x8->block != pw8::kBlock) return DWCONV_ERR_UNSUPPORTED;
+  if (!dtype_ok(dtype)) return DWCONV_ERR_UNSUPPORTED;
+  if (act < DWCONV_ACT_NONE || act > DWCONV_ACT_GELU) return DWCONV_ERR_INVALID_ARG;
+  g.act = act;
+  g.dtype = dtype;
+  g.yo = y_c_offset;
+  DW_TRY(make_slice(g.rows, g.cout, y_c_offset, y_c_total, &g.ys));
+  const int es = esize(dtype);
+  DW_TRY(check_ptr(bias, es, false));
+  if (g.rows == 0) return DWCONV_OK;
+  DW_TRY(check_ptr(y, es, true));
+  DW_TRY(check_workspace(workspace, workspace_bytes, pw8::workspace_bytes(g)));
+  return cuda_status(pw8::run(g, t.codes, t.scales, (const uint8_t*)w8->codes, w8->scales, bias, y, workspace, stream));
+}
+
+size_t dwconv_grad_norm_clip_workspace_size(int count, const dwconv_grad_t* grads) {
+  if (check_grads(count, grads) != DWCONV_OK) return 0;
+  return clip::workspace_bytes(count, grads);
+}
+
+dwconv_status_t dwconv_grad_norm_clip(int count, const dwconv_grad_t* grads, float max_norm, float* norm,
+                                      void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  DW_TRY(check_grads(count, grads));
+  if (!(max_norm > 0.f)) return DWCONV_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    if (grads[i].n == 0) continue;
+    const int es = esize(grads[i].dtype);
+    DW_TRY(check_ptr(grads[i].g, es, true));
+    DW_TRY(check_ptr(grads[i].out, es, false));
+  }
+  DW_TRY(check_ptr(norm, 4, false));
+  DW_TRY(check_workspace(workspace, workspace_bytes, clip::workspace_bytes(count, grads)));
+  return cuda_status(clip::run(count, grads, max_norm, norm, workspace, stream));
 }
 
 dwconv_status_t dwconv2d_fwd_multi(int nbranch, const dwconv2d_desc_t* descs, const void* x,

@@ -439,6 +439,129 @@ dwconv_status_t dwconv2d_bwd_nhwc(const dwconv2d_desc_t* desc, const void* x, co
  * "generic" or "invalid". Host only. */
 const char* dwconv2d_bwd_nhwc_plan_name(const dwconv2d_desc_t* desc);
 
+/* ---- around the layers of a channels-last block ---------------------------
+ * A row norm with the residual's addition, whose output may be 8-bit codes; a
+ * 1x1 layer that multiplies such codes; and the step that clips all
+ * gradients of a model. */
+
+/* An RMS norm over the C channels of a row (a pixel). x, residual, h, gres and
+ * gx hold `rows` rows, x_c_total values apart, and the norm's channels are
+ * [x_c_offset, x_c_offset + C) of each; y and gy likewise with y_*. 56 bytes. */
+typedef struct {
+  int64_t rows, C;                 /* rows >= 0, C >= 1 */
+  int32_t dtype;                   /* dwconv_dtype_t of every tensor but rstd */
+  float eps;                       /* finite, >= 0 */
+  int64_t x_c_offset, x_c_total;   /* total 0 means C */
+  int64_t y_c_offset, y_c_total;   /* total 0 means C */
+} dwconv_rms_desc_t;
+
+/* RMS norm with the residual's addition:
+ *   h = x + residual, rounded to desc->dtype (h = x where residual is NULL)
+ *   r = 1 / sqrt(average of h^2 over the row + eps),  y = (h * r) * gamma[c]
+ * in fp32, each output rounded once. The norm is taken of h as rounded, which
+ * is what the backward reads. gamma ([C]) may be NULL (1); h and rstd ([rows],
+ * fp32) are written unless NULL. The result goes to y, to the 8-bit
+ * checkpoint y8 (rows, C; codes of the unrounded y), or to both; at least one
+ * is not NULL. h may be the memory of x or of residual; otherwise outputs
+ * overlap neither inputs nor each other. A row of zeros with eps = 0 gives
+ * NaN. An infinity or a NaN in a row gives r = 0 or NaN, and NaN where it is. */
+dwconv_status_t dwconv_rms_norm(const dwconv_rms_desc_t* desc, const void* x, const void* residual,
+                                const void* gamma, void* h, void* y, float* rstd,
+                                const dwconv_act8_t* y8, cudaStream_t stream);
+
+/* Bytes of device workspace of dwconv_rms_norm_bwd; 0 if the descriptor is
+ * invalid. */
+size_t dwconv_rms_norm_bwd_workspace_size(const dwconv_rms_desc_t* desc);
+
+/* Gradients of dwconv_rms_norm, from h (the forward's; x where it had no
+ * residual), gy and the forward's rstd:
+ *   t = gy * gamma,  gx = r * (t - h * r^2 * average of t * h) + gres
+ *   ggamma[c] = sum over rows of gy * h * r
+ * gx is the gradient of both x and residual; gres, the gradient that reaches
+ * h past the norm, may be NULL (0). gx and ggamma ([C], desc->dtype) are
+ * overwritten and either may be NULL. gx may be the memory of gres; otherwise
+ * outputs overlap no input. The workspace (16-byte aligned, not used
+ * concurrently) is needed for ggamma. For rows == 0 ggamma becomes 0. */
+dwconv_status_t dwconv_rms_norm_bwd(const dwconv_rms_desc_t* desc, const void* h, const void* gy,
+                                    const void* gamma, const float* rstd, const void* gres, void* gx,
+                                    void* ggamma, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
+/* Kernel family of pass 0 (forward) or 1 (backward) for aligned pointers:
+ * "row" (a row is read once), "wide" (read twice) or "invalid". Host only. */
+const char* dwconv_rms_norm_plan_name(const dwconv_rms_desc_t* desc, int pass);
+
+/* The 8-bit weights of a 1x1 layer: e4m3 codes, one fp32 scale per block of
+ * 128 outputs x 128 channels (shorter at the ends), with the arithmetic of
+ * dwconv_act8_t: scale = fl(max|w| * fl(1 / 448)), code = nearest e4m3 to
+ * fl(w * fl(1 / scale)), value = code * scale. The rows of codes are `cin`
+ * rounded up to a multiple of 128 bytes apart and the codes behind a row are
+ * zeros. 32 bytes. */
+typedef struct {
+  int64_t cout, cin;   /* 1 .. 2^20 */
+  void* codes;         /* [cout, cin rounded up to 128] */
+  float* scales;       /* [ceil(cout / 128), ceil(cin / 128)] */
+} dwconv_weight8_t;
+
+/* Writes w8 from w: [cout, cin] of `dtype`, or, with transpose = 1, [cin,
+ * cout] (so that the weights of a layer also serve its input's gradient). */
+dwconv_status_t dwconv_weight8_encode(const void* w, const dwconv_weight8_t* w8, int transpose, int dtype,
+                                      cudaStream_t stream);
+
+/* Bytes of device workspace of dwconv2d_pointwise8 for these sizes (0 where
+ * it needs none, or where they are invalid). */
+size_t dwconv2d_pointwise8_workspace_size(int64_t rows, int64_t cin, int64_t cout);
+
+/* 1x1 (pointwise) convolution of a channels-last activation held in 8 bits:
+ *   y[p, off + o] = act(sum_c X[p, c] W[o, c] + bias[o]),   o < cout
+ * X and W being the values of x8 (e4m3, one scale per 128 channels; rows
+ * pixels, C = cin) and of w8. Within a block of 128 channels products of codes
+ * are added in fp32 on the tensor cores; a block's sum times the product of
+ * its two scales (one fp32 rounding) is added in fp32. y ([rows, y_c_total],
+ * only channels [y_c_offset, y_c_offset + cout) are written; total 0 means
+ * cout) and bias ([cout] or NULL) are of `dtype`, act is a dwconv_act_t, the
+ * result is rounded once. A row or a block of weights whose scale is NaN
+ * gives NaN. The input's gradient is the same product: of gy's codes
+ * (dwconv_act8_encode) with the transposed weights.
+ * Where cin is no multiple of 16 the workspace (16-byte aligned, not used
+ * concurrently) takes an aligned copy of the codes; w8's codes, or x8's with
+ * cin a multiple of 16, off a 16-byte boundary take a much slower kernel.
+ * Other kinds and blocks of x8 are DWCONV_ERR_UNSUPPORTED. */
+dwconv_status_t dwconv2d_pointwise8(const dwconv_act8_t* x8, const dwconv_weight8_t* w8, const void* bias,
+                                    int act, void* y, int64_t y_c_offset, int64_t y_c_total, int dtype,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Kernel family for aligned pointers: "row" (few pixels: thread blocks share
+ * the channels), "tile" or "invalid". Host only. */
+const char* dwconv2d_pointwise8_plan_name(int64_t rows, int64_t cin, int64_t cout);
+
+/* One gradient tensor of a model. 32 bytes. */
+typedef struct {
+  const void* g;   /* n values of dtype */
+  void* out;       /* where the clipped gradient goes: g itself, memory that
+                      overlaps no tensor of the call, or NULL (g only counts) */
+  int64_t n;       /* >= 0 */
+  int32_t dtype;   /* dwconv_dtype_t of g and out */
+  int32_t reserved;
+} dwconv_grad_t;
+
+/* Bytes of device workspace of dwconv_grad_norm_clip for these tensors (their
+ * pointers are not looked at); 0 if an argument is invalid or there is nothing
+ * to add up. */
+size_t dwconv_grad_norm_clip_workspace_size(int count, const dwconv_grad_t* grads);
+
+/* Norm over all gradients, and their clipping:
+ *   n = sqrt(sum of g^2 over all tensors),  out = g * min(1, max_norm / (n + 1e-6))
+ * with sums that no finite gradient overflows (n itself is an fp32: above its
+ * range *norm is infinite). max_norm > 0; INFINITY clips nothing. A NaN or an
+ * infinity among the gradients makes n NaN or infinite, and out NaN (n NaN) or
+ * 0 and NaN (n infinite) unless max_norm is INFINITY. norm (device memory) may
+ * be NULL. grads is read on the host during the call, which is two launches
+ * per 960 tensors. The same tensor may not appear twice with an out.
+ * The workspace (16-byte aligned) is not used concurrently. */
+dwconv_status_t dwconv_grad_norm_clip(int count, const dwconv_grad_t* grads, float max_norm, float* norm,
+                                      void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Static text for a status code. */
 const char* dwconv_status_string(dwconv_status_t status);
 
