@@ -36,39 +36,37 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr unsigned kSleepNs = 32;
-
 // Instruction descriptor of kind::f8f6f4, e4m3 x e4m3 with fp32 D, both operands K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+template <int CTAS>
 __device__ __forceinline__ void mma_f8(uint32_t dtmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(dtmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (CTAS == 1) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(dtmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(dtmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
 }
 
 // A block of 128 channels: four steps of 32, 32 bytes (2 descriptor units) apart. One thread.
+template <int CTAS>
 __device__ __forceinline__ void mma_block(uint32_t dtmem, const void* a, const void* b, uint32_t idesc) {
   const uint64_t ad = tc::desc_sw128(tma::smem_u32(a)), bd = tc::desc_sw128(tma::smem_u32(b));
 #pragma unroll
-  for (int k = 0; k < 4; ++k) mma_f8(dtmem, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+  for (int k = 0; k < 4; ++k) mma_f8<CTAS>(dtmem, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
 }
 
-// 32 or 16 consecutive fp32 columns of this warp's 32 lanes, one lane per thread, as pairs; not waited for
-__device__ __forceinline__ void ld_pairs32(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
+// 16 consecutive fp32 columns of this warp's 32 lanes, one lane per thread, as pairs; not waited for
 __device__ __forceinline__ void ld_pairs16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
@@ -78,14 +76,6 @@ __device__ __forceinline__ void ld_pairs16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 // Waits for this thread's loads; naming the registers keeps their uses behind the wait.
-__device__ __forceinline__ void ld_wait32(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               ::"memory");
-}
 __device__ __forceinline__ void ld_wait16(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
@@ -105,30 +95,9 @@ struct Ring {
 
 __device__ __forceinline__ unsigned char* align1024(unsigned char* p) { return p + ((1024 - (tma::smem_u32(p) & 1023)) & 1023); }
 
-// V values of y's row from column c on: bias, activation, one rounding
-template <typename T, int V>
-__device__ __forceinline__ void finish(const Pw& g, const T* bias, int c, float* v) {
-  if (bias) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] += ld(bias + (c + e < g.cout ? c + e : c));
-  }
-  norm::act_v<V>(g.act, v);
-}
+// ---- tile kernels -------------------------------------------------------------
 
-// ---- tile kernel --------------------------------------------------------------
-
-constexpr int kM = 128;
-
-template <int BN>
-struct Tile {
-  static constexpr int kEpi = BN;               // threads that read back
-  static constexpr int kThreads = kEpi + 64;    // and a producer and an MMA warp
-  static constexpr int kStages = 4;
-  static constexpr int kA = kM * kBlock, kB = BN * kBlock, kStage = kA + kB;
-  static constexpr int kCols = 2 * BN;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage;
-  static constexpr int kPerSm = BN == 128 ? 1 : 1;
-};
+constexpr int kM = 128;  // pixels of a thread block
 
 struct TGeom {
   Pw p;
@@ -137,27 +106,220 @@ struct TGeom {
   int vec_out;
 };
 
-template <typename T, int BN>
-__global__ void __launch_bounds__(Tile<BN>::kThreads, Tile<BN>::kPerSm)
+// acc += s * (NC columns of this warp's lanes), 16 at a time. freed() runs once all have been read.
+template <int NC, typename F>
+__device__ __forceinline__ void add_block(uint32_t taddr, f32x2 s2, f32x2* acc, F freed) {
+#pragma unroll
+  for (int q = 0; q < NC / 16; ++q) {
+    uint32_t d[16];
+    ld_pairs16(taddr + 16 * q, d);
+    ld_wait16(d);
+    if (q + 1 == NC / 16) freed();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) fma_f32x2(acc[8 * q + i], pair_at(d, i), s2);
+  }
+}
+
+// 32 bytes of a row, on 32 bytes
+__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+// 16 columns of this warp's 32 lanes back to tensor memory
+__device__ __forceinline__ void st_pairs16(uint32_t taddr, const f32x2* v) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    r[2 * i] = (uint32_t)v[i];
+    r[2 * i + 1] = (uint32_t)(v[i] >> 32);
+  }
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// The sums of a warp's 32 pixels x NC outputs (a thread has a pixel) to y:
+// bias, activation, one rounding; a thread stores 32 bytes of its row at a
+// time. Rows off 32 bytes go through 2 KB of shared memory instead, so that
+// neighbouring lanes store neighbouring elements. The sums are read from the
+// accumulator that they came from last (taddr, which is not free yet), times
+// s2: those of more than one block of channels were put back there, because
+// registers cannot be indexed: the code for all columns in a row took longer
+// to fetch than the sums to compute, and its registers cost the loop over the
+// channels its own.
+constexpr int kSt = 16;                        // columns at a time
+constexpr int warp_floats(int nc) { return 32 * kSt + nc; }  // staging and bias of a warp
+template <typename T, int NC>
+__device__ __forceinline__ void store_tile(const TGeom& g, T* y, int p0, int o0, uint32_t taddr, f32x2 s2, float* st) {
+  const int lane = threadIdx.x & 31;
+  const int rows = min((int)g.p.rows - p0, 32);  // at most 0: nothing to store
+  const int cols = rows > 0 ? g.p.cout - o0 : 0;
+  const float* bias = st + 32 * kSt;
+  T* yr = y + (int64_t)(p0 + lane) * g.p.ys + g.p.yo + o0;
+#pragma unroll 1
+  for (int c0 = 0; c0 < NC && c0 < cols; c0 += 32) {
+    uint32_t d[32];
+    ld_pairs16(taddr + c0, d);
+    ld_pairs16(taddr + c0 + 16, d + 16);
+    ld_wait16(d);
+    ld_wait16(d + 16);
+    f32x2 u[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(bias + c0 + 4 * i);
+      u[2 * i] = norm::fma2(pair_at(d, 2 * i), s2, b.x);
+      u[2 * i + 1] = norm::fma2(pair_at(d, 2 * i + 1), s2, b.y);
+    }
+    norm::act_p<16>(g.p.act, u);
+    if (g.vec_out && c0 + 32 <= cols) {
+      if (lane < rows) {
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) unpack_f32x2(u[i], v[2 * i], v[2 * i + 1]);
+        constexpr int VEC = Vec<T>::n;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2 * VEC) store32(yr + c0 + i, pack16<T>(v + i), pack16<T>(v + i + VEC));
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // a pixel's four 16-byte groups, each moved by its pixel: lanes do not meet in a bank
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<ulonglong2*>(st + lane * kSt + ((j ^ (lane >> 1)) & 3) * 4) =
+              make_ulonglong2(u[8 * h + 2 * j], u[8 * h + 2 * j + 1]);
+        __syncwarp();
+        const int k = lane & 15, c = c0 + kSt * h + k;
+        if (c < cols) {
+          T* yp = y + (int64_t)(p0 + (lane >> 4)) * g.p.ys + g.p.yo + o0 + c;
+#pragma unroll 8
+          for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + (lane >> 4);
+            if (r < rows) yp[2 * i * g.p.ys] = from_f<T>(st[r * kSt + (((k >> 2) ^ (r >> 1)) & 3) * 4 + (k & 3)]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+}
+
+// What a warp that reads back needs of a tile before its first block of
+// channels: fetched while the tile before it is stored.
+template <typename T, int NC>
+struct Ahead {
+  float sx, sw, bias[NC / 32];
+  __device__ __forceinline__ void fetch(const Pw& p, const float* sx_, const float* sw_, const T* b, int p0, int o0) {
+    const int lane = threadIdx.x & 31;
+    sx = __ldg(sx_ + (p0 + lane < (int)p.rows ? (int64_t)(p0 + lane) * p.nkb : 0));
+    sw = __ldg(sw_ + (o0 < p.cout ? o0 / kBlock : 0) * p.nkb);
+#pragma unroll
+    for (int k = 0; k < NC / 32; ++k) bias[k] = b && o0 + 32 * k + lane < p.cout ? ld(b + o0 + 32 * k + lane) : 0.f;
+  }
+  __device__ __forceinline__ void put_bias(float* st) const {
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < NC / 32; ++k) st[32 * kSt + 32 * k + (threadIdx.x & 31)] = bias[k];
+    __syncwarp();
+  }
+};
+
+// A warp that reads back, over its tiles: tile t's first pixel and output from
+// at(t, p0, o0), whose accumulators are n columns apart from tlane on.
+template <typename T, int NC, int ACC, typename At, typename Free>
+__device__ __forceinline__ void read_back(const TGeom& g, const float* sx, const float* sw, const T* bias, T* y, int first,
+                                          int step, uint32_t tlane, int n, float* st, uint64_t* accfull,
+                                          unsigned int* timeouts, volatile int* abortp, At at, Free free_acc) {
+  const int lane = threadIdx.x & 31, nkb = g.p.nkb;
+  uint32_t it = 0;
+  int p0, o0;
+  Ahead<T, NC> a;
+  if (first < g.tiles) {
+    at(first, p0, o0);
+    a.fetch(g.p, sx, sw, bias, p0, o0);
+  }
+  for (int t = first; t < g.tiles; t += step) {
+    a.put_bias(st);
+    const float* sxp = sx + (p0 + lane < (int)g.p.rows ? (int64_t)(p0 + lane) * nkb : 0);
+    const float* swp = sw + (o0 < g.p.cout ? o0 / kBlock : 0) * nkb;
+    f32x2 acc[NC / 2];
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
+    f32x2 s2 = 0ull;
+    for (int kb = 0; kb < nkb; ++kb, ++it) {
+      const float sc = __fmul_rn(a.sx, a.sw);
+      s2 = pack_f32x2(sc, sc);
+      if (kb + 1 < nkb) {
+        a.sx = __ldg(sxp + kb + 1);
+        a.sw = __ldg(swp + kb + 1);
+      }
+      bool ok = tc::wait(&accfull[it % ACC], (it / ACC) & 1, timeouts, abortp);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) *abortp = 1;
+      tc::fence_after();
+      auto freed = [&] {
+        if (kb + 1 < nkb) free_acc(it % ACC);  // the last one is still needed
+      };
+      if (ok && nkb > 1) add_block<NC>(tlane + (it % ACC) * n, s2, acc, freed);
+      else freed();
+    }
+    const int last = (it - 1) % ACC;
+    const int tp0 = p0, to0 = o0;
+    if (nkb > 1) {
+#pragma unroll
+      for (int q = 0; q < NC / 16; ++q) st_pairs16(tlane + last * n + 16 * q, acc + 8 * q);
+      asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+      s2 = pack_f32x2(1.f, 1.f);
+    }
+    if (t + step < g.tiles) {
+      at(t + step, p0, o0);
+      a.fetch(g.p, sx, sw, bias, p0, o0);
+    }
+    if (!*abortp) store_tile<T, NC>(g, y, tp0, to0, tlane + last * n, s2, st);
+    free_acc(last);
+  }
+}
+
+// One thread block, 128 pixels x 128 outputs, for calls of few tiles: four
+// accumulators take turns here, so that neither the MMAs nor the warps that
+// read back wait for the other's hand-over.
+struct Tile {
+  static constexpr int kN = 128, kNC = 64;        // outputs of a tile, of a warp that reads back
+  static constexpr int kAcc = 4;                   // accumulators (a power of two)
+  static constexpr int kEpi = 4 * kN / kNC;       // warps that read back
+  static constexpr int kThreads = 32 * kEpi + 64;  // and a producer and an MMA warp
+  static constexpr int kStages = 6;
+  static constexpr int kA = kM * kBlock, kB = kN * kBlock, kStage = kA + kB;
+  static constexpr int kCols = kAcc * kN;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpi * warp_floats(kNC) * 4;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(Tile::kThreads, 1)
 tile_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
             unsigned int* timeouts, const float* __restrict__ sx, const float* __restrict__ sw,
             const T* __restrict__ bias, T* __restrict__ y) {
-  typedef Tile<BN> K;
+  typedef Tile K;
   extern __shared__ unsigned char smdyn[];
-  __shared__ __align__(8) uint64_t full[K::kStages], empty[K::kStages], accfull[2], accfree[2], done;
+  __shared__ __align__(8) uint64_t full[K::kStages], empty[K::kStages], accfull[K::kAcc], accfree[K::kAcc], done;
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
   unsigned char* sm = align1024(smdyn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kProducer = K::kEpi / 32, kMma = kProducer + 1;
+  constexpr int kProducer = K::kEpi, kMma = kProducer + 1;
   if (tid == 0) {
     for (int s = 0; s < K::kStages; ++s) {
       tma::mbar_init(&full[s], 1);
       tma::mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < K::kAcc; ++s) {
       tma::mbar_init(&accfull[s], 1);
-      tma::mbar_init(&accfree[s], K::kEpi / 32);
+      tma::mbar_init(&accfree[s], K::kEpi);
     }
     tma::mbar_init(&done, 1);
     tma::fence_init();
@@ -183,7 +345,7 @@ tile_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
           unsigned char* st = sm + (size_t)r.s * K::kStage;
           tma::mbar_expect_tx(&full[r.s], K::kStage);
           tma::load_3d(st, &xmap, kb * kBlock, (int)mt * kM, 0, &full[r.s]);
-          tma::load_3d(st + K::kA, &wmap, kb * kBlock, nt * BN, 0, &full[r.s]);
+          tma::load_3d(st + K::kA, &wmap, kb * kBlock, nt * K::kN, 0, &full[r.s]);
           ++issued;
         }
       }
@@ -193,19 +355,19 @@ tile_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
     }
     __syncwarp();
   } else if (warp == kMma) {
-    constexpr uint32_t idesc = idesc_e4m3(kM, BN);
+    constexpr uint32_t idesc = idesc_e4m3(kM, K::kN);
     Ring r;
     uint32_t it = 0;
     for (int t = blockIdx.x; t < g.tiles; t += gridDim.x) {
       for (int kb = 0; kb < nkb; ++kb, ++it, r.next(K::kStages)) {
-        const int ab = it & 1;
-        const bool ok = !*abortp && (it < 2 || tc::wait(&accfree[ab], ((it >> 1) - 1) & 1, timeouts, abortp)) &&
-                        tc::wait(&full[r.s], r.ph, timeouts, abortp);
+        const int ab = it % K::kAcc;
+        const bool ok = tc::wait(&full[r.s], r.ph, timeouts, abortp) &&
+                        (it < K::kAcc || tc::wait(&accfree[ab], (it / K::kAcc - 1) & 1, timeouts, abortp));
         if (!__all_sync(0xffffffffu, ok)) { *abortp = 1; continue; }
         tc::fence_after();
         const unsigned char* st = sm + (size_t)r.s * K::kStage;
         if (tc::elect_one()) {
-          mma_block(tmem + ab * BN, st, st + K::kA, idesc);
+          mma_block<1>(tmem + ab * K::kN, st, st + K::kA, idesc);
           tc::commit(&empty[r.s]);
           tc::commit(&accfull[ab]);
         }
@@ -217,73 +379,179 @@ tile_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
     tc::wait(&done, 0, nullptr, nullptr);
     __syncwarp();
   } else {
-    const int col0 = (warp >> 2) * 128;  // this warpgroup's outputs of the tile
+    const int col0 = (warp >> 2) * K::kNC;  // this warp's outputs of the tile; its pixels are 32 (warp % 4) and on
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + col0;
-    uint32_t it = 0;
-    for (int t = blockIdx.x; t < g.tiles; t += gridDim.x) {
-      uint32_t mt;
-      const int nt = (int)g.d_nt.divmod((uint32_t)t, mt);
-      const int64_t p = (int64_t)mt * kM + (warp & 3) * 32 + lane;
-      const int o0 = nt * BN + col0;
-      const bool valid = p < g.p.rows && o0 < g.p.cout;
-      const float* sxp = sx + (valid ? p * nkb : 0);
-      const float* swp = sw + (int64_t)(valid ? o0 / kBlock : 0) * nkb;
-      float sxn = __ldg(sxp), swn = __ldg(swp);
-      f32x2 acc[64];
-#pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int ab = it & 1;
-        const float sc = __fmul_rn(sxn, swn);
-        if (kb + 1 < nkb) {
-          sxn = __ldg(sxp + kb + 1);
-          swn = __ldg(swp + kb + 1);
-        }
-        const f32x2 s2 = pack_f32x2(sc, sc);
-        bool ok = !*abortp && tc::wait(&accfull[ab], (it >> 1) & 1, timeouts, abortp);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) *abortp = 1;
-        tc::fence_after();
-        if (ok) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t d[32];
-            ld_pairs32(tlane + ab * BN + 32 * q, d);
-            ld_wait32(d);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) fma_f32x2(acc[16 * q + i], pair_at(d, i), s2);
-          }
-        }
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::arrive(&accfree[ab]);
-      }
-      if (!valid || *abortp) continue;
-      T* yp = y + p * g.p.ys + g.p.yo;
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int c = o0 + 8 * q;
-        if (c >= g.p.cout) break;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpack_f32x2(acc[4 * q + i], v[2 * i], v[2 * i + 1]);
-        finish<T, 8>(g.p, bias, c, v);
-        if (g.vec_out && c + 8 <= g.p.cout) {
-          uint4* dst = reinterpret_cast<uint4*>(yp + c);
-          dst[0] = pack16<T>(v);
-          if constexpr (sizeof(T) == 4) dst[1] = pack16<T>(v + 4);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < g.p.cout) yp[c + e] = from_f<T>(v[e]);
-        }
-      }
-    }
+    float* st = reinterpret_cast<float*>(sm + (size_t)K::kStages * K::kStage) + warp * warp_floats(K::kNC);
+    read_back<T, K::kNC, K::kAcc>(
+        g, sx, sw, bias, y, blockIdx.x, gridDim.x, tlane, K::kN, st, accfull, timeouts, abortp,
+        [&](int t, int& p0, int& o0) {
+          uint32_t mt;
+          o0 = (int)g.d_nt.divmod((uint32_t)t, mt) * K::kN + col0;
+          p0 = (int)mt * kM + (warp & 3) * 32;
+        },
+        [&](int ab) {
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::arrive(&accfree[ab]);
+        });
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   if (warp == kMma) tc::dealloc(tmem, K::kCols);
+}
+
+// A pair of thread blocks on two SMs, 256 pixels x 256 outputs: each holds
+// its 128 pixels and half of the weights, and one MMA reads both. That is 32 KB
+// per block of channels and SM where a block by itself reads 48 for 128 x 256.
+struct Pair {
+  static constexpr int kN = 256, kNC = 128;
+  static constexpr int kAcc = 2;
+  static constexpr int kEpi = 4 * kN / kNC;        // warps that read back
+  static constexpr int kThreads = 32 * kEpi + 128;  // and a warpgroup with a producer and an MMA warp
+  static constexpr int kStages = 6;
+  static constexpr int kA = kM * kBlock, kB = kN / 2 * kBlock, kStage = kA + kB;
+  static constexpr int kCols = kAcc * kN;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kEpi * warp_floats(kNC) * 4;
+};
+
+// A copy that counts on the barrier of the pair's first block
+__device__ __forceinline__ void load_pair(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(tma::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(0), "r"(tma::smem_u32(bar) & 0xFEFFFFFFu)
+      : "memory");
+}
+// Arrive on bar in both blocks of the pair once every tcgen05 operation so far is done
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+                   tma::smem_u32(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+// Arrive on bar of the pair's first block
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n"
+      " mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(tma::smem_u32(bar))
+      : "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
+pair_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+            unsigned int* timeouts, const float* __restrict__ sx, const float* __restrict__ sw,
+            const T* __restrict__ bias, T* __restrict__ y) {
+  typedef Pair K;
+  extern __shared__ unsigned char smdyn[];
+  __shared__ __align__(8) uint64_t full[K::kStages], empty[K::kStages], accfull[K::kAcc], accfree[K::kAcc], done;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ int abort_s;
+  unsigned char* sm = align1024(smdyn);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kProducer = K::kEpi, kMma = kProducer + 1;
+  const int rank = blockIdx.x & 1;  // in the pair; block 0 issues the MMAs and has the barriers they wait for
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (tid == 0) {
+    for (int s = 0; s < K::kStages; ++s) {
+      tma::mbar_init(&full[s], 1);
+      tma::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < K::kAcc; ++s) {
+      tma::mbar_init(&accfull[s], 1);
+      tma::mbar_init(&accfree[s], 2 * K::kEpi);  // the warps of both blocks that read back
+    }
+    tma::mbar_init(&done, 1);
+    tma::fence_init();
+    abort_s = 0;
+  }
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(tma::smem_u32(&tmem_base_s)),
+                 "r"(K::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+  }
+  tc::fence_before();
+  cg::this_cluster().sync();
+  tc::fence_after();
+  const uint32_t tmem = tmem_base_s;
+  volatile int* abortp = &abort_s;
+  const int nkb = g.p.nkb;
+
+  if (warp >= K::kEpi) {
+    // of the 168 registers a thread that the block was launched with: 128 x 56 + 256 x 224 = 384 x 168
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+    if (warp == kProducer) {
+      if (lane == 0) {
+        Ring r;
+        uint32_t issued = 0;
+        for (int t = pair; t < g.tiles && !*abortp; t += pairs) {
+          uint32_t mt;
+          const int nt = (int)g.d_nt.divmod((uint32_t)t, mt);
+          for (int kb = 0; kb < nkb && !*abortp; ++kb, r.next(K::kStages)) {
+            if (r.wrapped && !tc::wait(&empty[r.s], r.ph ^ 1, timeouts, abortp)) { *abortp = 1; break; }
+            unsigned char* st = sm + (size_t)r.s * K::kStage;
+            if (rank == 0) tma::mbar_expect_tx(&full[r.s], 2 * K::kStage);
+            load_pair(st, &xmap, kb * kBlock, ((int)mt * 2 + rank) * kM, &full[r.s]);
+            load_pair(st + K::kA, &wmap, kb * kBlock, nt * K::kN + rank * (K::kN / 2), &full[r.s]);
+            ++issued;
+          }
+        }
+        // every issued copy lands before the pair leaves
+        const uint32_t first = issued > (uint32_t)K::kStages ? issued - K::kStages : 0;
+        if (rank == 0)
+          for (uint32_t k = first; k < issued; ++k) tc::wait(&full[k % K::kStages], (k / K::kStages) & 1, nullptr, nullptr);
+      }
+      __syncwarp();
+    } else if (warp == kMma && rank == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(2 * kM, K::kN);
+      Ring r;
+      uint32_t it = 0;
+      for (int t = pair; t < g.tiles; t += pairs) {
+        for (int kb = 0; kb < nkb; ++kb, ++it, r.next(K::kStages)) {
+          const int ab = it % K::kAcc;
+          const bool ok = tc::wait(&full[r.s], r.ph, timeouts, abortp) &&
+                          (it < K::kAcc || tc::wait(&accfree[ab], (it / K::kAcc - 1) & 1, timeouts, abortp));
+          if (!__all_sync(0xffffffffu, ok)) { *abortp = 1; continue; }
+          tc::fence_after();
+          const unsigned char* st = sm + (size_t)r.s * K::kStage;
+          if (tc::elect_one()) {
+            mma_block<2>(tmem + ab * K::kN, st, st + K::kA, idesc);
+            commit_pair(&empty[r.s]);
+            commit_pair(&accfull[ab]);
+          }
+          __syncwarp();
+        }
+      }
+      if (tc::elect_one()) commit_pair(&done);
+      __syncwarp();
+      tc::wait(&done, 0, nullptr, nullptr);
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
+    const int col0 = (warp >> 2) * K::kNC;  // this warp's outputs of the tile; its pixels are 32 (warp % 4) and on
+    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + col0;
+    float* st = reinterpret_cast<float*>(sm + (size_t)K::kStages * K::kStage) + warp * warp_floats(K::kNC);
+    read_back<T, K::kNC, K::kAcc>(
+        g, sx, sw, bias, y, pair, pairs, tlane, K::kN, st, accfull, timeouts, abortp,
+        [&](int t, int& p0, int& o0) {
+          uint32_t mt;
+          o0 = (int)g.d_nt.divmod((uint32_t)t, mt) * K::kN + col0;
+          p0 = ((int)mt * 2 + rank) * kM + (warp & 3) * 32;
+        },
+        [&](int ab) {
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_first(&accfree[ab]);
+        });
+  }
+  tc::fence_before();
+  cg::this_cluster().sync();  // neither block leaves while the other's MMAs, copies or arrivals may reach it
+  tc::fence_after();
+  if (warp == kMma)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(K::kCols) : "memory");
 }
 
 // ---- row kernel ------------------------------------------------------------------
@@ -364,13 +632,13 @@ row_kernel(RGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_const
     Ring r;
     for (int it = 0; it < kb1 - kb0; ++it, r.next(K::kStages)) {
       const int ab = it & 1;
-      const bool ok = !*abortp && (it < 2 || tc::wait(&accfree[ab], ((it >> 1) - 1) & 1, timeouts, abortp)) &&
-                      tc::wait(&full[r.s], r.ph, timeouts, abortp);
+      const bool ok = tc::wait(&full[r.s], r.ph, timeouts, abortp) &&
+                      (it < 2 || tc::wait(&accfree[ab], ((it >> 1) - 1) & 1, timeouts, abortp));
       if (!__all_sync(0xffffffffu, ok)) { *abortp = 1; continue; }
       tc::fence_after();
       const unsigned char* st = sm + (size_t)r.s * K::kStage;
       if (tc::elect_one()) {
-        mma_block(tmem + ab * NP, st, st + K::kA, idesc);
+        mma_block<1>(tmem + ab * NP, st, st + K::kA, idesc);
         tc::commit(&empty[r.s]);
         tc::commit(&accfull[ab]);
       }
@@ -393,7 +661,7 @@ row_kernel(RGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_const
     const uint32_t tlane = tmem + ((uint32_t)(warp * 32) << 16);
     for (int it = 0; it < kb1 - kb0; ++it) {
       const int ab = it & 1;
-      bool ok = !*abortp && tc::wait(&accfull[ab], (it >> 1) & 1, timeouts, abortp);
+      bool ok = tc::wait(&accfull[ab], (it >> 1) & 1, timeouts, abortp);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) *abortp = 1;
       tc::fence_after();
@@ -438,11 +706,25 @@ row_kernel(RGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_const
   cl.sync();
   if (warp < 4 && o0 + tid < g.p.cout) {
     const int lo = rank * n / g.split, hi = (rank + 1) * n / g.split;
-    for (int p = lo; p < hi; ++p) {
-      float v = 0.f;
-      for (int k = 0; k < g.split; ++k) v += *cl.map_shared_rank(mine + p * 128 + tid, k);
-      finish<T, 1>(g.p, bias, o0 + tid, &v);
-      y[(p0 + p) * g.p.ys + g.p.yo + o0 + tid] = from_f<T>(v);
+    const float b = bias ? ld(bias + o0 + tid) : 0.f;
+    T* yp = y + p0 * g.p.ys + g.p.yo + o0 + tid;
+#pragma unroll 1
+    for (int p = lo; p < hi; p += 4) {  // four pixels' reads at a time
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = 0.f;
+      for (int k = 0; k < g.split; ++k) {
+        const float* theirs = cl.map_shared_rank(mine + tid, k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (p + e < hi) v[e] += theirs[(p + e) * 128];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += b;
+      norm::act_v<4>(g.p.act, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (p + e < hi) yp[(p + e) * g.p.ys] = from_f<T>(v[e]);
     }
   }
   cl.sync();  // no block leaves while others read its sums
@@ -492,30 +774,29 @@ cudaError_t allow_smem(KernelT kern, size_t smem, std::atomic<uint64_t>& done) {
   return e;
 }
 
-int64_t tiles_of(const Pw& g, int bn) { return ((g.rows + kM - 1) / kM) * ((g.cout + bn - 1) / bn); }
+int64_t tiles_of(const Pw& g, int m, int n) { return ((g.rows + m - 1) / m) * ((g.cout + n - 1) / n); }
 
-template <typename T, int BN>
-cudaError_t launch_tile(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
-                        const T* bias, T* y, cudaStream_t s) {
-  typedef Tile<BN> K;
+// KERN: tile_kernel or pair_kernel, of which K is the shape
+template <typename K, typename T, typename KernelT>
+cudaError_t launch_tiles(KernelT kern, bool pair, std::atomic<uint64_t>& ready, const Pw& g, int64_t ldx, const uint8_t* x,
+                         const float* sx, const uint8_t* w, const float* sw, const T* bias, T* y, cudaStream_t s) {
   alignas(64) CUtensorMap xmap{}, wmap{};
   if (!encode_bytes(&xmap, x, (uint64_t)(ldx == g.pitch ? g.pitch : g.cin), (uint64_t)g.rows, (uint64_t)ldx, kM) ||
-      !encode_bytes(&wmap, w, (uint64_t)g.pitch, (uint64_t)g.cout, (uint64_t)g.pitch, BN))
+      !encode_bytes(&wmap, w, (uint64_t)g.pitch, (uint64_t)g.cout, (uint64_t)g.pitch, K::kB / kBlock))
     return cudaErrorNotSupported;
   unsigned int* to = tma::timeout_counter();
   if (!to) return cudaErrorNotSupported;
-  static std::atomic<uint64_t> ready{0};
-  auto kern = tile_kernel<T, BN>;
   cudaError_t e = allow_smem(kern, K::kSmem, ready);
   if (e != cudaSuccess) return e;
   TGeom t{};
   t.p = g;
-  t.tiles = (int)tiles_of(g, BN);
-  t.d_nt = FastDiv((uint32_t)((g.cout + BN - 1) / BN));
+  t.tiles = (int)tiles_of(g, pair ? 2 * kM : kM, K::kN);
+  t.d_nt = FastDiv((uint32_t)((g.cout + K::kN - 1) / K::kN));
   const int es = (int)sizeof(T);
-  t.vec_out = g.ys * es % 16 == 0 && g.yo * es % 16 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0;
-  const int most = 152 * K::kPerSm;
-  kern<<<t.tiles < most ? t.tiles : most, K::kThreads, K::kSmem, s>>>(t, xmap, wmap, to, sx, sw, bias, y);
+  t.vec_out = g.ys * es % 32 == 0 && g.yo * es % 32 == 0 && reinterpret_cast<uintptr_t>(y) % 32 == 0;
+  const int most = pair ? 76 : 152;
+  const int n = t.tiles < most ? t.tiles : most;
+  kern<<<pair ? 2 * n : n, K::kThreads, K::kSmem, s>>>(t, xmap, wmap, to, sx, sw, bias, y);
   return cudaGetLastError();
 }
 
@@ -576,17 +857,29 @@ cudaError_t run_t(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, c
       default: return launch_row<T, 128>(g, ldx, x, sx, w, sw, bias, y, s);
     }
   }
-  if (tiles_of(g, 128) >= (int64_t(1) << 31)) return cudaErrorNotSupported;
-  if (tiles_of(g, 256) >= 152) return launch_tile<T, 256>(g, ldx, x, sx, w, sw, bias, y, s);
-  return launch_tile<T, 128>(g, ldx, x, sx, w, sw, bias, y, s);
+  static std::atomic<uint64_t> ready_tile{0}, ready_pair{0};
+  const int64_t tiles = tiles_of(g, kM, Tile::kN), pairs = tiles_of(g, 2 * kM, Pair::kN);
+  if (tiles >= (int64_t(1) << 31)) return cudaErrorNotSupported;
+  // Rounds of tiles times what a tile takes in cycles, as traced: a block of
+  // channels 600 and the rest 1500 by one thread block, 1130 and 1800 by a pair
+  // (four times the products). 12544 pixels, 512 -> 512 channels 12.3 against
+  // 13.5 us, 3136, 1024 -> 1024 12.2 against 10.5, 200704, 128 -> 128 22.5
+  // against 25.4, 2048, 2048 -> 2048 19.5 against 15.3.
+  const int64_t by_tile = (tiles + 151) / 152 * (g.nkb * 600 + 1500), by_pair = (pairs + 75) / 76 * (g.nkb * 1130 + 1800);
+  if (by_pair < by_tile) return launch_tiles<Pair, T>(pair_kernel<T>, true, ready_pair, g, ldx, x, sx, w, sw, bias, y, s);
+  return launch_tiles<Tile, T>(tile_kernel<T>, false, ready_tile, g, ldx, x, sx, w, sw, bias, y, s);
 }
 
 }  // namespace
 
+// The row kernel up to 32 pixels, and while tiles leave half of the SMs idle
+// and a tile's sum is long enough to be shared: 128 pixels, 4096 -> 4096
+// channels 12.8 us against 18.2 in tiles, 300, 4096 -> 512 9.4 against 17.5;
+// but 300, 1024 -> 1024 9.1 against 7.4.
 Plan plan(const Pw& g) {
-  if (g.rows > 128) return Plan::Tile;
   const int np = row_pixels(g), split = split_of(g, np);
-  return (int64_t)((g.nkb + split - 1) / split) * np * 4 <= 32 * 1024 ? Plan::Row : Plan::Tile;
+  if ((int64_t)((g.nkb + split - 1) / split) * np * 4 > 32 * 1024) return Plan::Tile;  // its table of scales
+  return g.rows <= 32 || (g.nkb >= 16 && tiles_of(g, kM, Tile::kN) <= 76) ? Plan::Row : Plan::Tile;
 }
 
 cudaError_t run_tc(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
