@@ -588,13 +588,15 @@ dwconv_status_t check_weight8(const dwconv_weight8_t* w8) {
   return check_ptr(w8->scales, 4, true);
 }
 
+constexpr int64_t kMaxGrads = int64_t(1) << 38;
+
 dwconv_status_t check_grads(int count, const dwconv_grad_t* grads) {
   if (count < 0 || (count > 0 && !grads)) return DWCONV_ERR_INVALID_ARG;
   int64_t total = 0;
   for (int i = 0; i < count; ++i) {
     if (!dtype_ok(grads[i].dtype)) return DWCONV_ERR_UNSUPPORTED;
     if (grads[i].n < 0) return DWCONV_ERR_INVALID_ARG;
-    if (grads[i].n > kMaxElems || (total += grads[i].n) > kMaxElems) return DWCONV_ERR_UNSUPPORTED;
+    if (grads[i].n > kMaxGrads || (total += grads[i].n) > kMaxGrads) return DWCONV_ERR_UNSUPPORTED;
   }
   return DWCONV_OK;
 }

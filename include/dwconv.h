@@ -552,13 +552,15 @@ size_t dwconv_grad_norm_clip_workspace_size(int count, const dwconv_grad_t* grad
 
 /* Norm over all gradients, and their clipping:
  *   n = sqrt(sum of g^2 over all tensors),  out = g * min(1, max_norm / (n + 1e-6))
- * with sums that no finite gradient overflows (n itself is an fp32: above its
- * range *norm is infinite). max_norm > 0; INFINITY clips nothing. A NaN or an
- * infinity among the gradients makes n NaN or infinite, and out NaN (n NaN) or
- * 0 and NaN (n infinite) unless max_norm is INFINITY. norm (device memory) may
- * be NULL. grads is read on the host during the call, which is two launches
- * per 960 tensors. The same tensor may not appear twice with an out.
- * The workspace (16-byte aligned) is not used concurrently. */
+ * with sums of squares that no finite gradient overflows; n itself is an fp32:
+ * above its range *norm is infinite and out 0. max_norm > 0; INFINITY clips
+ * nothing. A NaN among the gradients makes n NaN and every out NaN; an infinity
+ * makes n infinite, its own out NaN and the others 0; neither, with max_norm
+ * INFINITY, changes another gradient. norm (device memory) may be NULL. grads
+ * is read on the host during the call, which is one launch where there is little
+ * to do and two per 960 tensors otherwise. The tensors have 2^38 elements
+ * together at most (DWCONV_ERR_UNSUPPORTED). The same tensor may not appear
+ * twice with an out. The workspace (16-byte aligned) is not used concurrently. */
 dwconv_status_t dwconv_grad_norm_clip(int count, const dwconv_grad_t* grads, float max_norm, float* norm,
                                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
