@@ -42,8 +42,9 @@ constexpr int kUnit = 512;              // elements of a unit: 16 per lane
 constexpr int64_t kBlocks = 152 * 4;    // what the GPU holds at once
 constexpr int kCluster = 8;             // blocks of a cluster, units that it takes by itself
 constexpr int kAlone = 8 * kCluster * kWarps;
-// tensors per launch: the parameters are 1.3, 4 or 32 KB at most
-constexpr int kSmall = 40, kMid = 120, kBig = 960;
+// Tensors per launch, by sizes of the parameters (1.3 to 31 KB): a launch with
+// 31 KB of them takes 6 us longer than one with 4.
+constexpr int kSmall = 40, kMid = 120, kMore = 240, kMany = 480, kBig = 960;
 
 template <int N>
 struct Table {
@@ -96,45 +97,71 @@ __device__ __forceinline__ void add_squares(const float* v, float& s, double& d)
   }
 }
 
+// A unit of n elements: whole 16-byte vectors where its pointers allow it,
+// the elements behind them (or all, off 16 bytes) one by one. A lane's vectors
+// are on their way before the first is used.
 template <typename T>
 __device__ __forceinline__ void unit_squares(const T* g, int n, float& s, double& d) {
   constexpr int VEC = Vec<T>::n, K = kUnit / 32 / VEC;
   const int lane = threadIdx.x & 31;
-  if (n == kUnit && reinterpret_cast<uintptr_t>(g) % 16 == 0) {
+  if (reinterpret_cast<uintptr_t>(g) % 16 == 0) {
     uint4 u[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) u[k] = reinterpret_cast<const uint4*>(g)[k * 32 + lane];
+    for (int k = 0; k < K; ++k) {
+      u[k] = make_uint4(0, 0, 0, 0);
+      if ((k * 32 + lane + 1) * VEC <= n) u[k] = reinterpret_cast<const uint4*>(g)[k * 32 + lane];
+    }
+    const int rest = n % VEC;
+    float v[VEC];
+    if (lane < rest) {
+      v[0] = to_f<T>(g[n - rest + lane]);
+      add_squares<T, 1>(v, s, d);
+    }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float v[VEC];
       unpack16<T>(u[k], v);
       add_squares<T, VEC>(v, s, d);
     }
   } else {
-#pragma unroll 4
-    for (int i = lane; i < n; i += 32) {
-      const float v = to_f<T>(g[i]);
-      add_squares<T, 1>(&v, s, d);
+#pragma unroll 1
+    for (int i = lane; i < n; i += 128) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = i + 32 * k < n ? to_f<T>(g[i + 32 * k]) : 0.f;
+      add_squares<T, 4>(v, s, d);
     }
   }
 }
 
 template <typename T>
+__device__ __forceinline__ uint4 times(const uint4& u, float k) {
+  constexpr int VEC = Vec<T>::n;
+  float v[VEC];
+  unpack16<T>(u, v);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) v[e] *= k;
+  return pack16<T>(v);
+}
+template <typename T>
 __device__ __forceinline__ void unit_scale(const T* g, T* out, int n, float k) {
   constexpr int VEC = Vec<T>::n, K = kUnit / 32 / VEC;
   const int lane = threadIdx.x & 31;
-  if (n == kUnit && (reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) % 16 == 0) {
-    uint4 u[K];
+  if ((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(out)) % 16 == 0) {
+    const uint4* from = reinterpret_cast<const uint4*>(g) + lane;
+    uint4* to = reinterpret_cast<uint4*>(out) + lane;
+    if (n == kUnit) {
+      uint4 u[K];
 #pragma unroll
-    for (int q = 0; q < K; ++q) u[q] = reinterpret_cast<const uint4*>(g)[q * 32 + lane];
+      for (int q = 0; q < K; ++q) u[q] = from[q * 32];
 #pragma unroll
-    for (int q = 0; q < K; ++q) {
-      float v[VEC];
-      unpack16<T>(u[q], v);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] *= k;
-      reinterpret_cast<uint4*>(out)[q * 32 + lane] = pack16<T>(v);
+      for (int q = 0; q < K; ++q) to[q * 32] = times<T>(u[q], k);
+      return;
     }
+    const int whole = n / VEC;
+#pragma unroll 2
+    for (int q = lane; q < whole; q += 32, from += 32, to += 32) *to = times<T>(*from, k);
+    const int i = whole * VEC + lane;
+    if (i < n) out[i] = from_f<T>(to_f<T>(g[i]) * k);
   } else {
 #pragma unroll 4
     for (int i = lane; i < n; i += 32) out[i] = from_f<T>(to_f<T>(g[i]) * k);
@@ -383,9 +410,9 @@ cudaError_t run(int count, const dwconv_grad_t* grads, float most, float* norm, 
         return scale ? cudaSuccess
                : used <= kSmall ? launch_alone<kSmall>(grads, i, j, units, most, norm, s)
                                 : launch_alone<kMid>(grads, i, j, units, most, norm, s);
-      const cudaError_t r = used <= kSmall ? launch<kSmall>(grads, i, j, units, slot0, slots, scale != 0, most, norm, sums, s)
-                            : used <= kMid ? launch<kMid>(grads, i, j, units, slot0, slots, scale != 0, most, norm, sums, s)
-                                           : launch<kBig>(grads, i, j, units, slot0, slots, scale != 0, most, norm, sums, s);
+      auto* const go = used <= kSmall ? launch<kSmall> : used <= kMid ? launch<kMid> : used <= kMore ? launch<kMore>
+                       : used <= kMany ? launch<kMany> : launch<kBig>;
+      const cudaError_t r = go(grads, i, j, units, slot0, slots, scale != 0, most, norm, sums, s);
       slot0 += blocks_of(units);
       return r;
     });
