@@ -11,8 +11,14 @@
 // One pass: a row is read once into the registers of its threads, as stored
 // (h needs no more bits), its sum of squares goes through shuffles and, for
 // rows of several warps, one exchange in shared memory; the codes' maxima are
-// shuffles of the lanes that hold a block. Rows of more channels than 1024
-// threads hold are read twice, in spans.
+// shuffles of the lanes that hold a block. Arithmetic is on pairs of channels.
+// Rows of more channels than 1024 threads hold are read twice, in spans.
+//
+// Rows that begin off 16 bytes (odd channels) are read in the vectors that lie
+// on 16 bytes (rms.cuh): threads step over rows that begin alike. Their codes'
+// blocks begin anywhere in a vector, so codes are made from a copy of the row
+// in shared memory, four channels a lane. Only tensors that do not begin alike
+// are read element by element.
 //
 // Bound by memory: 4 to 6 operations per element against 2 to 7 bytes.
 #include "rms.cuh"
@@ -29,13 +35,300 @@ struct FGeom {
   float eps, inv_c;
 };
 
+template <int Q, int P>  // codes of P pairs (4 or 2)
+__device__ __forceinline__ void store_codes(uint8_t* q, const f32x2* f, float inv) {
+  if constexpr (P == 4)
+    *reinterpret_cast<uint2*>(q) = make_uint2(encode4<Q>(f[0], f[1], inv), encode4<Q>(f[2], f[3], inv));
+  else
+    *reinterpret_cast<uint32_t*>(q) = encode4<Q>(f[0], f[1], inv);
+}
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, f32x2 v) {
+  return max(m, max((uint32_t)v & 0x7fffffffu, (uint32_t)(v >> 32) & 0x7fffffffu));
+}
+
+// ---- rows that 256 threads hold ----------------------------------------------------
+
+constexpr int kNT = 256;
+// Blocks step over the rows; the next row's vectors are on their way while one
+// is worked on. RAG: rows begin anywhere, the step is a multiple of 8 of them,
+// and codes are made by one warp per row.
+template <typename T, int V, int NI, int Q, bool RAG>
+__global__ void __launch_bounds__(kNT, NI == 1 ? 4 : NI == 2 ? 3 : 2)
+fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, T* h, T* y, float* rstd, Act8 t) {
+  typedef typename Raw<T, V>::type R;
+  constexpr int P = V / 2;
+  constexpr bool kCopy = RAG && Q != kSrcFull;
+  __shared__ float part[2][kNT / 32];
+  __shared__ __align__(16) R copy[kCopy ? kNT / 32 : 1][kCopy ? NI * 32 + 1 : 1];
+  const int tid = threadIdx.x;
+  const int in_row = tid & (g.tpr - 1);
+  const int W = NI > 1 || g.tpr >= 32 ? 32 : g.tpr;  // rows of fewer than 32 lanes have one vector a lane
+  const int first = (in_row & ~(W - 1)) * NI + (in_row & (W - 1));
+  const int rpb = kNT >> g.log_tpr;
+  const int64_t step = (int64_t)gridDim.x * rpb;
+  int64_t row = (int64_t)blockIdx.x * rpb + (tid >> g.log_tpr);
+  const int ph = RAG ? phase_of(x + row * g.xs + g.xo) : 0;
+  const int nvec = (g.C + ph + V - 1) / V;
+  const int c0 = first * V - ph;  // first channel of item 0; item i is 32 V further
+  const int64_t xstep = step * g.xs, ystep = step * g.ys;
+  const T* xp = x + row * g.xs + g.xo;
+  const T* rp = res + (res ? row * g.xs + g.xo : 0);
+  T* hp = h + (h ? row * g.xs + g.xo : 0);
+  T* yp = y + (y ? row * g.ys + g.yo : 0);
+  f32x2 gm[NI][P];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) gm[i][e] = both(1.f);
+    if (gamma && first + i * W < nvec)
+      pairs_of<T, V>(RAG ? load_part<T, V>(gamma, c0 + i * W * V, g.C) : load_vec<T, V, false>(gamma, c0 + i * W * V, g.C), gm[i]);
+  }
+  R nx[NI], nr[NI];
+  auto fetch = [&](bool live) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (!live || first + i * W >= nvec) continue;
+      nx[i] = load_vec<T, V, RAG>(xp, c0 + i * W * V, g.C);
+      if (res) nr[i] = load_vec<T, V, RAG>(rp, c0 + i * W * V, g.C);
+    }
+  };
+  int flip = 0;
+  fetch(row < g.rows);
+  for (int64_t base = (int64_t)blockIdx.x * rpb; base < g.rows; base += step, row += step, flip ^= 1) {
+    const bool live = row < g.rows;
+    R hv[NI];
+    f32x2 s2 = 0ull;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (!live || first + i * W >= nvec) continue;
+      f32x2 a[P];
+      hv[i] = nx[i];
+      pairs_of<T, V>(hv[i], a);
+      if (res) {
+        f32x2 b[P];
+        pairs_of<T, V>(nr[i], b);
+#pragma unroll
+        for (int e = 0; e < P; ++e) a[e] = add_f32x2(a[e], b[e]);
+        hv[i] = vec_of<T, V>(a);
+        pairs_of<T, V>(hv[i], a);
+      }
+#pragma unroll
+      for (int e = 0; e < P; ++e) s2 = fma2(a[e], a[e], s2);
+    }
+    xp += xstep;
+    rp += xstep;
+    // the next row is read before this one's h is written: x or the residual may be h's memory, row by row
+    fetch(row + step < g.rows);
+    if (h) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (live && first + i * W < nvec) store_vec<T, V, RAG>(hp, c0 + i * W * V, g.C, hv[i]);
+      hp += xstep;
+    }
+    const float ss = row_sum<kNT>(sum2(s2), g.tpr, part[flip]);
+    const float r = __frsqrt_rn(fmaf(ss, g.inv_c, g.eps));
+    if (live && in_row == 0 && rstd) rstd[row] = r;
+    if constexpr (kCopy) {
+      R* mine = copy[tid >> 5];
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (live && first + i * 32 < nvec) mine[first + i * 32] = hv[i];
+      __syncwarp();
+    }
+    if (!kCopy || y) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const bool on = live && first + i * W < nvec;
+        f32x2 f[P];
+#pragma unroll
+        for (int e = 0; e < P; ++e) f[e] = 0ull;
+        if (on) {
+          pairs_of<T, V>(hv[i], f);
+#pragma unroll
+          for (int e = 0; e < P; ++e) f[e] = mul_f32x2(mul_f32x2(f[e], both(r)), gm[i][e]);
+          if (y) store_vec<T, V, RAG>(yp, c0 + i * W * V, g.C, vec_of<T, V>(f));
+        }
+        if constexpr (Q != kSrcFull && !RAG) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int e = 0; e < P; ++e) m = max_bits(m, f[e]);
+          const int block = 1 << t.shift;
+          for (int o = min(block / V, W) >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (on) {
+            const int c = c0 + i * W * V;
+            float inv;
+            const float s = scale_of<Q>(m, &inv);
+            store_codes<Q, P>(t.codes + row * g.C + c, f, inv);
+            if ((c & (block - 1)) == 0) t.scales[row * t.nblk + (c >> t.shift)] = s;
+          }
+        }
+      }
+      yp += ystep;
+    }
+    if constexpr (kCopy) {  // a warp per row, four channels a lane
+      const T* hs = reinterpret_cast<const T*>(copy[tid >> 5]) + ph;
+      const int block = 1 << t.shift;
+      uint8_t* q = t.codes + row * g.C;
+      for (int c = 4 * (tid & 31); c < g.C + 4 * (tid & 31); c += 128) {
+        float f[4];
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[e] = live && c + e < g.C ? __fmul_rn(to_f<T>(hs[c + e]), r) : 0.f;
+          if (gamma && live && c + e < g.C) f[e] = __fmul_rn(f[e], ld(gamma + c + e));
+          m = max(m, abs_bits(f[e]));
+        }
+        for (int o = block >> 3; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (live && c < g.C) {
+          float inv;
+          const float s = scale_of<Q>(m, &inv);
+          const uint32_t k = encode4<Q>(f[0], f[1], f[2], f[3], inv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < g.C) q[c + e] = (uint8_t)(k >> (8 * e));
+          if ((c & (block - 1)) == 0) t.scales[row * t.nblk + (c >> t.shift)] = s;
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// ---- wider rows, on 16 bytes ---------------------------------------------------------
+
+// Threads by the row: 512 or 1024 of them, or (no codes' registers in the way)
+// rows read twice.
+
 template <typename T, int V, int NI, int Q, int NT>
 __global__ void __launch_bounds__(NT)
-fwd_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, T* h, T* y,
-           float* rstd, Act8 t) {
+fwd_wide_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, T* h, T* y, float* rstd, Act8 t) {
   typedef typename Raw<T, V>::type R;
+  constexpr int P = V / 2;
   __shared__ float part[NT / 32];
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
+  const int in_row = tid & (g.tpr - 1);
+  const int W = g.tpr < 32 ? g.tpr : 32;
+  const int first = (in_row & ~(W - 1)) * NI + (in_row & (W - 1));  // vector of item 0; item i is i * W further
+  const int span = g.tpr * NI;
+  const int64_t row = (int64_t)blockIdx.x * (NT >> g.log_tpr) + (tid >> g.log_tpr);
+  const bool live = row < g.rows;
+  const T* xr = x + row * g.xs + g.xo;
+  const T* rr = res + (res ? row * g.xs + g.xo : 0);
+  T* hr = h + (h ? row * g.xs + g.xo : 0);
+
+  R hv[NI], gv[NI];
+  auto load_h = [&](int seg, bool again) {
+    // the second read of a row takes h where it was stored: x or the residual may be the same memory
+    const bool stored = again && h;
+    R rv[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int v = seg * span + first + i * W;
+      if (live && v < g.nvec) {
+        hv[i] = *reinterpret_cast<const R*>((stored ? hr : xr) + (int64_t)v * V);
+        if (res && !stored) rv[i] = *reinterpret_cast<const R*>(rr + (int64_t)v * V);
+      }
+    }
+    if (res && !stored) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        f32x2 a[P], b[P];
+        pairs_of<T, V>(hv[i], a);
+        pairs_of<T, V>(rv[i], b);
+#pragma unroll
+        for (int e = 0; e < P; ++e) a[e] = add_f32x2(a[e], b[e]);
+        hv[i] = vec_of<T, V>(a);
+      }
+    }
+    if (h && !again) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int v = seg * span + first + i * W;
+        if (live && v < g.nvec) *reinterpret_cast<R*>(hr + (int64_t)v * V) = hv[i];
+      }
+    }
+  };
+  auto load_gamma = [&](int seg) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int v = seg * span + first + i * W;
+      if (gamma && v < g.nvec) gv[i] = *reinterpret_cast<const R*>(gamma + (int64_t)v * V);
+    }
+  };
+
+  float ss = 0.f;
+  for (int seg = 0; seg < g.segs; ++seg) {
+    if (g.segs == 1) load_gamma(0);
+    load_h(seg, false);
+    f32x2 s2 = 0ull;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (!live || seg * span + first + i * W >= g.nvec) continue;
+      f32x2 a[P];
+      pairs_of<T, V>(hv[i], a);
+#pragma unroll
+      for (int e = 0; e < P; ++e) s2 = fma2(a[e], a[e], s2);
+    }
+    ss += sum2(s2);
+  }
+  ss = row_sum<NT>(ss, g.tpr, part);
+  const float r = __frsqrt_rn(fmaf(ss, g.inv_c, g.eps));
+  if (live && in_row == 0 && rstd) rstd[row] = r;
+
+  T* yr = y + (y ? row * g.ys + g.yo : 0);
+  for (int seg = 0; seg < g.segs; ++seg) {
+    if (g.segs > 1) {
+      load_gamma(seg);
+      load_h(seg, true);
+    }
+    const f32x2 r2 = both(r);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int v = seg * span + first + i * W;
+      const bool on = live && v < g.nvec;
+      f32x2 f[P];
+#pragma unroll
+      for (int e = 0; e < P; ++e) f[e] = 0ull;
+      if (on) {
+        pairs_of<T, V>(hv[i], f);
+#pragma unroll
+        for (int e = 0; e < P; ++e) f[e] = mul_f32x2(f[e], r2);
+        if (gamma) {
+          f32x2 gm[P];
+          pairs_of<T, V>(gv[i], gm);
+#pragma unroll
+          for (int e = 0; e < P; ++e) f[e] = mul_f32x2(f[e], gm[e]);
+        }
+        if (y) *reinterpret_cast<R*>(yr + (int64_t)v * V) = vec_of<T, V>(f);
+      }
+      if constexpr (Q != kSrcFull) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < P; ++e) m = max_bits(m, f[e]);
+        const int block = 1 << t.shift;
+        for (int o = min(block / V, W) >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (on) {
+          const int c = v * V;
+          float inv;
+          const float s = scale_of<Q>(m, &inv);
+          store_codes<Q, P>(t.codes + row * g.C + c, f, inv);
+          if ((c & (block - 1)) == 0) t.scales[row * t.nblk + (c >> t.shift)] = s;
+        }
+      }
+    }
+  }
+}
+
+// ---- element by element --------------------------------------------------------------
+
+template <typename T, int Q, int NT>
+__global__ void __launch_bounds__(NT)
+fwd_elem_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, T* h, T* y,
+           float* rstd, Act8 t) {
+  constexpr int V = 1, NI = 8;
+  typedef T R;
+  __shared__ float part[NT / 32];
+  const int tid = threadIdx.x;
   const int in_row = tid & (g.tpr - 1);
   const int W = g.tpr < 32 ? g.tpr : 32;
   const int first = (in_row & ~(W - 1)) * NI + (in_row & (W - 1));  // vector of item 0; item i is i * W further
@@ -105,14 +398,7 @@ fwd_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, T* h,
     }
     ss += s0 + s1;
   }
-  for (int o = W >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (g.tpr > 32) {
-    if (lane == 0) part[tid >> 5] = ss;
-    __syncthreads();
-    const int nw = g.tpr >> 5, w0 = (tid >> 5) & ~(nw - 1);
-    ss = lane < nw ? part[w0 + lane] : 0.f;
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  }
+  ss = row_sum<NT>(ss, g.tpr, part);
   const float r = __frsqrt_rn(fmaf(ss, g.inv_c, g.eps));
   if (live && in_row == 0 && rstd) rstd[row] = r;
 
@@ -177,111 +463,152 @@ fwd_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, T* h,
         float inv;
         const float s = scale_of<Q>(m[i], &inv);
         uint8_t* q = t.codes + row * g.C + c;
-        if constexpr (V == 8) {
-          *reinterpret_cast<uint2*>(q) = make_uint2(encode4<Q>(f[i][0], f[i][1], f[i][2], f[i][3], inv),
-                                                    encode4<Q>(f[i][4], f[i][5], f[i][6], f[i][7], inv));
-        } else if constexpr (V == 4) {
-          *reinterpret_cast<uint32_t*>(q) = encode4<Q>(f[i][0], f[i][1], f[i][2], f[i][3], inv);
-        } else {
-          *q = encode1<Q>(f[i][0], inv);
-        }
+        *q = encode1<Q>(f[i][0], inv);
         if ((c & (block - 1)) == 0) t.scales[row * t.nblk + (c >> t.shift)] = s;
       }
     }
   }
 }
 
+// ---- host -------------------------------------------------------------------------------
+
+void spread(Lay* l, int64_t nvec, int most) {
+  const int64_t need = (nvec + l->ni - 1) / l->ni;
+  l->tpr = pow2_at_least(need);
+  if (l->tpr < 4) l->tpr = 4;
+  if (l->tpr > most) l->tpr = most;
+  l->segs = (int)((need + l->tpr - 1) / l->tpr);
+}
+
 // Vectors per thread: one while all rows together are less than a wave of
-// threads (latency counts), else two, or four where 256 threads then hold a
-// row. Elements one by one are taken eight to a thread.
+// threads (latency counts), else two, or four where 256 threads then hold a row.
 Lay lay(const Rms& g, int V) {
   Lay l{};
   l.v = V;
   const int64_t nvec = g.C / V;
-  if (V == 1) {
-    l.ni = 8;
-  } else {
-    const bool wave = g.rows * nvec > 152 * 2048;
-    l.ni = nvec > 1024 ? 2 : !wave || nvec < 64 ? 1 : nvec < 128 ? 2 : 4;
-  }
-  const int64_t need = (nvec + l.ni - 1) / l.ni;
-  l.tpr = pow2_at_least(need);
-  if (l.tpr < 4) l.tpr = 4;
-  if (l.tpr > 1024) l.tpr = 1024;
+  const bool wave = g.rows * nvec > 152 * 2048;
+  l.ni = !wave && nvec <= 1024 ? 1 : nvec <= 64 ? 1 : nvec <= 512 ? 2 : nvec <= 1024 ? 4 : 2;
+  spread(&l, nvec, 1024);
+  l.nt = l.tpr > kNT ? l.tpr : kNT;
+  return l;
+}
+Lay lay_elem(const Rms& g) {
+  Lay l{};
+  l.v = 1;
+  l.ni = 8;
+  spread(&l, g.C, 1024);
   l.nt = l.tpr > 256 ? l.tpr : 256;
-  l.segs = (int)((need + l.tpr - 1) / l.tpr);
+  return l;
+}
+// A warp per row where there are codes; segs > 1: not one for the ragged form.
+Lay lay_ragged(const Rms& g, int V, bool codes) {
+  Lay l{};
+  l.v = V;
+  const int64_t nvec = (g.C + 2 * V - 2) / V;
+  l.ni = 1;
+  const int most = codes ? 32 : 64;
+  while (l.ni < 4 && l.ni * most < nvec) l.ni *= 2;
+  spread(&l, nvec, codes ? 32 : kNT);
+  if ((codes || l.ni > 1) && l.tpr < 32) l.tpr = 32;
+  l.nt = kNT;
   return l;
 }
 
-template <typename T, int V, int NI, int Q>
-cudaError_t launch(const Rms& g, const Lay& l, const T* x, const T* res, const T* gamma, T* h, T* y, float* rstd,
-                   const Act8& t, cudaStream_t s) {
+struct Args {
+  const void *x, *res, *gamma;
+  void *h, *y;
+  float* rstd;
+  Act8 t;
+};
+
+FGeom geom(const Rms& g, const Lay& l) {
   FGeom f{};
   f.rows = g.rows;
   f.xs = g.xs; f.xo = g.xo; f.ys = g.ys; f.yo = g.yo;
   f.C = g.C;
-  f.nvec = g.C / V;
+  f.nvec = g.C / l.v;
   f.tpr = l.tpr;
   while ((1 << f.log_tpr) < l.tpr) ++f.log_tpr;
   f.segs = l.segs;
   f.eps = g.eps;
   f.inv_c = 1.f / (float)g.C;
-  const int64_t rpb = l.nt / l.tpr, most = (int64_t(1) << 30);
-  for (int64_t r = 0; r < g.rows; r += most * rpb) {
-    f.rows = g.rows - r < most * rpb ? g.rows - r : most * rpb;
-    const unsigned grid = (unsigned)((f.rows + rpb - 1) / rpb);
-    Act8 u = t;
+  return f;
+}
+
+template <typename T, int Q, typename KernelT>
+cudaError_t launch(KernelT kern, const Rms& g, const Lay& l, const Args& a, cudaStream_t s) {
+  FGeom f = geom(g, l);
+  const int64_t rpb = l.nt / l.tpr, most = (int64_t(1) << 30) * rpb;
+  for (int64_t r = 0; r < g.rows; r += most) {  // grids of at most 2^30 blocks
+    f.rows = g.rows - r < most ? g.rows - r : most;
+    Act8 u = a.t;
     if (Q != kSrcFull) {
       u.codes += r * g.C;
-      u.scales += r * t.nblk;
+      u.scales += r * u.nblk;
     }
     const int64_t ox = r * g.xs, oy = r * g.ys;
-    const T* r2 = res ? res + ox : nullptr;
-    T* h2 = h ? h + ox : nullptr;
-    T* y2 = y ? y + oy : nullptr;
-    float* s2 = rstd ? rstd + r : nullptr;
-    if (l.nt == 256) fwd_kernel<T, V, NI, Q, 256><<<grid, 256, 0, s>>>(f, x + ox, r2, gamma, h2, y2, s2, u);
-    if constexpr (NI != 4) {
-      if (l.nt == 512) fwd_kernel<T, V, NI, Q, 512><<<grid, 512, 0, s>>>(f, x + ox, r2, gamma, h2, y2, s2, u);
-      if (l.nt == 1024) fwd_kernel<T, V, NI, Q, 1024><<<grid, 1024, 0, s>>>(f, x + ox, r2, gamma, h2, y2, s2, u);
-    }
+    kern<<<(unsigned)((f.rows + rpb - 1) / rpb), l.nt, 0, s>>>(
+        f, (const T*)a.x + ox, a.res ? (const T*)a.res + ox : nullptr, (const T*)a.gamma, a.h ? (T*)a.h + ox : nullptr,
+        a.y ? (T*)a.y + oy : nullptr, a.rstd ? a.rstd + r : nullptr, u);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
+template <typename T, int Q, bool RAG>
+cudaError_t run_rows(const Rms& g, const Lay& l, const Args& a, cudaStream_t s) {
+  constexpr int V = Vec<T>::n;
+  const int64_t rpb = kNT / l.tpr, all = (g.rows + rpb - 1) / rpb;
+  const int64_t held = 152 * (l.ni == 1 ? 4 : l.ni == 2 ? 3 : 2);  // by the kernels' registers: one wave
+  int64_t blocks = all < held ? all : held;
+  while (blocks * rpb % 8) ++blocks;
+  const FGeom f = geom(g, l);
+  const auto kern = l.ni == 1   ? fwd_rows_kernel<T, V, 1, Q, RAG>
+                    : l.ni == 2 ? fwd_rows_kernel<T, V, 2, Q, RAG>
+                                : fwd_rows_kernel<T, V, 4, Q, RAG>;
+  kern<<<(unsigned)blocks, kNT, 0, s>>>(f, (const T*)a.x, (const T*)a.res, (const T*)a.gamma, (T*)a.h, (T*)a.y, a.rstd, a.t);
+  return cudaGetLastError();
+}
+
 template <typename T, int Q>
-cudaError_t run(const Rms& g, const void* x, const void* res, const void* gamma, void* h, void* y, float* rstd,
-                const Act8& t, cudaStream_t s) {
-  constexpr int VEC = Vec<T>::n;
-  const bool v = vec_ok(g, VEC, on16(x) && on16(res) && on16(gamma) && on16(h) && on16(y), Q != kSrcFull ? t.codes : nullptr);
-  const Lay l = lay(g, v ? VEC : 1);
-#define GO(V_, NI_) return launch<T, V_, NI_, Q>(g, l, (const T*)x, (const T*)res, (const T*)gamma, (T*)h, (T*)y, rstd, t, s)
-  if (!v) GO(1, 8);
-  if (l.ni == 1) GO(VEC, 1);
-  if (l.ni == 2) GO(VEC, 2);
-  GO(VEC, 4);
-#undef GO
+cudaError_t run(const Rms& g, const Args& a, cudaStream_t s) {
+  constexpr int V = Vec<T>::n;
+  if (rows_on16(g, V) && on16(a.x) && on16(a.res) && on16(a.gamma) && on16(a.h) && on16(a.y) &&
+      (Q == kSrcFull || reinterpret_cast<uintptr_t>(a.t.codes) % V == 0)) {
+    const Lay l = lay(g, V);
+    if (l.nt == kNT) return run_rows<T, Q, false>(g, l, a, s);
+    if (l.nt == 512) return launch<T, Q>(l.ni == 1 ? fwd_wide_kernel<T, V, 1, Q, 512> : fwd_wide_kernel<T, V, 2, Q, 512>, g, l, a, s);
+    return launch<T, Q>(l.ni == 1 ? fwd_wide_kernel<T, V, 1, Q, 1024> : fwd_wide_kernel<T, V, 2, Q, 1024>, g, l, a, s);
+  }
+  const Lay l = lay_ragged(g, V, Q != kSrcFull);
+  if (l.segs == 1 && alike(a.x, a.res) && alike(a.x, a.h) && alike(a.x, a.y) && (!a.y || rows_alike(g, V)))
+    return run_rows<T, Q, true>(g, l, a, s);
+  const Lay e = lay_elem(g);
+  if (e.nt == 256) return launch<T, Q>(fwd_elem_kernel<T, Q, 256>, g, e, a, s);
+  if (e.nt == 512) return launch<T, Q>(fwd_elem_kernel<T, Q, 512>, g, e, a, s);
+  return launch<T, Q>(fwd_elem_kernel<T, Q, 1024>, g, e, a, s);
 }
 
 }  // namespace
 
 bool fwd_in_row(const Rms& g) {
-  const int VEC = g.dtype == DWCONV_F32 ? 4 : 8;
-  return lay(g, vec_ok(g, VEC, true, nullptr) ? VEC : 1).segs == 1;
+  const int V = g.dtype == DWCONV_F32 ? 4 : 8;
+  if (rows_on16(g, V)) return lay(g, V).segs == 1;
+  return lay_ragged(g, V, false).segs == 1 || lay_elem(g).segs == 1;
 }
 
 cudaError_t fwd(const Rms& g, const void* x, const void* residual, const void* gamma, void* h, void* y, float* rstd,
                 const Act8& t, cudaStream_t s) {
   if (g.rows == 0) return cudaSuccess;
+  const Args a{x, residual, gamma, h, y, rstd, t};
   cudaError_t e = cudaErrorInvalidValue;
   if (!t.codes) {
-    DWCONV_DISPATCH_DTYPE(g.dtype, T, e = run<T, kSrcFull>(g, x, residual, gamma, h, y, rstd, t, s));
+    DWCONV_DISPATCH_DTYPE(g.dtype, T, e = run<T, kSrcFull>(g, a, s));
   } else if (t.src == kSrcI8) {
-    DWCONV_DISPATCH_DTYPE(g.dtype, T, e = run<T, kSrcI8>(g, x, residual, gamma, h, y, rstd, t, s));
+    DWCONV_DISPATCH_DTYPE(g.dtype, T, e = run<T, kSrcI8>(g, a, s));
   } else {
-    DWCONV_DISPATCH_DTYPE(g.dtype, T, e = run<T, kSrcE4M3>(g, x, residual, gamma, h, y, rstd, t, s));
+    DWCONV_DISPATCH_DTYPE(g.dtype, T, e = run<T, kSrcE4M3>(g, a, s));
   }
   return e;
 }

@@ -7,13 +7,15 @@
 // of both x and the residual.
 //
 // Blocks walk over rows. A thread holds the same channels of every row that
-// it meets, so its share of ggamma stays in registers from row to row; the
-// next row's vectors are on their way while one is worked on. Row sums go
+// it meets (rows that begin off 16 bytes too: it steps over rows that begin
+// alike, rms.cuh), so its share of ggamma stays in registers from row to row;
+// the next row's vectors are on their way while one is worked on. Row sums go
 // through shuffles and, for rows of several warps, one exchange in shared
 // memory (two buffers in turn: one barrier per row). The blocks' shares go to
 // the workspace and a second launch adds them in a fixed order. Rows of more
-// channels than 512 threads hold are read twice by one block, and a kernel of
-// its own takes their ggamma, down the columns.
+// channels than 512 threads hold, and tensors that do not begin alike, are
+// read element by element, twice, by one block, and a kernel of its own takes
+// their ggamma, down the columns.
 //
 // Bound by memory: h, gy (and gres) read once, gx written once.
 #include "rms.cuh"
@@ -24,131 +26,121 @@ namespace {
 
 struct BGeom {
   int64_t rows, xs, xo, ys, yo;
-  int C, nvec, tpr, log_tpr;
+  int C, tpr, log_tpr;
   float inv_c;
 };
 
-template <int NT>
-__device__ __forceinline__ float row_sum(float s, int tpr, float* part) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int W = tpr < 32 ? tpr : 32;
-  for (int o = W >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (tpr > 32) {
-    if (lane == 0) part[tid >> 5] = s;
-    __syncthreads();
-    const int nw = tpr >> 5, w0 = (tid >> 5) & ~(nw - 1);
-    s = lane < nw ? part[w0 + lane] : 0.f;
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  }
-  return s;
-}
-
 // AHEAD: the next row's vectors are loaded before this one is worked on.
-template <typename T, int V, int NI, int NT, bool AHEAD>
-__global__ void __launch_bounds__(NT)
+template <typename T, int V, int NI, int NT, bool AHEAD, bool RAG>
+__global__ void __launch_bounds__(NT, NT == 256 ? (NI == 1 ? 3 : 2) : 1)
 bwd_kernel(BGeom g, const T* __restrict__ h, const T* __restrict__ gy, const T* __restrict__ gamma,
            const float* __restrict__ rstd, const T* gres, T* gx, float* __restrict__ shares) {
   typedef typename Raw<T, V>::type R;
+  constexpr int P = V / 2;
   __shared__ float part[2][NT / 32];
   extern __shared__ float cols[];  // [C], where a block's rows are joined
   const int tid = threadIdx.x;
   const int in_row = tid & (g.tpr - 1);
-  const int W = g.tpr < 32 ? g.tpr : 32;
+  const int W = NI > 1 || g.tpr >= 32 ? 32 : g.tpr;  // rows of fewer than 32 lanes have one vector a lane
   const int first = (in_row & ~(W - 1)) * NI + (in_row & (W - 1));
   const int rpb = NT >> g.log_tpr, grp = tid >> g.log_tpr;
-  const int64_t step = (int64_t)gridDim.x * rpb;
+  const int64_t step = (int64_t)gridDim.x * rpb;  // RAG: a multiple of 8
+  int64_t row = (int64_t)blockIdx.x * rpb + grp;
+  const int ph = RAG ? phase_of(h + row * g.xs + g.xo) : 0;
+  const int nvec = (g.C + ph + V - 1) / V;
+  const int c0 = first * V - ph;  // first channel of item 0; item i is 32 V further
+  const int64_t xstep = step * g.xs, ystep = step * g.ys;
+  const T* hp = h + row * g.xs + g.xo;
+  const T* yp = gy + row * g.ys + g.yo;
+  const T* rp = gres + (gres ? row * g.xs + g.xo : 0);
+  T* op = gx + (gx ? row * g.xs + g.xo : 0);
   dependents_may_start();
 
-  R gv[NI];
+  f32x2 gm[NI][P], acc[NI][P];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
-    if (gamma && first + i * W < g.nvec) gv[i] = *reinterpret_cast<const R*>(gamma + (int64_t)(first + i * W) * V);
-  float acc[NI][V];
+  for (int i = 0; i < NI; ++i) {
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[i][e] = 0.f;
+    for (int e = 0; e < P; ++e) {
+      gm[i][e] = both(1.f);
+      acc[i][e] = 0ull;
+    }
+    if (gamma && first + i * W < nvec)
+      pairs_of<T, V>(RAG ? load_part<T, V>(gamma, c0 + i * W * V, g.C) : load_vec<T, V, false>(gamma, c0 + i * W * V, g.C), gm[i]);
+  }
 
-  struct Row {
-    R h[NI], gy[NI], gr[NI];
-    float r;
-  };
-  auto fetch = [&](Row& q, int64_t row) {
-    if (row >= g.rows) return;
-    const T* hp = h + row * g.xs + g.xo;
-    const T* yp = gy + row * g.ys + g.yo;
-    const T* rp = gres ? gres + row * g.xs + g.xo : nullptr;
-    q.r = __ldg(rstd + row);
+  R nh[NI], ny[NI], nr[NI];
+  float next_r = 0.f;
+  auto fetch = [&](int64_t at) {  // the row that the pointers are at
+    next_r = 0.f;
+    if (at >= g.rows) return;
+    next_r = __ldg(rstd + at);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int v = first + i * W;
-      if (v >= g.nvec) continue;
-      q.h[i] = *reinterpret_cast<const R*>(hp + (int64_t)v * V);
-      q.gy[i] = *reinterpret_cast<const R*>(yp + (int64_t)v * V);
-      if (rp && gx) q.gr[i] = *reinterpret_cast<const R*>(rp + (int64_t)v * V);
+      if (first + i * W >= nvec) continue;
+      nh[i] = load_vec<T, V, RAG>(hp, c0 + i * W * V, g.C);
+      ny[i] = load_vec<T, V, RAG>(yp, c0 + i * W * V, g.C);
+      if (gres && gx) nr[i] = load_vec<T, V, RAG>(rp, c0 + i * W * V, g.C);
     }
   };
   int flip = 0;
-  Row now, next;
-  const int64_t row0 = (int64_t)blockIdx.x * rpb;
-  if (AHEAD) fetch(now, row0 + grp);
-  for (int64_t base = row0; base < g.rows; base += step, flip ^= 1) {  // the same for all threads of a block
-    const int64_t row = base + grp;
+  if (AHEAD) fetch(row);
+  for (int64_t base = (int64_t)blockIdx.x * rpb; base < g.rows; base += step, row += step, flip ^= 1) {  // the same for all threads of a block
     const bool live = row < g.rows;
-    if (AHEAD) fetch(next, row + step);
-    else fetch(now, row);
-    const float r = live ? now.r : 0.f;
-    float s0 = 0.f, s1 = 0.f;
+    if (!AHEAD) fetch(row);
+    const float r = next_r;
+    R gr[NI];
+    f32x2 s2 = 0ull, xh[NI][P], t[NI][P];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      if (!live || first + i * W >= g.nvec) continue;
-      float a[V], b[V], gm[V];
-      widen<T, V>(now.h[i], a);
-      widen<T, V>(now.gy[i], b);
-      if (gamma) widen<T, V>(gv[i], gm);
+      if (!live || first + i * W >= nvec) continue;
+      pairs_of<T, V>(nh[i], xh[i]);
+      pairs_of<T, V>(ny[i], t[i]);
+      if (gres) gr[i] = nr[i];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        acc[i][e] = fmaf(b[e], __fmul_rn(a[e], r), acc[i][e]);
-        const float t = gamma ? b[e] * gm[e] : b[e];
-        (e & 1 ? s1 : s0) = fmaf(t, a[e], e & 1 ? s1 : s0);
+      for (int e = 0; e < P; ++e) {
+        xh[i][e] = mul_f32x2(xh[i][e], both(r));
+        acc[i][e] = fma2(t[i][e], xh[i][e], acc[i][e]);
+        t[i][e] = mul_f32x2(t[i][e], gm[i][e]);
+        s2 = fma2(t[i][e], xh[i][e], s2);
       }
     }
+    hp += xstep;
+    yp += ystep;
+    rp += xstep;
+    if (AHEAD) fetch(row + step);
     if (gx) {
-      // (t . h) r / C: the mean of t * (h r)
-      const float c1 = __fmul_rn(__fmul_rn(row_sum<NT>(s0 + s1, g.tpr, part[flip]), r), g.inv_c);
-      T* op = gx + row * g.xs + g.xo;
+      // the mean of t * (h r), negated
+      const float c1 = -__fmul_rn(row_sum<NT>(sum2(s2), g.tpr, part[flip]), g.inv_c);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int v = first + i * W;
-        if (!live || v >= g.nvec) continue;
-        float a[V], b[V], gm[V], q[V], o[V];
-        widen<T, V>(now.h[i], a);
-        widen<T, V>(now.gy[i], b);
-        if (gamma) widen<T, V>(gv[i], gm);
-        if (gres) widen<T, V>(now.gr[i], q);
+        if (!live || first + i * W >= nvec) continue;
+        f32x2 q[P];
+        if (gres) pairs_of<T, V>(gr[i], q);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float t = gamma ? b[e] * gm[e] : b[e];
-          o[e] = fmaf(-__fmul_rn(a[e], r), c1, t);
-          o[e] = gres ? fmaf(o[e], r, q[e]) : __fmul_rn(o[e], r);
+        for (int e = 0; e < P; ++e) {
+          const f32x2 d = fma2(xh[i][e], both(c1), t[i][e]);
+          q[e] = gres ? fma2(d, both(r), q[e]) : mul_f32x2(d, both(r));
         }
-        *reinterpret_cast<R*>(op + (int64_t)v * V) = narrow<T, V>(o);
+        store_vec<T, V, RAG>(op, c0 + i * W * V, g.C, vec_of<T, V>(q));
       }
+      op += xstep;
     }
-    if (AHEAD) now = next;
   }
   if (!shares) return;
   // the block's rows in order, then one line of the workspace
+  float* mine = shares + (int64_t)blockIdx.x * g.C;
   for (int k = 0; k < rpb; ++k) {
     if (grp == k) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        if (first + i * W >= g.nvec) continue;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const int c = (first + i * W) * V + e;
-          const float u = k ? cols[c] + acc[i][e] : acc[i][e];
-          if (k == rpb - 1) shares[(int64_t)blockIdx.x * g.C + c] = u;
+          const int c = c0 + i * W * V + e;
+          if (c < 0 || c >= g.C) continue;
+          float lo, hi;
+          unpack_f32x2(acc[i][e / 2], lo, hi);
+          const float u = k ? cols[c] + (e & 1 ? hi : lo) : (e & 1 ? hi : lo);
+          if (k == rpb - 1) mine[c] = u;
           else cols[c] = u;
         }
       }
@@ -236,11 +228,11 @@ __global__ void zero_kernel(int C, T* ggamma) {
 // 16 channels at most per thread (their shares of ggamma are registers), and
 // at most 512 threads to a row.
 constexpr int kHeld = 16;
-Lay lay(const Rms& g, int V) {
+Lay lay(const Rms& g, int V, bool ragged) {
   Lay l{};
   l.v = V;
-  const int64_t nvec = g.C / V;
-  l.ni = V == 1 ? kHeld : nvec > 128 ? kHeld / V : 1;
+  const int64_t nvec = ragged ? (g.C + 2 * V - 2) / V : g.C / V;
+  l.ni = nvec <= 128 ? 1 : nvec <= 1024 ? 2 : kHeld / V;
   const int64_t need = (nvec + l.ni - 1) / l.ni;
   l.tpr = pow2_at_least(need);
   if (l.tpr < 4) l.tpr = 4;
@@ -250,56 +242,64 @@ Lay lay(const Rms& g, int V) {
   return l;
 }
 
-// Blocks that walk over the rows: as many as stay on the GPU at once, more
-// where a thread would add up over 4096 rows.
-constexpr int64_t kBlocks = 152 * 4, kMostRows = 4096;
+// Blocks that walk over the rows: as many as stay on the GPU at once, but four
+// rows each at least where a row is of several warps (the shares are read
+// again), more where a thread would add up over 4096 rows; rows in steps of 8.
+constexpr int64_t kMostRows = 4096;
 int64_t blocks_of(const Rms& g, const Lay& l) {
   const int64_t rpb = l.nt / l.tpr, all = (g.rows + rpb - 1) / rpb;
-  int64_t n = l.nt == 512 ? kBlocks / 2 : kBlocks;
+  int64_t n = 152 * (l.nt == 512 ? 1 : l.ni == 1 ? 3 : 2);
+  if (l.tpr > 32 && n > (all + 3) / 4) n = (all + 3) / 4;
   if ((all + n - 1) / n > kMostRows) n = (all + kMostRows - 1) / kMostRows;
-  return all < n ? all : n;
+  if (all < n) n = all;
+  while (n * rpb % 8) ++n;
+  return n;
 }
 int64_t chunks_of(const Rms& g) {
   const int64_t n = (g.rows + 63) / 64;
   return n < 1 ? 1 : n < 256 ? n : g.rows / kMostRows > 256 ? (g.rows / kMostRows < 65535 ? g.rows / kMostRows : 65535) : 256;
 }
 
-int64_t shares_of(const Rms& g, int V) {
-  const Lay l = lay(g, V);
-  return l.segs == 1 ? blocks_of(g, l) : chunks_of(g);
-}
-
-template <typename T, int V, int NI>
+template <typename T, int V, int NI, bool RAG>
 cudaError_t launch(const BGeom& f, const Lay& l, int64_t blocks, const T* h, const T* gy, const T* gamma,
                    const float* rstd, const T* gres, T* gx, float* ws, cudaStream_t s) {
   const size_t smem = ws && l.nt > l.tpr ? (size_t)f.C * 4 : 0;
-  if (l.nt == 256) bwd_kernel<T, V, NI, 256, true><<<(unsigned)blocks, 256, smem, s>>>(f, h, gy, gamma, rstd, gres, gx, ws);
-  else bwd_kernel<T, V, NI, 512, false><<<(unsigned)blocks, 512, smem, s>>>(f, h, gy, gamma, rstd, gres, gx, ws);
+  if constexpr (NI <= 2) {
+    if (l.nt == 256) {
+      bwd_kernel<T, V, NI, 256, true, RAG><<<(unsigned)blocks, 256, smem, s>>>(f, h, gy, gamma, rstd, gres, gx, ws);
+      return cudaGetLastError();
+    }
+  }
+  bwd_kernel<T, V, NI, 512, false, RAG><<<(unsigned)blocks, 512, smem, s>>>(f, h, gy, gamma, rstd, gres, gx, ws);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t run(const Rms& g, const T* h, const T* gy, const T* gamma, const float* rstd, const T* gres, T* gx,
                 T* ggamma, float* ws, cudaStream_t s) {
-  constexpr int VEC = Vec<T>::n;
+  constexpr int V = Vec<T>::n;
   cudaError_t e = cudaSuccess;
   if (g.rows == 0) {
     if (ggamma) zero_kernel<T><<<(g.C + 255) / 256, 256, 0, s>>>(g.C, ggamma);
     return cudaGetLastError();
   }
   if (!ggamma) ws = nullptr;
-  const int V = vec_ok(g, VEC, on16(h) && on16(gy) && on16(gamma) && on16(gres) && on16(gx), nullptr) ? VEC : 1;
-  const Lay l = lay(g, V);
+  const bool vec = rows_on16(g, V) && on16(h) && on16(gy) && on16(gamma) && on16(gres) && on16(gx);
+  const Lay l = lay(g, V, !vec);
   BGeom f{};
   f.rows = g.rows;
   f.xs = g.xs; f.xo = g.xo; f.ys = g.ys; f.yo = g.yo;
   f.C = g.C;
-  f.nvec = g.C / V;
   f.tpr = l.tpr;
   while ((1 << f.log_tpr) < l.tpr) ++f.log_tpr;
   f.inv_c = 1.f / (float)g.C;
   int64_t n;
-  if (l.segs > 1) {
+  if (l.segs == 1 && (vec || (alike(h, gy) && alike(h, gres) && alike(h, gx) && rows_alike(g, V)))) {
+    n = blocks_of(g, l);
+    const auto go = vec ? (l.ni == 1 ? launch<T, V, 1, false> : l.ni == 2 ? launch<T, V, 2, false> : launch<T, V, kHeld / V, false>)
+                        : (l.ni == 1 ? launch<T, V, 1, true> : l.ni == 2 ? launch<T, V, 2, true> : launch<T, V, kHeld / V, true>);
+    e = go(f, l, n, h, gy, gamma, rstd, gres, gx, ws, s);
+  } else {
     n = chunks_of(g);
     if (gx) {
       bwd_wide_kernel<T><<<(unsigned)(g.rows < 152 * 8 ? g.rows : 152 * 8), kWideNT, 0, s>>>(f, h, gy, gamma, rstd, gres, gx);
@@ -307,11 +307,6 @@ cudaError_t run(const Rms& g, const T* h, const T* gy, const T* gamma, const flo
     }
     if (ws) columns_kernel<T><<<dim3((g.C + 255) / 256, (unsigned)n), 256, 0, s>>>(f, (int)n, h, gy, rstd, ws);
     e = cudaGetLastError();
-  } else {
-    n = blocks_of(g, l);
-    if (V == 1) e = launch<T, 1, kHeld>(f, l, n, h, gy, gamma, rstd, gres, gx, ws, s);
-    else if (l.ni == 1) e = launch<T, VEC, 1>(f, l, n, h, gy, gamma, rstd, gres, gx, ws, s);
-    else e = launch<T, VEC, kHeld / VEC>(f, l, n, h, gy, gamma, rstd, gres, gx, ws, s);
   }
   if (e != cudaSuccess || !ws) return e;
   return launch_dependent(join_kernel<T>, dim3((g.C + kJoinCols - 1) / kJoinCols), dim3(kJoinCols * kJoinLanes), 0, s, g.C,
@@ -322,16 +317,16 @@ cudaError_t run(const Rms& g, const T* h, const T* gy, const T* gamma, const flo
 
 const char* plan_name(const Rms& g, int pass) {
   if (pass == 0) return fwd_in_row(g) ? "row" : "wide";
-  const int VEC = g.dtype == DWCONV_F32 ? 4 : 8;
-  return lay(g, vec_ok(g, VEC, true, nullptr) ? VEC : 1).segs == 1 ? "row" : "wide";
+  const int V = g.dtype == DWCONV_F32 ? 4 : 8;
+  return lay(g, V, !rows_on16(g, V)).segs == 1 && rows_alike(g, V) ? "row" : "wide";
 }
 
 size_t bwd_workspace_bytes(const Rms& g) {
-  const int VEC = g.dtype == DWCONV_F32 ? 4 : 8;
-  int64_t n = shares_of(g, 1);  // pointers off 16 bytes take elements one by one
-  if (g.C % VEC == 0) {
-    const int64_t m = shares_of(g, VEC);
-    if (m > n) n = m;
+  const int V = g.dtype == DWCONV_F32 ? 4 : 8;
+  int64_t n = chunks_of(g);  // pointers decide which kernel runs
+  for (int ragged = 0; ragged < 2; ++ragged) {
+    const Lay l = lay(g, V, ragged != 0);
+    if (l.segs == 1 && n < blocks_of(g, l)) n = blocks_of(g, l);
   }
   return (size_t)(n < 1 ? 1 : n) * g.C * sizeof(float);
 }

@@ -209,7 +209,10 @@ def test_rms_norm_bwd(dtype, gres):
         assert torch.equal(only, gx)
         again = filled(C, dtype=dtype)
         B.dwconv_rms_norm_bwd(d, h, gy, gm, rstd, gr, None, again, ws)
-        assert torch.equal(again, gg)
+        if i % 5 == 4:  # h off 16 bytes and gx on them: which kernel runs depends on gx
+            R.within(again, wg, sg, dtype, f"ggamma alone {rows}x{C}")
+        else:
+            assert torch.equal(again, gg)
         if gres:
             B.dwconv_rms_norm_bwd(d, h, gy, gm, rstd, gr, gr, None, None)  # over gres
             assert torch.equal(gr, gx)
