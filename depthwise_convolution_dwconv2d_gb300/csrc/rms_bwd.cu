@@ -30,72 +30,124 @@ struct BGeom {
   float inv_c;
 };
 
-// AHEAD: the next row's vectors are loaded before this one is worked on.
-template <typename T, int V, int NI, int NT, bool AHEAD, bool RAG>
-__global__ void __launch_bounds__(NT, NT == 256 ? (NI == 1 ? 3 : 2) : 1)
+// Rows on 16 bytes are fetched by asynchronous copies, S rows ahead, into the
+// thread's own slots of shared memory (no thread reads another's, so a thread
+// waits for its own copies only); others one row ahead, into registers.
+constexpr int stages_of(int ni, bool rag) { return rag ? 0 : ni == 1 ? 4 : 2; }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ uint4 read16(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+  return u;
+}
+
+// GRES: gres and gx are given.
+template <typename T, int V, int NI, int NT, bool RAG, bool GRES>
+__global__ void __launch_bounds__(NT, NT == 256 ? (RAG ? (NI == 1 ? 3 : 2) : (NI == 1 ? 4 : 2)) : 1)
 bwd_kernel(BGeom g, const T* __restrict__ h, const T* __restrict__ gy, const T* __restrict__ gamma,
            const float* __restrict__ rstd, const T* gres, T* gx, float* __restrict__ shares) {
   typedef typename Raw<T, V>::type R;
   constexpr int P = V / 2;
+  constexpr int S = stages_of(NI, RAG);
+  constexpr uint32_t kLine = NT * 16, kStage = 3 * NI * kLine;  // bytes of a vector of every thread, of a stage
   __shared__ float part[2][NT / 32];
-  extern __shared__ float cols[];  // [C], where a block's rows are joined
+  extern __shared__ __align__(16) unsigned char dyn[];
+  const uint32_t slots = (uint32_t)__cvta_generic_to_shared(dyn) + threadIdx.x * 16;
+  float* const cols = reinterpret_cast<float*>(dyn + (size_t)S * kStage);  // [C], where a block's rows are joined
   const int tid = threadIdx.x;
   const int in_row = tid & (g.tpr - 1);
-  const int W = NI > 1 || g.tpr >= 32 ? 32 : g.tpr;  // rows of fewer than 32 lanes have one vector a lane
+  const int W = g.tpr < 32 ? g.tpr : 32;
   const int first = (in_row & ~(W - 1)) * NI + (in_row & (W - 1));
   const int rpb = NT >> g.log_tpr, grp = tid >> g.log_tpr;
   const int64_t step = (int64_t)gridDim.x * rpb;  // RAG: a multiple of 8
-  int64_t row = (int64_t)blockIdx.x * rpb + grp;
+  const int64_t row = (int64_t)blockIdx.x * rpb + grp;
   const int ph = RAG ? phase_of(h + row * g.xs + g.xo) : 0;
   const int nvec = (g.C + ph + V - 1) / V;
-  const int c0 = first * V - ph;  // first channel of item 0; item i is 32 V further
+  const int c0 = first * V - ph, cstep = W * V;  // first channel of item 0, distance of the items
   const int64_t xstep = step * g.xs, ystep = step * g.ys;
   const T* hp = h + row * g.xs + g.xo;
   const T* yp = gy + row * g.ys + g.yo;
-  const T* rp = gres + (gres ? row * g.xs + g.xo : 0);
+  const T* rp = GRES ? gres + row * g.xs + g.xo : nullptr;
   T* op = gx + (gx ? row * g.xs + g.xo : 0);
+  const float* sp = rstd + row;
+  // rows of this thread, and of the block's first, which all of its threads walk over
+  const int mine = row < g.rows ? (int)((g.rows - row + step - 1) / step) : 0;
+  const int64_t left = g.rows - (int64_t)blockIdx.x * rpb;
+  const int all = left > 0 ? (int)((left + step - 1) / step) : 0;
   dependents_may_start();
 
+  bool on[NI];
   f32x2 gm[NI][P], acc[NI][P];
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
+    on[i] = first + i * W < nvec;
 #pragma unroll
     for (int e = 0; e < P; ++e) {
       gm[i][e] = both(1.f);
       acc[i][e] = 0ull;
     }
-    if (gamma && first + i * W < nvec)
-      pairs_of<T, V>(RAG ? load_part<T, V>(gamma, c0 + i * W * V, g.C) : load_vec<T, V, false>(gamma, c0 + i * W * V, g.C), gm[i]);
+    if (gamma && on[i])
+      pairs_of<T, V>(RAG ? load_part<T, V>(gamma, c0 + i * cstep, g.C) : load_vec<T, V, false>(gamma, c0 + i * cstep, g.C), gm[i]);
   }
 
-  R nh[NI], ny[NI], nr[NI];
-  float next_r = 0.f;
-  auto fetch = [&](int64_t at) {  // the row that the pointers are at
-    next_r = 0.f;
-    if (at >= g.rows) return;
-    next_r = __ldg(rstd + at);
+  R nh[NI], ny[NI], nr[NI];  // RAG: the row ahead
+  auto fetch = [&](int it, uint32_t to) {  // the row that the pointers are at
+    if (it < mine) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (first + i * W >= nvec) continue;
-      nh[i] = load_vec<T, V, RAG>(hp, c0 + i * W * V, g.C);
-      ny[i] = load_vec<T, V, RAG>(yp, c0 + i * W * V, g.C);
-      if (gres && gx) nr[i] = load_vec<T, V, RAG>(rp, c0 + i * W * V, g.C);
+      for (int i = 0; i < NI; ++i) {
+        if (!on[i]) continue;
+        const int c = c0 + i * cstep;
+        if constexpr (RAG) {
+          nh[i] = load_vec<T, V, true>(hp, c, g.C);
+          ny[i] = load_vec<T, V, true>(yp, c, g.C);
+          if (GRES) nr[i] = load_vec<T, V, true>(rp, c, g.C);
+        } else {
+          copy16(to + i * kLine, hp + c);
+          copy16(to + (NI + i) * kLine, yp + c);
+          if (GRES) copy16(to + (2 * NI + i) * kLine, rp + c);
+        }
+      }
     }
+    if constexpr (!RAG) asm volatile("cp.async.commit_group;" ::: "memory");
+    hp += xstep;
+    yp += ystep;
+    if (GRES) rp += xstep;
   };
-  int flip = 0;
-  if (AHEAD) fetch(row);
-  for (int64_t base = (int64_t)blockIdx.x * rpb; base < g.rows; base += step, row += step, flip ^= 1) {  // the same for all threads of a block
-    const bool live = row < g.rows;
-    if (!AHEAD) fetch(row);
-    const float r = next_r;
+  uint32_t from = slots, to = slots;
+  float next_r = mine > 0 ? __ldg(sp) : 0.f;
+#pragma unroll
+  for (int k = 0; k < (RAG ? 1 : S - 1); ++k) {
+    fetch(k, to);
+    to += kStage;
+  }
+  for (int it = 0; it < all; ++it) {
+    const bool live = it < mine;
+    const float r = live ? next_r : 0.f;
+    sp += step;
+    if (it + 1 < mine) next_r = __ldg(sp);
     R gr[NI];
+    if constexpr (!RAG) {
+      fetch(it + S - 1, to);
+      to = to == slots + (S - 1) * kStage ? slots : to + kStage;
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        nh[i] = read16(from + i * kLine);
+        ny[i] = read16(from + (NI + i) * kLine);
+        if (GRES) nr[i] = read16(from + (2 * NI + i) * kLine);
+      }
+      from = from == slots + (S - 1) * kStage ? slots : from + kStage;
+    }
     f32x2 s2 = 0ull, xh[NI][P], t[NI][P];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      if (!live || first + i * W >= nvec) continue;
+      if (!live || !on[i]) continue;
       pairs_of<T, V>(nh[i], xh[i]);
       pairs_of<T, V>(ny[i], t[i]);
-      if (gres) gr[i] = nr[i];
+      if (GRES) gr[i] = nr[i];
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         xh[i][e] = mul_f32x2(xh[i][e], both(r));
@@ -104,43 +156,40 @@ bwd_kernel(BGeom g, const T* __restrict__ h, const T* __restrict__ gy, const T* 
         s2 = fma2(t[i][e], xh[i][e], s2);
       }
     }
-    hp += xstep;
-    yp += ystep;
-    rp += xstep;
-    if (AHEAD) fetch(row + step);
-    if (gx) {
+    if constexpr (RAG) fetch(it + 1, 0);
+    if (GRES || gx) {
       // the mean of t * (h r), negated
-      const float c1 = -__fmul_rn(row_sum<NT>(sum2(s2), g.tpr, part[flip]), g.inv_c);
+      const float c1 = -__fmul_rn(row_sum<NT>(sum2(s2), g.tpr, part[it & 1]), g.inv_c);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        if (!live || first + i * W >= nvec) continue;
+        if (!live || !on[i]) continue;
         f32x2 q[P];
-        if (gres) pairs_of<T, V>(gr[i], q);
+        if (GRES) pairs_of<T, V>(gr[i], q);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
           const f32x2 d = fma2(xh[i][e], both(c1), t[i][e]);
-          q[e] = gres ? fma2(d, both(r), q[e]) : mul_f32x2(d, both(r));
+          q[e] = GRES ? fma2(d, both(r), q[e]) : mul_f32x2(d, both(r));
         }
-        store_vec<T, V, RAG>(op, c0 + i * W * V, g.C, vec_of<T, V>(q));
+        store_vec<T, V, RAG>(op, c0 + i * cstep, g.C, vec_of<T, V>(q));
       }
       op += xstep;
     }
   }
   if (!shares) return;
   // the block's rows in order, then one line of the workspace
-  float* mine = shares + (int64_t)blockIdx.x * g.C;
+  float* line = shares + (int64_t)blockIdx.x * g.C;
   for (int k = 0; k < rpb; ++k) {
     if (grp == k) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const int c = c0 + i * W * V + e;
+          const int c = c0 + i * cstep + e;
           if (c < 0 || c >= g.C) continue;
           float lo, hi;
           unpack_f32x2(acc[i][e / 2], lo, hi);
           const float u = k ? cols[c] + (e & 1 ? hi : lo) : (e & 1 ? hi : lo);
-          if (k == rpb - 1) mine[c] = u;
+          if (k == rpb - 1) line[c] = u;
           else cols[c] = u;
         }
       }
@@ -246,9 +295,9 @@ Lay lay(const Rms& g, int V, bool ragged) {
 // rows each at least where a row is of several warps (the shares are read
 // again), more where a thread would add up over 4096 rows; rows in steps of 8.
 constexpr int64_t kMostRows = 4096;
-int64_t blocks_of(const Rms& g, const Lay& l) {
+int64_t blocks_of(const Rms& g, const Lay& l, bool ragged) {
   const int64_t rpb = l.nt / l.tpr, all = (g.rows + rpb - 1) / rpb;
-  int64_t n = 152 * (l.nt == 512 ? 1 : l.ni == 1 ? 3 : 2);
+  int64_t n = 152 * (l.nt == 512 ? 1 : l.ni > 1 ? 2 : ragged ? 3 : 4);
   if (l.tpr > 32 && n > (all + 3) / 4) n = (all + 3) / 4;
   if ((all + n - 1) / n > kMostRows) n = (all + kMostRows - 1) / kMostRows;
   if (all < n) n = all;
@@ -260,18 +309,29 @@ int64_t chunks_of(const Rms& g) {
   return n < 1 ? 1 : n < 256 ? n : g.rows / kMostRows > 256 ? (g.rows / kMostRows < 65535 ? g.rows / kMostRows : 65535) : 256;
 }
 
+template <typename T, int V, int NI, int NT, bool RAG>
+cudaError_t launch_nt(const BGeom& f, int64_t blocks, const T* h, const T* gy, const T* gamma, const float* rstd,
+                      const T* gres, T* gx, float* ws, cudaStream_t s) {
+  // the slots, and a row of sums where a block has several rows
+  const size_t smem = (size_t)stages_of(NI, RAG) * 3 * NI * NT * 16 + (ws && NT > f.tpr ? (size_t)f.C * 4 : 0);
+  auto kern = gres && gx ? bwd_kernel<T, V, NI, NT, RAG, true> : bwd_kernel<T, V, NI, NT, RAG, false>;
+  if (smem > 46 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<(unsigned)blocks, NT, smem, s>>>(f, h, gy, gamma, rstd, gres, gx, ws);
+  return cudaGetLastError();
+}
 template <typename T, int V, int NI, bool RAG>
 cudaError_t launch(const BGeom& f, const Lay& l, int64_t blocks, const T* h, const T* gy, const T* gamma,
                    const float* rstd, const T* gres, T* gx, float* ws, cudaStream_t s) {
-  const size_t smem = ws && l.nt > l.tpr ? (size_t)f.C * 4 : 0;
-  if constexpr (NI <= 2) {
-    if (l.nt == 256) {
-      bwd_kernel<T, V, NI, 256, true, RAG><<<(unsigned)blocks, 256, smem, s>>>(f, h, gy, gamma, rstd, gres, gx, ws);
-      return cudaGetLastError();
-    }
+  if constexpr (NI == 1) {
+    return launch_nt<T, V, NI, 256, RAG>(f, blocks, h, gy, gamma, rstd, gres, gx, ws, s);
+  } else {
+    if constexpr (NI == 2)
+      if (l.nt == 256) return launch_nt<T, V, NI, 256, RAG>(f, blocks, h, gy, gamma, rstd, gres, gx, ws, s);
+    return launch_nt<T, V, NI, 512, RAG>(f, blocks, h, gy, gamma, rstd, gres, gx, ws, s);
   }
-  bwd_kernel<T, V, NI, 512, false, RAG><<<(unsigned)blocks, 512, smem, s>>>(f, h, gy, gamma, rstd, gres, gx, ws);
-  return cudaGetLastError();
 }
 
 template <typename T>
@@ -295,7 +355,7 @@ cudaError_t run(const Rms& g, const T* h, const T* gy, const T* gamma, const flo
   f.inv_c = 1.f / (float)g.C;
   int64_t n;
   if (l.segs == 1 && (vec || (alike(h, gy) && alike(h, gres) && alike(h, gx) && rows_alike(g, V)))) {
-    n = blocks_of(g, l);
+    n = blocks_of(g, l, !vec);
     const auto go = vec ? (l.ni == 1 ? launch<T, V, 1, false> : l.ni == 2 ? launch<T, V, 2, false> : launch<T, V, kHeld / V, false>)
                         : (l.ni == 1 ? launch<T, V, 1, true> : l.ni == 2 ? launch<T, V, 2, true> : launch<T, V, kHeld / V, true>);
     e = go(f, l, n, h, gy, gamma, rstd, gres, gx, ws, s);
@@ -326,7 +386,7 @@ size_t bwd_workspace_bytes(const Rms& g) {
   int64_t n = chunks_of(g);  // pointers decide which kernel runs
   for (int ragged = 0; ragged < 2; ++ragged) {
     const Lay l = lay(g, V, ragged != 0);
-    if (l.segs == 1 && n < blocks_of(g, l)) n = blocks_of(g, l);
+    if (l.segs == 1 && n < blocks_of(g, l, ragged != 0)) n = blocks_of(g, l, ragged != 0);
   }
   return (size_t)(n < 1 ? 1 : n) * g.C * sizeof(float);
 }
