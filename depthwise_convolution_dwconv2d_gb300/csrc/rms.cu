@@ -59,7 +59,9 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
   constexpr int P = V / 2;
   constexpr bool kCopy = RAG && Q != kSrcFull;
   __shared__ float part[2][kNT / 32];
+  constexpr int kCopyC = NI * 32 * V;
   __shared__ __align__(16) R copy[kCopy ? kNT / 32 : 1][kCopy ? NI * 32 + 1 : 1];
+  __shared__ __align__(16) float gs[kCopy ? kCopyC + 4 : 1];  // gamma
   const int tid = threadIdx.x;
   const int in_row = tid & (g.tpr - 1);
   const int W = NI > 1 || g.tpr >= 32 ? 32 : g.tpr;  // rows of fewer than 32 lanes have one vector a lane
@@ -84,16 +86,23 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
       pairs_of<T, V>(RAG ? load_part<T, V>(gamma, c0 + i * W * V, g.C) : load_vec<T, V, false>(gamma, c0 + i * W * V, g.C), gm[i]);
   }
   R nx[NI], nr[NI];
-  auto fetch = [&](bool live) {
+  auto fetch = [&](int64_t at) {  // the row that the pointers are at
+    const bool inner = inner_row(at, g.rows);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      if (!live || first + i * W >= nvec) continue;
-      nx[i] = load_vec<T, V, RAG>(xp, c0 + i * W * V, g.C);
-      if (res) nr[i] = load_vec<T, V, RAG>(rp, c0 + i * W * V, g.C);
+      if (at >= g.rows || first + i * W >= nvec) continue;
+      nx[i] = load_vec<T, V, RAG>(xp, c0 + i * W * V, g.C, inner);
+      if (res) nr[i] = load_vec<T, V, RAG>(rp, c0 + i * W * V, g.C, inner);
     }
   };
+  if constexpr (kCopy) {
+    for (int c = tid; c < kCopyC + 4; c += kNT) gs[c] = c < g.C && gamma ? ld(gamma + c) : 1.f;
+    R zero{};
+    if ((tid & 31) == 0) copy[tid >> 5][nvec] = zero;  // what lies behind a row's last vector
+    __syncthreads();
+  }
   int flip = 0;
-  fetch(row < g.rows);
+  fetch(row);
   for (int64_t base = (int64_t)blockIdx.x * rpb; base < g.rows; base += step, row += step, flip ^= 1) {
     const bool live = row < g.rows;
     R hv[NI];
@@ -118,7 +127,7 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
     xp += xstep;
     rp += xstep;
     // the next row is read before this one's h is written: x or the residual may be h's memory, row by row
-    fetch(row + step < g.rows);
+    fetch(row + step);
     if (h) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
@@ -166,26 +175,51 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
       yp += ystep;
     }
     if constexpr (kCopy) {  // a warp per row, four channels a lane
-      const T* hs = reinterpret_cast<const T*>(copy[tid >> 5]) + ph;
-      const int block = 1 << t.shift;
+      const char* hs = reinterpret_cast<const char*>(copy[tid >> 5]);
+      const int block = 1 << t.shift, shift = 16 * (ph & 3);
       uint8_t* q = t.codes + row * g.C;
+      const int off = (int)(reinterpret_cast<uintptr_t>(q) & 3);
       for (int c = 4 * (tid & 31); c < g.C + 4 * (tid & 31); c += 128) {
-        float f[4];
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t m = 0;
+        if (live && c < g.C) {
+          if constexpr (V == 8) {  // two aligned reads of 8 bytes, moved together
+            const uint64_t* p = reinterpret_cast<const uint64_t*>(hs + ((ph + c) & ~3) * 2);
+            uint64_t u = p[0];
+            if (shift) u = u >> shift | p[1] << (64 - shift);
+            const uint2 w = make_uint2((uint32_t)u, (uint32_t)(u >> 32));
+            const uint4 v = make_uint4(w.x, w.y, 0, 0);
+            float o[8];
+            unpack16<T>(v, o);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[e] = live && c + e < g.C ? __fmul_rn(to_f<T>(hs[c + e]), r) : 0.f;
-          if (gamma && live && c + e < g.C) f[e] = __fmul_rn(f[e], ld(gamma + c + e));
-          m = max(m, abs_bits(f[e]));
+            for (int e = 0; e < 4; ++e) f[e] = o[e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const float*>(hs + (ph + c + e) * 4);
+          }
+          const float4 gq = *reinterpret_cast<const float4*>(gs + c);
+          const float gv[4] = {gq.x, gq.y, gq.z, gq.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[e] = __fmul_rn(__fmul_rn(f[e], r), gv[e]);
+            m = max(m, abs_bits(f[e]));
+          }
         }
         for (int o = block >> 3; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (live && c < g.C) {
           float inv;
           const float s = scale_of<Q>(m, &inv);
           const uint32_t k = encode4<Q>(f[0], f[1], f[2], f[3], inv);
+          if (off == 0 && c + 4 <= g.C) {
+            *reinterpret_cast<uint32_t*>(q + c) = k;
+          } else if (off == 2 && c + 4 <= g.C) {
+            *reinterpret_cast<uint16_t*>(q + c) = (uint16_t)k;
+            *reinterpret_cast<uint16_t*>(q + c + 2) = (uint16_t)(k >> 16);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e < g.C) q[c + e] = (uint8_t)(k >> (8 * e));
+            for (int e = 0; e < 4; ++e)
+              if (c + e < g.C) q[c + e] = (uint8_t)(k >> (8 * e));
+          }
           if ((c & (block - 1)) == 0) t.scales[row * t.nblk + (c >> t.shift)] = s;
         }
       }

@@ -30,10 +30,16 @@ __device__ __forceinline__ typename Raw<T, V>::type narrow(const float* f) {
 // ---- rows that begin anywhere ---------------------------------------------------
 // A row whose first channel lies `ph` elements behind a 16-byte boundary is
 // read in the vectors that lie on 16 bytes: vector v holds the channels cb =
-// v * V - ph and on. The first and last ones reach over the row's ends; their
-// elements outside it are neither read nor written, and count as zeros. Rows a
-// multiple of 8 apart begin alike, so a thread that steps over rows that far
-// keeps its channels.
+// v * V - ph and on. The first and last ones reach over the row's ends: their
+// elements outside it belong to rows before and after it (or to what lies
+// between two rows), are read with the vector while that lies within the
+// tensor, count as zeros and are not written. Rows a multiple of 8 apart begin
+// alike, so a thread that steps over rows that far keeps its channels.
+
+// Rows whose vectors lie within the tensor: no vector reaches over 8 elements.
+__device__ __forceinline__ bool inner_row(int64_t row, int64_t rows) { return row >= 8 && row < rows - 8; }
+
+// element by element
 template <typename T, int V>
 __device__ __forceinline__ typename Raw<T, V>::type load_part(const T* row, int cb, int C) {
   alignas(16) T v[V];
@@ -41,19 +47,63 @@ __device__ __forceinline__ typename Raw<T, V>::type load_part(const T* row, int 
   for (int e = 0; e < V; ++e) v[e] = cb + e >= 0 && cb + e < C ? row[cb + e] : from_f<T>(0.f);
   return *reinterpret_cast<const typename Raw<T, V>::type*>(v);
 }
-template <typename T, int V>
-__device__ __forceinline__ void store_part(T* row, int cb, int C, const typename Raw<T, V>::type& u) {
-  alignas(16) T v[V];
-  *reinterpret_cast<typename Raw<T, V>::type*>(v) = u;
-#pragma unroll
-  for (int e = 0; e < V; ++e)
-    if (cb + e >= 0 && cb + e < C) row[cb + e] = v[e];
-}
 // RAG: rows that begin anywhere; otherwise cb >= 0 and cb + V <= C
 template <typename T, int V, bool RAG>
-__device__ __forceinline__ typename Raw<T, V>::type load_vec(const T* row, int cb, int C) {
-  if (RAG && (cb < 0 || cb + V > C)) return load_part<T, V>(row, cb, C);
-  return *reinterpret_cast<const typename Raw<T, V>::type*>(row + cb);
+__device__ __forceinline__ typename Raw<T, V>::type load_vec(const T* row, int cb, int C, bool inner = true) {
+  typedef typename Raw<T, V>::type R;
+  if constexpr (!RAG) return *reinterpret_cast<const R*>(row + cb);
+  const bool edge = cb < 0 || cb + V > C;
+  if (edge && !inner) return load_part<T, V>(row, cb, C);
+  R u = *reinterpret_cast<const R*>(row + cb);
+  if (edge) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (V == 4) {
+        if (cb + j < 0 || cb + j >= C) w[j] = 0;
+      } else {
+        if (cb + 2 * j < 0 || cb + 2 * j >= C) w[j] &= 0xffff0000u;
+        if (cb + 2 * j + 1 < 0 || cb + 2 * j + 1 >= C) w[j] &= 0xffffu;
+      }
+    }
+  }
+  return u;
+}
+// The elements of a vector over one of the row's ends, in pieces of 8, 4 and 2
+// bytes; over both, element by element.
+template <typename T, int V>
+__device__ __forceinline__ void store_part(T* row, int cb, int C, const typename Raw<T, V>::type& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  char* at = reinterpret_cast<char*>(row + cb);
+  if (cb < 0 && cb + V > C) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (cb + e < 0 || cb + e >= C) continue;
+      if constexpr (V == 4) *reinterpret_cast<uint32_t*>(at + 4 * e) = w[e];
+      else *reinterpret_cast<uint16_t*>(at + 2 * e) = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+    }
+    return;
+  }
+  constexpr int es = sizeof(T);
+  if (cb < 0) {  // the last m elements
+    const int m = V + cb;
+    if (m & (8 / es)) *reinterpret_cast<uint2*>(at + 8) = make_uint2(w[2], w[3]);
+    const uint32_t x = m & (8 / es) ? w[1] : w[3];
+    if (m & (4 / es)) *reinterpret_cast<uint32_t*>(at + 16 - (m & (12 / es)) * es) = x;
+    if constexpr (es == 2) {
+      const uint32_t z = m & 2 ? (m & 4 ? w[0] : w[2]) : x;
+      if (m & 1) *reinterpret_cast<uint16_t*>(at + 16 - m * 2) = (uint16_t)(z >> 16);
+    }
+  } else {  // the first m
+    const int m = C - cb;
+    if (m & (8 / es)) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+    const uint32_t x = m & (8 / es) ? w[2] : w[0];
+    if (m & (4 / es)) *reinterpret_cast<uint32_t*>(at + (m & (8 / es)) * es) = x;
+    if constexpr (es == 2) {
+      const uint32_t z = m & 2 ? (m & 4 ? w[3] : w[1]) : x;
+      if (m & 1) *reinterpret_cast<uint16_t*>(at + (m & 6) * 2) = (uint16_t)z;
+    }
+  }
 }
 template <typename T, int V, bool RAG>
 __device__ __forceinline__ void store_vec(T* row, int cb, int C, const typename Raw<T, V>::type& u) {

@@ -56,7 +56,6 @@ bwd_kernel(BGeom g, const T* __restrict__ h, const T* __restrict__ gy, const T* 
   __shared__ float part[2][NT / 32];
   extern __shared__ __align__(16) unsigned char dyn[];
   const uint32_t slots = (uint32_t)__cvta_generic_to_shared(dyn) + threadIdx.x * 16;
-  float* const cols = reinterpret_cast<float*>(dyn + (size_t)S * kStage);  // [C], where a block's rows are joined
   const int tid = threadIdx.x;
   const int in_row = tid & (g.tpr - 1);
   const int W = g.tpr < 32 ? g.tpr : 32;
@@ -101,9 +100,10 @@ bwd_kernel(BGeom g, const T* __restrict__ h, const T* __restrict__ gy, const T* 
         if (!on[i]) continue;
         const int c = c0 + i * cstep;
         if constexpr (RAG) {
-          nh[i] = load_vec<T, V, true>(hp, c, g.C);
-          ny[i] = load_vec<T, V, true>(yp, c, g.C);
-          if (GRES) nr[i] = load_vec<T, V, true>(rp, c, g.C);
+          const bool inner = inner_row(row + it * step, g.rows);
+          nh[i] = load_vec<T, V, true>(hp, c, g.C, inner);
+          ny[i] = load_vec<T, V, true>(yp, c, g.C, inner);
+          if (GRES) nr[i] = load_vec<T, V, true>(rp, c, g.C, inner);
         } else {
           copy16(to + i * kLine, hp + c);
           copy16(to + (NI + i) * kLine, yp + c);
@@ -176,25 +176,28 @@ bwd_kernel(BGeom g, const T* __restrict__ h, const T* __restrict__ gy, const T* 
     }
   }
   if (!shares) return;
-  // the block's rows in order, then one line of the workspace
+  // the block's rows in order, one line of shared memory each, then one line of the workspace
+  __syncthreads();  // the lines take the slots' place
+  float* lines = reinterpret_cast<float*>(dyn);  // [rpb][C]
   float* line = shares + (int64_t)blockIdx.x * g.C;
-  for (int k = 0; k < rpb; ++k) {
-    if (grp == k) {
+  float* to_line = rpb > 1 ? lines + grp * g.C : line;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
+  for (int i = 0; i < NI; ++i) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int c = c0 + i * cstep + e;
-          if (c < 0 || c >= g.C) continue;
-          float lo, hi;
-          unpack_f32x2(acc[i][e / 2], lo, hi);
-          const float u = k ? cols[c] + (e & 1 ? hi : lo) : (e & 1 ? hi : lo);
-          if (k == rpb - 1) line[c] = u;
-          else cols[c] = u;
-        }
-      }
+    for (int e = 0; e < V; ++e) {
+      const int c = c0 + i * cstep + e;
+      float lo, hi;
+      unpack_f32x2(acc[i][e / 2], lo, hi);
+      if (c >= 0 && c < g.C) to_line[c] = e & 1 ? hi : lo;
     }
-    if (k + 1 < rpb) __syncthreads();
+  }
+  if (rpb == 1) return;
+  __syncthreads();
+  for (int c = tid; c < g.C; c += NT) {
+    float u = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < rpb; ++k) u += lines[k * g.C + c];
+    line[c] = u;
   }
 }
 
@@ -244,14 +247,14 @@ columns_kernel(BGeom g, int chunks, const T* __restrict__ h, const T* __restrict
   shares[(int64_t)blockIdx.y * g.C + c] = acc;
 }
 
-// ggamma[c] = the shares' sum, in a fixed order: 8 columns and 64 row lanes a
-// block, each lane every 64th share, then the lanes in a tree.
-constexpr int kJoinCols = 8, kJoinLanes = 64;
+// ggamma[c] = the shares' sum, in a fixed order: 8 columns and 128 row lanes a
+// block, each lane every 128th share; then four lanes of a warp, then the warps.
+constexpr int kJoinCols = 8, kJoinLanes = 128;
 template <typename T>
 __global__ void __launch_bounds__(kJoinCols * kJoinLanes)
 join_kernel(int C, int n, const float* __restrict__ shares, T* __restrict__ ggamma) {
-  __shared__ float sm[kJoinLanes][kJoinCols + 1];
-  const int k = threadIdx.x % kJoinCols, l = threadIdx.x / kJoinCols;
+  __shared__ float sm[kJoinLanes / 4][kJoinCols + 1];
+  const int k = threadIdx.x % kJoinCols, l = threadIdx.x / kJoinCols, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * kJoinCols + k;
   wait_for_previous();
   float a = 0.f;
@@ -259,13 +262,15 @@ join_kernel(int C, int n, const float* __restrict__ shares, T* __restrict__ ggam
 #pragma unroll 8
     for (int b = l; b < n; b += kJoinLanes) a += shares[(int64_t)b * C + c];
   }
-  sm[l][k] = a;
+  a += __shfl_xor_sync(0xffffffffu, a, 8);
+  a += __shfl_xor_sync(0xffffffffu, a, 16);
+  if (lane < kJoinCols) sm[warp][lane] = a;
   __syncthreads();
-  for (int o = kJoinLanes / 2; o > 0; o >>= 1) {
-    if (l < o) sm[l][k] += sm[l + o][k];
-    __syncthreads();
-  }
-  if (l == 0 && c < C) ggamma[c] = from_f<T>(sm[0][k]);
+  if (warp >= kJoinCols) return;
+  a = sm[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if (lane == 0 && blockIdx.x * kJoinCols + warp < C) ggamma[blockIdx.x * kJoinCols + warp] = from_f<T>(a);
 }
 
 template <typename T>
@@ -312,8 +317,9 @@ int64_t chunks_of(const Rms& g) {
 template <typename T, int V, int NI, int NT, bool RAG>
 cudaError_t launch_nt(const BGeom& f, int64_t blocks, const T* h, const T* gy, const T* gamma, const float* rstd,
                       const T* gres, T* gx, float* ws, cudaStream_t s) {
-  // the slots, and a row of sums where a block has several rows
-  const size_t smem = (size_t)stages_of(NI, RAG) * 3 * NI * NT * 16 + (ws && NT > f.tpr ? (size_t)f.C * 4 : 0);
+  // the slots, then in their place a line of sums for each of the block's rows
+  const size_t slots = (size_t)stages_of(NI, RAG) * 3 * NI * NT * 16, lines = ws && NT > f.tpr ? (size_t)(NT / f.tpr) * f.C * 4 : 0;
+  const size_t smem = slots > lines ? slots : lines;
   auto kern = gres && gx ? bwd_kernel<T, V, NI, NT, RAG, true> : bwd_kernel<T, V, NI, NT, RAG, false>;
   if (smem > 46 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
