@@ -47,6 +47,20 @@ __device__ __forceinline__ typename Raw<T, V>::type load_part(const T* row, int 
   for (int e = 0; e < V; ++e) v[e] = cb + e >= 0 && cb + e < C ? row[cb + e] : from_f<T>(0.f);
   return *reinterpret_cast<const typename Raw<T, V>::type*>(v);
 }
+// zeros in place of the elements outside the row
+template <typename T, int V>
+__device__ __forceinline__ void clear_part(typename Raw<T, V>::type& u, int cb, int C) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (V == 4) {
+      if (cb + j < 0 || cb + j >= C) w[j] = 0;
+    } else {
+      if (cb + 2 * j < 0 || cb + 2 * j >= C) w[j] &= 0xffff0000u;
+      if (cb + 2 * j + 1 < 0 || cb + 2 * j + 1 >= C) w[j] &= 0xffffu;
+    }
+  }
+}
 // RAG: rows that begin anywhere; otherwise cb >= 0 and cb + V <= C
 template <typename T, int V, bool RAG>
 __device__ __forceinline__ typename Raw<T, V>::type load_vec(const T* row, int cb, int C, bool inner = true) {
@@ -55,18 +69,7 @@ __device__ __forceinline__ typename Raw<T, V>::type load_vec(const T* row, int c
   const bool edge = cb < 0 || cb + V > C;
   if (edge && !inner) return load_part<T, V>(row, cb, C);
   R u = *reinterpret_cast<const R*>(row + cb);
-  if (edge) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (V == 4) {
-        if (cb + j < 0 || cb + j >= C) w[j] = 0;
-      } else {
-        if (cb + 2 * j < 0 || cb + 2 * j >= C) w[j] &= 0xffff0000u;
-        if (cb + 2 * j + 1 < 0 || cb + 2 * j + 1 >= C) w[j] &= 0xffffu;
-      }
-    }
-  }
+  if (edge) clear_part<T, V>(u, cb, C);
   return u;
 }
 // The elements of a vector over one of the row's ends, in pieces of 8, 4 and 2
