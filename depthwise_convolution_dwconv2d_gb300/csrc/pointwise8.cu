@@ -60,18 +60,48 @@ encode_weights_kernel(int64_t cout, int64_t cin, int64_t pitch, bool transpose, 
 
 // ---- aligned copy of codes -----------------------------------------------------
 
-// Rows of cin bytes to rows of pitch bytes, zeros behind them; 16 bytes a thread.
+// Rows of cin bytes to rows of pitch bytes, zeros behind them; 16 bytes a
+// thread, put together from the aligned words that hold them. Words that reach
+// over an end of the tensor are read byte by byte.
 __global__ void __launch_bounds__(256)
-align_codes_kernel(int64_t rows, int cin, int64_t pitch, const uint8_t* __restrict__ x, uint8_t* __restrict__ out) {
-  const int64_t vecs = pitch / 16, total = rows * vecs;
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / vecs;
-    const int c = (int)(i - r * vecs) * 16;
+align_codes_kernel(int64_t rows, int cin, int64_t pitch, FastDiv d_vecs, const uint8_t* __restrict__ x, uint8_t* __restrict__ out) {
+  const uint64_t total = (uint64_t)rows * (uint64_t)(pitch / 16);
+  const uint8_t* const end = x + rows * cin;
+  for (uint64_t i = blockIdx.x * (uint64_t)256 + threadIdx.x; i < total; i += (uint64_t)gridDim.x * 256) {
+    int64_t r;
+    int c;
+    if (total < (uint64_t(1) << 32)) {
+      uint32_t q;
+      c = (int)d_vecs.divmod((uint32_t)i, q) * 16;
+      r = q;
+    } else {
+      r = (int64_t)(i / (uint64_t)d_vecs.d);
+      c = (int)(i - (uint64_t)r * d_vecs.d) * 16;
+    }
     const uint8_t* p = x + r * cin + c;
-    uint32_t v[4] = {0, 0, 0, 0};
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 3);
+    const uint8_t* w0 = p - off;
+    uint32_t v[4];
+    if (c < cin && w0 >= x && w0 + 20 <= end) {
+      uint32_t w[5];
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (c + k < cin) v[k >> 2] |= (uint32_t)__ldg(p + k) << (8 * (k & 3));
+      for (int k = 0; k < 5; ++k) w[k] = __ldg(reinterpret_cast<const uint32_t*>(w0) + k);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = __funnelshift_r(w[k], w[k + 1], 8 * off);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int left = cin - c - 4 * k;  // bytes of this word within the row
+        v[k] = left >= 4 ? v[k] : left <= 0 ? 0 : v[k] & (0xffffffffu >> (32 - 8 * left));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + 4 * k + e < cin) v[k] |= (uint32_t)__ldg(p + 4 * k + e) << (8 * e);
+      }
+    }
     *reinterpret_cast<uint4*>(out + r * pitch + c) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
@@ -145,7 +175,7 @@ cudaError_t run(const Pw& g, const uint8_t* x, const float* sx, const uint8_t* w
   const bool w16 = reinterpret_cast<uintptr_t>(w) % 16 == 0;
   if (w16 && g.cin % 16 != 0) {
     const int64_t total = g.rows * (g.pitch / 16), blocks = (total + 255) / 256;
-    align_codes_kernel<<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), 256, 0, s>>>(g.rows, g.cin, g.pitch, x, (uint8_t*)ws);
+    align_codes_kernel<<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), 256, 0, s>>>(g.rows, g.cin, g.pitch, FastDiv((uint32_t)(g.pitch / 16)), x, (uint8_t*)ws);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = run_tc(g, g.pitch, (const uint8_t*)ws, sx, w, sw, bias, y, s);
   } else if (w16 && reinterpret_cast<uintptr_t>(x) % 16 == 0) {

@@ -7,13 +7,15 @@
 // accumulators take turns, so that a block's MMAs run while the one before is
 // read back.
 //
-// Tile kernel (many pixels): a tile is 128 pixels (M) x 128 or 256 outputs
-// (N). Roles: a producer lane (tensor-map copies), an MMA warp, and a
-// warpgroup per 128 outputs that reads back and adds: a thread has one pixel
-// and 128 outputs, hence one scale of x and one of w per block. Persistent.
+// Tile kernels (many pixels): 128 pixels (M) x 128 outputs (N) by a thread
+// block, or 256 x 256 by a pair of them. Roles: two producer lanes (tensor-map
+// copies; one lane's follow one another, 491 cycles for 128 rows of 128 bytes,
+// so one of them would hold 32 KB a stage to 983), an MMA warp, and warps that
+// read back and add: a thread has one pixel and 64 or 128 outputs, hence one
+// scale of x and one of w per block. Persistent.
 //
 // Row kernel (few pixels, where the weights are all there is to read): the
-// roles of the operands are swapped, 128 outputs (M) x 16 to 128 pixels (N),
+// roles of the operands are swapped, 128 outputs (M) x 16 to 64 pixels (N),
 // and a cluster of up to 8 thread blocks shares the channels' blocks of a
 // tile, so that all SMs read weights. Their sums are joined through the
 // cluster's shared memory in a fixed order.
@@ -92,6 +94,39 @@ struct Ring {
     if (++s == stages) { s = 0; ph ^= 1; wrapped = true; }
   }
 };
+
+// Every copy that a producer issued lands before the block leaves (those of a
+// stage that both have issued to).
+template <int STAGES>
+__device__ __forceinline__ void drain(uint64_t* full, uint32_t issued) {
+  const uint32_t first = issued > (uint32_t)STAGES ? issued - STAGES : 0;
+  for (uint32_t k = first; k < issued; ++k) tc::wait(&full[k % STAGES], (k / STAGES) & 1, nullptr, nullptr);
+}
+
+// One of two MMA warps: the blocks of channels which, which + 2, ... of `total`
+// of this thread block's. A warp by itself takes 900 cycles from one to the
+// next (two barriers of 200 each, issue and commits 350), longer than the MMAs.
+// issue(accumulator, stage) runs in one lane and commits.
+template <int STAGES, int ACC, typename Issue>
+__device__ __forceinline__ void mma_loop(int which, uint32_t total, uint64_t* full, uint64_t* accfree, unsigned int* timeouts,
+                                         volatile int* abortp, Issue issue) {
+  Ring r;
+  if (which) r.next(STAGES);
+  for (uint32_t it = which; it < total; it += 2) {
+    const int ab = it % ACC;
+    const bool ok = tc::wait(&full[r.s], r.ph, timeouts, abortp) &&
+                    (it < ACC || tc::wait(&accfree[ab], (it / ACC - 1) & 1, timeouts, abortp));
+    if (__all_sync(0xffffffffu, ok)) {
+      tc::fence_after();
+      if (tc::elect_one()) issue(ab, r.s);
+      __syncwarp();
+    } else {
+      *abortp = 1;
+    }
+    r.next(STAGES);
+    r.next(STAGES);
+  }
+}
 
 __device__ __forceinline__ unsigned char* align1024(unsigned char* p) { return p + ((1024 - (tma::smem_u32(p) & 1023)) & 1023); }
 
@@ -292,7 +327,7 @@ struct Tile {
   static constexpr int kN = 128, kNC = 64;        // outputs of a tile, of a warp that reads back
   static constexpr int kAcc = 4;                   // accumulators (a power of two)
   static constexpr int kEpi = 4 * kN / kNC;       // warps that read back
-  static constexpr int kThreads = 32 * kEpi + 64;  // and a producer and an MMA warp
+  static constexpr int kThreads = 32 * kEpi + 128;  // and two producers and two MMA warps
   static constexpr int kStages = 6;
   static constexpr int kA = kM * kBlock, kB = kN * kBlock, kStage = kA + kB;
   static constexpr int kCols = kAcc * kN;
@@ -311,7 +346,7 @@ tile_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
   __shared__ int abort_s;
   unsigned char* sm = align1024(smdyn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kProducer = K::kEpi, kMma = kProducer + 1;
+  constexpr int kProducer = K::kEpi, kMma = kProducer + 2;
   if (tid == 0) {
     for (int s = 0; s < K::kStages; ++s) {
       tma::mbar_init(&full[s], 1);
@@ -321,7 +356,7 @@ tile_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
       tma::mbar_init(&accfull[s], 1);
       tma::mbar_init(&accfree[s], K::kEpi);
     }
-    tma::mbar_init(&done, 1);
+    tma::mbar_init(&done, 2);  // both MMA warps
     tma::fence_init();
     abort_s = 0;
   }
@@ -333,8 +368,9 @@ tile_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
   volatile int* abortp = &abort_s;
   const int nkb = g.p.nkb;
 
-  if (warp == kProducer) {
+  if (warp == kProducer || warp == kProducer + 1) {
     if (lane == 0) {
+      const bool first_one = warp == kProducer;  // x's copies, and the bytes of both; the other one w's
       Ring r;
       uint32_t issued = 0;
       for (int t = blockIdx.x; t < g.tiles && !*abortp; t += gridDim.x) {
@@ -343,37 +379,27 @@ tile_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
         for (int kb = 0; kb < nkb && !*abortp; ++kb, r.next(K::kStages)) {
           if (r.wrapped && !tc::wait(&empty[r.s], r.ph ^ 1, timeouts, abortp)) { *abortp = 1; break; }
           unsigned char* st = sm + (size_t)r.s * K::kStage;
-          tma::mbar_expect_tx(&full[r.s], K::kStage);
-          tma::load_3d(st, &xmap, kb * kBlock, (int)mt * kM, 0, &full[r.s]);
-          tma::load_3d(st + K::kA, &wmap, kb * kBlock, nt * K::kN, 0, &full[r.s]);
+          if (first_one) {
+            tma::mbar_expect_tx(&full[r.s], K::kStage);
+            tma::load_3d(st, &xmap, kb * kBlock, (int)mt * kM, 0, &full[r.s]);
+          } else {
+            tma::load_3d(st + K::kA, &wmap, kb * kBlock, nt * K::kN, 0, &full[r.s]);
+          }
           ++issued;
         }
       }
-      // every issued copy lands before the block leaves
-      const uint32_t first = issued > (uint32_t)K::kStages ? issued - K::kStages : 0;
-      for (uint32_t k = first; k < issued; ++k) tc::wait(&full[k % K::kStages], (k / K::kStages) & 1, nullptr, nullptr);
+      drain<K::kStages>(full, issued);
     }
     __syncwarp();
-  } else if (warp == kMma) {
+  } else if (warp >= kMma) {
     constexpr uint32_t idesc = idesc_e4m3(kM, K::kN);
-    Ring r;
-    uint32_t it = 0;
-    for (int t = blockIdx.x; t < g.tiles; t += gridDim.x) {
-      for (int kb = 0; kb < nkb; ++kb, ++it, r.next(K::kStages)) {
-        const int ab = it % K::kAcc;
-        const bool ok = tc::wait(&full[r.s], r.ph, timeouts, abortp) &&
-                        (it < K::kAcc || tc::wait(&accfree[ab], (it / K::kAcc - 1) & 1, timeouts, abortp));
-        if (!__all_sync(0xffffffffu, ok)) { *abortp = 1; continue; }
-        tc::fence_after();
-        const unsigned char* st = sm + (size_t)r.s * K::kStage;
-        if (tc::elect_one()) {
-          mma_block<1>(tmem + ab * K::kN, st, st + K::kA, idesc);
-          tc::commit(&empty[r.s]);
-          tc::commit(&accfull[ab]);
-        }
-        __syncwarp();
-      }
-    }
+    const uint32_t mine = (int)blockIdx.x < g.tiles ? (g.tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    mma_loop<K::kStages, K::kAcc>(warp - kMma, mine * nkb, full, accfree, timeouts, abortp, [&](int ab, int stage) {
+      const unsigned char* st = sm + (size_t)stage * K::kStage;
+      mma_block<1>(tmem + ab * K::kN, st, st + K::kA, idesc);
+      tc::commit(&empty[stage]);
+      tc::commit(&accfull[ab]);
+    });
     if (tc::elect_one()) tc::commit(&done);
     __syncwarp();
     tc::wait(&done, 0, nullptr, nullptr);
@@ -408,7 +434,7 @@ struct Pair {
   static constexpr int kN = 256, kNC = 128;
   static constexpr int kAcc = 2;
   static constexpr int kEpi = 4 * kN / kNC;        // warps that read back
-  static constexpr int kThreads = 32 * kEpi + 128;  // and a warpgroup with a producer and an MMA warp
+  static constexpr int kThreads = 32 * kEpi + 128;  // and a warpgroup of two producers and two MMA warps
   static constexpr int kStages = 6;
   static constexpr int kA = kM * kBlock, kB = kN / 2 * kBlock, kStage = kA + kB;
   static constexpr int kCols = kAcc * kN;
@@ -450,7 +476,7 @@ pair_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
   __shared__ int abort_s;
   unsigned char* sm = align1024(smdyn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kProducer = K::kEpi, kMma = kProducer + 1;
+  constexpr int kProducer = K::kEpi, kMma = kProducer + 2;
   const int rank = blockIdx.x & 1;  // in the pair; block 0 issues the MMAs and has the barriers they wait for
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (tid == 0) {
@@ -462,7 +488,7 @@ pair_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
       tma::mbar_init(&accfull[s], 1);
       tma::mbar_init(&accfree[s], 2 * K::kEpi);  // the warps of both blocks that read back
     }
-    tma::mbar_init(&done, 1);
+    tma::mbar_init(&done, 2);  // both MMA warps
     tma::fence_init();
     abort_s = 0;
   }
@@ -482,8 +508,9 @@ pair_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
   if (warp >= K::kEpi) {
     // of the 168 registers a thread that the block was launched with: 128 x 56 + 256 x 224 = 384 x 168
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
-    if (warp == kProducer) {
+    if (warp == kProducer || warp == kProducer + 1) {
       if (lane == 0) {
+        const bool first_one = warp == kProducer;  // x's copies, and block 0's the bytes of all; the other one w's
         Ring r;
         uint32_t issued = 0;
         for (int t = pair; t < g.tiles && !*abortp; t += pairs) {
@@ -492,38 +519,27 @@ pair_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
           for (int kb = 0; kb < nkb && !*abortp; ++kb, r.next(K::kStages)) {
             if (r.wrapped && !tc::wait(&empty[r.s], r.ph ^ 1, timeouts, abortp)) { *abortp = 1; break; }
             unsigned char* st = sm + (size_t)r.s * K::kStage;
-            if (rank == 0) tma::mbar_expect_tx(&full[r.s], 2 * K::kStage);
-            load_pair(st, &xmap, kb * kBlock, ((int)mt * 2 + rank) * kM, &full[r.s]);
-            load_pair(st + K::kA, &wmap, kb * kBlock, nt * K::kN + rank * (K::kN / 2), &full[r.s]);
+            if (first_one) {
+              if (rank == 0) tma::mbar_expect_tx(&full[r.s], 2 * K::kStage);
+              load_pair(st, &xmap, kb * kBlock, ((int)mt * 2 + rank) * kM, &full[r.s]);
+            } else {
+              load_pair(st + K::kA, &wmap, kb * kBlock, nt * K::kN + rank * (K::kN / 2), &full[r.s]);
+            }
             ++issued;
           }
         }
-        // every issued copy lands before the pair leaves
-        const uint32_t first = issued > (uint32_t)K::kStages ? issued - K::kStages : 0;
-        if (rank == 0)
-          for (uint32_t k = first; k < issued; ++k) tc::wait(&full[k % K::kStages], (k / K::kStages) & 1, nullptr, nullptr);
+        if (rank == 0) drain<K::kStages>(full, issued);
       }
       __syncwarp();
-    } else if (warp == kMma && rank == 0) {
+    } else if (warp >= kMma && rank == 0) {
       constexpr uint32_t idesc = idesc_e4m3(2 * kM, K::kN);
-      Ring r;
-      uint32_t it = 0;
-      for (int t = pair; t < g.tiles; t += pairs) {
-        for (int kb = 0; kb < nkb; ++kb, ++it, r.next(K::kStages)) {
-          const int ab = it % K::kAcc;
-          const bool ok = tc::wait(&full[r.s], r.ph, timeouts, abortp) &&
-                          (it < K::kAcc || tc::wait(&accfree[ab], (it / K::kAcc - 1) & 1, timeouts, abortp));
-          if (!__all_sync(0xffffffffu, ok)) { *abortp = 1; continue; }
-          tc::fence_after();
-          const unsigned char* st = sm + (size_t)r.s * K::kStage;
-          if (tc::elect_one()) {
-            mma_block<2>(tmem + ab * K::kN, st, st + K::kA, idesc);
-            commit_pair(&empty[r.s]);
-            commit_pair(&accfull[ab]);
-          }
-          __syncwarp();
-        }
-      }
+      const uint32_t mine = pair < g.tiles ? (g.tiles - 1 - pair) / pairs + 1 : 0;
+      mma_loop<K::kStages, K::kAcc>(warp - kMma, mine * nkb, full, accfree, timeouts, abortp, [&](int ab, int stage) {
+        const unsigned char* st = sm + (size_t)stage * K::kStage;
+        mma_block<2>(tmem + ab * K::kN, st, st + K::kA, idesc);
+        commit_pair(&empty[stage]);
+        commit_pair(&accfull[ab]);
+      });
       if (tc::elect_one()) commit_pair(&done);
       __syncwarp();
       tc::wait(&done, 0, nullptr, nullptr);
@@ -558,9 +574,9 @@ pair_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
 
 template <int NP>
 struct Row {
-  static constexpr int kThreads = 128 + 64;
+  static constexpr int kThreads = 128 + 128;  // a warpgroup that reads back, two producers and two MMA warps
   static constexpr int kA = 128 * kBlock, kB = NP * kBlock, kStage = kA + kB;
-  static constexpr int kStages = NP <= 32 ? 5 : NP == 64 ? 4 : 3;  // two blocks fit an SM
+  static constexpr int kStages = NP <= 32 ? 5 : 4;  // two blocks fit an SM
   static constexpr int kCols = 2 * NP < 32 ? 32 : 2 * NP;
   static constexpr int kTab = 32 * 1024;  // the block's scales, at most
   static constexpr size_t kJoin = (size_t)NP * 128 * 4;
@@ -585,7 +601,7 @@ row_kernel(RGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_const
   unsigned char* sm = align1024(smdyn);
   float* tab = reinterpret_cast<float*>(sm + (size_t)K::kStages * K::kStage);  // [block of channels][pixel]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kProducer = 4, kMma = 5;
+  constexpr int kProducer = 4, kMma = 6;
   const int rank = blockIdx.x % g.split, o0 = blockIdx.x / g.split * 128;
   const int64_t p0 = (int64_t)blockIdx.y * NP;
   const int nkb = g.p.nkb;
@@ -599,7 +615,7 @@ row_kernel(RGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_const
       tma::mbar_init(&accfull[s], 1);
       tma::mbar_init(&accfree[s], 4);
     }
-    tma::mbar_init(&done, 1);
+    tma::mbar_init(&done, 2);  // both MMA warps
     tma::fence_init();
     abort_s = 0;
   }
@@ -611,39 +627,33 @@ row_kernel(RGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_const
   volatile int* abortp = &abort_s;
   f32x2 acc[NP / 2];
 
-  if (warp == kProducer) {
+  if (warp == kProducer || warp == kProducer + 1) {
     if (lane == 0) {
+      const bool first_one = warp == kProducer;  // w's copies, and the bytes of both; the other one x's
       Ring r;
       uint32_t issued = 0;
       for (int kb = kb0; kb < kb1 && !*abortp; ++kb, r.next(K::kStages)) {
         if (r.wrapped && !tc::wait(&empty[r.s], r.ph ^ 1, timeouts, abortp)) { *abortp = 1; break; }
         unsigned char* st = sm + (size_t)r.s * K::kStage;
-        tma::mbar_expect_tx(&full[r.s], K::kStage);
-        tma::load_3d(st, &wmap, kb * kBlock, o0, 0, &full[r.s]);
-        tma::load_3d(st + K::kA, &xmap, kb * kBlock, (int)p0, 0, &full[r.s]);
+        if (first_one) {
+          tma::mbar_expect_tx(&full[r.s], K::kStage);
+          tma::load_3d(st, &wmap, kb * kBlock, o0, 0, &full[r.s]);
+        } else {
+          tma::load_3d(st + K::kA, &xmap, kb * kBlock, (int)p0, 0, &full[r.s]);
+        }
         ++issued;
       }
-      const uint32_t first = issued > (uint32_t)K::kStages ? issued - K::kStages : 0;
-      for (uint32_t k = first; k < issued; ++k) tc::wait(&full[k % K::kStages], (k / K::kStages) & 1, nullptr, nullptr);
+      drain<K::kStages>(full, issued);
     }
     __syncwarp();
-  } else if (warp == kMma) {
+  } else if (warp >= kMma) {
     constexpr uint32_t idesc = idesc_e4m3(128, NP);
-    Ring r;
-    for (int it = 0; it < kb1 - kb0; ++it, r.next(K::kStages)) {
-      const int ab = it & 1;
-      const bool ok = tc::wait(&full[r.s], r.ph, timeouts, abortp) &&
-                      (it < 2 || tc::wait(&accfree[ab], ((it >> 1) - 1) & 1, timeouts, abortp));
-      if (!__all_sync(0xffffffffu, ok)) { *abortp = 1; continue; }
-      tc::fence_after();
-      const unsigned char* st = sm + (size_t)r.s * K::kStage;
-      if (tc::elect_one()) {
-        mma_block<1>(tmem + ab * NP, st, st + K::kA, idesc);
-        tc::commit(&empty[r.s]);
-        tc::commit(&accfull[ab]);
-      }
-      __syncwarp();
-    }
+    mma_loop<K::kStages, 2>(warp - kMma, kb1 - kb0, full, accfree, timeouts, abortp, [&](int ab, int stage) {
+      const unsigned char* st = sm + (size_t)stage * K::kStage;
+      mma_block<1>(tmem + ab * NP, st, st + K::kA, idesc);
+      tc::commit(&empty[stage]);
+      tc::commit(&accfull[ab]);
+    });
     if (tc::elect_one()) tc::commit(&done);
     __syncwarp();
     tc::wait(&done, 0, nullptr, nullptr);
@@ -844,7 +854,7 @@ cudaError_t launch_row(const Pw& g, int64_t ldx, const uint8_t* x, const float* 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-int row_pixels(const Pw& g) { return g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : 128; }
+int row_pixels(const Pw& g) { return g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : 64; }
 
 template <typename T>
 cudaError_t run_t(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
@@ -853,8 +863,7 @@ cudaError_t run_t(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, c
     switch (row_pixels(g)) {
       case 16: return launch_row<T, 16>(g, ldx, x, sx, w, sw, bias, y, s);
       case 32: return launch_row<T, 32>(g, ldx, x, sx, w, sw, bias, y, s);
-      case 64: return launch_row<T, 64>(g, ldx, x, sx, w, sw, bias, y, s);
-      default: return launch_row<T, 128>(g, ldx, x, sx, w, sw, bias, y, s);
+      default: return launch_row<T, 64>(g, ldx, x, sx, w, sw, bias, y, s);
     }
   }
   static std::atomic<uint64_t> ready_tile{0}, ready_pair{0};
@@ -863,8 +872,8 @@ cudaError_t run_t(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, c
   // Rounds of tiles times what a tile takes in cycles, as traced: a block of
   // channels 600 and the rest 1500 by one thread block, 1130 and 1800 by a pair
   // (four times the products). 12544 pixels, 512 -> 512 channels 12.3 against
-  // 13.5 us, 3136, 1024 -> 1024 12.2 against 10.5, 200704, 128 -> 128 22.5
-  // against 25.4, 2048, 2048 -> 2048 19.5 against 15.3.
+  // 13.8 us, 3136, 1024 -> 1024 11.8 against 10.6, 200704, 128 -> 128 22.2
+  // against 25.6, 2048, 2048 -> 2048 18.6 against 15.5.
   const int64_t by_tile = (tiles + 151) / 152 * (g.nkb * 600 + 1500), by_pair = (pairs + 75) / 76 * (g.nkb * 1130 + 1800);
   if (by_pair < by_tile) return launch_tiles<Pair, T>(pair_kernel<T>, true, ready_pair, g, ldx, x, sx, w, sw, bias, y, s);
   return launch_tiles<Tile, T>(tile_kernel<T>, false, ready_tile, g, ldx, x, sx, w, sw, bias, y, s);
@@ -872,14 +881,14 @@ cudaError_t run_t(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, c
 
 }  // namespace
 
-// The row kernel up to 32 pixels, and while tiles leave half of the SMs idle
-// and a tile's sum is long enough to be shared: 128 pixels, 4096 -> 4096
-// channels 12.8 us against 18.2 in tiles, 300, 4096 -> 512 9.4 against 17.5;
-// but 300, 1024 -> 1024 9.1 against 7.4.
+// The row kernel up to 32 pixels, and while clusters of two and more find room
+// and there is a long enough sum to share: 128 pixels, 4096 -> 4096 channels
+// 11.6 us against 16.3 in tiles, 300, 4096 -> 512 8.6 against 16.2, 77, 1536 ->
+// 1984 7.4 against 8.6; but 196, 512 -> 512 7.9 against 5.8.
 Plan plan(const Pw& g) {
   const int np = row_pixels(g), split = split_of(g, np);
   if ((int64_t)((g.nkb + split - 1) / split) * np * 4 > 32 * 1024) return Plan::Tile;  // its table of scales
-  return g.rows <= 32 || (g.nkb >= 16 && tiles_of(g, kM, Tile::kN) <= 76) ? Plan::Row : Plan::Tile;
+  return g.rows <= 32 || (g.nkb >= 10 && tiles_of(g, np, 128) <= 96) ? Plan::Row : Plan::Tile;
 }
 
 cudaError_t run_tc(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,

@@ -127,7 +127,7 @@ def test_pointwise8_arguments():
 def test_pointwise8_plans():
     name = B.dwconv2d_pointwise8_plan_name
     assert name(1, 4096, 4096) == name(32, 64, 64) == name(128, 4096, 4096) == "row"
-    assert name(33, 64, 64) == name(12544, 512, 512) == name(4096, 4096, 4096) == "tile"
+    assert name(33, 64, 64) == name(196, 512, 512) == name(12544, 512, 512) == name(4096, 4096, 4096) == "tile"
     assert name(1, 1 << 20, 64) in ("row", "tile")
     assert name(-1, 64, 64) == name(1, 0, 64) == name(1, 64, (1 << 20) + 1) == "invalid"
 
