@@ -6,6 +6,7 @@
 // over blocks b of 128 channels. The sum within a block is one of products of
 // e4m3 values, exact in fp32 but for the additions; each block's sum is
 // multiplied by the product of its two scales and added in fp32.
+#include "dependent.cuh"
 #include "norm.cuh"
 #include "pointwise8.h"
 #include "vec.cuh"
@@ -65,6 +66,7 @@ encode_weights_kernel(int64_t cout, int64_t cin, int64_t pitch, bool transpose, 
 // over an end of the tensor are read byte by byte.
 __global__ void __launch_bounds__(256)
 align_codes_kernel(int64_t rows, int cin, int64_t pitch, FastDiv d_vecs, const uint8_t* __restrict__ x, uint8_t* __restrict__ out) {
+  dependents_may_start();
   const uint64_t total = (uint64_t)rows * (uint64_t)(pitch / 16);
   const uint8_t* const end = x + rows * cin;
   for (uint64_t i = blockIdx.x * (uint64_t)256 + threadIdx.x; i < total; i += (uint64_t)gridDim.x * 256) {
@@ -177,9 +179,9 @@ cudaError_t run(const Pw& g, const uint8_t* x, const float* sx, const uint8_t* w
     const int64_t total = g.rows * (g.pitch / 16), blocks = (total + 255) / 256;
     align_codes_kernel<<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), 256, 0, s>>>(g.rows, g.cin, g.pitch, FastDiv((uint32_t)(g.pitch / 16)), x, (uint8_t*)ws);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = run_tc(g, g.pitch, (const uint8_t*)ws, sx, w, sw, bias, y, s);
+    e = run_tc(g, g.pitch, (const uint8_t*)ws, true, sx, w, sw, bias, y, s);
   } else if (w16 && reinterpret_cast<uintptr_t>(x) % 16 == 0) {
-    e = run_tc(g, g.cin, x, sx, w, sw, bias, y, s);
+    e = run_tc(g, g.cin, x, false, sx, w, sw, bias, y, s);
   }
   if (e != cudaErrorNotSupported) return e;
   DWCONV_DISPATCH_DTYPE(g.dtype, T, e = any<T>(g, x, sx, w, sw, (const T*)bias, (T*)y, s));

@@ -32,10 +32,11 @@ cudaError_t encode_weights(int64_t cout, int64_t cin, bool transpose, int dtype,
 cudaError_t run(const Pw& g, const uint8_t* x, const float* sx, const uint8_t* w, const float* sw, const void* bias,
                 void* y, void* ws, cudaStream_t s);
 
-// pointwise8_tc.cu: x's rows ldx bytes apart, x, w and ldx on 16 bytes;
-// cudaErrorNotSupported where the tensor maps or the device refuse.
-cudaError_t run_tc(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
-                   const void* bias, void* y, cudaStream_t s);
+// pointwise8_tc.cu: x's rows ldx bytes apart, x, w and ldx on 16 bytes; copied:
+// the launch before this one writes x. cudaErrorNotSupported where the tensor
+// maps or the device refuse.
+cudaError_t run_tc(const Pw& g, int64_t ldx, const uint8_t* x, bool copied, const float* sx, const uint8_t* w,
+                   const float* sw, const void* bias, void* y, cudaStream_t s);
 
 }  // namespace pw8
 }  // namespace dwconv

@@ -27,6 +27,7 @@
 
 #include <cooperative_groups.h>
 
+#include "dependent.cuh"
 #include "norm.cuh"
 #include "pointwise8.h"
 #include "tc.cuh"
@@ -371,6 +372,7 @@ tile_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
   if (warp == kProducer || warp == kProducer + 1) {
     if (lane == 0) {
       const bool first_one = warp == kProducer;  // x's copies, and the bytes of both; the other one w's
+      if (first_one) wait_for_previous();  // the aligned copy of x
       Ring r;
       uint32_t issued = 0;
       for (int t = blockIdx.x; t < g.tiles && !*abortp; t += gridDim.x) {
@@ -511,6 +513,7 @@ pair_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
     if (warp == kProducer || warp == kProducer + 1) {
       if (lane == 0) {
         const bool first_one = warp == kProducer;  // x's copies, and block 0's the bytes of all; the other one w's
+        if (first_one) wait_for_previous();  // the aligned copy of x
         Ring r;
         uint32_t issued = 0;
         for (int t = pair; t < g.tiles && !*abortp; t += pairs) {
@@ -630,6 +633,7 @@ row_kernel(RGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_const
   if (warp == kProducer || warp == kProducer + 1) {
     if (lane == 0) {
       const bool first_one = warp == kProducer;  // w's copies, and the bytes of both; the other one x's
+      if (!first_one) wait_for_previous();  // the aligned copy of x
       Ring r;
       uint32_t issued = 0;
       for (int kb = kb0; kb < kb1 && !*abortp; ++kb, r.next(K::kStages)) {
@@ -789,7 +793,7 @@ int64_t tiles_of(const Pw& g, int m, int n) { return ((g.rows + m - 1) / m) * ((
 // KERN: tile_kernel or pair_kernel, of which K is the shape
 template <typename K, typename T, typename KernelT>
 cudaError_t launch_tiles(KernelT kern, bool pair, std::atomic<uint64_t>& ready, const Pw& g, int64_t ldx, const uint8_t* x,
-                         const float* sx, const uint8_t* w, const float* sw, const T* bias, T* y, cudaStream_t s) {
+                         bool copied, const float* sx, const uint8_t* w, const float* sw, const T* bias, T* y, cudaStream_t s) {
   alignas(64) CUtensorMap xmap{}, wmap{};
   if (!encode_bytes(&xmap, x, (uint64_t)(ldx == g.pitch ? g.pitch : g.cin), (uint64_t)g.rows, (uint64_t)ldx, kM) ||
       !encode_bytes(&wmap, w, (uint64_t)g.pitch, (uint64_t)g.cout, (uint64_t)g.pitch, K::kB / kBlock))
@@ -806,6 +810,9 @@ cudaError_t launch_tiles(KernelT kern, bool pair, std::atomic<uint64_t>& ready, 
   t.vec_out = g.ys * es % 32 == 0 && g.yo * es % 32 == 0 && reinterpret_cast<uintptr_t>(y) % 32 == 0;
   const int most = pair ? 76 : 152;
   const int n = t.tiles < most ? t.tiles : most;
+  if (copied)
+    return launch_dependent(kern, dim3(pair ? 2 * n : n), dim3(K::kThreads), K::kSmem, s, t, (const CUtensorMap)xmap,
+                            (const CUtensorMap)wmap, to, sx, sw, bias, y);
   kern<<<pair ? 2 * n : n, K::kThreads, K::kSmem, s>>>(t, xmap, wmap, to, sx, sw, bias, y);
   return cudaGetLastError();
 }
@@ -820,7 +827,7 @@ int split_of(const Pw& g, int np) {
 }
 
 template <typename T, int NP>
-cudaError_t launch_row(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
+cudaError_t launch_row(const Pw& g, int64_t ldx, const uint8_t* x, bool copied, const float* sx, const uint8_t* w, const float* sw,
                        const T* bias, T* y, cudaStream_t s) {
   typedef Row<NP> K;
   alignas(64) CUtensorMap xmap{}, wmap{};
@@ -838,18 +845,20 @@ cudaError_t launch_row(const Pw& g, int64_t ldx, const uint8_t* x, const float* 
   r.p = g;
   r.split = split_of(g, NP);
   const int held = (g.nkb + r.split - 1) / r.split;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)r.split;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)r.split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // dependent.cuh
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((g.cout + 127) / 128 * r.split), (unsigned)((g.rows + NP - 1) / NP));
   cfg.blockDim = dim3(K::kThreads);
   cfg.dynamicSmemBytes = 1024 + (size_t)K::kStages * K::kStage + (size_t)held * NP * 4;
   cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = copied ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, r, (const CUtensorMap)xmap, (const CUtensorMap)wmap, to, sx, sw, bias, y);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -857,13 +866,13 @@ cudaError_t launch_row(const Pw& g, int64_t ldx, const uint8_t* x, const float* 
 int row_pixels(const Pw& g) { return g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : 64; }
 
 template <typename T>
-cudaError_t run_t(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
+cudaError_t run_t(const Pw& g, int64_t ldx, const uint8_t* x, bool copied, const float* sx, const uint8_t* w, const float* sw,
                   const T* bias, T* y, cudaStream_t s) {
   if (plan(g) == Plan::Row) {
     switch (row_pixels(g)) {
-      case 16: return launch_row<T, 16>(g, ldx, x, sx, w, sw, bias, y, s);
-      case 32: return launch_row<T, 32>(g, ldx, x, sx, w, sw, bias, y, s);
-      default: return launch_row<T, 64>(g, ldx, x, sx, w, sw, bias, y, s);
+      case 16: return launch_row<T, 16>(g, ldx, x, copied, sx, w, sw, bias, y, s);
+      case 32: return launch_row<T, 32>(g, ldx, x, copied, sx, w, sw, bias, y, s);
+      default: return launch_row<T, 64>(g, ldx, x, copied, sx, w, sw, bias, y, s);
     }
   }
   static std::atomic<uint64_t> ready_tile{0}, ready_pair{0};
@@ -875,8 +884,8 @@ cudaError_t run_t(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, c
   // 13.8 us, 3136, 1024 -> 1024 11.8 against 10.6, 200704, 128 -> 128 22.2
   // against 25.6, 2048, 2048 -> 2048 18.6 against 15.5.
   const int64_t by_tile = (tiles + 151) / 152 * (g.nkb * 600 + 1500), by_pair = (pairs + 75) / 76 * (g.nkb * 1130 + 1800);
-  if (by_pair < by_tile) return launch_tiles<Pair, T>(pair_kernel<T>, true, ready_pair, g, ldx, x, sx, w, sw, bias, y, s);
-  return launch_tiles<Tile, T>(tile_kernel<T>, false, ready_tile, g, ldx, x, sx, w, sw, bias, y, s);
+  if (by_pair < by_tile) return launch_tiles<Pair, T>(pair_kernel<T>, true, ready_pair, g, ldx, x, copied, sx, w, sw, bias, y, s);
+  return launch_tiles<Tile, T>(tile_kernel<T>, false, ready_tile, g, ldx, x, copied, sx, w, sw, bias, y, s);
 }
 
 }  // namespace
@@ -891,11 +900,11 @@ Plan plan(const Pw& g) {
   return g.rows <= 32 || (g.nkb >= 10 && tiles_of(g, np, 128) <= 96) ? Plan::Row : Plan::Tile;
 }
 
-cudaError_t run_tc(const Pw& g, int64_t ldx, const uint8_t* x, const float* sx, const uint8_t* w, const float* sw,
+cudaError_t run_tc(const Pw& g, int64_t ldx, const uint8_t* x, bool copied, const float* sx, const uint8_t* w, const float* sw,
                    const void* bias, void* y, cudaStream_t s) {
   if (g.rows >= (int64_t(1) << 31) - 256) return cudaErrorNotSupported;  // coordinates of a copy are 32 bits
   cudaError_t e = cudaErrorInvalidValue;
-  DWCONV_DISPATCH_DTYPE(g.dtype, T, e = run_t<T>(g, ldx, x, sx, w, sw, (const T*)bias, (T*)y, s));
+  DWCONV_DISPATCH_DTYPE(g.dtype, T, e = run_t<T>(g, ldx, x, copied, sx, w, sw, (const T*)bias, (T*)y, s));
   return e;
 }
 
