@@ -49,6 +49,7 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t m, f32x2 v) {
 // ---- rows that 256 threads hold ----------------------------------------------------
 
 constexpr int kNT = 256;
+__device__ uint4 kNone[1];  // read in place of what does not exist
 // Blocks step over the rows; the next row's vectors are on their way while one
 // is worked on. RAG: rows begin anywhere, the step is a multiple of 8 of them,
 // and codes are made by one warp per row.
@@ -65,13 +66,14 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
   const int tid = threadIdx.x;
   const int in_row = tid & (g.tpr - 1);
   const int W = NI > 1 || g.tpr >= 32 ? 32 : g.tpr;  // rows of fewer than 32 lanes have one vector a lane
-  const int first = (in_row & ~(W - 1)) * NI + (in_row & (W - 1));
+  const int st = NI > 1 ? g.tpr : 32;  // from item to item, in vectors: all warps have as many; in channels:
+  const int cst = st * V;
   const int rpb = kNT >> g.log_tpr;
   const int64_t step = (int64_t)gridDim.x * rpb;
   int64_t row = (int64_t)blockIdx.x * rpb + (tid >> g.log_tpr);
   const int ph = RAG ? phase_of(x + row * g.xs + g.xo) : 0;
   const int nvec = (g.C + ph + V - 1) / V;
-  const int c0 = first * V - ph;  // first channel of item 0; item i is 32 V further
+  const int c0 = in_row * V - ph;  // first channel of item 0
   const int64_t xstep = step * g.xs, ystep = step * g.ys;
   const T* xp = x + row * g.xs + g.xo;
   const T* rp = res + (res ? row * g.xs + g.xo : 0);
@@ -82,17 +84,22 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
   for (int i = 0; i < NI; ++i) {
 #pragma unroll
     for (int e = 0; e < P; ++e) gm[i][e] = both(1.f);
-    if (gamma && first + i * W < nvec)
-      pairs_of<T, V>(RAG ? load_part<T, V>(gamma, c0 + i * W * V, g.C) : load_vec<T, V, false>(gamma, c0 + i * W * V, g.C), gm[i]);
+    if (gamma && in_row + i * st < nvec)
+      pairs_of<T, V>(load_ends<T, V, RAG>(gamma, c0 + i * cst, g.C), gm[i]);
   }
   R nx[NI], nr[NI];
-  auto fetch = [&](int64_t at) {  // the row that the pointers are at
+  auto over = [&](int i) { return RAG && (c0 + i * cst < 0 || c0 + i * cst + V > g.C); };  // the row's ends
+  // The row that the pointers are at. Nothing here uses what is read, and no
+  // read hangs on a condition (one that does not exist reads zeros instead):
+  // both made the reads wait for one another (3073 x 2130 fp32: 63.6 us, 24.0
+  // without). Vectors over the tensor's ends are read where they are used.
+  auto fetch = [&](int64_t at) {
     const bool inner = inner_row(at, g.rows);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      if (at >= g.rows || first + i * W >= nvec) continue;
-      nx[i] = load_vec<T, V, RAG>(xp, c0 + i * W * V, g.C, inner);
-      if (res) nr[i] = load_vec<T, V, RAG>(rp, c0 + i * W * V, g.C, inner);
+      const bool no = at >= g.rows || in_row + i * st >= nvec || (RAG && !inner && over(i));
+      nx[i] = *(no ? (const R*)kNone : reinterpret_cast<const R*>(xp + c0 + i * cst));
+      if (res) nr[i] = *(no ? (const R*)kNone : reinterpret_cast<const R*>(rp + c0 + i * cst));
     }
   };
   if constexpr (kCopy) {
@@ -109,18 +116,24 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
     f32x2 s2 = 0ull;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      if (!live || first + i * W >= nvec) continue;
+      if (!live || in_row + i * st >= nvec) continue;
       f32x2 a[P];
-      hv[i] = nx[i];
-      pairs_of<T, V>(hv[i], a);
+      const bool apart = over(i) && !inner_row(row, g.rows);
+      if (apart) hv[i] = load_part<T, V>(xp, c0 + i * cst, g.C);
+      else hv[i] = nx[i];
       if (res) {
+        R rv;
+        if (apart) rv = load_part<T, V>(rp, c0 + i * cst, g.C);
+        else rv = nr[i];
         f32x2 b[P];
-        pairs_of<T, V>(nr[i], b);
+        pairs_of<T, V>(hv[i], a);
+        pairs_of<T, V>(rv, b);
 #pragma unroll
         for (int e = 0; e < P; ++e) a[e] = add_f32x2(a[e], b[e]);
         hv[i] = vec_of<T, V>(a);
-        pairs_of<T, V>(hv[i], a);
       }
+      if (over(i)) clear_part<T, V>(hv[i], c0 + i * cst, g.C);
+      pairs_of<T, V>(hv[i], a);
 #pragma unroll
       for (int e = 0; e < P; ++e) s2 = fma2(a[e], a[e], s2);
     }
@@ -131,7 +144,7 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
     if (h) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        if (live && first + i * W < nvec) store_vec<T, V, RAG>(hp, c0 + i * W * V, g.C, hv[i]);
+        if (live && in_row + i * st < nvec) store_vec<T, V, RAG>(hp, c0 + i * cst, g.C, hv[i]);
       hp += xstep;
     }
     const float ss = row_sum<kNT>(sum2(s2), g.tpr, part[flip]);
@@ -141,13 +154,13 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
       R* mine = copy[tid >> 5];
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        if (live && first + i * 32 < nvec) mine[first + i * 32] = hv[i];
+        if (live && in_row + i * st < nvec) mine[in_row + i * st] = hv[i];
       __syncwarp();
     }
     if (!kCopy || y) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const bool on = live && first + i * W < nvec;
+        const bool on = live && in_row + i * st < nvec;
         f32x2 f[P];
 #pragma unroll
         for (int e = 0; e < P; ++e) f[e] = 0ull;
@@ -155,7 +168,7 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
           pairs_of<T, V>(hv[i], f);
 #pragma unroll
           for (int e = 0; e < P; ++e) f[e] = mul_f32x2(mul_f32x2(f[e], both(r)), gm[i][e]);
-          if (y) store_vec<T, V, RAG>(yp, c0 + i * W * V, g.C, vec_of<T, V>(f));
+          if (y) store_vec<T, V, RAG>(yp, c0 + i * cst, g.C, vec_of<T, V>(f));
         }
         if constexpr (Q != kSrcFull && !RAG) {
           uint32_t m = 0;
@@ -164,7 +177,7 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
           const int block = 1 << t.shift;
           for (int o = min(block / V, W) >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
           if (on) {
-            const int c = c0 + i * W * V;
+            const int c = c0 + i * cst;
             float inv;
             const float s = scale_of<Q>(m, &inv);
             store_codes<Q, P>(t.codes + row * g.C + c, f, inv);

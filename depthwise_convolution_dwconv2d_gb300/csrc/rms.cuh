@@ -61,16 +61,10 @@ __device__ __forceinline__ void clear_part(typename Raw<T, V>::type& u, int cb, 
     }
   }
 }
-// RAG: rows that begin anywhere; otherwise cb >= 0 and cb + V <= C
 template <typename T, int V, bool RAG>
-__device__ __forceinline__ typename Raw<T, V>::type load_vec(const T* row, int cb, int C, bool inner = true) {
-  typedef typename Raw<T, V>::type R;
-  if constexpr (!RAG) return *reinterpret_cast<const R*>(row + cb);
-  const bool edge = cb < 0 || cb + V > C;
-  if (edge && !inner) return load_part<T, V>(row, cb, C);
-  R u = *reinterpret_cast<const R*>(row + cb);
-  if (edge) clear_part<T, V>(u, cb, C);
-  return u;
+__device__ __forceinline__ typename Raw<T, V>::type load_ends(const T* row, int cb, int C) {
+  if constexpr (RAG) return load_part<T, V>(row, cb, C);
+  else return *reinterpret_cast<const typename Raw<T, V>::type*>(row + cb);
 }
 // The elements of a vector over one of the row's ends, in pieces of 8, 4 and 2
 // bytes; over both, element by element.

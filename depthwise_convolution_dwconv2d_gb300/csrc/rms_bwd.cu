@@ -94,7 +94,7 @@ bwd_kernel(BGeom g, const T* __restrict__ h, const T* __restrict__ gy, const T* 
       acc[i][e] = 0ull;
     }
     if (gamma && on[i])
-      pairs_of<T, V>(RAG ? load_part<T, V>(gamma, c0 + i * cstep, g.C) : load_vec<T, V, false>(gamma, c0 + i * cstep, g.C), gm[i]);
+      pairs_of<T, V>(load_ends<T, V, RAG>(gamma, c0 + i * cstep, g.C), gm[i]);
   }
 
   auto fetch = [&](int it, uint32_t to) {  // the row that the pointers are at
