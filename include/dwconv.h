@@ -464,7 +464,8 @@ typedef struct {
  * checkpoint y8 (rows, C; codes of the unrounded y), or to both; at least one
  * is not NULL. h may be the memory of x or of residual; otherwise outputs
  * overlap neither inputs nor each other. A row of zeros with eps = 0 gives
- * NaN. An infinity or a NaN in a row gives r = 0 or NaN, and NaN where it is. */
+ * NaN. An infinity or a NaN in a row gives r = 0 or NaN, and NaN where it is;
+ * a row whose squares add up to more than fp32 holds gives r = 0 as well. */
 dwconv_status_t dwconv_rms_norm(const dwconv_rms_desc_t* desc, const void* x, const void* residual,
                                 const void* gamma, void* h, void* y, float* rstd,
                                 const dwconv_act8_t* y8, cudaStream_t stream);
@@ -520,7 +521,7 @@ size_t dwconv2d_pointwise8_workspace_size(int64_t rows, int64_t cin, int64_t cou
  * its two scales (one fp32 rounding) is added in fp32. y ([rows, y_c_total],
  * only channels [y_c_offset, y_c_offset + cout) are written; total 0 means
  * cout) and bias ([cout] or NULL) are of `dtype`, act is a dwconv_act_t, the
- * result is rounded once. A row or a block of weights whose scale is NaN
+ * result is rounded once; y overlaps no input. A row or a block of weights whose scale is NaN
  * gives NaN. The input's gradient is the same product: of gy's codes
  * (dwconv_act8_encode) with the transposed weights.
  * Where cin is no multiple of 16 the workspace (16-byte aligned, not used

@@ -141,6 +141,39 @@ def test_rms_norm_many_narrow_rows():
         check_fwd(70001, C, dtype, True, True, True, None, 0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_rms_norm_ragged_rows_in_several_rounds(dtype):
+    """Rows off 16 bytes, more of them than blocks take at once: the tensor's first and last rows and those between."""
+    for i, (rows, C) in enumerate(((17, 513), (900, 515), (701, 1030), (950, 2031), (640, 2047), (4001, 217), (70001, 3), (6000, 437))):
+        check_fwd(rows, C, dtype, i % 2 == 0, want_h=i % 3 != 1, want_y=True, kind=None, block=0, gamma=i % 4 != 3, off=i % 3)
+
+
+@pytest.mark.parametrize("kind,block", [("e4m3", 128), ("i8", 32)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_rms_norm_ragged_rows_to_codes(dtype, kind, block):
+    for i, (rows, C) in enumerate(((17, 130), (5000, 218), (3000, 505), (2500, 723), (2001, 1013), (300, 1031), (9000, 31), (40000, 5))):
+        check_fwd(rows, C, dtype, i % 2 == 0, want_h=i % 3 != 1, want_y=i % 2 == 1, kind=kind, block=block, gamma=i % 4 != 3)
+
+
+def test_rms_norm_in_place_ragged():
+    """Reads that reach over a row's ends while the rows beside it are written: the same results."""
+    for rows, C, dtype in ((5000, 77, "bf16"), (700, 2131, "f16"), (3000, 501, "f32")):
+        g = gen(C)
+        x, res, gm = normal(g, rows, C, dtype=dtype), normal(g, rows, C, dtype=dtype), normal(g, C, dtype=dtype)
+        d = B.make_rms_desc(rows, C, EPS, dtype)
+        h, y = filled(rows, C, dtype=dtype), filled(rows, C, dtype=dtype)
+        B.dwconv_rms_norm(d, x, res, gm, h, y)
+        for k in range(2):
+            a, b, z = x.clone(), res.clone(), filled(rows, C, dtype=dtype)
+            B.dwconv_rms_norm(d, a, b, gm, (a, b)[k], z)
+            assert torch.equal((a, b)[k], h) and torch.equal(z, y)
+        gx, rstd = filled(rows, C, dtype=dtype), filled(rows)
+        B.dwconv_rms_norm(d, x, res, gm, None, y, rstd)
+        B.dwconv_rms_norm_bwd(d, h, y, gm, rstd, res, gx, None, None)
+        B.dwconv_rms_norm_bwd(d, h, y, gm, rstd, res, res, None, None)
+        assert torch.equal(res, gx)
+
+
 def test_rms_norm_in_place():
     """h over x or over the residual, rows kept in registers and rows read twice: the same results."""
     for rows, C, dtype in ((5, 200, "bf16"), (3, 4096, "f16"), (2, 40000, "bf16"), (2, 9001, "f32")):
@@ -334,6 +367,37 @@ def test_pointwise8(dtype):
 def test_pointwise8_activations(act):
     for rows, cin, cout, dtype in ((5, 256, 200, "f32"), (300, 200, 130, "bf16"), (300, 256, 512, "f32"), (129, 128, 260, "f16")):
         check_product(rows, cin, cout, dtype, act)
+
+
+def test_pointwise8_around_the_choice_of_kernel():
+    """Pixels and channels on both sides of every bound between the kernels, and between their shapes."""
+    for rows, cin, cout in ((16, 640, 130), (17, 640, 130), (32, 144, 200), (33, 144, 200), (64, 1280, 130), (65, 1280, 130), (64, 1152, 130),
+                            (77, 1554, 1983), (301, 1290, 520), (384, 2048, 2048), (385, 2048, 2048), (1, 128 * 270, 64), (40, 128 * 130, 24),
+                            (256, 1024, 256), (257, 1024, 257), (3105, 256, 1100), (4999, 1000, 1000)):
+        check_product(rows, cin, cout, "bf16", "silu" if rows % 2 else "none")
+
+
+def test_pointwise8_behind_its_copy():
+    """Calls one after another that use one workspace, and read codes that the call before them writes: the same results."""
+    rows = 2000
+    g = gen(6)
+    x, gm = normal(g, rows, 300), normal(g, 300, mean=1.0)
+    x8, d = new_act8(rows, 300, 128), B.make_rms_desc(rows, 300, EPS, "f32")
+    sizes = ((300, 200), (300, 77), (300, 1024))
+    w8 = [weight8_of(normal(g, o, i, std=0.06)) for i, o in sizes]
+    ys = [filled(rows, o) for _, o in sizes]
+    ws, intact = room(max(B.dwconv2d_pointwise8_workspace_size(rows, i, o) for i, o in sizes))
+    for _ in range(3):
+        for t in ys:
+            t.fill_(-7)
+        x.mul_(-1.5)
+        B.dwconv_rms_norm(d, x, None, gm, None, None, None, x8)
+        for w, y in zip(w8, ys):
+            B.dwconv2d_pointwise8(x8, w, None, "none", y, ws)
+        for w, y in zip(w8, ys):
+            want, slack = K.product(*x8.tensors, *w.tensors, None, "none")
+            R.within(y, want, slack, "f32")
+        assert intact()
 
 
 def test_pointwise8_codes_at_any_byte():
