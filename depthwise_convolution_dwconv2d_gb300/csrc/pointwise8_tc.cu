@@ -878,12 +878,13 @@ cudaError_t run_t(const Pw& g, int64_t ldx, const uint8_t* x, bool copied, const
   static std::atomic<uint64_t> ready_tile{0}, ready_pair{0};
   const int64_t tiles = tiles_of(g, kM, Tile::kN), pairs = tiles_of(g, 2 * kM, Pair::kN);
   if (tiles >= (int64_t(1) << 31)) return cudaErrorNotSupported;
-  // Rounds of tiles times what a tile takes in cycles, as traced: a block of
-  // channels 600 and the rest 1500 by one thread block, 1130 and 1800 by a pair
-  // (four times the products). 12544 pixels, 512 -> 512 channels 12.3 against
-  // 13.8 us, 3136, 1024 -> 1024 11.8 against 10.6, 200704, 128 -> 128 22.2
-  // against 25.6, 2048, 2048 -> 2048 18.6 against 15.5.
-  const int64_t by_tile = (tiles + 151) / 152 * (g.nkb * 600 + 1500), by_pair = (pairs + 75) / 76 * (g.nkb * 1130 + 1800);
+  // Measured: a call of tiles takes 2.9 us and per round 0.4 us a block of
+  // channels and 1.35; a call of pairs (four times the products) 3.8, 0.6 and
+  // 1.6. In tiles against pairs: 12544 pixels, 512 -> 512 channels 12.5 and
+  // 13.8 us, 3136, 1024 -> 1024 12.2 and 10.9, 200704, 128 -> 128 22.3 and
+  // 25.3, 10569, 2688 -> 1296 68.3 and 57.5, 8192, 4096 -> 4096 195 and 144.
+  const int64_t by_tile = 2900 + (tiles + 151) / 152 * (g.nkb * 400 + 1350);
+  const int64_t by_pair = 3800 + (pairs + 75) / 76 * (g.nkb * 600 + 1600);
   if (by_pair < by_tile) return launch_tiles<Pair, T>(pair_kernel<T>, true, ready_pair, g, ldx, x, copied, sx, w, sw, bias, y, s);
   return launch_tiles<Tile, T>(tile_kernel<T>, false, ready_tile, g, ldx, x, copied, sx, w, sw, bias, y, s);
 }
