@@ -46,29 +46,31 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t m, f32x2 v) {
   return max(m, max((uint32_t)v & 0x7fffffffu, (uint32_t)(v >> 32) & 0x7fffffffu));
 }
 
-// ---- rows that 256 threads hold ----------------------------------------------------
+// ---- rows that 256 or 512 threads hold ---------------------------------------------
 
 constexpr int kNT = 256;
 __device__ uint4 kNone[1];  // read in place of what does not exist
 // Blocks step over the rows; the next row's vectors are on their way while one
 // is worked on. RAG: rows begin anywhere, the step is a multiple of 8 of them,
-// and codes are made by one warp per row.
-template <typename T, int V, int NI, int Q, bool RAG>
-__global__ void __launch_bounds__(kNT, NI == 1 ? 4 : NI == 2 ? 3 : 2)
+// and codes are made by one warp per row. 512 threads: rows of 1025 to 2048
+// vectors, of which a block of 1024 threads to a row by itself, without the
+// next row on its way, took 34.5 us for 1432 x 4736 fp32 with residual, to codes.
+template <typename T, int V, int NI, int Q, bool RAG, int NT = kNT>
+__global__ void __launch_bounds__(NT, NT > kNT ? 1 : NI == 1 ? 4 : NI == 2 ? 3 : 2)
 fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, T* h, T* y, float* rstd, Act8 t) {
   typedef typename Raw<T, V>::type R;
   constexpr int P = V / 2;
   constexpr bool kCopy = RAG && Q != kSrcFull;
-  __shared__ float part[2][kNT / 32];
+  __shared__ float part[2][NT / 32];
   constexpr int kCopyC = NI * 32 * V;
-  __shared__ __align__(16) R copy[kCopy ? kNT / 32 : 1][kCopy ? NI * 32 + 1 : 1];
+  __shared__ __align__(16) R copy[kCopy ? NT / 32 : 1][kCopy ? NI * 32 + 1 : 1];
   __shared__ __align__(16) float gs[kCopy ? kCopyC + 4 : 1];  // gamma
   const int tid = threadIdx.x;
   const int in_row = tid & (g.tpr - 1);
   const int W = NI > 1 || g.tpr >= 32 ? 32 : g.tpr;  // rows of fewer than 32 lanes have one vector a lane
   const int st = NI > 1 ? g.tpr : 32;  // from item to item, in vectors: all warps have as many; in channels:
   const int cst = st * V;
-  const int rpb = kNT >> g.log_tpr;
+  const int rpb = NT >> g.log_tpr;
   const int64_t step = (int64_t)gridDim.x * rpb;
   int64_t row = (int64_t)blockIdx.x * rpb + (tid >> g.log_tpr);
   const int ph = RAG ? phase_of(x + row * g.xs + g.xo) : 0;
@@ -103,7 +105,7 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
     }
   };
   if constexpr (kCopy) {
-    for (int c = tid; c < kCopyC + 4; c += kNT) gs[c] = c < g.C && gamma ? ld(gamma + c) : 1.f;
+    for (int c = tid; c < kCopyC + 4; c += NT) gs[c] = c < g.C && gamma ? ld(gamma + c) : 1.f;
     R zero{};
     if ((tid & 31) == 0) copy[tid >> 5][nvec] = zero;  // what lies behind a row's last vector
     __syncthreads();
@@ -147,7 +149,7 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
         if (live && in_row + i * st < nvec) store_vec<T, V, RAG>(hp, c0 + i * cst, g.C, hv[i]);
       hp += xstep;
     }
-    const float ss = row_sum<kNT>(sum2(s2), g.tpr, part[flip]);
+    const float ss = row_sum<NT>(sum2(s2), g.tpr, part[flip]);
     const float r = __frsqrt_rn(fmaf(ss, g.inv_c, g.eps));
     if (live && in_row == 0 && rstd) rstd[row] = r;
     if constexpr (kCopy) {
@@ -528,13 +530,13 @@ void spread(Lay* l, int64_t nvec, int most) {
 }
 
 // Vectors per thread: one while all rows together are less than a wave of
-// threads (latency counts), else two, or four where 256 threads then hold a row.
+// threads (latency counts), else two, or four where 256 or 512 threads then hold a row.
 Lay lay(const Rms& g, int V) {
   Lay l{};
   l.v = V;
   const int64_t nvec = g.C / V;
   const bool wave = g.rows * nvec > 152 * 2048;
-  l.ni = !wave && nvec <= 1024 ? 1 : nvec <= 64 ? 1 : nvec <= 512 ? 2 : nvec <= 1024 ? 4 : 2;
+  l.ni = !wave && nvec <= 1024 ? 1 : nvec <= 64 ? 1 : nvec <= 512 ? 2 : nvec <= 1024 || (wave && nvec <= 2048) ? 4 : 2;
   spread(&l, nvec, 1024);
   l.nt = l.tpr > kNT ? l.tpr : kNT;
   return l;
@@ -555,9 +557,9 @@ Lay lay_ragged(const Rms& g, int V, bool codes) {
   l.ni = 1;
   const int most = codes ? 32 : 64;
   while (l.ni < 4 && l.ni * most < nvec) l.ni *= 2;
-  spread(&l, nvec, codes ? 32 : kNT);
+  spread(&l, nvec, codes ? 32 : 2 * kNT);
   if ((codes || l.ni > 1) && l.tpr < 32) l.tpr = 32;
-  l.nt = kNT;
+  l.nt = l.tpr > kNT ? l.tpr : kNT;
   return l;
 }
 
@@ -606,15 +608,17 @@ cudaError_t launch(KernelT kern, const Rms& g, const Lay& l, const Args& a, cuda
 template <typename T, int Q, bool RAG>
 cudaError_t run_rows(const Rms& g, const Lay& l, const Args& a, cudaStream_t s) {
   constexpr int V = Vec<T>::n;
-  const int64_t rpb = kNT / l.tpr, all = (g.rows + rpb - 1) / rpb;
-  const int64_t held = 152 * (l.ni == 1 ? 4 : l.ni == 2 ? 3 : 2);  // by the kernels' registers: one wave
+  const int64_t rpb = l.nt / l.tpr, all = (g.rows + rpb - 1) / rpb;
+  const int64_t held = 152 * (l.nt > kNT ? 1 : l.ni == 1 ? 4 : l.ni == 2 ? 3 : 2);  // by the kernels' registers: one wave
   int64_t blocks = all < held ? all : held;
   while (blocks * rpb % 8) ++blocks;
   const FGeom f = geom(g, l);
-  const auto kern = l.ni == 1   ? fwd_rows_kernel<T, V, 1, Q, RAG>
+  constexpr int kMore = RAG && Q != kSrcFull ? kNT : 2 * kNT;  // ragged rows to codes: a warp each
+  const auto kern = l.nt > kNT  ? fwd_rows_kernel<T, V, 4, Q, RAG, kMore>
+                    : l.ni == 1 ? fwd_rows_kernel<T, V, 1, Q, RAG>
                     : l.ni == 2 ? fwd_rows_kernel<T, V, 2, Q, RAG>
                                 : fwd_rows_kernel<T, V, 4, Q, RAG>;
-  kern<<<(unsigned)blocks, kNT, 0, s>>>(f, (const T*)a.x, (const T*)a.res, (const T*)a.gamma, (T*)a.h, (T*)a.y, a.rstd, a.t);
+  kern<<<(unsigned)blocks, l.nt, 0, s>>>(f, (const T*)a.x, (const T*)a.res, (const T*)a.gamma, (T*)a.h, (T*)a.y, a.rstd, a.t);
   return cudaGetLastError();
 }
 
@@ -624,7 +628,7 @@ cudaError_t run(const Rms& g, const Args& a, cudaStream_t s) {
   if (rows_on16(g, V) && on16(a.x) && on16(a.res) && on16(a.gamma) && on16(a.h) && on16(a.y) &&
       (Q == kSrcFull || reinterpret_cast<uintptr_t>(a.t.codes) % V == 0)) {
     const Lay l = lay(g, V);
-    if (l.nt == kNT) return run_rows<T, Q, false>(g, l, a, s);
+    if (l.nt == kNT || l.ni == 4) return run_rows<T, Q, false>(g, l, a, s);
     if (l.nt == 512) return launch<T, Q>(l.ni == 1 ? fwd_wide_kernel<T, V, 1, Q, 512> : fwd_wide_kernel<T, V, 2, Q, 512>, g, l, a, s);
     return launch<T, Q>(l.ni == 1 ? fwd_wide_kernel<T, V, 1, Q, 1024> : fwd_wide_kernel<T, V, 2, Q, 1024>, g, l, a, s);
   }
