@@ -15,10 +15,8 @@
 // Rows of more channels than 1024 threads hold are read twice, in spans.
 //
 // Rows that begin off 16 bytes (odd channels) are read in the vectors that lie
-// on 16 bytes (rms.cuh): threads step over rows that begin alike. Their codes'
-// blocks begin anywhere in a vector, so codes are made from a copy of the row
-// in shared memory, four channels a lane. Only tensors that do not begin alike
-// are read element by element.
+// on 16 bytes (rms.cuh): threads step over rows that begin alike. Only tensors
+// that do not begin alike are read element by element.
 //
 // Bound by memory: 4 to 6 operations per element against 2 to 7 bytes.
 #include "rms.cuh"
@@ -46,13 +44,29 @@ __device__ __forceinline__ uint32_t max_bits(uint32_t m, f32x2 v) {
   return max(m, max((uint32_t)v & 0x7fffffffu, (uint32_t)(v >> 32) & 0x7fffffffu));
 }
 
+// The codes' blocks k0 and k1 of the V channels from c on, of which the first
+// `cut` are k0's (k1 = k0 and cut = V where there is one block).
+struct Span { int k0, k1, cut; };
+template <int V>
+__device__ __forceinline__ Span span_of(int c, int C, int shift) {
+  Span s;
+  s.k0 = max(c, 0) >> shift;
+  s.k1 = min(c + V, C) - 1 >> shift;
+  s.cut = s.k1 > s.k0 ? (s.k1 << shift) - c : V;
+  return s;
+}
+
 // ---- rows that 256 or 512 threads hold ---------------------------------------------
 
 constexpr int kNT = 256;
 __device__ uint4 kNone[1];  // read in place of what does not exist
 // Blocks step over the rows; the next row's vectors are on their way while one
-// is worked on. RAG: rows begin anywhere, the step is a multiple of 8 of them,
-// and codes are made by one warp per row. 512 threads: rows of 1025 to 2048
+// is worked on. RAG: rows begin anywhere and the step is a multiple of 8 of
+// them; the maxima of the codes' blocks meet in shared memory (the largest of
+// bit patterns: in any order the same). Brought together by shuffles first they
+// took longer (6000 x 2131 fp16 with residual to codes 76 us against 63.5; from
+// a copy of the row, a warp each, 41 against 39 at 13470 x 723, and no row of
+// more than 1016 channels). 512 threads: rows of 1025 to 2048
 // vectors, of which a block of 1024 threads to a row by itself, without the
 // next row on its way, took 34.5 us for 1432 x 4736 fp32 with residual, to codes.
 template <typename T, int V, int NI, int Q, bool RAG, int NT = kNT>
@@ -60,11 +74,9 @@ __global__ void __launch_bounds__(NT, NT > kNT ? 1 : NI == 1 ? 4 : NI == 2 ? 3 :
 fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, T* h, T* y, float* rstd, Act8 t) {
   typedef typename Raw<T, V>::type R;
   constexpr int P = V / 2;
-  constexpr bool kCopy = RAG && Q != kSrcFull;
+  constexpr bool kSplit = RAG && Q != kSrcFull;  // a block of codes begins anywhere in a vector
   __shared__ float part[2][NT / 32];
-  constexpr int kCopyC = NI * 32 * V;
-  __shared__ __align__(16) R copy[kCopy ? NT / 32 : 1][kCopy ? NI * 32 + 1 : 1];
-  __shared__ __align__(16) float gs[kCopy ? kCopyC + 4 : 1];  // gamma
+  __shared__ uint32_t maxima[2][kSplit ? NT * NI * V / 32 + NT / 4 : 1];  // of the codes' blocks, for each row in turn
   const int tid = threadIdx.x;
   const int in_row = tid & (g.tpr - 1);
   const int W = NI > 1 || g.tpr >= 32 ? 32 : g.tpr;  // rows of fewer than 32 lanes have one vector a lane
@@ -104,12 +116,13 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
       if (res) nr[i] = *(no ? (const R*)kNone : reinterpret_cast<const R*>(rp + c0 + i * cst));
     }
   };
-  if constexpr (kCopy) {
-    for (int c = tid; c < kCopyC + 4; c += NT) gs[c] = c < g.C && gamma ? ld(gamma + c) : 1.f;
-    R zero{};
-    if ((tid & 31) == 0) copy[tid >> 5][nvec] = zero;  // what lies behind a row's last vector
+  const int line = (tid >> g.log_tpr) * t.nblk;  // of the maxima
+  if constexpr (kSplit) {
+    for (int k = tid; k < rpb * t.nblk; k += NT) maxima[0][k] = maxima[1][k] = 0;
     __syncthreads();
   }
+  // where x's rows are as far apart as the codes', their vectors are whole ones too
+  const bool whole = kSplit && (reinterpret_cast<uintptr_t>(t.codes) + row * g.C - ph) % V == 0;
   int flip = 0;
   fetch(row);
   for (int64_t base = (int64_t)blockIdx.x * rpb; base < g.rows; base += step, row += step, flip ^= 1) {
@@ -152,14 +165,12 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
     const float ss = row_sum<NT>(sum2(s2), g.tpr, part[flip]);
     const float r = __frsqrt_rn(fmaf(ss, g.inv_c, g.eps));
     if (live && in_row == 0 && rstd) rstd[row] = r;
-    if constexpr (kCopy) {
-      R* mine = copy[tid >> 5];
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (live && in_row + i * st < nvec) mine[in_row + i * st] = hv[i];
-      __syncwarp();
+    uint32_t* mx = maxima[flip] + (kSplit ? line : 0);
+    if constexpr (kSplit) {
+      if (g.tpr <= 32) __syncwarp();
+      for (int k = in_row; k < t.nblk; k += g.tpr) maxima[flip ^ 1][line + k] = 0;  // the next row's
     }
-    if (!kCopy || y) {
+    {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const bool on = live && in_row + i * st < nvec;
@@ -172,7 +183,24 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
           for (int e = 0; e < P; ++e) f[e] = mul_f32x2(mul_f32x2(f[e], both(r)), gm[i][e]);
           if (y) store_vec<T, V, RAG>(yp, c0 + i * cst, g.C, vec_of<T, V>(f));
         }
-        if constexpr (Q != kSrcFull && !RAG) {
+        if constexpr (kSplit) {
+          const Span b = span_of<V>(c0 + i * cst, g.C, t.shift);
+          uint32_t m = 0;
+          if (b.k1 == b.k0) {
+#pragma unroll
+            for (int e = 0; e < P; ++e) m = max_bits(m, f[e]);
+          } else {
+            uint32_t m1 = 0;
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              const uint32_t lo = (uint32_t)f[e] & 0x7fffffffu, hi = (uint32_t)(f[e] >> 32) & 0x7fffffffu;
+              m = max(m, max(2 * e < b.cut ? lo : 0, 2 * e + 1 < b.cut ? hi : 0));
+              m1 = max(m1, max(2 * e < b.cut ? 0 : lo, 2 * e + 1 < b.cut ? 0 : hi));
+            }
+            if (on) atomicMax(mx + b.k1, m1);
+          }
+          if (on) atomicMax(mx + b.k0, m);
+        } else if constexpr (Q != kSrcFull) {
           uint32_t m = 0;
 #pragma unroll
           for (int e = 0; e < P; ++e) m = max_bits(m, f[e]);
@@ -189,56 +217,40 @@ fwd_rows_kernel(FGeom g, const T* x, const T* res, const T* __restrict__ gamma, 
       }
       yp += ystep;
     }
-    if constexpr (kCopy) {  // a warp per row, four channels a lane
-      const char* hs = reinterpret_cast<const char*>(copy[tid >> 5]);
-      const int block = 1 << t.shift, shift = 16 * (ph & 3);
+    if constexpr (kSplit) {
+      if (g.tpr <= 32) __syncwarp();
+      else __syncthreads();
       uint8_t* q = t.codes + row * g.C;
-      const int off = (int)(reinterpret_cast<uintptr_t>(q) & 3);
-      for (int c = 4 * (tid & 31); c < g.C + 4 * (tid & 31); c += 128) {
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t m = 0;
-        if (live && c < g.C) {
-          if constexpr (V == 8) {  // two aligned reads of 8 bytes, moved together
-            const uint64_t* p = reinterpret_cast<const uint64_t*>(hs + ((ph + c) & ~3) * 2);
-            uint64_t u = p[0];
-            if (shift) u = u >> shift | p[1] << (64 - shift);
-            const uint2 w = make_uint2((uint32_t)u, (uint32_t)(u >> 32));
-            const uint4 v = make_uint4(w.x, w.y, 0, 0);
-            float o[8];
-            unpack16<T>(v, o);
+      float* sc = t.scales + row * t.nblk;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = o[e];
-          } else {
+      for (int i = 0; i < NI; ++i) {
+        if (!live || in_row + i * st >= nvec) continue;
+        const int c = c0 + i * cst;
+        const Span b = span_of<V>(c, g.C, t.shift);
+        float inv0, inv1;
+        const float s0 = scale_of<Q>(mx[b.k0], &inv0);
+        inv1 = inv0;
+        if (b.k1 != b.k0) sc[b.k1] = scale_of<Q>(mx[b.k1], &inv1);
+        if (c <= b.k0 << t.shift) sc[b.k0] = s0;
+        f32x2 f[P];
+        pairs_of<T, V>(hv[i], f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const float*>(hs + (ph + c + e) * 4);
-          }
-          const float4 gq = *reinterpret_cast<const float4*>(gs + c);
-          const float gv[4] = {gq.x, gq.y, gq.z, gq.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[e] = __fmul_rn(__fmul_rn(f[e], r), gv[e]);
-            m = max(m, abs_bits(f[e]));
-          }
+        for (int e = 0; e < P; ++e) {
+          f[e] = mul_f32x2(mul_f32x2(f[e], both(r)), gm[i][e]);
+          f[e] = mul_f32x2(f[e], pack_f32x2(2 * e < b.cut ? inv0 : inv1, 2 * e + 1 < b.cut ? inv0 : inv1));
         }
-        for (int o = block >> 3; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (live && c < g.C) {
-          float inv;
-          const float s = scale_of<Q>(m, &inv);
-          const uint32_t k = encode4<Q>(f[0], f[1], f[2], f[3], inv);
-          if (off == 0 && c + 4 <= g.C) {
-            *reinterpret_cast<uint32_t*>(q + c) = k;
-          } else if (off == 2 && c + 4 <= g.C) {
-            *reinterpret_cast<uint16_t*>(q + c) = (uint16_t)k;
-            *reinterpret_cast<uint16_t*>(q + c + 2) = (uint16_t)(k >> 16);
-          } else {
+        uint32_t w[2] = {encode4<Q>(f[0], f[1], 1.f), 0};
+        if constexpr (V == 8) w[1] = encode4<Q>(f[2], f[3], 1.f);
+        uint8_t* at = q + c;
+        if (c >= 0 && c + V <= g.C && whole) {
+          if constexpr (V == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+          else *reinterpret_cast<uint32_t*>(at) = w[0];
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (c + e < g.C) q[c + e] = (uint8_t)(k >> (8 * e));
-          }
-          if ((c & (block - 1)) == 0) t.scales[row * t.nblk + (c >> t.shift)] = s;
+          for (int e = 0; e < V; ++e)
+            if (c + e >= 0 && c + e < g.C) at[e] = (uint8_t)(w[e / 4] >> (8 * (e & 3)));
         }
       }
-      __syncwarp();
     }
   }
 }
@@ -549,16 +561,16 @@ Lay lay_elem(const Rms& g) {
   l.nt = l.tpr > 256 ? l.tpr : 256;
   return l;
 }
-// A warp per row where there are codes; segs > 1: not one for the ragged form.
-Lay lay_ragged(const Rms& g, int V, bool codes) {
+// segs > 1: not one for the ragged form.
+Lay lay_ragged(const Rms& g, int V) {
   Lay l{};
   l.v = V;
   const int64_t nvec = (g.C + 2 * V - 2) / V;
   l.ni = 1;
-  const int most = codes ? 32 : 64;
+  const int most = g.rows * nvec > 152 * 2048 ? 64 : kNT;  // as above: latency counts
   while (l.ni < 4 && l.ni * most < nvec) l.ni *= 2;
-  spread(&l, nvec, codes ? 32 : 2 * kNT);
-  if ((codes || l.ni > 1) && l.tpr < 32) l.tpr = 32;
+  spread(&l, nvec, 2 * kNT);
+  if (l.ni > 1 && l.tpr < 32) l.tpr = 32;
   l.nt = l.tpr > kNT ? l.tpr : kNT;
   return l;
 }
@@ -613,8 +625,7 @@ cudaError_t run_rows(const Rms& g, const Lay& l, const Args& a, cudaStream_t s) 
   int64_t blocks = all < held ? all : held;
   while (blocks * rpb % 8) ++blocks;
   const FGeom f = geom(g, l);
-  constexpr int kMore = RAG && Q != kSrcFull ? kNT : 2 * kNT;  // ragged rows to codes: a warp each
-  const auto kern = l.nt > kNT  ? fwd_rows_kernel<T, V, 4, Q, RAG, kMore>
+  const auto kern = l.nt > kNT  ? fwd_rows_kernel<T, V, 4, Q, RAG, 2 * kNT>
                     : l.ni == 1 ? fwd_rows_kernel<T, V, 1, Q, RAG>
                     : l.ni == 2 ? fwd_rows_kernel<T, V, 2, Q, RAG>
                                 : fwd_rows_kernel<T, V, 4, Q, RAG>;
@@ -632,7 +643,7 @@ cudaError_t run(const Rms& g, const Args& a, cudaStream_t s) {
     if (l.nt == 512) return launch<T, Q>(l.ni == 1 ? fwd_wide_kernel<T, V, 1, Q, 512> : fwd_wide_kernel<T, V, 2, Q, 512>, g, l, a, s);
     return launch<T, Q>(l.ni == 1 ? fwd_wide_kernel<T, V, 1, Q, 1024> : fwd_wide_kernel<T, V, 2, Q, 1024>, g, l, a, s);
   }
-  const Lay l = lay_ragged(g, V, Q != kSrcFull);
+  const Lay l = lay_ragged(g, V);
   if (l.segs == 1 && alike(a.x, a.res) && alike(a.x, a.h) && alike(a.x, a.y) && (!a.y || rows_alike(g, V)))
     return run_rows<T, Q, true>(g, l, a, s);
   const Lay e = lay_elem(g);
@@ -646,7 +657,7 @@ cudaError_t run(const Rms& g, const Args& a, cudaStream_t s) {
 bool fwd_in_row(const Rms& g) {
   const int V = g.dtype == DWCONV_F32 ? 4 : 8;
   if (rows_on16(g, V)) return lay(g, V).segs == 1;
-  return lay_ragged(g, V, false).segs == 1 || lay_elem(g).segs == 1;
+  return lay_ragged(g, V).segs == 1 || lay_elem(g).segs == 1;
 }
 
 cudaError_t fwd(const Rms& g, const void* x, const void* residual, const void* gamma, void* h, void* y, float* rstd,
