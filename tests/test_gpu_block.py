@@ -155,6 +155,40 @@ def test_rms_norm_ragged_rows_to_codes(dtype, kind, block):
         check_fwd(rows, C, dtype, i % 2 == 0, want_h=i % 3 != 1, want_y=i % 2 == 1, kind=kind, block=block, gamma=i % 4 != 3)
 
 
+def test_rms_norm_slices_and_codes_at_any_byte():
+    """Codes whose rows do not lie as x's do, or begin at an odd byte: no byte around them is written."""
+    for rows, C, xo, xt, by, dtype, block in ((700, 205, 3, 219, 0, "bf16", 32), (700, 205, 0, 0, 3, "f16", 64), (1000, 131, 0, 133, 1, "f32", 128),
+                                              (900, 128, 0, 0, 5, "bf16", 128), (650, 2100, 1, 2101, 2, "bf16", 32), (1, 7, 2, 9, 1, "f16", 32)):
+        g = gen(C)
+        x = torch.full((rows, xt or C), float("nan"), dtype=R.DT[dtype], device="cuda")
+        x[:, xo:xo + C] = normal(g, rows, C, dtype=dtype)
+        gm = normal(g, C, dtype=dtype)
+        buf = torch.full((rows * C + by + 64,), 0x55, dtype=torch.uint8, device="cuda")
+        codes = buf[by:by + rows * C].view(rows, C).view(torch.float8_e4m3fn)
+        y8 = B.make_act8("e4m3", block, codes, torch.full((rows, -(-C // block)), -1.0, device="cuda"))
+        B.dwconv_rms_norm(B.make_rms_desc(rows, C, EPS, dtype, xo, xt), x, None, gm, None, None, None, y8)
+        check_codes(y8, K.rms_fwd(x[:, xo:xo + C], None, gm, EPS, dtype)[2], "e4m3", block, (rows, C))
+        assert bool((buf[:by] == 0x55).all()) and bool((buf[by + rows * C:] == 0x55).all())
+
+
+def test_rms_norm_special_values_in_ragged_rows():
+    """Infinities, NaN and zeros stay in their rows and blocks where blocks begin inside a vector."""
+    x = normal(gen(1), 40, 333, dtype="bf16")
+    x[21] = 0
+    x[22, 100] = float("inf")
+    x[23, 332] = float("nan")
+    y, rstd, y8 = filled(40, 333, dtype="bf16"), filled(40), new_act8(40, 333, 32)
+    B.dwconv_rms_norm(B.make_rms_desc(40, 333, EPS, "bf16"), x, None, None, None, y, rstd, y8)
+    codes, scales = y8.tensors
+    assert bool((y[21] == 0).all()) and bool(scales[21].eq(0).all())
+    assert float(rstd[22]) == 0 and bool(scales[22, 3].isnan()) and int(scales[22].isnan().sum()) == 1
+    assert bool(y[23].isnan().all()) and bool(scales[23].isnan().all())
+    rest = [r for r in range(40) if r not in (22, 23)]
+    assert bool(y[rest].isfinite().all()) and bool(scales[rest].isfinite().all())
+    B.dwconv_rms_norm(B.make_rms_desc(40, 333, 0.0, "bf16"), x, None, None, None, None, rstd, y8)
+    assert bool(scales[21].isnan().all()) and bool(scales[[20, 24]].isfinite().all())
+
+
 def test_rms_norm_in_place_ragged():
     """Reads that reach over a row's ends while the rows beside it are written: the same results."""
     for rows, C, dtype in ((5000, 77, "bf16"), (700, 2131, "f16"), (3000, 501, "f32")):
