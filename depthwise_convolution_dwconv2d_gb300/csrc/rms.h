@@ -29,10 +29,11 @@ cudaError_t bwd(const Rms& g, const void* h, const void* gy, const void* gamma, 
                 void* gx, void* ggamma, float* ws, cudaStream_t s);
 
 // ---- how rows are laid over threads (rms.cu, rms_bwd.cu) --------------------
-// tpr threads (a power of two) hold a row, each NI vectors of V channels: a
-// group of W = min(tpr, 32) lanes owns W * NI neighbouring vectors, lane l
-// vectors l, l + W, ... of them, so that accesses are whole lines and a block
-// of channels of a checkpoint stays within a warp.
+// tpr threads (a power of two) hold a row, each NI vectors of V channels.
+// Neighbouring lanes hold neighbouring vectors, so that accesses are whole lines
+// and a block of channels of a checkpoint stays within a warp; from item to
+// item a thread goes on by tpr vectors (the forward that steps over rows) or by
+// a warp's (the others).
 struct Lay {
   int v;        // channels per vector: 16 bytes' worth, or 1
   int ni;       // vectors per thread
