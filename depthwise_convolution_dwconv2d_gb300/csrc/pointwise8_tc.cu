@@ -96,12 +96,18 @@ struct Ring {
   }
 };
 
-// Every copy that a producer issued lands before the block leaves (those of a
-// stage that both have issued to).
+// Before a block leaves, every copy that a producer issued has landed (those of
+// a stage that both have issued to), and so has every arrival that frees one of
+// its stages: those of the last STAGES nobody else waits for, and in a pair
+// they come from the other block. full: null where the copies count elsewhere.
+// After a give-up the arrivals may never come and are not waited for.
 template <int STAGES>
-__device__ __forceinline__ void drain(uint64_t* full, uint32_t issued) {
+__device__ __forceinline__ void drain(uint64_t* full, uint64_t* empty, uint32_t issued, volatile int* abortp) {
   const uint32_t first = issued > (uint32_t)STAGES ? issued - STAGES : 0;
-  for (uint32_t k = first; k < issued; ++k) tc::wait(&full[k % STAGES], (k / STAGES) & 1, nullptr, nullptr);
+  for (uint32_t k = first; k < issued; ++k) {
+    if (full) tc::wait(&full[k % STAGES], (k / STAGES) & 1, nullptr, nullptr);
+    tc::wait(&empty[k % STAGES], (k / STAGES) & 1, nullptr, abortp);
+  }
 }
 
 // One of two MMA warps: the blocks of channels which, which + 2, ... of `total`
@@ -390,7 +396,7 @@ tile_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
           ++issued;
         }
       }
-      drain<K::kStages>(full, issued);
+      drain<K::kStages>(full, empty, issued, abortp);
     }
     __syncwarp();
   } else if (warp >= kMma) {
@@ -531,21 +537,23 @@ pair_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
             ++issued;
           }
         }
-        if (rank == 0) drain<K::kStages>(full, issued);
+        drain<K::kStages>(rank == 0 ? full : nullptr, empty, issued, abortp);
       }
       __syncwarp();
-    } else if (warp >= kMma && rank == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(2 * kM, K::kN);
-      const uint32_t mine = pair < g.tiles ? (g.tiles - 1 - pair) / pairs + 1 : 0;
-      mma_loop<K::kStages, K::kAcc>(warp - kMma, mine * nkb, full, accfree, timeouts, abortp, [&](int ab, int stage) {
-        const unsigned char* st = sm + (size_t)stage * K::kStage;
-        mma_block<2>(tmem + ab * K::kN, st, st + K::kA, idesc);
-        commit_pair(&empty[stage]);
-        commit_pair(&accfull[ab]);
-      });
-      if (tc::elect_one()) commit_pair(&done);
-      __syncwarp();
-      tc::wait(&done, 0, nullptr, nullptr);
+    } else {
+      if (rank == 0) {
+        constexpr uint32_t idesc = idesc_e4m3(2 * kM, K::kN);
+        const uint32_t mine = pair < g.tiles ? (g.tiles - 1 - pair) / pairs + 1 : 0;
+        mma_loop<K::kStages, K::kAcc>(warp - kMma, mine * nkb, full, accfree, timeouts, abortp, [&](int ab, int stage) {
+          const unsigned char* st = sm + (size_t)stage * K::kStage;
+          mma_block<2>(tmem + ab * K::kN, st, st + K::kA, idesc);
+          commit_pair(&empty[stage]);
+          commit_pair(&accfull[ab]);
+        });
+        if (tc::elect_one()) commit_pair(&done);
+        __syncwarp();
+      }
+      tc::wait(&done, 0, nullptr, nullptr);  // block 1 too: its MMAs' ends arrive from block 0
       __syncwarp();
     }
   } else {
@@ -567,7 +575,11 @@ pair_kernel(TGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_cons
         });
   }
   tc::fence_before();
-  cg::this_cluster().sync();  // neither block leaves while the other's MMAs, copies or arrivals may reach it
+  // Neither block leaves while the other's MMAs, copies or arrivals may reach it.
+  // This orders the threads; what they started is waited for before: copies,
+  // freed stages (drain), sums (every accfull by the warps that read back) and
+  // done, in both blocks.
+  cg::this_cluster().sync();
   tc::fence_after();
   if (warp == kMma)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(K::kCols) : "memory");
@@ -647,7 +659,7 @@ row_kernel(RGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_const
         }
         ++issued;
       }
-      drain<K::kStages>(full, issued);
+      drain<K::kStages>(full, empty, issued, abortp);
     }
     __syncwarp();
   } else if (warp >= kMma) {
