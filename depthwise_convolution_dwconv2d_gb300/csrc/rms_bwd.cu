@@ -219,10 +219,11 @@ bwd_wide_kernel(BGeom g, const T* __restrict__ h, const T* __restrict__ gy, cons
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int c = c0 + k * kWideNT;
-        if (c < g.C) s[k] = fmaf(gamma ? ld(yp + c) * ld(gamma + c) : ld(yp + c), ld(hp + c), s[k]);
+        // t * (h r), as in the rows that registers hold: t * h can leave fp32 where this does not
+        if (c < g.C) s[k] = fmaf(gamma ? ld(yp + c) * ld(gamma + c) : ld(yp + c), __fmul_rn(ld(hp + c), r), s[k]);
       }
     }
-    const float c1 = __fmul_rn(__fmul_rn(row_sum<kWideNT>((s[0] + s[1]) + (s[2] + s[3]), kWideNT, part), r), g.inv_c);
+    const float c1 = __fmul_rn(row_sum<kWideNT>((s[0] + s[1]) + (s[2] + s[3]), kWideNT, part), g.inv_c);
     for (int c = threadIdx.x; c < g.C; c += kWideNT) {
       const float t = gamma ? ld(yp + c) * ld(gamma + c) : ld(yp + c);
       const float o = fmaf(-__fmul_rn(ld(hp + c), r), c1, t);

@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 import block_ref as K
 import train_ref as R
 from depthwise_convolution_dwconv2d_gb300 import binding as B
-from test_gpu_block import EPS, _lib, _no_wait_gave_up, act8_of, filled, gen, normal, room, run_clip, weight8_of  # noqa: F401
+from test_gpu_block import EPS, _lib, _no_wait_gave_up, act8_of, filled, gen, normal, offset_view, room, run_clip, weight8_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,28 @@ def test_pairs_leave_nothing_behind():
                     call()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for (_, o), w in zip(calls, want))
+
+
+# ---- RMS norm, backward ------------------------------------------------------------
+
+
+@pytest.mark.parametrize("size,gsize", [(2.0 ** 50, 2.0 ** 83), (2.0 ** -56, 2.0 ** -83)])
+def test_rms_norm_bwd_keeps_its_range_in_every_kernel(size, gsize):
+    """t * h leaves fp32 (or its normal numbers) where t * (h r) does not: rows in registers, rows that do not begin alike,
+    rows too wide, with gamma and without."""
+    for rows, C, dtype, apart, gamma in ((5, 200, "f32", False, True), (5, 200, "f32", True, True), (4, 77, "bf16", True, False),
+                                         (300, 96, "bf16", True, True), (2, 40000, "bf16", False, True), (3, 9001, "f32", False, False)):
+        g = gen(C)
+        h, gy = normal(g, rows, C, std=size).to(R.DT[dtype]), normal(g, rows, C, std=gsize).to(R.DT[dtype])
+        gm = normal(g, C, dtype=dtype, std=0.2, mean=1.0) if gamma else None
+        rstd = (1 / torch.sqrt(h.double().square().mean(-1))).float()
+        if apart:
+            h = offset_view(h)
+        d = B.make_rms_desc(rows, C, 0.0, dtype)
+        gx, gg = filled(rows, C, dtype=dtype), filled(C, dtype=dtype)
+        ws, intact = room(B.dwconv_rms_norm_bwd_workspace_size(d))
+        B.dwconv_rms_norm_bwd(d, h, gy, gm, rstd, None, gx, gg, ws)
+        wx, wg, sx, sg = K.rms_bwd(h, gy, gm, rstd, None)
+        R.within(gx, wx, sx, dtype, f"gx {rows}x{C}")
+        R.within(gg, wg, sg, dtype, f"ggamma {rows}x{C}")
+        assert intact()
