@@ -659,7 +659,7 @@ cudaError_t run(const Rms& g, const Args& a, cudaStream_t s) {
 bool fwd_in_row(const Rms& g) {
   const int V = g.dtype == DWCONV_F32 ? 4 : 8;
   if (rows_on16(g, V)) return lay(g, V).segs == 1;
-  return lay_ragged(g, V).segs == 1 || lay_elem(g).segs == 1;
+  return (lay_ragged(g, V).segs == 1 && rows_alike(g, V)) || lay_elem(g).segs == 1;
 }
 
 cudaError_t fwd(const Rms& g, const void* x, const void* residual, const void* gamma, void* h, void* y, float* rstd,

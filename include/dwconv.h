@@ -488,8 +488,9 @@ dwconv_status_t dwconv_rms_norm_bwd(const dwconv_rms_desc_t* desc, const void* h
                                     void* ggamma, void* workspace, size_t workspace_bytes,
                                     cudaStream_t stream);
 
-/* Kernel family of pass 0 (forward) or 1 (backward) for aligned pointers:
- * "row" (a row is read once), "wide" (read twice) or "invalid". Host only. */
+/* Kernel family of pass 0 (a forward that writes y) or 1 (backward) for
+ * aligned pointers: "row" (a row is read once), "wide" (read twice) or
+ * "invalid". Host only. */
 const char* dwconv_rms_norm_plan_name(const dwconv_rms_desc_t* desc, int pass);
 
 /* The 8-bit weights of a 1x1 layer: e4m3 codes, one fp32 scale per block of

@@ -1,0 +1,42 @@
+"""The entry points around a block's layers on the host: which kernel a call maps to on both sides of each bound."""
+import pytest
+
+from depthwise_convolution_dwconv2d_gb300 import binding as B
+from depthwise_convolution_dwconv2d_gb300 import build as BLD
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    BLD.build()
+    return B.load()
+
+
+def plans(C, dtype, rows=5, **kw):
+    d = B.make_rms_desc(rows, C, dtype=dtype, **kw)
+    return tuple(B.dwconv_rms_norm_plan_name(d, k) for k in (0, 1))
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 8), ("f16", 8), ("f32", 4)])
+def test_rms_plans_on_both_sides_of_each_bound(dtype, V):
+    """Forward: 2048 vectors of 16 bytes to a row, or 8192 elements where its tensors do not begin alike. Backward: 8192
+    channels; never without rows that begin alike."""
+    for rows in (1, 5, 100_000):
+        assert plans(2048 * V, dtype, rows)[0] == "row" and plans(2049 * V, dtype, rows)[0] == "wide"
+        assert plans(8192, dtype, rows)[1] == "row" and plans(8192 + V, dtype, rows)[1] == "wide"
+        # off 16 bytes a row may reach over V - 1 elements in front of it
+        assert plans(2047 * V + 1, dtype, rows)[0] == "row" and plans(2048 * V + 1, dtype, rows)[0] == "wide"
+        assert plans(8192 - V + 1, dtype, rows)[1] == "row" and plans(8193, dtype, rows)[1] == "wide"
+        # x and y do not begin alike: slices of other widths, other offsets
+        for kw in (dict(x_c_total=20_001, y_c_total=20_000), dict(x_c_offset=1, x_c_total=20_000, y_c_total=20_000)):
+            assert plans(8192, dtype, rows, **kw) == ("row", "wide")
+            assert plans(8193, dtype, rows, **kw) == plans(8200, dtype, rows, **kw) == ("wide", "wide")
+            assert plans(64, dtype, rows, **kw) == ("row", "wide")
+    # off 16 bytes but alike
+    kw = dict(x_c_offset=3, x_c_total=20_001, y_c_offset=3, y_c_total=20_001)
+    assert plans(8000, dtype, **kw) == ("row", "row")
+
+
+def test_rms_plan_of_a_wider_slice():
+    """12000 channels of rows 12001 apart into rows of their own: no kernel holds such a row."""
+    assert plans(12000, "bf16", x_c_total=12001) == ("wide", "wide")
+    assert plans(12000, "bf16", x_c_total=12001, y_c_total=12001) == ("row", "wide")
