@@ -147,7 +147,16 @@ def weight8_pitch(cin) -> int:
 
 def make_weight8(cout, cin, codes, scales) -> Weight8:
     """8-bit weights over ``codes`` ([cout, weight8_pitch(cin)], one byte each) and ``scales``
-    ([ceil(cout / 128), ceil(cin / 128)], fp32)."""
+    ([ceil(cout / 128), ceil(cin / 128)], fp32). Tensors of another type or row length, or too small, are refused
+    (rows of ``cin`` codes that are no multiple of 128 among them); raw addresses are taken as they are."""
+    if hasattr(codes, "numel"):
+        pitch = weight8_pitch(cin)
+        if codes.element_size() != 1 or codes.numel() < cout * pitch or (len(codes.shape) > 1 and codes.shape[-1] != pitch):
+            raise ValueError(f"codes must hold [{cout}, {pitch}] values of one byte, not {tuple(codes.shape)} of {codes.dtype}")
+    if hasattr(scales, "numel"):
+        blocks = (-(-cout // 128), -(-cin // 128))
+        if str(scales.dtype) != "torch.float32" or scales.numel() < blocks[0] * blocks[1]:
+            raise ValueError(f"scales must hold {list(blocks)} fp32 values, not {tuple(scales.shape)} of {scales.dtype}")
     t = Weight8(cout, cin, _ptr(codes), _ptr(scales))
     t.tensors = (codes, scales)
     return t

@@ -40,3 +40,21 @@ def test_rms_plan_of_a_wider_slice():
     """12000 channels of rows 12001 apart into rows of their own: no kernel holds such a row."""
     assert plans(12000, "bf16", x_c_total=12001) == ("wide", "wide")
     assert plans(12000, "bf16", x_c_total=12001, y_c_total=12001) == ("row", "wide")
+
+
+def test_weights_too_small_for_their_sizes_are_refused():
+    """Kernels write and read whole rows of 128 codes: rows of cin codes, the natural shape, end before those do."""
+    torch = pytest.importorskip("torch")
+    codes = lambda *s, t=torch.float8_e4m3fn: torch.empty(*s, dtype=t)  # noqa: E731
+    scales = torch.empty(2, 3)
+    for good in (codes(200, 384), codes(200, 384, t=torch.uint8), codes(200 * 384 + 5), codes(1, 200, 384)):
+        w8 = B.make_weight8(200, 300, good, scales)
+        assert w8.codes == good.data_ptr() and w8.scales == scales.data_ptr() and w8.tensors[0] is good
+    for bad in (codes(200, 300), codes(199, 384), codes(200 * 384 - 1), codes(200, 512), codes(384, 200), codes(200, 384, t=torch.bfloat16)):
+        with pytest.raises(ValueError, match="codes"):
+            B.make_weight8(200, 300, bad, scales)
+    for bad in (torch.empty(2, 2), torch.empty(5), torch.empty(2, 3, dtype=torch.float64), torch.empty(2, 3, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError, match="scales"):
+            B.make_weight8(200, 300, codes(200, 384), bad)
+    B.make_weight8(200, 300, 0x1000, 0x2000)  # addresses: nothing to look at
+    B.make_weight8(200, 300, codes(200, 384), torch.empty(3, 3))
