@@ -730,9 +730,16 @@ row_kernel(RGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_const
   }
   cg::cluster_group cl = cg::this_cluster();
   cl.sync();
-  if (warp < 4 && o0 + tid < g.p.cout) {
+  if (warp < 4) {
+    // Sums are whole only if no block of the cluster gave up: otherwise nothing
+    // is stored, as in the tile kernels. A lane looks at one block's flag; the
+    // read is on its way beside those of the first sums (waited for before
+    // them it took 0.25 of 6 us, 0.08 here).
+    const int gave_up = lane < g.split ? *cl.map_shared_rank(&abort_s, lane) : 0;
+    bool whole = false;
+    const bool in = o0 + tid < g.p.cout;
     const int lo = rank * n / g.split, hi = (rank + 1) * n / g.split;
-    const float b = bias ? ld(bias + o0 + tid) : 0.f;
+    const float b = bias && in ? ld(bias + o0 + tid) : 0.f;
     T* yp = y + p0 * g.p.ys + g.p.yo + o0 + tid;
 #pragma unroll 1
     for (int p = lo; p < hi; p += 4) {  // four pixels' reads at a time
@@ -748,9 +755,10 @@ row_kernel(RGeom g, const __grid_constant__ CUtensorMap xmap, const __grid_const
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += b;
       norm::act_v<4>(g.p.act, v);
+      if (p == lo) whole = __all_sync(0xffffffffu, gave_up == 0);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (p + e < hi) yp[(p + e) * g.p.ys] = from_f<T>(v[e]);
+        if (whole && in && p + e < hi) yp[(p + e) * g.p.ys] = from_f<T>(v[e]);
     }
   }
   cl.sync();  // no block leaves while others read its sums
