@@ -24,6 +24,7 @@ inline int64_t pitch_of(int64_t cin) { return (cin + kBlock - 1) / kBlock * kBlo
 
 enum class Plan { Row, Tile };
 Plan plan(const Pw& g);
+bool by_pairs(const Pw& g);  // Plan::Tile: by pairs of thread blocks
 // rows of codes that are no multiple of 16 bytes are copied to rows that are
 size_t workspace_bytes(const Pw& g);
 

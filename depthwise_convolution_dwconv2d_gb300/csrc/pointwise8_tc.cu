@@ -896,16 +896,8 @@ cudaError_t run_t(const Pw& g, int64_t ldx, const uint8_t* x, bool copied, const
     }
   }
   static std::atomic<uint64_t> ready_tile{0}, ready_pair{0};
-  const int64_t tiles = tiles_of(g, kM, Tile::kN), pairs = tiles_of(g, 2 * kM, Pair::kN);
-  if (tiles >= (int64_t(1) << 31)) return cudaErrorNotSupported;
-  // Measured: a call of tiles takes 2.9 us and per round 0.4 us a block of
-  // channels and 1.35; a call of pairs (four times the products) 3.8, 0.6 and
-  // 1.6. In tiles against pairs: 12544 pixels, 512 -> 512 channels 12.5 and
-  // 13.8 us, 3136, 1024 -> 1024 12.2 and 10.9, 200704, 128 -> 128 22.3 and
-  // 25.3, 10569, 2688 -> 1296 68.3 and 57.5, 8192, 4096 -> 4096 195 and 144.
-  const int64_t by_tile = 2900 + (tiles + 151) / 152 * (g.nkb * 400 + 1350);
-  const int64_t by_pair = 3800 + (pairs + 75) / 76 * (g.nkb * 600 + 1600);
-  if (by_pair < by_tile) return launch_tiles<Pair, T>(pair_kernel<T>, true, ready_pair, g, ldx, x, copied, sx, w, sw, bias, y, s);
+  if (tiles_of(g, kM, Tile::kN) >= (int64_t(1) << 31)) return cudaErrorNotSupported;
+  if (by_pairs(g)) return launch_tiles<Pair, T>(pair_kernel<T>, true, ready_pair, g, ldx, x, copied, sx, w, sw, bias, y, s);
   return launch_tiles<Tile, T>(tile_kernel<T>, false, ready_tile, g, ldx, x, copied, sx, w, sw, bias, y, s);
 }
 
@@ -919,6 +911,18 @@ Plan plan(const Pw& g) {
   const int np = row_pixels(g), split = split_of(g, np);
   if ((int64_t)((g.nkb + split - 1) / split) * np * 4 > 32 * 1024) return Plan::Tile;  // its table of scales
   return g.rows <= 32 || (g.nkb >= 10 && tiles_of(g, np, 128) <= 96) ? Plan::Row : Plan::Tile;
+}
+
+bool by_pairs(const Pw& g) {
+  const int64_t tiles = tiles_of(g, kM, Tile::kN), pairs = tiles_of(g, 2 * kM, Pair::kN);
+  // Measured: a call of tiles takes 2.9 us and per round 0.4 us a block of
+  // channels and 1.35; a call of pairs (four times the products) 3.8, 0.6 and
+  // 1.6. In tiles against pairs: 12544 pixels, 512 -> 512 channels 12.5 and
+  // 13.8 us, 3136, 1024 -> 1024 12.2 and 10.9, 200704, 128 -> 128 22.3 and
+  // 25.3, 10569, 2688 -> 1296 68.3 and 57.5, 8192, 4096 -> 4096 195 and 144.
+  const int64_t by_tile = 2900 + (tiles + 151) / 152 * (g.nkb * 400 + 1350);
+  const int64_t by_pair = 3800 + (pairs + 75) / 76 * (g.nkb * 600 + 1600);
+  return by_pair < by_tile;
 }
 
 cudaError_t run_tc(const Pw& g, int64_t ldx, const uint8_t* x, bool copied, const float* sx, const uint8_t* w, const float* sw,

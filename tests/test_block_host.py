@@ -1,8 +1,16 @@
 """The entry points around a block's layers on the host: which kernel a call maps to on both sides of each bound."""
+import os
+import shutil
+import subprocess
+
 import pytest
 
+from block_pairs import PAIRS
 from depthwise_convolution_dwconv2d_gb300 import binding as B
 from depthwise_convolution_dwconv2d_gb300 import build as BLD
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "depthwise_convolution_dwconv2d_gb300", "csrc")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -58,3 +66,20 @@ def test_weights_too_small_for_their_sizes_are_refused():
             B.make_weight8(200, 300, codes(200, 384), bad)
     B.make_weight8(200, 300, 0x1000, 0x2000)  # addresses: nothing to look at
     B.make_weight8(200, 300, codes(200, 384), torch.empty(3, 3))
+
+
+def test_products_that_pairs_take(tmp_path):
+    """The GPU tests' products by pairs of thread blocks are that (the plan's name does not tell them from tiles)."""
+    nvcc = shutil.which("nvcc") or ("/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else None)
+    if nvcc is None:
+        pytest.skip("nvcc not found")
+    exe = str(tmp_path / "check_pointwise8")
+    r = subprocess.run([nvcc, "-std=c++17", "-O1", "-gencode", "arch=compute_103a,code=sm_103a", "--expt-relaxed-constexpr",
+                        "-I", os.path.join(ROOT, "include"), "-I", CSRC, os.path.join(ROOT, "tests", "host", "check_pointwise8.cu"),
+                        os.path.join(CSRC, "tma.cu"), "-o", exe, "-lcuda"], capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stderr[-3000:]
+    r = subprocess.run([exe] + [str(n) for c in PAIRS for n in c[:3]], capture_output=True, text=True, timeout=60)
+    got = [line.split() for line in r.stdout.splitlines()]
+    assert got == [["pair", str(c[5]), str(-(-c[1] // 128))] for c in PAIRS]
+    assert any(c[5] > 1 and -(-c[1] // 128) % 2 for c in PAIRS) and any(c[5] > 1 and -(-c[1] // 128) % 2 == 0 for c in PAIRS)
+    assert all(B.dwconv2d_pointwise8_plan_name(*c[:3]) == "tile" for c in PAIRS)

@@ -5,9 +5,10 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import block_ref as K
+from block_pairs import PAIRS
 import train_ref as R
 from depthwise_convolution_dwconv2d_gb300 import binding as B
-from test_gpu_block import EPS, _lib, _no_wait_gave_up, act8_of, filled, gen, normal, offset_view, room, run_clip, weight8_of  # noqa: F401
+from test_gpu_block import EPS, _lib, _no_wait_gave_up, act8_of, check_product, filled, gen, normal, offset_view, room, run_clip, weight8_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -46,6 +47,26 @@ def test_pairs_leave_nothing_behind():
                     call()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for (_, o), w in zip(calls, want))
+
+
+@pytest.mark.parametrize("rows,cin,cout,dtype,act,rounds", PAIRS)
+def test_pairs(rows, cin, cout, dtype, act, rounds):
+    y = check_product(rows, cin, cout, dtype, act)
+    assert torch.equal(check_product(rows, cin, cout, dtype, act), y)
+
+
+def test_pairs_to_slices():
+    """Several tiles per pair into channels of wider rows, in vectors and in pieces: what lies between is not written."""
+    rows, cin, cout = 2700, 896, 2816
+    g = gen(2)
+    x8, w8 = act8_of(normal(g, rows, cin)), weight8_of(normal(g, cout, cin, std=0.05))
+    want, slack = K.product(*x8.tensors, *w8.tensors, None, "none")
+    for off, total, dtype in ((16, 2848, "bf16"), (3, 2823, "f16"), (8, 2832, "f32")):
+        y = filled(rows, total, dtype=dtype)
+        B.dwconv2d_pointwise8(x8, w8, None, "none", y, None, 0, off, total)
+        R.within(y[:, off:off + cout], want, slack, dtype)
+        y[:, off:off + cout] = -7
+        assert bool((y == -7).all())
 
 
 # ---- RMS norm, backward ------------------------------------------------------------
