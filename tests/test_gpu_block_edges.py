@@ -92,3 +92,72 @@ def test_rms_norm_bwd_keeps_its_range_in_every_kernel(size, gsize):
         R.within(gx, wx, sx, dtype, f"gx {rows}x{C}")
         R.within(gg, wg, sg, dtype, f"ggamma {rows}x{C}")
         assert intact()
+
+
+@pytest.mark.parametrize("rows,C,dtype,apart", [(7_600_000, 7, "f32", False), (1_000_003, 7, "f32", True), (160_000, 1032, "bf16", False),
+                                                (300_001, 77, "f16", False), (70_000, 77, "f16", True), (120_000_001, 1, "bf16", False),
+                                                (20_000, 9001, "bf16", False)])
+def test_rms_norm_bwd_long_chains(rows, C, dtype, apart):
+    """ggamma where a thread adds up hundreds to thousands of rows. Of small whole numbers every partial sum is exact in 32
+    bits, so no row may be missing or counted twice. Of others: at most 4096 additions in a thread, 64 rows of a block and
+    join's 16 + 7 behind them, a product and r's per term."""
+    g = gen(C)
+    d = B.make_rms_desc(rows, C, EPS, dtype)
+    ws, intact = room(B.dwconv_rms_norm_bwd_workspace_size(d))
+
+    def ggamma(h, gy, rstd):
+        if apart:
+            h = offset_view(h)
+        gg = filled(C, dtype=dtype)
+        B.dwconv_rms_norm_bwd(d, h, gy, None, rstd, None, None, gg, ws)
+        assert intact()
+        return gg
+
+    h = (2 * torch.randint(0, 2, (rows, C), generator=g, device="cuda", dtype=torch.int8) - 1).to(R.DT[dtype])
+    gy = torch.randint(-1, 2, (rows, C), generator=g, device="cuda", dtype=torch.int8).to(R.DT[dtype])
+    exact = (h.to(torch.int8) * gy.to(torch.int8)).sum(0, dtype=torch.int64)
+    assert int(exact.abs().max()) < 2 ** 24
+    assert torch.equal(ggamma(h, gy, torch.ones(rows, device="cuda")), exact.float().to(R.DT[dtype]))
+    h *= 1 + torch.rand(C, generator=g, device="cuda").to(h.dtype)
+    rstd = 0.5 + torch.rand(rows, generator=g, device="cuda")
+    got = ggamma(h, gy, rstd)
+    want, size = (torch.stack([f(gy[:, c].double() * (h[:, c].double() * rstd.double())).sum() for c in range(C)]) for f in (lambda v: v, torch.abs))
+    R.within(got, want, (4096 + 64 + 16 + 7 + 3) * K.U * size, dtype)
+
+
+# ---- clipping -----------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype,big", [("f32", 1e30), ("bf16", 1e30), ("f32", 1e-30), ("bf16", 1e-30), ("f32", 1e-42), ("f16", 6e-8)])
+def test_clip_scales_what_lies_beyond_the_range_of_squares(dtype, big):
+    """Every out, where squares leave fp32 on either side: beside ordinary values and alone, clipped hard, little and not at all."""
+    g = gen(4)
+    for std in (0.0, 1.0):
+        grads = [normal(g, 10000, dtype=dtype, std=std), (torch.randn(5001, generator=g, device="cuda") * big).to(R.DT[dtype])]
+        n = float(K.clip(grads, 1.0)[0])
+        for part in (0.5, 0.999, 2.0, 1e-3):
+            most = float(torch.tensor(part * max(n, 1e-6)).float())
+            want = K.clip(grads, most)[1]
+            outs = [torch.full_like(t, -7) for t in grads]
+            got = run_clip(grads, most, outs)
+            assert abs(float(got) - n) <= float(K.slack_norm(n)) + 2.0 ** -149
+            for o, w in zip(outs, want):
+                R.within(o, w, 2 * K.slack_norm(w.abs()), dtype, f"{big} {std} {part}")
+
+
+@pytest.mark.parametrize("sizes", [[5000, 77], [700_000, 77]])  # in one cluster, in two launches
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_clip_by_infinity_changes_no_other_gradient(sizes, bad):
+    """max_norm INFINITY: an infinity or a NaN shows in the norm and stays where it is; all else is written as it was."""
+    for dtype in ("f32", "f16", "bf16"):
+        g = gen(1)
+        grads = [normal(g, n, dtype=dtype) for n in sizes]
+        grads[0][77] = bad
+        outs = [torch.full_like(t, -7) for t in grads]
+        n = run_clip(grads, float("inf"), outs)
+        assert bool(n.isnan()) if bad != bad else float(n) == float("inf")
+        for o, t in zip(outs, grads):
+            assert torch.equal(o.nan_to_num(nan=123.0), t.nan_to_num(nan=123.0))
+        before = [t.clone() for t in grads]
+        run_clip(grads, float("inf"))
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(grads, before))
