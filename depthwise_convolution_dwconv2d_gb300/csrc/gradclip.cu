@@ -40,8 +40,14 @@ namespace cg = cooperative_groups;
 constexpr int kNT = 512, kWarps = kNT / 32;
 constexpr int kUnit = 512;              // elements of a unit: 16 per lane
 constexpr int64_t kBlocks = 152 * 4;    // what the GPU holds at once
-constexpr int kCluster = 8;             // blocks of a cluster, units that it takes by itself
-constexpr int kAlone = 8 * kCluster * kWarps;
+constexpr int kCluster = 8;             // blocks of a cluster
+// Units that one cluster takes by itself: one a warp. fp32, 4 tensors, in one
+// launch against two, back to back in a graph / whole calls with a cold L2, us:
+// 2820 elements 4.6 / 16.3 against 5.0 / 20.9; 65536 5.4 / 16.2 against 5.7 /
+// 19.5; 131072 6.9 / 18.1 against 5.9 / 19.8; 262144 9.2 / 21.8 against 5.7 /
+// 20.1; 524288 14.3 / 28.1 against 6.2 / 19.5. 100 tensors: 65536 7.7 / 21.0
+// against 6.4 / 22.4, 131072 8.9 / 22.6 against 6.8 / 22.3.
+constexpr int kAlone = kCluster * kWarps;
 // Tensors per launch, by sizes of the parameters (1.3 to 31 KB): a launch with
 // 31 KB of them takes 6 us longer than one with 4.
 constexpr int kSmall = 40, kMid = 120, kMore = 240, kMany = 480, kBig = 960;
@@ -405,7 +411,6 @@ cudaError_t run(int count, const dwconv_grad_t* grads, float most, float* norm, 
   for (int scale = 0; scale < 2 && e == cudaSuccess; ++scale) {
     int slot0 = 0;
     e = over_launches(count, grads, [&](int i, int j, int used, int64_t units) {
-      // all in one cluster: 2820 elements 8.9 us in two launches, 5.8 in one
       if (launches == 1 && units <= kAlone && used <= kMid)
         return scale ? cudaSuccess
                : used <= kSmall ? launch_alone<kSmall>(grads, i, j, units, most, norm, s)

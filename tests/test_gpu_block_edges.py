@@ -161,3 +161,20 @@ def test_clip_by_infinity_changes_no_other_gradient(sizes, bad):
         before = [t.clone() for t in grads]
         run_clip(grads, float("inf"))
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(grads, before))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_clip_around_the_choice_of_launches(dtype):
+    """One cluster takes 128 units of 512 elements and 120 tensors: sizes on both sides, against 64 bits, repeated bitwise."""
+    for sizes in ([65536], [65537], [512] * 120, [512] * 121, [500] * 119 + [4608], [500] * 119 + [4609], [131072], [70001, 3], [262145]):
+        g = gen(len(sizes))
+        grads = [normal(g, n, dtype=dtype, std=0.1) for n in sizes]
+        most = float(torch.tensor(0.3 * float(K.clip(grads, 1.0)[0])).float())
+        n, want = K.clip(grads, most)
+        outs = [torch.full_like(t, -7) for t in grads]
+        got = run_clip(grads, most, outs)
+        assert abs(float(got) - float(n)) <= float(K.slack_norm(n)), sizes[-1]
+        for o, w in zip(outs, want):
+            R.within(o, w, 2 * K.slack_norm(w.abs()), dtype)
+        again = [torch.full_like(t, -7) for t in grads]
+        assert torch.equal(run_clip(grads, most, again), got) and all(torch.equal(a, o) for a, o in zip(again, outs))
