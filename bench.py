@@ -29,8 +29,9 @@ With no flags every workload is timed, one after another, and ONE JSON line
 is printed (rank 0). Its headline (``value``, ``config``, ``roofline``,
 ``e2e``, ``cpu_baseline``) is the large-kernel sweep, in TFLOP/s of
 valid-tap FMAs (the largest workload, and the compute-bound one);
-``configs`` holds a record per workload with ms, GB/s, TFLOP/s, a roofline
-for every kernel family, an end-to-end figure and the oracle's CPU time.
+``configs`` holds each workload's figures in short. Its whole record (ms,
+GB/s, TFLOP/s, a roofline for every kernel family, every layer, an end-to-end
+figure and the oracle's CPU time) goes to stderr, behind "details: ".
 ``value`` is measured with every input resident in HBM and L2 flushed before
 every call; ``e2e`` is the same metric with pinned host buffers copied in and
 results copied out inside the timed region (copies on two side streams,
@@ -912,6 +913,46 @@ def gpu_arm(args, names, rank, world):
     return recs, items_of, fma_tflops, peaks
 
 
+def summary(r):
+    """A workload's figures for the metric line. The whole record (every family's roofline, every layer) is some
+    thousand characters a workload: with all of them the line had 43 KB and was read back cut. It goes to stderr."""
+    pick = lambda d, *keys: {k: d[k] for k in keys if d and k in d}  # noqa: E731
+    return {**pick(r, "value", "unit", "ms_per_step", "dtype", "gpu_launches"),
+            "roofline": pick(r.get("roofline"), "bound", "achieved", "unit", "frac", "kernel", "share"),
+            "e2e": (r.get("e2e") or {}).get("value"), "graph_replay_ms": (r.get("graph_replay") or {}).get("ms_per_step"),
+            "cpu_value": (r.get("cpu_baseline") or {}).get("value")}
+
+
+def metric_line(args, recs, head, world, fma_tflops):
+    """The one line: the headline workload's figures, the others in short."""
+    h = recs[head]
+    head_clocks = clock_summary(h["clock_lines"])
+    lines = [ln for r in recs.values() for ln in r["clock_lines"]]
+    return {
+        "metric": METRIC, "value": h["value"], "unit": h["unit"], "n_gpus": world, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": h["ms_per_step"], "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None, "dtype": h["dtype"],
+        "data": "synthetic (SplitMix64 + Box-Muller, seed 0)",
+        "config": {"workload": h["workload"], "name": head,
+                   **({"layers": args.layers} if args.layers else {}),
+                   **({"batch_override": args.batch} if args.batch else {}),
+                   "parallelism": f"replicas x{world} (no collective)",
+                   "l2": "flushed before every call (2x L2 written, then a clean 2x L2 buffer read: inputs "
+                         "not cached, no dirty lines left); inputs resident in HBM",
+                   "step_bytes": h["step_bytes"], "step_fma_valid": h["step_fma_valid"],
+                   "GBps": h["GBps"], "tflops_valid": h["TFLOPs_valid"]},
+        "roofline": h["roofline"],
+        "e2e": h["e2e"],
+        "gpu_launches": h["gpu_launches"],
+        "gpu_launches_all_workloads": sum(r["gpu_launches"] for r in recs.values()),
+        "clocks": head_clocks or clock_summary(lines),
+        "clocks_all_workloads": clock_summary(lines),
+        "fp32_fma_probe_tflops": round(fma_tflops, 2),
+        **({"cpu_baseline": h["cpu_baseline"]} if "cpu_baseline" in h else {}),
+        "configs": {n: summary(r) for n, r in recs.items()},
+    }
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -967,33 +1008,9 @@ def main():
         if not args.no_cpu_baseline:
             for n in recs:
                 recs[n]["cpu_baseline"] = cpu_baseline(n, items_of[n], args.cpu_seconds, recs[n]["unit"])
-        h = recs[head]
-        head_clocks = clock_summary(h["clock_lines"])
-        lines = [ln for r in recs.values() for ln in r.pop("clock_lines")]
-        out = {
-            "metric": METRIC, "value": h["value"], "unit": h["unit"], "n_gpus": world, "steps": args.steps,
-            "warmup": args.warmup, "ms_per_step": h["ms_per_step"], "higher_is_better": True,
-            "scaling": "weak", "vs_baseline": None, "dtype": h["dtype"],
-            "data": "synthetic (SplitMix64 + Box-Muller, seed 0)",
-            "config": {"workload": h["workload"], "name": head,
-                       **({"layers": args.layers} if args.layers else {}),
-                       **({"batch_override": args.batch} if args.batch else {}),
-                       "parallelism": f"replicas x{world} (no collective)",
-                       "l2": "flushed before every call (2x L2 written, then a clean 2x L2 buffer read: inputs "
-                             "not cached, no dirty lines left); inputs resident in HBM",
-                       "step_bytes": h["step_bytes"], "step_fma_valid": h["step_fma_valid"],
-                       "GBps": h["GBps"], "tflops_valid": h["TFLOPs_valid"]},
-            "roofline": h["roofline"],
-            "e2e": h["e2e"],
-            "gpu_launches": h["gpu_launches"],
-            "gpu_launches_all_workloads": sum(r["gpu_launches"] for r in recs.values()),
-            "clocks": head_clocks or clock_summary(lines),
-            "clocks_all_workloads": clock_summary(lines),
-            "fp32_fma_probe_tflops": round(fma_tflops, 2),
-            **({"cpu_baseline": h["cpu_baseline"]} if "cpu_baseline" in h else {}),
-            "configs": recs,
-        }
-        print(json.dumps(out))
+        print("details: " + json.dumps({n: {k: v for k, v in r.items() if k != "clock_lines"} for n, r in recs.items()}),
+              file=sys.stderr, flush=True)
+        print(json.dumps(metric_line(args, recs, head, world, fma_tflops)))
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
