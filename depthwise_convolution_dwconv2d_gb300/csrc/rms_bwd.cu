@@ -15,7 +15,9 @@
 // the workspace and a second launch adds them in a fixed order. Rows of more
 // channels than 512 threads hold, and tensors that do not begin alike, are
 // read element by element, twice, by one block, and a kernel of its own takes
-// their ggamma, down the columns.
+// their ggamma, down the columns. Both are laid out for wide rows (2000 x 30000
+// bf16 with gres 354 us, 72 the floor); narrow ones that do not begin alike
+// leave most of their threads idle (200704 x 128 bf16 560 us against 45).
 //
 // Bound by memory: h, gy (and gres) read once, gx written once.
 #include "rms.cuh"
